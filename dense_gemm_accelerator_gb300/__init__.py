@@ -54,6 +54,15 @@ SIGNATURES = {
                                   _I64, _VP]),
     "dga_spmv_csr": (_CI, [_I64, _I64, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "dga_spmv_csr_workspace_size": (_SZ, [_I64, _I64]),
+    "dga_mx_quantize": (_CI, [_CI, _CI, _CI, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP]),
+    "dga_mx_row_bytes": (_I64, [_I64]),
+    "dga_mx_scales_size": (_SZ, [_CI, _I64, _I64]),
+    "dga_mx_dequantize": (_CI, [_CI, _CI, _I64, _I64, _VP, _I64, _VP, _VP, _VP, _I64, _VP]),
+    "dga_mx_gemm": (_CI, [_CI, _CI, _I64, _I64, _I64, _VP, _VP, _I64, _VP, _VP, _VP, _I64, _VP, _VP,
+                          _VP, _VP, _I64, _VP, _VP]),
+    "dga_mx_linear": (_CI, [_CI, _CI, _CI, _I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP,
+                            _VP, _VP, _I64, _VP, _SZ, _VP]),
+    "dga_mx_linear_workspace_size": (_SZ, [_CI, _I64, _I64]),
     "dga_probe_fp32_fma": (_CI, [_CI, _I64, _VP, _I64, _VP, _VP]),
     "dga_probe_fp32_fma_out_floats": (_I64, []),
     "dga_probe_int8_mma": (_CI, [_I64, _VP, _I64, _VP, _VP]),
@@ -175,6 +184,42 @@ def dga_spmv_csr(rows, cols, nnz, row_offsets, column_indices, values, alpha, x,
 
 def dga_spmv_csr_workspace_size(rows, nnz):
     return lib().dga_spmv_csr_workspace_size(rows, nnz)
+
+
+def dga_mx_quantize(format, in_dtype, transpose, rows, cols, X, ldx, tensor_scale, codes, ld_codes,
+                    scales, stream):
+    return lib().dga_mx_quantize(format, in_dtype, transpose, rows, cols, X, ldx, tensor_scale, codes,
+                                 ld_codes, scales, stream)
+
+
+def dga_mx_row_bytes(K):
+    return lib().dga_mx_row_bytes(K)
+
+
+def dga_mx_scales_size(format, rows, K):
+    return lib().dga_mx_scales_size(format, rows, K)
+
+
+def dga_mx_dequantize(format, out_dtype, rows, cols, codes, ld_codes, scales, tensor_scale, Y, ldy,
+                      stream):
+    return lib().dga_mx_dequantize(format, out_dtype, rows, cols, codes, ld_codes, scales,
+                                   tensor_scale, Y, ldy, stream)
+
+
+def dga_mx_gemm(format, out_dtype, M, N, K, alpha, A_codes, lda, A_scales, A_tensor_scale, B_codes, ldb,
+                B_scales, B_tensor_scale, beta, C, ldc, bias, stream):
+    return lib().dga_mx_gemm(format, out_dtype, M, N, K, alpha, A_codes, lda, A_scales, A_tensor_scale,
+                             B_codes, ldb, B_scales, B_tensor_scale, beta, C, ldc, bias, stream)
+
+
+def dga_mx_linear(format, x_dtype, out_dtype, M, N, K, X, ldx, x_tensor_scale, W_codes, ldw, W_scales,
+                  W_tensor_scale, bias, Y, ldy, workspace, workspace_bytes, stream):
+    return lib().dga_mx_linear(format, x_dtype, out_dtype, M, N, K, X, ldx, x_tensor_scale, W_codes, ldw,
+                               W_scales, W_tensor_scale, bias, Y, ldy, workspace, workspace_bytes, stream)
+
+
+def dga_mx_linear_workspace_size(format, M, K):
+    return lib().dga_mx_linear_workspace_size(format, M, K)
 
 
 def dga_probe_fp32_fma(packed, iters, out, out_floats, flops, stream):
@@ -370,3 +415,7 @@ def linear_backward(X, W, G, need_bias=True):
     dW = gemm(G.t(), X)
     db = sum_rows(G) if need_bias else None
     return dX, dW, db
+
+
+from .mx import (MXFP4, NVFP4, MXTensor, mx_dequantize, mx_gemm, mx_linear_backward,  # noqa: E402,F401
+                 mx_linear_forward, mx_quantize)

@@ -191,6 +191,8 @@ int fail_cuda(cudaError_t e) {
 
 int note_cuda_error(cudaError_t e) { return fail_cuda(e); }
 
+void set_last_launches(int n) { t_last_launches = n; }
+
 cudaError_t current_device_info(DeviceInfo* out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -412,12 +414,13 @@ int dga_last_launch_count(void) { return t_last_launches; }
 int dga_sync_status(dga_stream_t stream) {
     cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail_cuda(e);
-    int st = 0, st_skinny = 0, st_spmv = 0;
+    int st = 0, st_skinny = 0, st_spmv = 0, st_mx = 0;
     e = tc_status_take(&st);
     if (e == cudaSuccess) e = skinny_status_take(&st_skinny);
     if (e == cudaSuccess) e = spmv_status_take(&st_spmv);
+    if (e == cudaSuccess) e = mx_status_take(&st_mx);
     if (e != cudaSuccess) return fail_cuda(e);
-    if (st != 0 || st_skinny != 0) return DGA_ERR_DEVICE_TIMEOUT;
+    if (st != 0 || st_skinny != 0 || st_mx != 0) return DGA_ERR_DEVICE_TIMEOUT;
     return st_spmv != 0 ? DGA_ERR_BAD_INDEX : DGA_OK;
 }
 

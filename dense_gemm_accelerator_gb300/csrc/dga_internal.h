@@ -93,6 +93,54 @@ cudaError_t fma_probe_launch(int packed, int64_t iters, float* out, int sm_count
 cudaError_t naive_probe_launch(int64_t M, int64_t N, int64_t K, const float* A, const float* B,
                                float* C, cudaStream_t stream);
 
+// ---- 4-bit microscaled matrices (layout in mx_common.cuh)
+
+struct MxMatrix {
+    const void* codes;
+    int64_t ld;           // bytes between rows of codes
+    const void* scales;
+    const float* factor;  // device pointer, or null for 1
+};
+
+struct MxQuantArgs {
+    int format, in_dtype;
+    bool transpose;
+    int64_t rows, cols;  // of X
+    const void* X;
+    int64_t ldx;
+    const float* factor;
+    uint8_t* codes;
+    int64_t ld_codes;
+    uint8_t* scales;
+    cudaStream_t stream;
+};
+
+// C <- alpha * fA * fB * A * B^T + beta * C + bias, A: M x K, B: N x K.
+struct MxGemmArgs {
+    int format, out_dtype;
+    int64_t M, N, K;
+    float alpha, beta;
+    MxMatrix A, B;
+    void* C;
+    int64_t ldc;
+    const void* bias;  // N values of the output type, or null
+    bool after_quantize;  // launched right behind the quantisation of A
+    cudaStream_t stream;
+};
+
+cudaError_t mx_quantize_launch(const MxQuantArgs& a, const DeviceInfo& dev);
+cudaError_t mx_dequantize_launch(int format, int out_dtype, const MxMatrix& q, int64_t rows, int64_t K,
+                                 void* Y, int64_t ldy, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t mx_gemm_launch(const MxGemmArgs& a, const DeviceInfo& dev, int* launches);
+// Reads and clears this device's status word of the 4-bit products.
+cudaError_t mx_status_take(int* status);
+
+// Sets what dga_last_launch_count() returns on this host thread.
+void set_last_launches(int n);
+
+// The driver's tensor-map encoder as an opaque pointer, or null.
+void* tensor_map_encoder();
+
 bool tc_supports(const GemmArgs& a);
 size_t tc_workspace_size(const GemmArgs& a);
 // tc_workspace_size plus what the split last wave can use (optional)

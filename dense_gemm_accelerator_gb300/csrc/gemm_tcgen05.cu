@@ -1600,6 +1600,8 @@ cudaError_t launch_pack_f32(const void* src, int64_t ld_src, bool transposed, in
 
 }  // namespace
 
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
+
 bool tc_supports(const GemmArgs& a) {
     const bool fp = (a.in_dtype == DGA_BF16 && (a.out_dtype == DGA_F32 || a.out_dtype == DGA_BF16)) ||
                     (a.in_dtype == DGA_F16 && (a.out_dtype == DGA_F32 || a.out_dtype == DGA_F16)) ||

@@ -1,0 +1,666 @@
+// mx_gemm.cu -- products of 4-bit microscaled matrices on the tensor cores.
+//
+//   C <- alpha * fA * fB * sum_k a(i,k) b(j,k) + beta * C + bias(j)
+//
+// a(i,k) and b(j,k) are E2M1 codes times their block scales, fA and fB the
+// tensors' fp32 factors.  tcgen05.mma's block-scaled kinds multiply the codes
+// and the scales inside the MMA and accumulate in fp32: the products of codes
+// and scales are exact, so fp32 accumulation is the only rounding before the
+// epilogue's.
+//
+// Two kernels, both fed by TMA (codes as 128-byte swizzle rows of 256 values;
+// scale tiles of 512 bytes, copied from shared to tensor memory by
+// tcgen05.cp just before the MMAs that use them):
+//
+//   pair    a cluster of two CTAs per 256 x 256 tile of C, persistent; for
+//           many rows, where the tensor cores' rate is the bound
+//   skinny  one CTA per 128 rows of B and all (up to 256) rows of A, with the
+//           operands' roles swapped: B's rows fill the MMA's M = 128, A's rows
+//           its N, so that a few rows of A waste nothing; the K axis is shared
+//           by a cluster and its parts joined through distributed shared
+//           memory in a fixed order.  For few rows the bytes of B are the
+//           bound.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "dga_internal.h"
+#include "epilogue.cuh"
+#include "mx_common.cuh"
+#include "ptx.cuh"
+
+namespace dga {
+
+__device__ int g_mx_status;  // non-zero: a bounded wait expired (role code)
+
+namespace {
+
+constexpr uint64_t kWaitLimitNs = 4000000000ull;  // 4 s
+constexpr int kRowBytes = 128;                    // one stage of a row: 256 codes
+constexpr int kStageK = 256;
+enum : int { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3 };
+
+// Scale tiles (4 blocks) of one stage's 256 values.
+__host__ __device__ constexpr int scale_tiles(int format) { return kStageK / (4 * mx_block(format)); }
+
+struct MxParams {
+    int64_t M, N;
+    void* C;
+    int64_t ldc;
+    float alpha, beta;
+    const float* fa;
+    const float* fb;
+    const void* bias;
+    uint32_t tiles_m, tiles_n, num_tiles, num_kb, group_m;
+};
+
+__device__ __forceinline__ void record_failure(int role, volatile int* abort_flag) {
+    atomicCAS(&g_mx_status, 0, role);
+    *abort_flag = 1;
+}
+
+__device__ __forceinline__ float total_alpha(const MxParams& p) {
+    float a = p.alpha;
+    if (p.fa != nullptr) a *= __ldg(p.fa);
+    if (p.fb != nullptr) a *= __ldg(p.fb);
+    return a;
+}
+
+template <typename TOut>
+__device__ __forceinline__ void put(const MxParams& p, float alpha, int64_t row, int64_t col, float acc) {
+    TOut* dst = static_cast<TOut*>(p.C) + row * p.ldc + col;
+    const float old = p.beta != 0.0f ? OutT<TOut>::load(dst) : 0.0f;
+    const float bv = p.bias != nullptr ? OutT<TOut>::load(static_cast<const TOut*>(p.bias) + col) : 0.0f;
+    OutT<TOut>::store(dst, axpby(alpha, acc, p.beta, old) + bv);
+}
+
+// ---- the pair kernel -------------------------------------------------------------
+
+constexpr int kPairStages = 5;
+
+template <int kFormat>
+struct PairPlan {
+    static constexpr int kSf = scale_tiles(kFormat);
+    static constexpr uint32_t kA = 128 * kRowBytes;
+    static constexpr uint32_t kB = 128 * kRowBytes;
+    static constexpr uint32_t kSfa = kSf * kMxTileBytes;
+    static constexpr uint32_t kSfb = 2 * kSf * kMxTileBytes;
+    static constexpr uint32_t kStage = kA + kB + kSfa + kSfb;
+    static constexpr uint32_t kBar = kPairStages * kStage;
+    // full[S], empty[S], acc_full[2], acc_free, drain, then tmem slot + abort flag
+    static constexpr uint32_t kBarBytes = (2 * kPairStages + 4) * 8 + 16;
+    static constexpr uint32_t kEpi = (kBar + kBarBytes + 127) / 128 * 128;
+    static constexpr uint32_t kTotal = kEpi + 4 * 32 * 33 * 4;
+    static constexpr uint32_t kLaunch = kTotal + 1024;
+    // tensor memory: two accumulators of 256 columns that share 48 (the
+    // scales of a stage take the last 48 of the 512): accumulator 0 in
+    // columns 0-255, accumulator 1 in 208-463.  The epilogue reads the shared
+    // columns first, after which the next tile's MMAs may start.
+    static constexpr uint32_t kAcc1 = 208;
+    static constexpr uint32_t kSfCol = 464;
+    static constexpr uint32_t kSfCols = 12 * kSf;  // 4 for A and 8 for B per scale tile
+    static_assert(kStage % 1024 == 0, "stages keep the swizzle atoms aligned");
+    static_assert(kSfCol + kSfCols <= 512, "scales fit behind the accumulators");
+};
+
+template <typename TOut>
+__device__ __forceinline__ void store_block(const MxParams& p, float alpha, uint32_t* stage, int lane,
+                                            int64_t row_base, int64_t col_base, const uint32_t (&v)[32]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) stage[lane * 33 + j] = v[j];
+    __syncwarp();
+    const int64_t col = col_base + lane;
+    const bool col_ok = col < p.N;
+    const float bv = (p.bias != nullptr && col_ok) ? OutT<TOut>::load(static_cast<const TOut*>(p.bias) + col) : 0.0f;
+#pragma unroll 4
+    for (int i = 0; i < 32; ++i) {
+        const int64_t row = row_base + i;
+        if (col_ok && row < p.M) {
+            TOut* dst = static_cast<TOut*>(p.C) + row * p.ldc + col;
+            const float old = p.beta != 0.0f ? OutT<TOut>::load(dst) : 0.0f;
+            OutT<TOut>::store(dst, axpby(alpha, __uint_as_float(stage[i * 33 + lane]), p.beta, old) + bv);
+        }
+    }
+    __syncwarp();  // the next block reuses the square
+}
+
+__device__ __forceinline__ void tile_coords(uint32_t t, const MxParams& p, uint32_t& tm, uint32_t& tn) {
+    const uint32_t group_size = p.group_m * p.tiles_n;
+    const uint32_t group = t / group_size, first_m = group * p.group_m;
+    const uint32_t gm = min(p.tiles_m - first_m, p.group_m), r = t % group_size;
+    tm = first_m + r % gm;
+    tn = r / gm;
+}
+
+template <int kFormat, typename TOut>
+__global__ void __launch_bounds__(192, 1)
+    mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb,
+                        MxParams p) {
+    using S = PairPlan<kFormat>;
+    constexpr bool kE8M0 = kFormat == DGA_MXFP4;
+    constexpr uint32_t kIdesc0 = idesc_mx(kE8M0, 256, 256, 0), kIdesc2 = idesc_mx(kE8M0, 256, 256, 2);
+    constexpr uint16_t kBothCtas = 0x3;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBar);
+    uint64_t* empty = full + kPairStages;
+    uint64_t* acc_full = empty + kPairStages;
+    uint64_t* acc_free = acc_full + 2;
+    uint64_t* drain = acc_free + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) mbar_init(&acc_full[b], 1);
+        mbar_init(acc_free, 8);  // one lane of each epilogue warp of both CTAs
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmSa);
+        tma_prefetch_desc(&tmSb);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t cluster_id = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            for (uint32_t t = cluster_id; ok && t < p.num_tiles; t += n_clusters) {
+                uint32_t tm, tn;
+                tile_coords(t, p, tm, tn);
+                const int32_t a_row = static_cast<int32_t>(tm * 256 + rank * 128);
+                const int32_t b_row = static_cast<int32_t>(tn * 256 + rank * 128);
+                for (uint32_t kb = 0; kb < p.num_kb; ++kb) {
+                    if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
+                        record_failure(kRoleProducer, abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* dst = smem + stage * S::kStage;
+                    if (leader) mbar_arrive_expect_tx(&full[stage], 2 * S::kStage);
+                    const uint32_t bar = map_to_cta(smem_u32(&full[stage]), 0);
+                    const int32_t x = static_cast<int32_t>(kb * kRowBytes);
+                    const int32_t sx = static_cast<int32_t>(kb * (S::kSf * kMxTileBytes / 8));
+                    tma_load_2d_pair(dst, &tmA, bar, x, a_row);
+                    tma_load_2d_pair(dst + S::kA, &tmB, bar, x, b_row);
+                    tma_load_2d_pair(dst + S::kA + S::kB, &tmSa, bar, sx, a_row / 128);
+                    // each CTA's MMA half reads all 256 of the tile's B scales
+                    tma_load_2d_pair(dst + S::kA + S::kB + S::kSfa, &tmSb, bar, sx, static_cast<int32_t>(tn * 2));
+                    if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+                }
+            }
+            if (!ok) __nanosleep(20000);  // let copies already issued land before teardown
+        }
+    } else if (warp == 1) {
+        if (leader && lane == 0) {
+            uint32_t stage = 0, phase = 0, i = 0, fill = 0;
+            bool ok = true;
+            for (uint32_t t = cluster_id; ok && t < p.num_tiles; t += n_clusters, ++i) {
+                if (i > 0 && !mbar_wait_bounded<true>(acc_free, (i - 1) & 1, abort_flag, kWaitLimitNs)) {
+                    record_failure(kRoleMma, abort_flag);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + (i & 1 ? S::kAcc1 : 0u);
+                for (uint32_t kb = 0; kb < p.num_kb; ++kb) {
+                    if (!mbar_wait_bounded<true>(&full[stage], phase, abort_flag, kWaitLimitNs)) {
+                        record_failure(kRoleMma, abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(smem + stage * S::kStage);
+                    const uint32_t sf_addr = a_addr + S::kA + S::kB;
+                    // MXFP4's scales of a stage take 24 columns: two stages' worth in turn
+                    const uint32_t sfa = tmem + S::kSfCol + (kE8M0 ? (fill & 1) * S::kSfCols : 0u);
+                    const uint32_t sfb = sfa + 4 * S::kSf;
+                    ++fill;
+#pragma unroll
+                    for (int j = 0; j < S::kSf; ++j) {
+                        tc_cp_scales<true>(sfa + 4 * j, smem_desc_scales(sf_addr + j * kMxTileBytes));
+                        tc_cp_scales<true>(sfb + 8 * j, smem_desc_scales(sf_addr + S::kSfa + j * kMxTileBytes));
+                        tc_cp_scales<true>(sfb + 8 * j + 4, smem_desc_scales(sf_addr + S::kSfa + (S::kSf + j) * kMxTileBytes));
+                    }
+                    const uint64_t a_desc = smem_desc_kmajor_sw128(a_addr);
+                    const uint64_t b_desc = smem_desc_kmajor_sw128(a_addr + S::kA);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int j = kE8M0 ? k / 2 : k;  // the scale tile of these 64 values
+                        tc_mma_mx<kE8M0, true>(d, a_desc + 2 * k, b_desc + 2 * k,
+                                               kE8M0 && (k & 1) ? kIdesc2 : kIdesc0, sfa + 4 * j, sfb + 8 * j,
+                                               (kb > 0 || k > 0) ? 1u : 0u);
+                    }
+                    tc_commit_pair_multicast(&empty[stage], kBothCtas);
+                    if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+                tc_commit_pair_multicast(&acc_full[i & 1], kBothCtas);
+            }
+            tc_commit_pair_multicast(drain, 0x1);
+            volatile int never = 0;
+            mbar_wait_bounded(drain, 0, &never, kWaitLimitNs);
+        }
+    } else {
+        const int quarter = warp & 3;
+        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + S::kEpi + (warp - 2) * (32 * 33 * 4));
+        const float alpha = total_alpha(p);
+        uint32_t i = 0;
+        for (uint32_t t = cluster_id; t < p.num_tiles; t += n_clusters, ++i) {
+            uint32_t tm, tn;
+            tile_coords(t, p, tm, tn);
+            const int64_t row_base = static_cast<int64_t>(tm) * 256 + rank * 128 + quarter * 32;
+            const int64_t col0 = static_cast<int64_t>(tn) * 256;
+            if (!mbar_wait_bounded<true>(&acc_full[i & 1], (i >> 1) & 1, abort_flag, kWaitLimitNs)) {
+                record_failure(kRoleEpilogue, abort_flag);
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + lane_base + (i & 1 ? S::kAcc1 : 0u);
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+                // accumulator 0 from its end, 1 from its start: the columns
+                // they share are in the first two blocks
+                const int block = i & 1 ? c : 7 - c;
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(d + block * 32, r);
+                tmem_ld_wait();
+                if (c == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(acc_free), 0));
+                }
+                store_block<TOut>(p, alpha, stage, lane, row_base, col0 + block * 32, r);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();  // no CTA frees TMEM or exits while its peer may still touch it
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ---- the skinny kernel -------------------------------------------------------------
+
+// kN: rows of A the tile holds (16 to 256).  Two CTAs share an SM where the
+// tile is small enough, so that one's start overlaps the other's end.
+template <int kFormat, int kN>
+struct SkinnyPlan {
+    static constexpr int kSf = scale_tiles(kFormat);
+    static constexpr int kSfRows = kN > 128 ? 2 : 1;
+    static constexpr uint32_t kW = 128 * kRowBytes;
+    static constexpr uint32_t kX = kN * kRowBytes;
+    static constexpr uint32_t kSw = kSf * kMxTileBytes;
+    static constexpr uint32_t kSx = kSfRows * kSf * kMxTileBytes;
+    static constexpr uint32_t kStage = kW + kX + kSw + kSx;
+    static constexpr int kCtas = kN <= 64 ? 2 : 1;
+    static constexpr uint32_t kBudget = (kCtas == 2 ? 110u : 220u) * 1024;
+    static constexpr int kStages = kBudget / kStage;
+    static constexpr uint32_t kBar = kStages * kStage;
+    // full[S], empty[S], acc_full, then tmem slot + abort flag
+    static constexpr uint32_t kLaunch = kBar + (2 * kStages + 1) * 8 + 16 + 1024;
+    static constexpr uint32_t kSfCol = kN;  // the scales behind the accumulator
+    static constexpr uint32_t kUsed = kN + 4 * kSf * (1 + kSfRows);
+    static constexpr uint32_t kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
+    static_assert(kStage % 1024 == 0, "stages keep the swizzle atoms aligned");
+    static_assert(kBar >= kN * 128 * 4, "the partial sums fit the ring");
+    static_assert(kStages >= 3, "a ring");
+};
+
+template <int kFormat, int kN, typename TOut>
+__global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
+    mx_gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                          const __grid_constant__ CUtensorMap tmSw, const __grid_constant__ CUtensorMap tmSx,
+                          MxParams p, uint32_t splits) {
+    using S = SkinnyPlan<kFormat, kN>;
+    constexpr bool kE8M0 = kFormat == DGA_MXFP4;
+    constexpr uint32_t kIdesc0 = idesc_mx(kE8M0, 128, kN, 0), kIdesc2 = idesc_mx(kE8M0, 128, kN, 2);
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBar);
+    uint64_t* empty = full + S::kStages;
+    uint64_t* acc_full = empty + S::kStages;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the cluster is one tile's K parts
+    const uint32_t tile = blockIdx.x / splits, part = blockIdx.x % splits;
+    const uint32_t kb0 = part * p.num_kb / splits, kb1 = (part + 1) * p.num_kb / splits;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, S::kTmem);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const int32_t w_row = static_cast<int32_t>(tile * 128);
+            auto load_w = [&](uint32_t stage, uint32_t kb) {
+                uint8_t* dst = smem + stage * S::kStage;
+                mbar_arrive_expect_tx(&full[stage], S::kStage);
+                tma_load_2d(dst, &tmW, &full[stage], static_cast<int32_t>(kb * kRowBytes), w_row);
+                tma_load_2d(dst + S::kW + S::kX, &tmSw, &full[stage], static_cast<int32_t>(kb * (S::kSf * kMxTileBytes / 8)),
+                            static_cast<int32_t>(tile));
+            };
+            auto load_x = [&](uint32_t stage, uint32_t kb) {
+                uint8_t* dst = smem + stage * S::kStage;
+                tma_load_2d(dst + S::kW, &tmX, &full[stage], static_cast<int32_t>(kb * kRowBytes), 0);
+                tma_load_2d(dst + S::kW + S::kX + S::kSw, &tmSx, &full[stage],
+                            static_cast<int32_t>(kb * (S::kSf * kMxTileBytes / 8)), 0);
+            };
+            // a launch right behind the quantisation of A loads B's first
+            // stages before it waits: only A is that kernel's output
+            const uint32_t first = min(kb1 - kb0, static_cast<uint32_t>(S::kStages));
+            for (uint32_t s = 0; s < first; ++s) load_w(s, kb0 + s);
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            for (uint32_t s = 0; s < first; ++s) load_x(s, kb0 + s);
+            uint32_t stage = 0, phase = 0;
+            for (uint32_t kb = kb0 + first; kb < kb1; ++kb) {
+                if (!mbar_wait_bounded(&empty[stage], phase, abort_flag, kWaitLimitNs)) {
+                    record_failure(kRoleProducer, abort_flag);
+                    break;
+                }
+                load_w(stage, kb);
+                load_x(stage, kb);
+                if (++stage == S::kStages) { stage = 0; phase ^= 1; }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            for (uint32_t kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs)) {
+                    record_failure(kRoleMma, abort_flag);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t w_addr = smem_u32(smem + stage * S::kStage);
+                const uint32_t sf_addr = w_addr + S::kW + S::kX;
+                const uint32_t sfw = tmem + S::kSfCol, sfx = sfw + 4 * S::kSf;
+#pragma unroll
+                for (int j = 0; j < S::kSf; ++j) {
+                    tc_cp_scales<false>(sfw + 4 * j, smem_desc_scales(sf_addr + j * kMxTileBytes));
+#pragma unroll
+                    for (int b = 0; b < S::kSfRows; ++b)
+                        tc_cp_scales<false>(sfx + 4 * (S::kSfRows * j + b),
+                                            smem_desc_scales(sf_addr + S::kSw + (b * S::kSf + j) * kMxTileBytes));
+                }
+                const uint64_t w_desc = smem_desc_kmajor_sw128(w_addr);
+                const uint64_t x_desc = smem_desc_kmajor_sw128(w_addr + S::kW);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int j = kE8M0 ? k / 2 : k;
+                    tc_mma_mx<kE8M0, false>(tmem, w_desc + 2 * k, x_desc + 2 * k,
+                                            kE8M0 && (k & 1) ? kIdesc2 : kIdesc0, sfw + 4 * j,
+                                            sfx + 4 * S::kSfRows * j, (kb > kb0 || k > 0) ? 1u : 0u);
+                }
+                tc_commit(&empty[stage]);
+                if (++stage == S::kStages) { stage = 0; phase ^= 1; }
+            }
+            tc_commit(acc_full);
+        }
+    }
+    __syncwarp();
+    // every MMA of this CTA is done, and with them every copy into the ring
+    const bool ok = mbar_wait_bounded(acc_full, 0, abort_flag, kWaitLimitNs);
+    if (!ok) record_failure(kRoleEpilogue, abort_flag);
+    tc_fence_after();
+    const int quarter = warp & 3;
+    const int w_in = quarter * 32 + lane;  // this thread's row of the tile
+    const int64_t col = static_cast<int64_t>(tile) * 128 + w_in;  // a row of B: a column of C
+    const int rows = static_cast<int>(p.M);
+    float* red = reinterpret_cast<float*>(smem);
+    if (warp >= 2 && ok) {
+        const float alpha = total_alpha(p);
+        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+        constexpr int kStep = kN < 32 ? 16 : 32;
+#pragma unroll 1
+        for (int c = 0; c < kN && c < rows; c += kStep) {
+            uint32_t r[kStep];
+            if constexpr (kStep == 16) tmem_ld_32x32b_x16(tmem + lane_base + c, r);
+            else tmem_ld_32x32b_x32(tmem + lane_base + c, r);
+            tmem_ld_wait();
+            if (splits == 1) {
+#pragma unroll
+                for (int j = 0; j < kStep; ++j)
+                    if (c + j < rows && col < p.N) put<TOut>(p, alpha, c + j, col, __uint_as_float(r[j]));
+            } else {
+#pragma unroll
+                for (int j = 0; j < kStep; ++j) red[(c + j) * 128 + w_in] = __uint_as_float(r[j]);
+            }
+        }
+    }
+    if (splits > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 2 && col < p.N) {
+            const float alpha = total_alpha(p);
+            for (int j = static_cast<int>(part); j < rows; j += static_cast<int>(splits)) {
+                const uint32_t addr = smem_u32(red + j * 128 + w_in);
+                float sum = 0.0f;
+                for (uint32_t q = 0; q < splits; ++q) sum += ld_shared_cluster_f32(map_to_cta(addr, q));
+                put<TOut>(p, alpha, j, col, sum);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while another reads its sums
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, S::kTmem);
+    }
+}
+
+// ---- C <- beta C + bias, where there is nothing to multiply -------------------------
+
+template <typename TOut>
+__global__ void __launch_bounds__(256) mx_no_product_kernel(MxParams p) {
+    const int64_t total = p.M * p.N;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * 256)
+        put<TOut>(p, 0.0f, i / p.N, i % p.N, 0.0f);
+}
+
+// ---- host side ------------------------------------------------------------------------
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+cudaError_t make_map(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base,
+                     int64_t inner, int64_t outer, int64_t stride_bytes, uint32_t box_inner, uint32_t box_outer) {
+    auto fn = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+    if (!fn) return cudaErrorNotSupported;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride_bytes)};
+    cuuint32_t box[2] = {box_inner, box_outer};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Codes: rows of ceil(K/2) bytes (past them, and past the last row, the copy
+// fills zeros: the code of 0).
+cudaError_t codes_map(CUtensorMap* map, const MxMatrix& m, int64_t rows, int64_t K, uint32_t box_rows) {
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, m.codes, (K + 1) / 2, rows, m.ld,
+                    kRowBytes, box_rows);
+}
+
+// Scales: one row of 8-byte words per 128 rows of the matrix.
+cudaError_t scales_map(CUtensorMap* map, int format, const MxMatrix& m, int64_t rows, int64_t K, uint32_t box_rows) {
+    const int64_t tiles_k = mx_tiles_k(format, K);
+    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, CU_TENSOR_MAP_SWIZZLE_NONE, m.scales,
+                    tiles_k * (kMxTileBytes / 8), (rows + 127) / 128, tiles_k * kMxTileBytes,
+                    static_cast<uint32_t>(scale_tiles(format) * kMxTileBytes / 8), box_rows);
+}
+
+template <typename Kern>
+cudaError_t launch(Kern kern, unsigned grid, unsigned cluster, int smem, bool pdl, cudaStream_t s,
+                   const CUtensorMap* maps, const MxParams& p, uint32_t splits) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(192);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    if constexpr (std::is_same_v<Kern, void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, MxParams)>)
+        return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p);
+    else
+        return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p, splits);
+}
+
+template <int kFormat, int kN, typename TOut>
+cudaError_t launch_skinny(const MxGemmArgs& a, MxParams p, const DeviceInfo& dev) {
+    using S = SkinnyPlan<kFormat, kN>;
+    CUtensorMap m[4];
+    cudaError_t e = codes_map(&m[0], a.B, a.N, a.K, 128);
+    if (e == cudaSuccess) e = codes_map(&m[1], a.A, a.M, a.K, kN);
+    if (e == cudaSuccess) e = scales_map(&m[2], kFormat, a.B, a.N, a.K, 1);
+    if (e == cudaSuccess) e = scales_map(&m[3], kFormat, a.A, a.M, a.K, S::kSfRows);
+    if (e != cudaSuccess) return e;
+    // parts of K: as many as fill the machine's CTA slots, each at least two stages
+    const int64_t tiles = (a.N + 127) / 128, slots = static_cast<int64_t>(dev.sm_count) * S::kCtas;
+    uint32_t splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= slots && p.num_kb >= splits * 4) splits *= 2;
+    return launch(mx_gemm_skinny_kernel<kFormat, kN, TOut>, static_cast<unsigned>(tiles * splits), splits,
+                  static_cast<int>(S::kLaunch), a.after_quantize, a.stream, m, p, splits);
+}
+
+template <int kFormat, typename TOut>
+cudaError_t launch_pair(const MxGemmArgs& a, MxParams p, const DeviceInfo& dev) {
+    using S = PairPlan<kFormat>;
+    CUtensorMap m[4];
+    cudaError_t e = codes_map(&m[0], a.A, a.M, a.K, 128);
+    if (e == cudaSuccess) e = codes_map(&m[1], a.B, a.N, a.K, 128);
+    if (e == cudaSuccess) e = scales_map(&m[2], kFormat, a.A, a.M, a.K, 1);
+    if (e == cudaSuccess) e = scales_map(&m[3], kFormat, a.B, a.N, a.K, 2);
+    if (e != cudaSuccess) return e;
+    p.tiles_m = static_cast<uint32_t>((a.M + 255) / 256);
+    p.tiles_n = static_cast<uint32_t>((a.N + 255) / 256);
+    p.num_tiles = p.tiles_m * p.tiles_n;
+    // tile rows walked together: their A panels stay in L2 while B passes
+    const double panel = 256.0 * static_cast<double>(a.K) / 2;
+    p.group_m = std::min(p.tiles_m, std::max(8u, std::min(64u, static_cast<uint32_t>(32.0 * 1024 * 1024 / panel))));
+    const unsigned clusters = std::min<unsigned>(p.num_tiles, dev.sm_count / 2);
+    return launch(mx_gemm_pair_kernel<kFormat, TOut>, 2 * clusters, 2, static_cast<int>(S::kLaunch),
+                  a.after_quantize, a.stream, m, p, 1);
+}
+
+template <int kFormat, typename TOut>
+cudaError_t launch_as(const MxGemmArgs& a, const DeviceInfo& dev) {
+    MxParams p{};
+    p.M = a.M;
+    p.N = a.N;
+    p.C = a.C;
+    p.ldc = a.ldc;
+    p.alpha = a.alpha;
+    p.beta = a.beta;
+    p.fa = a.A.factor;
+    p.fb = a.B.factor;
+    p.bias = a.bias;
+    if (a.K == 0 || a.alpha == 0.0f) {
+        const int64_t blocks = std::min<int64_t>((a.M * a.N + 255) / 256, static_cast<int64_t>(dev.sm_count) * 16);
+        mx_no_product_kernel<TOut><<<static_cast<unsigned>(blocks), 256, 0, a.stream>>>(p);
+        return cudaGetLastError();
+    }
+    p.num_kb = static_cast<uint32_t>((a.K + kStageK - 1) / kStageK);
+    if (a.M <= 16) return launch_skinny<kFormat, 16, TOut>(a, p, dev);
+    if (a.M <= 32) return launch_skinny<kFormat, 32, TOut>(a, p, dev);
+    if (a.M <= 64) return launch_skinny<kFormat, 64, TOut>(a, p, dev);
+    if (a.M <= 128) return launch_skinny<kFormat, 128, TOut>(a, p, dev);
+    if (a.M <= 256) return launch_skinny<kFormat, 256, TOut>(a, p, dev);
+    return launch_pair<kFormat, TOut>(a, p, dev);
+}
+
+}  // namespace
+
+cudaError_t mx_gemm_launch(const MxGemmArgs& a, const DeviceInfo& dev, int* launches) {
+    cudaError_t e;
+    const bool mx = a.format == DGA_MXFP4;
+    switch (a.out_dtype) {
+    case DGA_F32: e = mx ? launch_as<DGA_MXFP4, float>(a, dev) : launch_as<DGA_NVFP4, float>(a, dev); break;
+    case DGA_BF16: e = mx ? launch_as<DGA_MXFP4, __nv_bfloat16>(a, dev) : launch_as<DGA_NVFP4, __nv_bfloat16>(a, dev); break;
+    default: e = mx ? launch_as<DGA_MXFP4, __half>(a, dev) : launch_as<DGA_NVFP4, __half>(a, dev); break;
+    }
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+cudaError_t mx_status_take(int* status) {
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_mx_status, sizeof v);
+    if (e != cudaSuccess) return e;
+    if (v != 0) {
+        int zero = 0;
+        e = cudaMemcpyToSymbol(g_mx_status, &zero, sizeof zero);
+    }
+    *status = v;
+    return e;
+}
+
+}  // namespace dga

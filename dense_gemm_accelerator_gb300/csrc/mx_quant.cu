@@ -1,0 +1,382 @@
+// mx_quant.cu -- a matrix to 4-bit microscaled form and back.
+//
+// For each block of 32 (MXFP4) or 16 (NVFP4) consecutive values of a row,
+// with m = max |x| over the block:
+//   MXFP4  scale 2^e, e = floor(log2 m) - 2 held to [-127, 127] (2 being the
+//          exponent of E2M1's largest value): the MX specification's rule
+//   NVFP4  scale s = E4M3(min(448, m / (6 g))), g the tensor's factor (1 if
+//          there is none), rounded to nearest even; the unit is s g
+//   code   E2M1(x / unit), nearest even, magnitudes over 6 becoming 6
+// A block with an infinity or a NaN gets a NaN scale, so that it reads back
+// as NaN; an all-zero block gets the smallest scale.
+//
+// Every step is exact or correctly rounded in fp32, so the codes and scales
+// are those of the definition, whatever the order of the work: 2^-e is a
+// power of two; x / unit is the correctly rounded quotient.
+//
+// Bound by memory: 2 or 4 bytes read and 0.53 or 0.56 written per value.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "dga_internal.h"
+#include "mx_common.cuh"
+
+namespace dga {
+namespace {
+
+template <typename T> struct MxIn;
+template <> struct MxIn<float> {
+    __device__ __forceinline__ static float f(float v) { return v; }
+};
+template <> struct MxIn<__nv_bfloat16> {
+    __device__ __forceinline__ static float f(__nv_bfloat16 v) { return __bfloat162float(v); }
+};
+template <> struct MxIn<__half> {
+    __device__ __forceinline__ static float f(__half v) { return __half2float(v); }
+};
+
+// Magnitude bits of x: ordered like |x|, with infinity and NaN on top.
+__device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// One block's scale byte and what its values are divided by: MXFP4
+// multiplies by `inv`, the exact 2^-e; NVFP4 divides by `unit`.
+struct BlockScale {
+    uint8_t byte;
+    float unit, inv;
+};
+
+template <int kFormat>
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g) {
+    BlockScale b;
+    const bool finite = amax_bits < 0x7f800000u;
+    if constexpr (kFormat == DGA_MXFP4) {
+        // biased exponent of the scale: floor(log2 m) + 127 - 2, at least 0
+        // (a subnormal m has exponent field 0); at most 252
+        const uint32_t e = amax_bits >> 23;
+        const uint32_t s = e > 2 ? e - 2 : 0;
+        b.byte = finite ? static_cast<uint8_t>(s) : uint8_t(0xff);
+        b.inv = finite ? __uint_as_float((254u - s) << 23) : 0.0f;
+        b.unit = 0.0f;  // not used
+    } else {
+        const float r = __fdiv_rn(__uint_as_float(amax_bits), __fmul_rn(6.0f, g));
+        uint16_t two;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(r));
+        b.byte = finite ? static_cast<uint8_t>(two & 0xff) : uint8_t(0x7f);
+        uint32_t h2;  // the scale back as fp16 (exact)
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
+        const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(h2 & 0xffff)));
+        b.unit = finite ? __fmul_rn(s, g) : 0.0f;
+        b.inv = b.unit > 0.0f ? __frcp_rn(b.unit) : 0.0f;
+    }
+    return b;
+}
+
+// x over the block's unit.  NVFP4: the correctly rounded quotient from the
+// correctly rounded reciprocal, one residual and one correction (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor",
+// 1990); units so small or large that the residual would leave fp32's range
+// take the plain division.  A zero unit gives a zero of x's sign.
+template <int kFormat>
+__device__ __forceinline__ float over_unit(float x, const BlockScale& b) {
+    if constexpr (kFormat == DGA_MXFP4) {
+        return x * b.inv;
+    } else {
+        if (b.unit >= 0x1p-90f && b.unit <= 0x1p90f) {
+            const float q = x * b.inv;
+            return copysignf(fmaf(fmaf(-q, b.unit, x), b.inv, q), x);  // the sign of a zero too
+        }
+        return b.unit > 0.0f ? __fdiv_rn(x, b.unit) : copysignf(0.0f, x);
+    }
+}
+
+// Eight values to eight codes, value i in bits 4i..4i+3.
+__device__ __forceinline__ uint32_t codes8(const float (&t)[8]) {
+    uint32_t out;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(out)
+        : "f"(t[0]), "f"(t[1]), "f"(t[2]), "f"(t[3]), "f"(t[4]), "f"(t[5]), "f"(t[6]), "f"(t[7]));
+    return out;
+}
+
+// Eight codes to their values.
+__device__ __forceinline__ void values8(uint32_t c, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(c));
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v[2 * q] = __half2float(__ushort_as_half(static_cast<uint16_t>(h[q] & 0xffff)));
+        v[2 * q + 1] = __half2float(__ushort_as_half(static_cast<uint16_t>(h[q] >> 16)));
+    }
+}
+
+// Eight consecutive values of a row, zero past its end.  `vec`: the row's
+// groups of eight are 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void load8(const T* __restrict__ row, int64_t k, int64_t K, bool vec,
+                                      float (&x)[8]) {
+    if (vec && k + 8 <= K) {
+        T v[8];
+        if constexpr (sizeof(T) == 2) {
+            *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(row + k));
+        } else {
+            reinterpret_cast<uint4*>(v)[0] = __ldg(reinterpret_cast<const uint4*>(row + k));
+            reinterpret_cast<uint4*>(v)[1] = __ldg(reinterpret_cast<const uint4*>(row + k) + 1);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = MxIn<T>::f(v[q]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = k + q < K ? MxIn<T>::f(row[k + q]) : 0.0f;
+    }
+}
+
+// ---- along rows ------------------------------------------------------------
+//
+// A warp takes 256 consecutive values of a row, a lane eight of them: one
+// 16-byte load (two for fp32), a maximum over the 4 (MXFP4) or 2 (NVFP4)
+// lanes of a block, one 4-byte store of codes, so that a warp reads and
+// writes whole cache lines.  The four scales of a tile's row are gathered
+// into one 4-byte store.
+template <int kFormat, typename T>
+__global__ void __launch_bounds__(256) mx_quant_rows_kernel(const T* __restrict__ X, int64_t ldx,
+                                                            int64_t rows, int64_t K, bool vec,
+                                                            const float* __restrict__ factor,
+                                                            uint8_t* __restrict__ codes,
+                                                            int64_t ldc, uint8_t* __restrict__ scales,
+                                                            int64_t tiles_k, int64_t chunks,
+                                                            int64_t row_bytes) {
+    // a product launched behind this kernel may start now: it waits for this
+    // grid's end before it reads what is written here
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int kLanes = mx_block(kFormat) / 8;  // lanes of a block
+    const int lane = threadIdx.x & 31;
+    const float g = (kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f;
+    const int64_t total = rows * chunks;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < total;
+         u += static_cast<int64_t>(gridDim.x) * 8) {
+        const int64_t r = u / chunks, k = (u - r * chunks) * 256 + lane * 8;
+        float x[8];
+        load8(X + r * ldx, k, K, vec, x);
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) m = max(m, mag_bits(x[q]));
+#pragma unroll
+        for (int d = 1; d < kLanes; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+        BlockScale b = block_scale<kFormat>(m, g);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = over_unit<kFormat>(x[q], b);
+        if ((k >> 1) < row_bytes) *reinterpret_cast<uint32_t*>(codes + r * ldc + (k >> 1)) = codes8(x);
+        // four blocks' scales to the first lane of the four; a block past the
+        // row's end has scale 0 (its codes are 0 too)
+        uint32_t w = k < K ? b.byte : 0u;
+        w |= __shfl_down_sync(0xffffffffu, w, kLanes) << 8;
+        w |= __shfl_down_sync(0xffffffffu, w, 2 * kLanes) << 16;
+        const int64_t s = k / mx_block(kFormat);
+        if (lane % (4 * kLanes) == 0 && (s >> 2) < tiles_k)
+            *reinterpret_cast<uint32_t*>(scales + mx_scale_offset(r, s, tiles_k)) = w;
+    }
+}
+
+// ---- along columns -----------------------------------------------------------
+//
+// The transpose of X (rows x cols) in 4 bits: cols rows of K = rows values.
+// A CTA takes 128 (k) x 64 (columns) of X through shared memory; a thread
+// quantises one block (MXFP4) or two (NVFP4) of one column, reading down the
+// tile (consecutive lanes on consecutive columns), and the codes go back
+// through shared memory so that each row of the result gets 64 consecutive
+// bytes.
+template <int kFormat, typename T>
+__global__ void __launch_bounds__(256) mx_quant_cols_kernel(const T* __restrict__ X, int64_t ldx,
+                                                            int64_t K, int64_t cols, bool vec,
+                                                            const float* __restrict__ factor,
+                                                            uint8_t* __restrict__ codes,
+                                                            int64_t ldc, uint8_t* __restrict__ scales,
+                                                            int64_t tiles_k, int64_t blocks_k,
+                                                            int64_t row_bytes) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int kPad = 16 / sizeof(T);
+    __shared__ __align__(16) T tile[128][64 + kPad];
+    __shared__ __align__(16) uint32_t out[64][16 + 4];
+    const int t = threadIdx.x;
+    const int64_t k0 = (blockIdx.x % blocks_k) * 128, c0 = (blockIdx.x / blocks_k) * 64;
+    const float g = (kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f;
+    constexpr int kVec = 16 / sizeof(T);       // values of one 16-byte load
+    constexpr int kPerRow = 64 / kVec;         // loads of a tile row
+#pragma unroll
+    for (int i = 0; i < 128 * kPerRow / 256; ++i) {
+        const int idx = i * 256 + t, kk = idx / kPerRow, cc = idx % kPerRow * kVec;
+        const int64_t k = k0 + kk, c = c0 + cc;
+        const T* src = X + k * ldx + c;
+        if (vec && k < K && c + kVec <= cols) {
+            *reinterpret_cast<uint4*>(&tile[kk][cc]) = __ldg(reinterpret_cast<const uint4*>(src));
+        } else {
+#pragma unroll
+            for (int q = 0; q < kVec; ++q)
+                tile[kk][cc + q] = (k < K && c + q < cols) ? src[q] : T(0.0f);
+        }
+    }
+    __syncthreads();
+    const int col = t & 63, quarter = t >> 6;  // 32 values of a column per thread
+    constexpr int kB = mx_block(kFormat), kPer = 32 / kB;
+    const int64_t c = c0 + col;
+    uint32_t word = 0, four[4];
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+        float x[kB];
+        uint32_t m = 0;
+#pragma unroll
+        for (int q = 0; q < kB; ++q) {
+            x[q] = MxIn<T>::f(tile[quarter * 32 + p * kB + q][col]);
+            m = max(m, mag_bits(x[q]));
+        }
+        const BlockScale b = block_scale<kFormat>(m, g);
+#pragma unroll
+        for (int o = 0; o < kB / 8; ++o) {
+            float y[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) y[q] = over_unit<kFormat>(x[o * 8 + q], b);
+            four[p * (kB / 8) + o] = codes8(y);
+        }
+        const int64_t k = k0 + quarter * 32 + p * kB;
+        word |= (k < K ? static_cast<uint32_t>(b.byte) : 0u) << (8 * p);
+    }
+    *reinterpret_cast<uint4*>(&out[col][quarter * 4]) = make_uint4(four[0], four[1], four[2], four[3]);
+    // the scales of this thread's 32 values: one byte, or two
+    const int64_t s = (k0 + quarter * 32) / kB;
+    if (c < cols && (s >> 2) < tiles_k) {
+        uint8_t* dst = scales + mx_scale_offset(c, s, tiles_k);
+        if constexpr (kPer == 1) *dst = static_cast<uint8_t>(word);
+        else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(word);
+    }
+    __syncthreads();
+    const int orow = t >> 2, ow = (t & 3) * 4;  // 16 bytes of a result row per thread
+    const int64_t byte = (k0 >> 1) + ow * 4;
+    if (c0 + orow < cols && byte < row_bytes)
+        *reinterpret_cast<uint4*>(codes + (c0 + orow) * ldc + byte) = *reinterpret_cast<const uint4*>(&out[orow][ow]);
+}
+
+// ---- back to values ------------------------------------------------------------
+
+template <typename T>
+__device__ __forceinline__ T mx_out(float v);
+template <> __device__ __forceinline__ float mx_out<float>(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 mx_out<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half mx_out<__half>(float v) { return __float2half_rn(v); }
+
+__device__ __forceinline__ float scale_value(int format, uint8_t byte) {
+    if (format == DGA_MXFP4)  // 2^(byte - 127): byte 0 is the subnormal 2^-127, 255 NaN
+        return byte == 0 ? __uint_as_float(0x00400000u)
+                         : (byte == 255 ? __uint_as_float(0x7fffffffu) : __uint_as_float(static_cast<uint32_t>(byte) << 23));
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(byte)));
+    return __half2float(__ushort_as_half(static_cast<uint16_t>(h2 & 0xffff)));
+}
+
+// A lane reads eight codes (4 bytes) and writes eight values: code times
+// (scale times factor), rounded once to the output type.
+template <int kFormat, typename T>
+__global__ void __launch_bounds__(256) mx_dequant_kernel(int64_t rows, int64_t K,
+                                                         const uint8_t* __restrict__ codes, int64_t ldc,
+                                                         const uint8_t* __restrict__ scales,
+                                                         int64_t tiles_k,
+                                                         const float* __restrict__ factor,
+                                                         T* __restrict__ Y, int64_t ldy, bool vec,
+                                                         int64_t groups) {
+    const float g = (kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f;
+    const int64_t total = rows * groups;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < total;
+         u += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = u / groups, k = (u - r * groups) * 8;
+        float v[8];
+        values8(__ldg(reinterpret_cast<const uint32_t*>(codes + r * ldc + (k >> 1))), v);
+        const float s = scale_value(kFormat, __ldg(scales + mx_scale_offset(r, k / mx_block(kFormat), tiles_k))) * g;
+        T y[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) y[q] = mx_out<T>(v[q] * s);
+        T* dst = Y + r * ldy + k;
+        if (vec && k + 8 <= K) {
+            if constexpr (sizeof(T) == 2) {
+                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(y);
+            } else {
+                reinterpret_cast<uint4*>(dst)[0] = reinterpret_cast<const uint4*>(y)[0];
+                reinterpret_cast<uint4*>(dst)[1] = reinterpret_cast<const uint4*>(y)[1];
+            }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (k + q < K) dst[q] = y[q];
+        }
+    }
+}
+
+template <int kFormat, typename T>
+cudaError_t quantize_as(const MxQuantArgs& a, const DeviceInfo& dev) {
+    const T* X = static_cast<const T*>(a.X);
+    constexpr int64_t kVec = 16 / sizeof(T);
+    const bool vec = aligned(a.X, 16) && a.ldx % kVec == 0;
+    const int64_t K = a.transpose ? a.rows : a.cols;
+    const int64_t tiles_k = mx_tiles_k(kFormat, K), row_bytes = mx_row_bytes(K);
+    if (!a.transpose) {
+        const int64_t chunks = (K + 255) / 256;
+        const int64_t units = a.rows * chunks;
+        const int64_t blocks = std::min<int64_t>((units + 7) / 8, static_cast<int64_t>(dev.sm_count) * 64);
+        mx_quant_rows_kernel<kFormat, T><<<static_cast<unsigned>(blocks), 256, 0, a.stream>>>(
+            X, a.ldx, a.rows, K, vec, a.factor, a.codes, a.ld_codes, a.scales, tiles_k, chunks, row_bytes);
+    } else {
+        const int64_t blocks_k = (K + 127) / 128, blocks = blocks_k * ((a.cols + 63) / 64);
+        if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        mx_quant_cols_kernel<kFormat, T><<<static_cast<unsigned>(blocks), 256, 0, a.stream>>>(
+            X, a.ldx, K, a.cols, vec, a.factor, a.codes, a.ld_codes, a.scales, tiles_k, blocks_k, row_bytes);
+    }
+    return cudaGetLastError();
+}
+
+template <int kFormat, typename T>
+cudaError_t dequantize_as(const MxMatrix& q, int64_t rows, int64_t K, void* Y, int64_t ldy,
+                          const DeviceInfo& dev, cudaStream_t stream) {
+    constexpr int64_t kVec = 16 / sizeof(T);
+    const bool vec = aligned(Y, 16) && ldy % kVec == 0;
+    const int64_t groups = (K + 7) / 8, total = rows * groups;
+    const int64_t blocks = std::min<int64_t>((total + 255) / 256, static_cast<int64_t>(dev.sm_count) * 64);
+    mx_dequant_kernel<kFormat, T><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
+        rows, K, static_cast<const uint8_t*>(q.codes), q.ld, static_cast<const uint8_t*>(q.scales),
+        mx_tiles_k(kFormat, K), q.factor, static_cast<T*>(Y), ldy, vec, groups);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t mx_quantize_launch(const MxQuantArgs& a, const DeviceInfo& dev) {
+    const bool mx = a.format == DGA_MXFP4;
+    switch (a.in_dtype) {
+    case DGA_F32: return mx ? quantize_as<DGA_MXFP4, float>(a, dev) : quantize_as<DGA_NVFP4, float>(a, dev);
+    case DGA_BF16: return mx ? quantize_as<DGA_MXFP4, __nv_bfloat16>(a, dev) : quantize_as<DGA_NVFP4, __nv_bfloat16>(a, dev);
+    default: return mx ? quantize_as<DGA_MXFP4, __half>(a, dev) : quantize_as<DGA_NVFP4, __half>(a, dev);
+    }
+}
+
+cudaError_t mx_dequantize_launch(int format, int out_dtype, const MxMatrix& q, int64_t rows, int64_t K,
+                                 void* Y, int64_t ldy, const DeviceInfo& dev, cudaStream_t stream) {
+    const bool mx = format == DGA_MXFP4;
+    switch (out_dtype) {
+    case DGA_F32: return mx ? dequantize_as<DGA_MXFP4, float>(q, rows, K, Y, ldy, dev, stream) : dequantize_as<DGA_NVFP4, float>(q, rows, K, Y, ldy, dev, stream);
+    case DGA_BF16: return mx ? dequantize_as<DGA_MXFP4, __nv_bfloat16>(q, rows, K, Y, ldy, dev, stream) : dequantize_as<DGA_NVFP4, __nv_bfloat16>(q, rows, K, Y, ldy, dev, stream);
+    default: return mx ? dequantize_as<DGA_MXFP4, __half>(q, rows, K, Y, ldy, dev, stream) : dequantize_as<DGA_NVFP4, __half>(q, rows, K, Y, ldy, dev, stream);
+    }
+}
+
+}  // namespace dga

@@ -342,4 +342,67 @@ __device__ __forceinline__ void tc_commit_pair_multicast(uint64_t* bar, uint16_t
         : "memory");
 }
 
+// ------------------------------------- block-scaled 4-bit MMA (kind::mxf4*) --
+//
+// E2M1 operands, two values to a byte, K-major in 128-byte swizzle rows (256
+// values); one MMA takes 64 values of K (32 bytes of a row).  The scales lie
+// in tensor memory: the 128 rows of a scale tile in 4 columns, row r in lane
+// r % 32 (repeated in the four 32-lane quarters) of column r / 32, whose 4
+// bytes are the scales of 4 consecutive blocks.  tcgen05.cp brings a tile
+// there from its 512 bytes in shared memory.
+
+// Instruction descriptor of the block-scaled kinds: bits 4-5 / 29-30 which
+// bytes of a scale column B / A use (0, or 2 for the upper half), bits 7-9 and
+// 10-11 the operand types (1 = E2M1), bits 17-22 N >> 3, bit 23 the scale type
+// (0 = E4M3, 1 = E8M0), bits 24-28 M >> 4; K-major, K = 64.
+__host__ __device__ constexpr uint32_t idesc_mx(bool e8m0, uint32_t m, uint32_t n, uint32_t half) {
+    return (half << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | ((e8m0 ? 1u : 0u) << 23) |
+           ((m >> 4) << 24) | (half << 29);
+}
+
+// Descriptor of a scale tile in shared memory for tcgen05.cp: 32 rows of 16
+// bytes, no swizzle, groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(1) << 16;
+    d |= static_cast<uint64_t>(128 >> 4) << 32;
+    d |= static_cast<uint64_t>(1) << 46;
+    return d;
+}
+
+// One scale tile to 4 columns of tensor memory (of this CTA; of both CTAs of
+// the pair, each from its own shared memory).
+template <bool kPair>
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
+    if constexpr (kPair)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// D[tmem] (+)= A * B with block scales; kE8M0: blocks of 32 and E8M0 scales,
+// else blocks of 16 and E4M3 scales.
+template <bool kE8M0, bool kPair>
+__device__ __forceinline__ void tc_mma_mx(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                          uint32_t accumulate) {
+#define DGA_MX_MMA(group, kind_vec)                                                             \
+    asm volatile(                                                                               \
+        "{\n\t.reg .pred p;\n\t"                                                                \
+        "setp.ne.b32 p, %6, 0;\n\t"                                                             \
+        "tcgen05.mma.cta_group::" group "." kind_vec " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::\
+            "r"(d_tmem),                                                                        \
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)               \
+        : "memory")
+    if constexpr (kE8M0) {
+        if constexpr (kPair) DGA_MX_MMA("2", "kind::mxf4.block_scale.scale_vec::2X");
+        else DGA_MX_MMA("1", "kind::mxf4.block_scale.scale_vec::2X");
+    } else {
+        if constexpr (kPair) DGA_MX_MMA("2", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+        else DGA_MX_MMA("1", "kind::mxf4nvf4.block_scale.scale_vec::4X");
+    }
+#undef DGA_MX_MMA
+}
+
 }  // namespace dga

@@ -1,0 +1,190 @@
+"""4-bit microscaled matrices: quantisation, products and the fully-connected
+layer, as PyTorch-tensor forms of the ``dga_mx_*`` entry points (include/dga.h
+has the formats, roundings and errors).  All work runs in the library's CUDA
+kernels on the current stream of the tensors' device; scratch and results
+come from PyTorch's caching allocator.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import (BF16, F16, F32, OK, DgaError, dga_mx_linear_workspace_size, dga_mx_row_bytes,
+               dga_mx_scales_size, lib, sum_rows)
+
+MXFP4, NVFP4 = 0, 1
+
+_CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+_TORCH = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
+
+
+class MXTensor:
+    """A rows x cols matrix in 4 bits, quantised along its columns.
+
+    codes: (rows, row_bytes) uint8, two E2M1 codes to a byte; scales: the tiled
+    block scales; tensor_scale: a 1-element fp32 tensor, or None for 1."""
+    __slots__ = ("format", "rows", "cols", "codes", "scales", "tensor_scale")
+
+    def __init__(self, format, rows, cols, codes, scales, tensor_scale=None):
+        self.format, self.rows, self.cols = format, rows, cols
+        self.codes, self.scales, self.tensor_scale = codes, scales, tensor_scale
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def __repr__(self):
+        return (f"MXTensor({'MXFP4' if self.format == MXFP4 else 'NVFP4'}, "
+                f"{self.rows}x{self.cols}, {self.codes.device})")
+
+
+def _stream(device, stream):
+    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+
+
+def _check(st, what):
+    if st != OK:
+        raise DgaError(st, what)
+
+
+def _factor(t, format, device):
+    """The device pointer of a tensor scale."""
+    if t is None:
+        return None
+    if format != NVFP4:
+        raise ValueError("tensor_scale needs the NVFP4 format")
+    if t.dtype != torch.float32 or t.numel() != 1 or t.device != device:
+        raise ValueError("tensor_scale must be one float32 value on the tensor's device")
+    return t.data_ptr()
+
+
+def _rows_of(T, name):
+    """(leading dimension) of a row-major 2-D tensor."""
+    if T.dim() != 2 or (T.stride(1) != 1 and T.shape[1] > 1):
+        raise ValueError(f"{name} must be 2-D and row-major")
+    return max(T.stride(0), T.shape[1], 1)
+
+
+def mx_quantize(X, format=MXFP4, transpose=False, tensor_scale=None, stream=None):
+    """X (rows x cols, float32, bfloat16 or float16, row- or column-major) to an
+    :class:`MXTensor` quantised along its rows, or, with transpose=True, the
+    MXTensor of X's transpose (quantised along X's columns)."""
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D")
+    if X.dtype not in _CODE:
+        raise TypeError("X must be float32, bfloat16 or float16")
+    if not X.is_cuda:
+        raise ValueError("X must be a CUDA tensor")
+    if X.stride(1) != 1 and X.shape[1] > 1 and X.stride(0) == 1:
+        X, transpose = X.t(), not transpose  # a column-major X is its transpose, row-major
+    ldx = _rows_of(X, "X")
+    rows, cols = X.shape
+    R, K = (cols, rows) if transpose else (rows, cols)
+    dev = X.device
+    row_bytes = dga_mx_row_bytes(K)
+    codes = torch.empty((R, row_bytes), dtype=torch.uint8, device=dev)
+    scales = torch.empty(dga_mx_scales_size(format, R, K), dtype=torch.uint8, device=dev)
+    _check(lib().dga_mx_quantize(format, _CODE[X.dtype], int(transpose), rows, cols, X.data_ptr(), ldx,
+                                 _factor(tensor_scale, format, dev), codes.data_ptr(), row_bytes,
+                                 scales.data_ptr(), _stream(dev, stream)), "dga_mx_quantize")
+    return MXTensor(format, R, K, codes, scales, tensor_scale)
+
+
+def mx_dequantize(Q, out_dtype=F32, stream=None):
+    """The values an MXTensor stands for, rounded once to out_dtype."""
+    Y = torch.empty((Q.rows, Q.cols), dtype=_TORCH[out_dtype], device=Q.device)
+    _check(lib().dga_mx_dequantize(Q.format, out_dtype, Q.rows, Q.cols, Q.codes.data_ptr(),
+                                   Q.codes.stride(0), Q.scales.data_ptr(),
+                                   _factor(Q.tensor_scale, Q.format, Q.device), Y.data_ptr(),
+                                   max(Q.cols, 1), _stream(Q.device, stream)), "dga_mx_dequantize")
+    return Y
+
+
+def _output(C, M, N, beta, out_dtype, device):
+    if C is None:
+        if beta != 0:
+            raise ValueError("beta != 0 needs C")
+        return torch.empty((M, N), dtype=_TORCH[out_dtype], device=device), max(N, 1)
+    if tuple(C.shape) != (M, N) or C.dtype not in _CODE or C.device != device:
+        raise ValueError(f"the output must be a ({M}, {N}) float32, bfloat16 or float16 tensor on {device}")
+    return C, _rows_of(C, "the output")
+
+
+def _bias(bias, N, C):
+    if bias is None:
+        return None
+    if bias.dim() != 1 or bias.numel() != N or (N > 1 and bias.stride(0) != 1) or bias.dtype != C.dtype \
+            or bias.device != C.device:
+        raise ValueError("bias must be a contiguous vector of the output's length, type and device")
+    return bias.data_ptr()
+
+
+def mx_gemm(A, B, C=None, alpha=1.0, beta=0.0, out_dtype=BF16, bias=None, stream=None):
+    """C <- alpha * A @ B^T + beta * C (+ bias) of MXTensors A (M x K) and B
+    (N x K) of one format; returns C, allocated as out_dtype when None."""
+    if A.format != B.format:
+        raise TypeError("A and B must have the same format")
+    if A.cols != B.cols:
+        raise ValueError(f"shape mismatch: A {A.shape}, B {B.shape} (the products run along the columns)")
+    if A.device != B.device:
+        raise ValueError("A and B must be on the same device")
+    dev = A.codes.device
+    C, ldc = _output(C, A.rows, B.rows, beta, out_dtype, dev)
+    a, b = ctypes.c_float(alpha), ctypes.c_float(beta)
+    _check(lib().dga_mx_gemm(A.format, _CODE[C.dtype], A.rows, B.rows, A.cols, ctypes.byref(a),
+                             A.codes.data_ptr(), A.codes.stride(0), A.scales.data_ptr(),
+                             _factor(A.tensor_scale, A.format, dev), B.codes.data_ptr(),
+                             B.codes.stride(0), B.scales.data_ptr(),
+                             _factor(B.tensor_scale, B.format, dev), ctypes.byref(b), C.data_ptr(),
+                             ldc, _bias(bias, B.rows, C), _stream(dev, stream)), "dga_mx_gemm")
+    return C
+
+
+def mx_linear_forward(X, W, bias=None, Y=None, tensor_scale=None, workspace=None, stream=None):
+    """Y = X @ W^T + bias for X [batch, in] (float32, bfloat16 or float16) and a
+    4-bit weight W, an MXTensor [out, in]: X is quantised in W's format
+    (tensor_scale: its factor) and multiplied.  Y, of X's type unless given."""
+    if X.dtype not in _CODE:
+        raise TypeError("X must be float32, bfloat16 or float16")
+    ldx = _rows_of(X, "X")
+    M, K = X.shape
+    if K != W.cols:
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {W.shape}")
+    dev = X.device
+    if W.codes.device != dev:
+        raise ValueError("X and W must be on the same device")
+    N = W.rows
+    Y, ldy = _output(Y, M, N, 0, _CODE[X.dtype], dev)
+    if workspace is None:
+        workspace = torch.empty(dga_mx_linear_workspace_size(W.format, M, K), dtype=torch.uint8, device=dev)
+    _check(lib().dga_mx_linear(W.format, _CODE[X.dtype], _CODE[Y.dtype], M, N, K, X.data_ptr(), ldx,
+                               _factor(tensor_scale, W.format, dev), W.codes.data_ptr(),
+                               W.codes.stride(0), W.scales.data_ptr(),
+                               _factor(W.tensor_scale, W.format, dev), _bias(bias, N, Y), Y.data_ptr(),
+                               ldy, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               _stream(dev, stream)), "dga_mx_linear")
+    return Y
+
+
+def mx_linear_backward(X, W, G, format=MXFP4, tensor_scales=(None, None, None), need_bias=True, stream=None):
+    """Gradients of Y = X W^T + b for the output gradient G [batch, out], with
+    4-bit products (the roundings' own gradient taken as 1): dX = G W with G
+    and W quantised along out, dW = G^T X with G and X quantised along the
+    batch, both of G's type; db = the batch sum of G (fp32, unquantised).
+    tensor_scales: the factors of X, W and G."""
+    if X.shape[0] != G.shape[0] or X.shape[1] != W.shape[1] or G.shape[1] != W.shape[0]:
+        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}, G {tuple(G.shape)}")
+    if G.dtype not in _CODE:
+        raise TypeError("G must be float32, bfloat16 or float16")
+    sx, sw, sg = tensor_scales
+    out = _CODE[G.dtype]
+    dX = mx_gemm(mx_quantize(G, format, False, sg, stream), mx_quantize(W, format, True, sw, stream),
+                 out_dtype=out, stream=stream)
+    dW = mx_gemm(mx_quantize(G, format, True, sg, stream), mx_quantize(X, format, True, sx, stream),
+                 out_dtype=out, stream=stream)
+    return dX, dW, (sum_rows(G, stream=stream) if need_bias else None)

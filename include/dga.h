@@ -381,6 +381,103 @@ int dga_spmv_csr(int64_t rows, int64_t cols, int64_t nnz, const int32_t* row_off
  * (152 SMs assumed when no device can be queried); 0 for rows <= 0. */
 size_t dga_spmv_csr_workspace_size(int64_t rows, int64_t nnz);
 
+/* 4-bit microscaled formats of the dga_mx_* calls.  Values are E2M1 (0, 1/2,
+ * 1, 3/2, 2, 3, 4, 6 and their negatives); blocks run along the rows.
+ *   DGA_MXFP4  a power-of-two scale (E8M0) per 32 values, as the OCP
+ *              Microscaling Formats specification has it
+ *   DGA_NVFP4  an E4M3 scale per 16 values and an fp32 factor per tensor   */
+typedef enum { DGA_MXFP4 = 0, DGA_NVFP4 = 1 } dga_mx_format;
+
+/*
+ * dga_mx_quantize -- a row-major matrix X (rows x cols, leading dimension ldx;
+ * DGA_F32, DGA_BF16 or DGA_F16) to 4 bits: R rows of K values, R x K being X
+ * itself or, with transpose = 1, its transpose (quantised along X's columns,
+ * as the products of a layer's gradients need it).
+ *
+ * For a block with m = max |x|:
+ *   DGA_MXFP4  scale 2^e, e = floor(log2 m) - 2 held to [-127, 127]
+ *   DGA_NVFP4  scale E4M3(min(448, m / (6 f))), f = *tensor_scale or 1; the
+ *              value's unit is scale * f
+ * and each value becomes the E2M1 number nearest to x / unit (ties to the even
+ * code, magnitudes above 6 to 6).  All of it is correctly rounded fp32
+ * arithmetic, so results do not depend on how the work is split.  A block
+ * with an infinity or a NaN gets a NaN scale (every value of it reads back as
+ * NaN); a zero unit gives zero codes.
+ *
+ *   tensor_scale  device pointer to one positive float, or NULL for 1;
+ *                 DGA_NVFP4 only.  max|X| / 2688 uses E4M3's whole range;
+ *                 rounded up to a power of two it keeps the scaling exact.
+ *   codes         device, R rows of dga_mx_row_bytes(K) bytes, ld_codes bytes
+ *                 apart (a multiple of 16): value k in byte k/2, the even one
+ *                 in the low half; a row's unused codes are written as 0
+ *   scales        device, dga_mx_scales_size(format, R, K) bytes: 512-byte
+ *                 tiles of 128 rows x 4 blocks, the scale of row r and block s
+ *                 at byte (r%32)*16 + (r/32%4)*4 + s%4 of tile
+ *                 (r/128)*ceil(blocks/4) + s/4; blocks past K are written as
+ *                 0, rows past R are not written (and never used)
+ * codes and scales must be 16-byte aligned.  Errors: DGA_ERR_UNSUPPORTED for a
+ * format or type; -3 transpose, -4 rows, -5 cols (outside [0, 2^31)), -6 X,
+ * -7 ldx, -8 tensor_scale with DGA_MXFP4, -9 codes, -10 ld_codes, -11 scales;
+ * DGA_ERR_OVERLAP.  rows == 0 or cols == 0 is a no-op.  One launch.
+ */
+int dga_mx_quantize(dga_mx_format format, dga_dtype in_dtype, int transpose, int64_t rows,
+                    int64_t cols, const void* X, int64_t ldx, const float* tensor_scale,
+                    void* codes, int64_t ld_codes, void* scales, dga_stream_t stream);
+
+/* Bytes of one row of K codes (0 for K <= 0), and of the scales of rows x K. */
+int64_t dga_mx_row_bytes(int64_t K);
+size_t dga_mx_scales_size(dga_mx_format format, int64_t rows, int64_t K);
+
+/*
+ * dga_mx_dequantize -- Y (rows x cols, row-major, ldy; DGA_F32, DGA_BF16 or
+ * DGA_F16) <- what a 4-bit matrix stands for: code * (scale * tensor_scale),
+ * rounded once to the output type.  Errors: DGA_ERR_UNSUPPORTED, -3 rows,
+ * -4 cols, -5 codes, -6 ld_codes, -7 scales, -8 tensor_scale, -9 Y, -10 ldy,
+ * DGA_ERR_OVERLAP.  One launch.
+ */
+int dga_mx_dequantize(dga_mx_format format, dga_dtype out_dtype, int64_t rows, int64_t cols,
+                      const void* codes, int64_t ld_codes, const void* scales,
+                      const float* tensor_scale, void* Y, int64_t ldy, dga_stream_t stream);
+
+/*
+ * dga_mx_gemm -- C <- alpha * A * B^T + beta * C + bias of 4-bit matrices of
+ * one format, A: M x K and B: N x K (both quantised along K), C: M x N
+ * row-major of DGA_F32, DGA_BF16 or DGA_F16, computed by the tensor cores'
+ * block-scaled products with fp32 accumulation.
+ *   alpha, beta       HOST pointers to float; beta == 0: C is not read;
+ *                     alpha == 0 or K == 0: A and B are not read
+ *   *_tensor_scale    device pointers to the tensors' factors, or NULL for 1
+ *   bias              N values of the output type added to every row, or NULL
+ * Results repeat bit for bit.  Errors: DGA_ERR_UNSUPPORTED; -3 M, -4 N, -5 K,
+ * -6 alpha, -7..-10 A's codes, lda, scales, tensor_scale, -11..-14 B's,
+ * -15 beta, -16 C, -17 ldc; DGA_ERR_OVERLAP when C meets an operand or the
+ * bias.  No workspace; one launch.
+ */
+int dga_mx_gemm(dga_mx_format format, dga_dtype out_dtype, int64_t M, int64_t N, int64_t K,
+                const float* alpha, const void* A_codes, int64_t lda, const void* A_scales,
+                const float* A_tensor_scale, const void* B_codes, int64_t ldb,
+                const void* B_scales, const float* B_tensor_scale, const float* beta, void* C,
+                int64_t ldc, const void* bias, dga_stream_t stream);
+
+/*
+ * dga_mx_linear -- the fully-connected layer on a 4-bit weight: X (M x K,
+ * row-major, x_dtype) is quantised into the workspace and
+ * Y <- X W^T + bias (M x N, row-major, out_dtype; types DGA_F32, DGA_BF16 or
+ * DGA_F16).  The same result as dga_mx_quantize and dga_mx_gemm; the product
+ * starts loading W while X is being quantised.
+ *   workspace   device, 16-byte aligned, dga_mx_linear_workspace_size bytes
+ * Errors: DGA_ERR_UNSUPPORTED; -4 M, -5 N, -6 K, -7 X, -8 ldx,
+ * -9 x_tensor_scale, -10..-13 W's codes, ldw, scales, tensor_scale, -15 Y,
+ * -16 ldy, -17 workspace; DGA_ERR_WORKSPACE, DGA_ERR_OVERLAP.
+ */
+int dga_mx_linear(dga_mx_format format, dga_dtype x_dtype, dga_dtype out_dtype, int64_t M,
+                  int64_t N, int64_t K, const void* X, int64_t ldx, const float* x_tensor_scale,
+                  const void* W_codes, int64_t ldw, const void* W_scales,
+                  const float* W_tensor_scale, const void* bias, void* Y, int64_t ldy,
+                  void* workspace, size_t workspace_bytes, dga_stream_t stream);
+
+size_t dga_mx_linear_workspace_size(dga_mx_format format, int64_t M, int64_t K);
+
 /* Library version: major*10000 + minor*100 + patch. */
 int dga_version(void);
 
