@@ -63,6 +63,9 @@ SIGNATURES = {
     "dga_mx_linear": (_CI, [_CI, _CI, _CI, _I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP,
                             _VP, _VP, _I64, _VP, _SZ, _VP]),
     "dga_mx_linear_workspace_size": (_SZ, [_CI, _I64, _I64]),
+    "dga_orthogonalize": (_CI, [_CI, _CI, _I64, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _CI, _VP,
+                                ctypes.c_float, _VP, _SZ, _VP]),
+    "dga_orthogonalize_workspace_size": (_SZ, [_CI, _I64, _I64, _I64]),
     "dga_probe_fp32_fma": (_CI, [_CI, _I64, _VP, _I64, _VP, _VP]),
     "dga_probe_fp32_fma_out_floats": (_I64, []),
     "dga_probe_int8_mma": (_CI, [_I64, _VP, _I64, _VP, _VP]),
@@ -220,6 +223,17 @@ def dga_mx_linear(format, x_dtype, out_dtype, M, N, K, X, ldx, x_tensor_scale, W
 
 def dga_mx_linear_workspace_size(format, M, K):
     return lib().dga_mx_linear_workspace_size(format, M, K)
+
+
+def dga_orthogonalize(in_dtype, out_dtype, batch, rows, cols, G, ldg, stride_g, O, ldo, stride_o, steps,
+                      coefficients, eps, workspace, workspace_bytes, stream):
+    return lib().dga_orthogonalize(in_dtype, out_dtype, batch, rows, cols, G, ldg, stride_g, O, ldo,
+                                   stride_o, steps, coefficients, eps, workspace, workspace_bytes,
+                                   stream)
+
+
+def dga_orthogonalize_workspace_size(out_dtype, batch, rows, cols):
+    return lib().dga_orthogonalize_workspace_size(out_dtype, batch, rows, cols)
 
 
 def dga_probe_fp32_fma(packed, iters, out, out_floats, flops, stream):
@@ -419,3 +433,4 @@ def linear_backward(X, W, G, need_bias=True):
 
 from .mx import (MXFP4, NVFP4, MXTensor, mx_dequantize, mx_gemm, mx_linear_backward,  # noqa: E402,F401
                  mx_linear_forward, mx_quantize)
+from .muon import QUINTIC, orthogonalize  # noqa: E402,F401

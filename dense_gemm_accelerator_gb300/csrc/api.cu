@@ -407,6 +407,58 @@ int dga_spmv_csr(int64_t rows, int64_t cols, int64_t nnz, const int32_t* row_off
     return DGA_OK;
 }
 
+size_t dga_orthogonalize_workspace_size(dga_dtype out_dtype, int64_t batch, int64_t rows, int64_t cols) {
+    if (out_dtype != DGA_F32 && out_dtype != DGA_BF16 && out_dtype != DGA_F16) return 0;
+    if (batch <= 0 || rows <= 0 || cols <= 0 || !ortho_supports(batch, rows, cols)) return 0;
+    return ortho_workspace_size(out_dtype, batch, rows, cols);
+}
+
+int dga_orthogonalize(dga_dtype in_dtype, dga_dtype out_dtype, int64_t batch, int64_t rows, int64_t cols,
+                      const void* G, int64_t ldg, int64_t stride_g, void* O, int64_t ldo, int64_t stride_o,
+                      int steps, const float* coefficients, float eps, void* workspace,
+                      size_t workspace_bytes, dga_stream_t stream) {
+    auto is_float = [](int t) { return t == DGA_F32 || t == DGA_BF16 || t == DGA_F16; };
+    if (!is_float(in_dtype) || !is_float(out_dtype)) return DGA_ERR_UNSUPPORTED;
+    constexpr int64_t kMax = int64_t{1} << 31;
+    if (batch < 0 || batch > 65535) return -3;
+    if (rows < 0 || rows >= kMax) return -4;
+    if (cols < 0 || cols >= kMax) return -5;
+    if (steps < 1 || steps > 1000) return -12;
+    if (!coefficients) return -13;
+    if (!(eps >= 0.0f)) return -14;
+    t_last_launches = 0;
+    if (batch == 0 || rows == 0 || cols == 0) return DGA_OK;
+    if (!G) return -6;
+    if (ldg < cols) return -7;
+    // matrices may repeat or interleave on the input side, not on the output's
+    if (stride_g < 0) return -8;
+    if (!O) return -9;
+    if (ldo < cols) return -10;
+    if (batch > 1 && stride_o < (rows - 1) * ldo + cols) return -11;
+    if (!ortho_supports(batch, rows, cols)) return DGA_ERR_UNSUPPORTED;
+    if (workspace_bytes > 0 && (!workspace || !aligned(workspace, 256))) return -15;
+    const size_t need = ortho_workspace_size(out_dtype, batch, rows, cols);
+    if (workspace_bytes < need) return DGA_ERR_WORKSPACE;
+    const int64_t gs = static_cast<int64_t>(elem_size(in_dtype)), os = static_cast<int64_t>(elem_size(out_dtype));
+    const uintptr_t w0 = reinterpret_cast<uintptr_t>(workspace), w1 = w0 + need;
+    const uintptr_t g0 = reinterpret_cast<uintptr_t>(G);
+    const uintptr_t g1 = g0 + static_cast<uintptr_t>(((batch - 1) * stride_g + (rows - 1) * ldg + cols) * gs);
+    const uintptr_t o0 = reinterpret_cast<uintptr_t>(O);
+    const uintptr_t o1 = o0 + static_cast<uintptr_t>(((batch - 1) * stride_o + (rows - 1) * ldo + cols) * os);
+    if (overlaps(w0, w1, g0, g1) || overlaps(w0, w1, o0, o1)) return DGA_ERR_OVERLAP;
+    DeviceInfo dev;
+    cudaError_t e = current_device_info(&dev);
+    if (e != cudaSuccess) return fail_cuda(e);
+    if (dev.major != 10 || dev.minor != 3) return DGA_ERR_DEVICE;
+    OrthoArgs a{in_dtype, out_dtype, batch, rows, cols, G, ldg, stride_g, O, ldo, stride_o, steps,
+                coefficients, eps, workspace, reinterpret_cast<cudaStream_t>(stream)};
+    int launches = 0;
+    e = ortho_launch(a, dev, &launches);
+    if (e != cudaSuccess) return fail_cuda(e);
+    t_last_launches = launches;
+    return DGA_OK;
+}
+
 int dga_last_path(void) { return t_last_path; }
 
 int dga_last_launch_count(void) { return t_last_launches; }
@@ -414,13 +466,14 @@ int dga_last_launch_count(void) { return t_last_launches; }
 int dga_sync_status(dga_stream_t stream) {
     cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail_cuda(e);
-    int st = 0, st_skinny = 0, st_spmv = 0, st_mx = 0;
+    int st = 0, st_skinny = 0, st_spmv = 0, st_mx = 0, st_ns = 0;
     e = tc_status_take(&st);
     if (e == cudaSuccess) e = skinny_status_take(&st_skinny);
     if (e == cudaSuccess) e = spmv_status_take(&st_spmv);
     if (e == cudaSuccess) e = mx_status_take(&st_mx);
+    if (e == cudaSuccess) e = ns_status_take(&st_ns);
     if (e != cudaSuccess) return fail_cuda(e);
-    if (st != 0 || st_skinny != 0 || st_mx != 0) return DGA_ERR_DEVICE_TIMEOUT;
+    if (st != 0 || st_skinny != 0 || st_mx != 0 || st_ns != 0) return DGA_ERR_DEVICE_TIMEOUT;
     return st_spmv != 0 ? DGA_ERR_BAD_INDEX : DGA_OK;
 }
 

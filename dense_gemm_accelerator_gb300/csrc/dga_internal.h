@@ -135,6 +135,28 @@ cudaError_t mx_gemm_launch(const MxGemmArgs& a, const DeviceInfo& dev, int* laun
 // Reads and clears this device's status word of the 4-bit products.
 cudaError_t mx_status_take(int* status);
 
+// ---- Newton-Schulz orthogonalisation of `batch` matrices (validated arguments)
+
+struct OrthoArgs {
+    int in_dtype, out_dtype;
+    int64_t batch, rows, cols;
+    const void* G;
+    int64_t ldg, stride_g;
+    void* O;
+    int64_t ldo, stride_o;
+    int steps;
+    const float* coefficients;  // host, 3 * steps
+    float eps;
+    void* ws;
+    cudaStream_t stream;
+};
+
+bool ortho_supports(int64_t batch, int64_t rows, int64_t cols);
+size_t ortho_workspace_size(int out_dtype, int64_t batch, int64_t rows, int64_t cols);
+cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launches);
+// Reads and clears this device's status word of the orthogonalisation.
+cudaError_t ns_status_take(int* status);
+
 // Sets what dga_last_launch_count() returns on this host thread.
 void set_last_launches(int n);
 

@@ -1,0 +1,970 @@
+// newton_schulz.cu -- an update's orthogonalisation by Newton-Schulz products.
+//
+// G (one matrix or a batch) is scaled to X = G / (|G|_F + eps), transposed
+// where it has more rows than columns (m <= n from here on), and each step
+// replaces X by a odd quintic of it,
+//
+//     A = X X^T,   B = b A + c A^2,   X <- a X + B X,
+//
+// which drives every singular value of X towards 1: the iteration of K.
+// Jordan, "Muon: An optimizer for hidden layers in neural networks" (2024).
+// A step costs m^2 n + m^3 + 2 m^2 n operations when the symmetric A and B
+// are formed by their upper triangle alone, as they are here.
+//
+// Numbers.  X, A and B live in the workspace as fp16, times 2^12 (their
+// entries stay far below 16 in magnitude, and what is small keeps its
+// digits), and are multiplied by tcgen05 with fp32 accumulation.
+//   * X is held as the sum of two fp16 numbers, hi + lo: 22 bits.  A one-word
+//     X would round every step's a X, an error in all directions, which the
+//     following steps amplify by up to a per step where X's singular values
+//     are small (simulated: 1e-2 to 4e-2 off for momentum of low rank).
+//   * 16-bit output: the products take hi alone.  Their roundings multiply A,
+//     B or X by 1 + O(2^-12) on either side and so stay within X's own
+//     singular subspaces: 1e-4 to 1.7e-3 off, at or below the output's own
+//     rounding (1.7e-3).
+//   * fp32 output, and matrices of up to kSmallRows rows, whose time goes to
+//     launches and not to products: hi lo + lo hi + hi hi, 22-bit operands.
+//     The tensor cores' fp32 accumulation cuts off instead of rounding, half a
+//     unit of the sum lost per MMA on average (2.2e-5 off the result at K =
+//     4099 x 3), so the hi hi products are accumulated in chunks of 128 values
+//     of K, added up in registers with rounding: as exact as fp32 products of
+//     the same formula.  The cross products, 2^-11 of the sum, come first and
+//     make one chunk.
+//
+// Two product kernels share one epilogue, value = c_old * old + c_acc * sum,
+// stored as hi (and lo), at its mirror place too for the symmetric products,
+// or as the result: `pair` (256 x 256 tiles on CTA pairs, persistent) where
+// there are enough tiles to fill the machine, `tile` (128 x 128 tiles, K shared
+// by a cluster and joined through distributed shared memory in a fixed order)
+// below.  Every launch is a programmatic dependent of the one before.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "dga_internal.h"
+#include "epilogue.cuh"
+#include "ptx.cuh"
+
+namespace dga {
+
+__device__ int g_ns_status;  // non-zero: a bounded wait expired (role code)
+
+namespace {
+
+constexpr uint64_t kWaitLimitNs = 4000000000ull;  // 4 s
+constexpr float kScale = 4096.0f;                 // stored = kScale * value
+constexpr int kSmallRows = 256;
+constexpr uint32_t kChunk = 2;  // K blocks of one chunk of the hi hi product where sums are chunked
+constexpr uint32_t kBoxBytes = 64 * 64 * 2;  // an MN-major box: 64 columns x 64 k
+enum : int { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3 };
+
+struct NsParams {
+    // tiles: of each matrix, all tiles_m x tiles_n or, sym, those with tm <= tn
+    uint32_t tiles_m, tiles_n, sym, per_matrix, num_tiles;
+    uint32_t num_kb, segs;  // K blocks of 64; 1 product (hi hi), or 3 (hi lo, lo hi, hi hi)
+    uint32_t q_mn;          // the second operand is read MN-major (rows along K)
+    uint32_t p_rows, q_rows;  // rows of one matrix in each operand's map
+    // value = c_old * (old_h + old_l) + c_acc * sum; old_* may be null
+    float c_old, c_acc;
+    const __half* old_h;
+    const __half* old_l;
+    __half* out_h;  // null: the last step, to `result`
+    __half* out_l;  // null: hi alone
+    int64_t rows, ld, stride;  // of old and out: padded rows, row and matrix strides
+    void* result;
+    int result_type, transposed;
+    int64_t m, n, ldo, stride_o;
+};
+
+__device__ __forceinline__ void record_failure(int role, volatile int* abort_flag) {
+    atomicCAS(&g_ns_status, 0, role);
+    *abort_flag = 1;
+}
+
+__device__ __forceinline__ void ns_tile(const NsParams& p, uint32_t t, uint32_t& matrix, uint32_t& tm, uint32_t& tn) {
+    matrix = t / p.per_matrix;
+    const uint32_t r = t - matrix * p.per_matrix;
+    if (p.sym) {
+        // column by column of the upper triangle: r = tn (tn + 1) / 2 + tm
+        uint32_t c = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+        while (c * (c + 1) / 2 > r) --c;
+        while ((c + 1) * (c + 2) / 2 <= r) ++c;
+        tn = c;
+        tm = r - c * (c + 1) / 2;
+    } else {
+        tm = r % p.tiles_m;
+        tn = r / p.tiles_m;
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// 32 columns (col .. col+31) of one row per lane.  mirror: the tile is off the
+// diagonal of a symmetric product, so that its transpose is stored too.
+__device__ __forceinline__ void ns_store(const NsParams& p, uint32_t matrix, int64_t row, int64_t col, bool mirror,
+                                         float (&v)[32]) {
+    const bool in = row < p.rows && col < p.ld;  // padded sizes are multiples of 64
+    const int64_t at = matrix * p.stride + row * p.ld + col;
+    if (in) {
+        if (p.old_h != nullptr) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 h = *reinterpret_cast<const uint4*>(p.old_h + at + q * 8);
+                uint4 l = make_uint4(0, 0, 0, 0);
+                if (p.old_l != nullptr) l = *reinterpret_cast<const uint4*>(p.old_l + at + q * 8);
+                const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float2 a = unpack2(hw[w]), b = unpack2(lw[w]);
+                    float& x = v[q * 8 + w * 2];
+                    float& y = v[q * 8 + w * 2 + 1];
+                    x = fmaf(p.c_old, a.x + b.x, p.c_acc * x);
+                    y = fmaf(p.c_old, a.y + b.y, p.c_acc * y);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= p.c_acc;
+        }
+    }
+    if (p.out_h == nullptr) {
+        // the result: rows of m x n, or (transposed) of n x m
+        auto put = [&](int64_t i, float x) {
+            if (p.result_type == DGA_F32) static_cast<float*>(p.result)[i] = x;
+            else if (p.result_type == DGA_BF16) static_cast<__nv_bfloat16*>(p.result)[i] = __float2bfloat16_rn(x);
+            else static_cast<__half*>(p.result)[i] = __float2half_rn(x);
+        };
+        const int64_t base = matrix * p.stride_o;
+        if (row < p.m) {
+            const int64_t step = p.transposed ? p.ldo : 1, first = base + (p.transposed ? col * p.ldo + row : row * p.ldo + col);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (col + j < p.n) put(first + j * step, v[j]);
+        }
+        return;
+    }
+    if (!in) return;
+    uint32_t h[16], l[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        h[j] = pack2(v[2 * j], v[2 * j + 1]);
+        const float2 f = unpack2(h[j]);
+        l[j] = pack2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        *reinterpret_cast<uint4*>(p.out_h + at + q * 8) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
+        if (p.out_l != nullptr)
+            *reinterpret_cast<uint4*>(p.out_l + at + q * 8) = make_uint4(l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]);
+    }
+    if (mirror) {
+        // element (col + j, row): consecutive lanes on consecutive columns
+        const int64_t mt = matrix * p.stride + col * p.ld + row;
+        uint16_t* oh = reinterpret_cast<uint16_t*>(p.out_h) + mt;
+        uint16_t* ol = reinterpret_cast<uint16_t*>(p.out_l) + mt;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            oh[j * p.ld] = static_cast<uint16_t>(j & 1 ? h[j / 2] >> 16 : h[j / 2]);
+            if (p.out_l != nullptr) ol[j * p.ld] = static_cast<uint16_t>(j & 1 ? l[j / 2] >> 16 : l[j / 2]);
+        }
+    }
+}
+
+// Chunked sums: whether K block kb (of the three segments in a row) begins a
+// chunk of the range that starts at kb0, and how many chunks kb0 .. kb1 has.
+__device__ __forceinline__ bool chunk_begins(const NsParams& p, uint32_t kb, uint32_t kb0) {
+    return kb == kb0 || (kb >= 2 * p.num_kb && (kb - 2 * p.num_kb) % kChunk == 0);
+}
+__device__ __forceinline__ uint32_t chunk_count(const NsParams& p, uint32_t kb0, uint32_t kb1) {
+    const uint32_t lo = 2 * p.num_kb, h0 = max(kb0, lo) - lo;
+    uint32_t n = kb0 < lo ? 1 : 0;
+    if (kb1 > lo) n += (kb1 - lo - 1) / kChunk - h0 / kChunk + 1;
+    return n;
+}
+
+struct NsMaps {
+    CUtensorMap p_h, p_l, q_h, q_l;
+};
+
+// ---- the tile kernel: 128 x 128, K parts in a cluster ---------------------------------
+
+constexpr int kTileStages = 3;  // two CTAs to an SM: a launch's start overlaps the last one's end
+constexpr uint32_t kTileStage = 2 * 128 * 128;
+constexpr uint32_t kTileBar = kTileStages * kTileStage;
+constexpr uint32_t kTileLaunch = kTileBar + (2 * kTileStages + 4) * 8 + 16 + 1024;
+static_assert(kTileBar >= 128 * 128 * 4, "the partial sums fit the ring");
+
+// Threads: producer warp, MMA warp, epilogue warps (4, or 8 with half the
+// columns each where they keep the chunks' sum in registers).
+constexpr int tile_threads(bool chunked) { return chunked ? 320 : 192; }
+
+template <bool kChunked>
+__global__ void __launch_bounds__(tile_threads(kChunked), 2)
+    ns_tile_kernel(const __grid_constant__ NsMaps maps, NsParams p, uint32_t splits) {
+    constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 128, 128);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kTileBar);
+    uint64_t* empty = full + kTileStages;
+    uint64_t* acc_full = empty + kTileStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    constexpr uint32_t kCols = kChunked ? 256 : 128;  // two accumulators, or one
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t t = blockIdx.x / splits, part = blockIdx.x % splits;
+    // this part's K blocks, of all segments in a row
+    const uint32_t total_kb = p.num_kb * p.segs;
+    const uint32_t kb0 = part * total_kb / splits, kb1 = (part + 1) * total_kb / splits;
+    uint32_t matrix, tm, tn;
+    ns_tile(p, t, matrix, tm, tn);
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kTileStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 8);
+        }
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, kCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            const int32_t p_row = static_cast<int32_t>(matrix * p.p_rows + tm * 128);
+            for (uint32_t kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
+                    record_failure(kRoleProducer, abort_flag);
+                    __nanosleep(20000);  // let copies already issued land
+                    break;
+                }
+                uint8_t* dst = smem + stage * kTileStage;
+                mbar_arrive_expect_tx(&full[stage], kTileStage);
+                const uint32_t seg = kb / p.num_kb + (kChunked ? 0 : 2);
+                const int32_t k = static_cast<int32_t>((kChunked ? kb - seg * p.num_kb : kb) * 64);
+                tma_load_2d(dst, seg == 1 ? &maps.p_l : &maps.p_h, &full[stage], k, p_row);
+                const CUtensorMap* q = seg == 0 ? &maps.q_l : &maps.q_h;
+                if (p.q_mn) {
+                    const int32_t row = static_cast<int32_t>(matrix * p.q_rows) + k;
+                    tma_load_2d(dst + 128 * 128, q, &full[stage], static_cast<int32_t>(tn * 128), row);
+                    tma_load_2d(dst + 128 * 128 + kBoxBytes, q, &full[stage], static_cast<int32_t>(tn * 128 + 64), row);
+                } else {
+                    tma_load_2d(dst + 128 * 128, q, &full[stage], k, static_cast<int32_t>(matrix * p.q_rows + tn * 128));
+                }
+                if (++stage == kTileStages) { stage = 0; phase ^= 1; }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0, chunk = 0;
+            const uint32_t idesc = idesc_major(kIdesc, 0, p.q_mn);
+            const uint32_t q_step = p.q_mn ? (16 * 128) >> 4 : 32 >> 4;
+            for (uint32_t kb = kb0; kb < kb1; ++kb) {
+                const bool first = kChunked ? chunk_begins(p, kb, kb0) : kb == kb0;
+                if (kChunked && first && !mbar_wait_bounded(&acc_empty[chunk & 1], (chunk >> 1 & 1) ^ 1, abort_flag, kWaitLimitNs)) {
+                    record_failure(kRoleMma, abort_flag);
+                    break;
+                }
+                if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs)) {
+                    record_failure(kRoleMma, abort_flag);
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t addr = smem_u32(smem + stage * kTileStage);
+                const uint64_t pd = smem_desc_kmajor_sw128(addr);
+                const uint64_t qd = p.q_mn ? smem_desc_mnmajor_sw128(addr + 128 * 128, kBoxBytes)
+                                           : smem_desc_kmajor_sw128(addr + 128 * 128);
+                const uint32_t d = tmem + (kChunked ? (chunk & 1) * 128 : 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc_mma<kFmtF16>(d, pd + 2 * k, qd + q_step * k, idesc, (!first || k > 0) ? 1u : 0u);
+                tc_commit(&empty[stage]);
+                if (++stage == kTileStages) { stage = 0; phase ^= 1; }
+                if (kChunked && (kb + 1 == kb1 || chunk_begins(p, kb + 1, kb0))) {
+                    tc_commit(&acc_full[chunk & 1]);
+                    ++chunk;
+                }
+            }
+            if (!kChunked) tc_commit(&acc_full[0]);
+        }
+    }
+    __syncwarp();
+    const int quarter = warp & 3, r_in = quarter * 32 + lane;
+    const int64_t row = static_cast<int64_t>(tm) * 128 + r_in, col0 = static_cast<int64_t>(tn) * 128;
+    const bool mirror = p.sym && tm != tn;
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    float* red = reinterpret_cast<float*>(smem);
+    // the last commit: every MMA of this CTA, and with them every copy into the ring
+    const uint32_t n_chunks = kChunked ? chunk_count(p, kb0, kb1) : 1;
+    bool ok = true;
+    if constexpr (kChunked) {
+        if (warp >= 2) {
+            const int half = (warp - 2) >> 2;  // 64 columns
+            float sum[64];
+#pragma unroll
+            for (int j = 0; j < 64; ++j) sum[j] = 0.0f;
+            for (uint32_t ch = 0; ch < n_chunks; ++ch) {
+                if (!mbar_wait_bounded(&acc_full[ch & 1], ch >> 1 & 1, abort_flag, kWaitLimitNs)) {
+                    record_failure(kRoleEpilogue, abort_flag);
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(tmem + lane_base + (ch & 1) * 128 + half * 64 + c * 16, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(r[j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&acc_empty[ch & 1]);
+            }
+            if (splits == 1) {
+                if (ok) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float v[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = sum[c * 32 + j];
+                        ns_store(p, matrix, row, col0 + half * 64 + c * 32, mirror, v);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 64; ++j) red[(half * 64 + j) * 128 + r_in] = sum[j];
+            }
+        }
+    } else {
+        ok = mbar_wait_bounded(&acc_full[0], 0, abort_flag, kWaitLimitNs);
+        if (!ok) record_failure(kRoleEpilogue, abort_flag);
+        tc_fence_after();
+        if (warp >= 2 && ok) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(tmem + lane_base + c * 32, r);
+                tmem_ld_wait();
+                if (splits == 1) {
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                    ns_store(p, matrix, row, col0 + c * 32, mirror, v);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) red[(c * 32 + j) * 128 + r_in] = __uint_as_float(r[j]);
+                }
+            }
+        }
+    }
+    if (splits > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 2) {
+            // each CTA joins and stores its share of the columns, 32 at a time
+            const uint32_t first = part + (kChunked ? ((warp - 2) >> 2) * splits : 0u);
+            for (uint32_t c = first; c < 4; c += kChunked ? 2 * splits : splits) {
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                for (uint32_t q = 0; q < splits; ++q) {
+                    const uint32_t addr = map_to_cta(smem_u32(red + c * 32 * 128 + r_in), q);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] += ld_shared_cluster_f32(addr + j * 512);
+                }
+                ns_store(p, matrix, row, col0 + c * 32, mirror, v);
+            }
+        }
+        __syncwarp();
+        cluster_sync();  // no CTA leaves while another reads its sums
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kCols);
+    }
+}
+
+// ---- the pair kernel: 256 x 256 on two CTAs, persistent --------------------------------
+
+constexpr int kPairStages = 6;
+constexpr uint32_t kPairStage = 2 * 128 * 128;  // each CTA's half of both operands
+constexpr uint32_t kPairBar = kPairStages * kPairStage;
+constexpr uint32_t kPairLaunch = kPairBar + (2 * kPairStages + 5) * 8 + 16 + 1024;
+
+// Epilogue warps: 4, or 16 with 64 columns each where they keep the chunks'
+// sum in registers.
+constexpr int pair_threads(bool chunked) { return chunked ? 576 : 192; }
+
+template <bool kChunked>
+__global__ void __launch_bounds__(pair_threads(kChunked), 1)
+    ns_pair_kernel(const __grid_constant__ NsMaps maps, NsParams p) {
+    constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 256, 256);
+    constexpr uint16_t kBothCtas = 0x3;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairBar);
+    uint64_t* empty = full + kPairStages;
+    uint64_t* acc_full = empty + kPairStages;
+    uint64_t* acc_empty = acc_full + 2;
+    uint64_t* drain = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+
+    if (warp == 0 && lane == 0) {
+        for (int s = 0; s < kPairStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], kChunked ? 32 : 8);  // one lane of each epilogue warp of both CTAs
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t cluster_id = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+    const uint32_t total_kb = p.num_kb * p.segs;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            for (uint32_t t = cluster_id; ok && t < p.num_tiles; t += n_clusters) {
+                uint32_t matrix, tm, tn;
+                ns_tile(p, t, matrix, tm, tn);
+                const int32_t p_row = static_cast<int32_t>(matrix * p.p_rows + tm * 256 + rank * 128);
+                const int32_t q_at = static_cast<int32_t>(tn * 256 + rank * 128);
+                const int32_t q_row = static_cast<int32_t>(matrix * p.q_rows);
+                uint32_t seg = kChunked ? 0 : 2, k = 0;
+                for (uint32_t kb = 0; kb < total_kb; ++kb) {
+                    if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
+                        record_failure(kRoleProducer, abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* dst = smem + stage * kPairStage;
+                    if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kPairStage);
+                    const uint32_t bar = map_to_cta(smem_u32(&full[stage]), 0);
+                    tma_load_2d_pair(dst, seg == 1 ? &maps.p_l : &maps.p_h, bar, static_cast<int32_t>(k * 64), p_row);
+                    const CUtensorMap* q = seg == 0 ? &maps.q_l : &maps.q_h;
+                    if (p.q_mn) {
+                        const int32_t row = q_row + static_cast<int32_t>(k * 64);
+                        tma_load_2d_pair(dst + 128 * 128, q, bar, q_at, row);
+                        tma_load_2d_pair(dst + 128 * 128 + kBoxBytes, q, bar, q_at + 64, row);
+                    } else {
+                        tma_load_2d_pair(dst + 128 * 128, q, bar, static_cast<int32_t>(k * 64), q_row + q_at);
+                    }
+                    if (++k == p.num_kb) { k = 0; ++seg; }
+                    if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+                }
+            }
+            if (!ok) __nanosleep(20000);  // let copies already issued land before teardown
+        }
+    } else if (warp == 1) {
+        if (leader && lane == 0) {
+            uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
+            const uint32_t idesc = idesc_major(kIdesc, 0, p.q_mn);
+            const uint32_t q_step = p.q_mn ? (16 * 128) >> 4 : 32 >> 4;
+            bool ok = true;
+            for (uint32_t t = cluster_id; ok && t < p.num_tiles; t += n_clusters) {
+                uint32_t d = 0;
+                for (uint32_t kb = 0; kb < total_kb; ++kb) {
+                    const bool first = kChunked ? chunk_begins(p, kb, 0) : kb == 0;
+                    if (first) {
+                        if (!mbar_wait_bounded<true>(&acc_empty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs)) {
+                            record_failure(kRoleMma, abort_flag);
+                            ok = false;
+                            break;
+                        }
+                        d = tmem + acc * 256;
+                    }
+                    if (!mbar_wait_bounded<true>(&full[stage], phase, abort_flag, kWaitLimitNs)) {
+                        record_failure(kRoleMma, abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t addr = smem_u32(smem + stage * kPairStage);
+                    const uint64_t pd = smem_desc_kmajor_sw128(addr);
+                    const uint64_t qd = p.q_mn ? smem_desc_mnmajor_sw128(addr + 128 * 128, kBoxBytes)
+                                               : smem_desc_kmajor_sw128(addr + 128 * 128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_pair<kFmtF16>(d, pd + 2 * k, qd + q_step * k, idesc, (!first || k > 0) ? 1u : 0u);
+                    tc_commit_pair_multicast(&empty[stage], kBothCtas);
+                    if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+                    if (kb + 1 == total_kb || (kChunked && chunk_begins(p, kb + 1, 0))) {
+                        tc_commit_pair_multicast(&acc_full[acc], kBothCtas);
+                        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                    }
+                }
+            }
+            tc_commit_pair_multicast(drain, 0x1);
+            volatile int never = 0;
+            mbar_wait_bounded(drain, 0, &never, kWaitLimitNs);
+        }
+    } else {
+        const int quarter = warp & 3;
+        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+        uint32_t acc = 0, acc_phase = 0;
+        bool ok = true;
+        for (uint32_t t = cluster_id; ok && t < p.num_tiles; t += n_clusters) {
+            uint32_t matrix, tm, tn;
+            ns_tile(p, t, matrix, tm, tn);
+            const int64_t row = static_cast<int64_t>(tm) * 256 + rank * 128 + quarter * 32 + lane;
+            const int64_t col0 = static_cast<int64_t>(tn) * 256;
+            const bool mirror = p.sym && tm != tn;
+            if constexpr (kChunked) {
+                const int group = (warp - 2) >> 2;  // 64 columns
+                float sum[64];
+#pragma unroll
+                for (int j = 0; j < 64; ++j) sum[j] = 0.0f;
+                const uint32_t n_chunks = chunk_count(p, 0, total_kb);
+                for (uint32_t ch = 0; ch < n_chunks; ++ch) {
+                    if (!mbar_wait_bounded<true>(&acc_full[acc], acc_phase, abort_flag, kWaitLimitNs)) {
+                        record_failure(kRoleEpilogue, abort_flag);
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(tmem + lane_base + acc * 256 + group * 64 + c * 16, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(r[j]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
+                    if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = sum[c * 32 + j];
+                    ns_store(p, matrix, row, col0 + group * 64 + c * 32, mirror, v);
+                }
+            } else {
+                if (!mbar_wait_bounded<true>(&acc_full[acc], acc_phase, abort_flag, kWaitLimitNs)) {
+                    record_failure(kRoleEpilogue, abort_flag);
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t r[32];
+                    float v[32];
+                    tmem_ld_32x32b_x32(tmem + lane_base + acc * 256 + c * 32, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                    ns_store(p, matrix, row, col0 + c * 32, mirror, v);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
+                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    __syncwarp();
+    cluster_sync();  // no CTA frees TMEM or exits while its peer may still touch it
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ---- the norm and the first X ------------------------------------------------------------
+
+template <typename T> __device__ __forceinline__ float ns_in(T v);
+template <> __device__ __forceinline__ float ns_in<float>(float v) { return v; }
+template <> __device__ __forceinline__ float ns_in<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float ns_in<__half>(__half v) { return __half2float(v); }
+
+// The block's sum in thread 0, in a fixed order.
+__device__ __forceinline__ float block_sum(float s) {
+    __shared__ float part[8];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += part[w];
+    return s;
+}
+
+// Sums of squares: block (x, matrix) adds rows x, x + gridDim.x, ...
+template <typename T>
+__global__ void __launch_bounds__(256) ns_squares_kernel(const T* __restrict__ G, int64_t rows, int64_t cols,
+                                                         int64_t ldg, int64_t stride_g, bool vec,
+                                                         float* __restrict__ partial) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    constexpr int kVec = 16 / sizeof(T);
+    const T* base = G + blockIdx.y * stride_g;
+    float s = 0.0f;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const T* row = base + r * ldg;
+        if (vec) {
+            for (int64_t c = threadIdx.x * kVec; c < cols; c += 256 * kVec) {
+                if (c + kVec <= cols) {
+                    T v[kVec];
+                    *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(row + c);
+#pragma unroll
+                    for (int q = 0; q < kVec; ++q) s = fmaf(ns_in(v[q]), ns_in(v[q]), s);
+                } else {
+                    for (int64_t q = c; q < cols; ++q) s = fmaf(ns_in(row[q]), ns_in(row[q]), s);
+                }
+            }
+        } else {
+            for (int64_t c = threadIdx.x; c < cols; c += 256) s = fmaf(ns_in(row[c]), ns_in(row[c]), s);
+        }
+    }
+    s = block_sum(s);
+    if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = s;
+}
+
+// X = G / (|G| + eps) as hi and lo, zero in the padding; 64 x 64 tiles through
+// shared memory, transposed on the way for a tall G.
+template <typename T>
+__global__ void __launch_bounds__(256) ns_first_kernel(const T* __restrict__ G, int64_t rows, int64_t cols, int64_t ldg,
+                                                       int64_t stride_g, bool transposed,
+                                                       const float* __restrict__ partial, int parts, float eps,
+                                                       __half* __restrict__ xh, __half* __restrict__ xl, int64_t ld,
+                                                       int64_t stride, uint32_t tiles_c) {
+    __shared__ float tile[64][65];
+    __shared__ float unit;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float s = 0.0f;
+    for (int i = threadIdx.x; i < parts; i += 256) s += partial[blockIdx.y * parts + i];
+    s = block_sum(s);
+    if (threadIdx.x == 0) unit = kScale / (sqrtf(s) + eps);
+    __syncthreads();
+    const float u = unit;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x / tiles_c) * 64, c0 = static_cast<int64_t>(blockIdx.x % tiles_c) * 64;
+    // X's rows r0.., columns c0..: G's rows g0.., columns h0..
+    const int64_t g0 = transposed ? c0 : r0, h0 = transposed ? r0 : c0;
+    const T* base = G + blockIdx.y * stride_g;
+    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
+#pragma unroll 4
+    for (int i = y; i < 64; i += 4) {
+        const int64_t r = g0 + i, c = h0 + x;
+        const float v = r < rows && c < cols ? ns_in(base[r * ldg + c]) * u : 0.0f;
+        if (transposed) tile[x][i] = v;
+        else tile[i][x] = v;
+    }
+    __syncthreads();
+    // 16 consecutive columns of a row per thread
+    const int tr = threadIdx.x >> 2, tc = (threadIdx.x & 3) * 16;
+    uint32_t h[8], l[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a = tile[tr][tc + 2 * j], b = tile[tr][tc + 2 * j + 1];
+        h[j] = pack2(a, b);
+        const float2 f = unpack2(h[j]);
+        l[j] = pack2(a - f.x, b - f.y);
+    }
+    const int64_t at = blockIdx.y * stride + (r0 + tr) * ld + c0 + tc;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        *reinterpret_cast<uint4*>(xh + at + q * 8) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
+        *reinterpret_cast<uint4*>(xl + at + q * 8) = make_uint4(l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]);
+    }
+}
+
+// ---- host side ------------------------------------------------------------------------------
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// rows x ld fp16, boxes of 64 columns (one 128-byte row) x box_rows
+cudaError_t half_map(CUtensorMap* map, const __half* base, int64_t rows, int64_t ld, uint32_t box_rows) {
+    auto fn = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+    if (!fn) return cudaErrorNotSupported;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(ld), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+    cuuint32_t box[2] = {64, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+constexpr int kMaxParts = 128;  // partial sums of squares per matrix
+
+struct NsPlan {
+    int64_t m, n, mp, np;  // m <= n, and padded to the K block
+    bool transposed, split;
+    size_t x_bytes, a_bytes, total;  // one X (hi or lo), one A or B (hi or lo)
+};
+
+NsPlan plan_of(int out_dtype, int64_t batch, int64_t rows, int64_t cols) {
+    NsPlan pl{};
+    pl.transposed = rows > cols;
+    pl.m = std::min(rows, cols);
+    pl.n = std::max(rows, cols);
+    pl.mp = round_up(pl.m, 64);
+    pl.np = round_up(pl.n, 64);
+    pl.split = out_dtype == DGA_F32 || pl.m <= kSmallRows;
+    pl.x_bytes = static_cast<size_t>(batch * pl.mp * pl.np) * 2;
+    pl.a_bytes = static_cast<size_t>(batch * pl.mp * pl.mp) * 2;
+    // partial sums; X now and next, hi and lo; A and B, hi and (split) lo
+    pl.total = static_cast<size_t>(round_up(batch * kMaxParts * 4, 256)) + 4 * pl.x_bytes + (pl.split ? 4 : 2) * pl.a_bytes;
+    return pl;
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, unsigned cluster, int smem, bool pdl, cudaStream_t s, A... args) {
+    if (smem > 0) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (pdl) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n].val.clusterDim.x = cluster;
+        attr[n].val.clusterDim.y = 1;
+        attr[n++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
+// One product: pair kernel where its tiles can occupy most of the machine's
+// CTA pairs, else the tile kernel with K in as many parts as there are idle
+// CTA slots.
+cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_t rows, int64_t cols,
+                           const DeviceInfo& dev, cudaStream_t s) {
+    auto tiles = [&](int64_t size) {
+        p.tiles_m = static_cast<uint32_t>((rows + size - 1) / size);
+        p.tiles_n = static_cast<uint32_t>((cols + size - 1) / size);
+        p.per_matrix = p.sym ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
+        const int64_t all = batch * p.per_matrix;
+        p.num_tiles = static_cast<uint32_t>(all);
+        return all;
+    };
+    const bool chunked = p.segs == 3;
+    const int64_t pairs = dev.sm_count / 2;
+    const int64_t big = tiles(256);
+    if (big >= pairs * 3 / 4)
+        return launch(chunked ? ns_pair_kernel<true> : ns_pair_kernel<false>,
+                      dim3(static_cast<unsigned>(2 * std::min(big, pairs))), pair_threads(chunked), 2,
+                      static_cast<int>(kPairLaunch), true, s, maps, p);
+    const int64_t small = tiles(128);
+    uint32_t splits = 1;
+    while (splits < 4 && small * splits * 2 <= 2 * dev.sm_count && p.num_kb * p.segs >= splits * 4) splits *= 2;
+    return launch(chunked ? ns_tile_kernel<true> : ns_tile_kernel<false>, dim3(static_cast<unsigned>(small * splits)),
+                  tile_threads(chunked), splits, static_cast<int>(kTileLaunch), true, s, maps, p, splits);
+}
+
+template <typename T>
+cudaError_t launch_first(const OrthoArgs& a, const NsPlan& pl, float* partial, __half* xh, __half* xl, cudaStream_t s) {
+    const T* G = static_cast<const T*>(a.G);
+    constexpr int64_t kVec = 16 / sizeof(T);
+    const bool vec = aligned(G, 16) && a.ldg % kVec == 0 && (a.batch == 1 || a.stride_g % kVec == 0);
+    const int parts = static_cast<int>(std::min<int64_t>(a.rows, kMaxParts));
+    cudaError_t e = launch(ns_squares_kernel<T>, dim3(parts, static_cast<unsigned>(a.batch)), 256, 1, 0, false, s, G, a.rows,
+                           a.cols, a.ldg, a.stride_g, vec, partial);
+    if (e != cudaSuccess) return e;
+    const uint32_t tiles_c = static_cast<uint32_t>(pl.np / 64);
+    return launch(ns_first_kernel<T>, dim3(static_cast<unsigned>(pl.mp / 64 * tiles_c), static_cast<unsigned>(a.batch)), 256, 1, 0,
+                  true, s, G, a.rows, a.cols, a.ldg, a.stride_g, pl.transposed, static_cast<const float*>(partial), parts, a.eps,
+                  xh, xl, pl.np, pl.mp * pl.np, tiles_c);
+}
+
+}  // namespace
+
+size_t ortho_workspace_size(int out_dtype, int64_t batch, int64_t rows, int64_t cols) {
+    return plan_of(out_dtype, batch, rows, cols).total;
+}
+
+bool ortho_supports(int64_t batch, int64_t rows, int64_t cols) {
+    const NsPlan pl = plan_of(DGA_F32, batch, rows, cols);
+    const int64_t limit = (int64_t{1} << 31) - 256;  // rows and tiles are counted in 32 bits
+    return batch <= 65535 && pl.np < limit && batch * pl.mp < limit && pl.mp / 64 * (pl.np / 64) * batch < limit;
+}
+
+cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launches) {
+    const NsPlan pl = plan_of(a.out_dtype, a.batch, a.rows, a.cols);
+    uint8_t* ws = static_cast<uint8_t*>(a.ws);
+    float* partial = reinterpret_cast<float*>(ws);
+    ws += round_up(a.batch * kMaxParts * 4, 256);
+    __half *xh[2], *xl[2], *ah, *al, *bh, *bl;
+    auto take = [&](size_t bytes) {
+        __half* q = reinterpret_cast<__half*>(ws);
+        ws += bytes;
+        return q;
+    };
+    for (int i = 0; i < 2; ++i) {
+        xh[i] = take(pl.x_bytes);
+        xl[i] = take(pl.x_bytes);
+    }
+    ah = take(pl.a_bytes);
+    bh = take(pl.a_bytes);
+    al = pl.split ? take(pl.a_bytes) : nullptr;
+    bl = pl.split ? take(pl.a_bytes) : nullptr;
+
+    cudaError_t e = a.in_dtype == DGA_F32    ? launch_first<float>(a, pl, partial, xh[0], xl[0], a.stream)
+                    : a.in_dtype == DGA_BF16 ? launch_first<__nv_bfloat16>(a, pl, partial, xh[0], xl[0], a.stream)
+                                             : launch_first<__half>(a, pl, partial, xh[0], xl[0], a.stream);
+    if (e != cudaSuccess) return e;
+    *launches += 2;
+
+    // maps: rows of 64-column boxes; 128-row boxes serve K-major operands, 64-row ones the MN-major X
+    const int64_t all_rows = a.batch * pl.mp;
+    CUtensorMap x_h[2], x_l[2], xk_h[2], xk_l[2], ma_h, ma_l, mb_h, mb_l;
+    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+        e = half_map(&x_h[i], xh[i], all_rows, pl.np, 128);
+        if (e == cudaSuccess) e = half_map(&x_l[i], xl[i], all_rows, pl.np, 128);
+        if (e == cudaSuccess) e = half_map(&xk_h[i], xh[i], all_rows, pl.np, 64);
+        if (e == cudaSuccess) e = half_map(&xk_l[i], xl[i], all_rows, pl.np, 64);
+    }
+    if (e == cudaSuccess) e = half_map(&ma_h, ah, all_rows, pl.mp, 128);
+    if (e == cudaSuccess) e = half_map(&mb_h, bh, all_rows, pl.mp, 128);
+    if (e == cudaSuccess && pl.split) e = half_map(&ma_l, al, all_rows, pl.mp, 128);
+    if (e == cudaSuccess && pl.split) e = half_map(&mb_l, bl, all_rows, pl.mp, 128);
+    if (e != cudaSuccess) return e;
+    if (!pl.split) {
+        ma_l = ma_h;
+        mb_l = mb_h;
+    }
+
+    NsParams base{};
+    base.segs = pl.split ? 3 : 1;
+    base.p_rows = base.q_rows = static_cast<uint32_t>(pl.mp);
+    base.rows = pl.mp;
+    base.m = pl.m;
+    base.n = pl.n;
+    base.result = a.O;
+    base.result_type = a.out_dtype;
+    base.transposed = pl.transposed;
+    base.ldo = a.ldo;
+    base.stride_o = a.stride_o;
+    for (int step = 0; step < a.steps; ++step) {
+        const float ca = a.coefficients[3 * step], cb = a.coefficients[3 * step + 1], cc = a.coefficients[3 * step + 2];
+        const int now = step & 1, next = now ^ 1;
+        NsParams p = base;
+        p.sym = 1;
+        p.ld = pl.mp;
+        p.stride = pl.mp * pl.mp;
+        // A = X X^T
+        p.num_kb = static_cast<uint32_t>(pl.np / 64);
+        p.c_acc = 1.0f / kScale;
+        p.out_h = ah;
+        p.out_l = al;
+        e = launch_product(p, NsMaps{x_h[now], x_l[now], x_h[now], x_l[now]}, a.batch, pl.mp, pl.mp, dev, a.stream);
+        if (e != cudaSuccess) return e;
+        // B = b A + c A^2
+        p.num_kb = static_cast<uint32_t>(pl.mp / 64);
+        p.c_old = cb;
+        p.c_acc = cc / kScale;
+        p.old_h = ah;
+        p.old_l = al;
+        p.out_h = bh;
+        p.out_l = bl;
+        e = launch_product(p, NsMaps{ma_h, ma_l, ma_h, ma_l}, a.batch, pl.mp, pl.mp, dev, a.stream);
+        if (e != cudaSuccess) return e;
+        // X <- a X + B X
+        const bool last = step + 1 == a.steps;
+        p.sym = 0;
+        p.q_mn = 1;
+        p.ld = pl.np;
+        p.stride = pl.mp * pl.np;
+        p.c_old = last ? ca / kScale : ca;
+        p.c_acc = last ? 1.0f / (kScale * kScale) : 1.0f / kScale;
+        p.old_h = xh[now];
+        p.old_l = xl[now];
+        p.out_h = last ? nullptr : xh[next];
+        p.out_l = last ? nullptr : xl[next];
+        e = launch_product(p, NsMaps{mb_h, mb_l, xk_h[now], xk_l[now]}, a.batch, pl.mp, pl.np, dev, a.stream);
+        if (e != cudaSuccess) return e;
+        *launches += 3;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t ns_status_take(int* status) {
+    int v = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(&v, g_ns_status, sizeof v);
+    if (e != cudaSuccess) return e;
+    if (v != 0) {
+        int zero = 0;
+        e = cudaMemcpyToSymbol(g_ns_status, &zero, sizeof zero);
+    }
+    *status = v;
+    return e;
+}
+
+}  // namespace dga

@@ -478,6 +478,43 @@ int dga_mx_linear(dga_mx_format format, dga_dtype x_dtype, dga_dtype out_dtype, 
 
 size_t dga_mx_linear_workspace_size(dga_mx_format format, int64_t M, int64_t K);
 
+/*
+ * dga_orthogonalize -- orthogonalises an update (the Muon optimiser's step):
+ * for each of `batch` row-major matrices G (rows x cols, leading dimension
+ * ldg, stride_g elements apart),
+ *     X = G / (|G|_F + eps);  `steps` times, with (a, b, c) the step's
+ *     coefficients:  A = X X^T,  X <- a X + (b A + c A^2) X;  O = X
+ * (X transposed where rows > cols, which gives the same O with the smaller A),
+ * the Newton-Schulz iteration of K. Jordan, "Muon: An optimizer for hidden
+ * layers in neural networks" (2024), whose quintic is (3.4445, -4.7750,
+ * 2.0315) in each of 5 steps.  An all-zero G gives 0; an infinity or NaN
+ * anywhere in a matrix makes that matrix's O NaN (or, with infinities, 0).
+ *
+ * G and O: DGA_F32, DGA_BF16 or DGA_F16, each its own.  All products run on
+ * the tensor cores with fp32 accumulation from operands of 22 bits for
+ * DGA_F32 output (as exact as fp32 products) and 11 bits otherwise, X itself
+ * being kept to 22 bits; intermediates of magnitude 16 or more overflow (the
+ * quintic above stays below 4).  Results repeat bit for bit.
+ *   coefficients  HOST, 3 * steps floats: a, b, c of each step
+ *   O             may be G itself or overlap it
+ *   workspace     device, 256-byte aligned, of
+ *                 dga_orthogonalize_workspace_size(...) bytes; must not
+ *                 overlap G or O
+ * Errors: DGA_ERR_UNSUPPORTED (types; sizes past 32-bit tile counts), -3 batch
+ * (over 65535), -4 rows, -5 cols, -6 G, -7 ldg, -8 stride_g < 0, -9 O, -10
+ * ldo, -11 stride_o (outputs overlap), -12 steps (outside [1, 1000]), -13
+ * coefficients, -14 eps < 0 or NaN, -15 workspace; DGA_ERR_WORKSPACE,
+ * DGA_ERR_OVERLAP.  batch, rows or cols of 0 is a no-op.  2 + 3 * steps
+ * launches.
+ */
+int dga_orthogonalize(dga_dtype in_dtype, dga_dtype out_dtype, int64_t batch, int64_t rows,
+                      int64_t cols, const void* G, int64_t ldg, int64_t stride_g, void* O,
+                      int64_t ldo, int64_t stride_o, int steps, const float* coefficients,
+                      float eps, void* workspace, size_t workspace_bytes, dga_stream_t stream);
+
+size_t dga_orthogonalize_workspace_size(dga_dtype out_dtype, int64_t batch, int64_t rows,
+                                        int64_t cols);
+
 /* Library version: major*10000 + minor*100 + patch. */
 int dga_version(void);
 
