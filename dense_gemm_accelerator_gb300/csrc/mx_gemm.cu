@@ -9,8 +9,8 @@
 // epilogue's.
 //
 // Two kernels, both fed by TMA (codes as 128-byte swizzle rows of 256 values;
-// scale tiles of 512 bytes, copied from shared to tensor memory by
-// tcgen05.cp just before the MMAs that use them):
+// scale tiles of 512 bytes, moved on to tensor memory before the MMAs that use
+// them):
 //
 //   pair    a cluster of two CTAs per 256 x 256 tile of C, persistent; for
 //           many rows, where the tensor cores' rate is the bound
@@ -25,7 +25,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
-#include <type_traits>
+#include <cstring>
 
 #include "dga_internal.h"
 #include "epilogue.cuh"
@@ -41,7 +41,7 @@ namespace {
 constexpr uint64_t kWaitLimitNs = 4000000000ull;  // 4 s
 constexpr int kRowBytes = 128;                    // one stage of a row: 256 codes
 constexpr int kStageK = 256;
-enum : int { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3 };
+enum : int { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3, kRoleScales = 4 };
 
 // Scale tiles (4 blocks) of one stage's 256 values.
 __host__ __device__ constexpr int scale_tiles(int format) { return kStageK / (4 * mx_block(format)); }
@@ -55,6 +55,7 @@ struct MxParams {
     const float* fb;
     const void* bias;
     uint32_t tiles_m, tiles_n, num_tiles, num_kb, group_m;
+    uint32_t tma_store;  // C can be stored by TMA, and is not read
 };
 
 __device__ __forceinline__ void record_failure(int role, volatile int* abort_flag) {
@@ -89,21 +90,22 @@ struct PairPlan {
     static constexpr uint32_t kSfa = kSf * kMxTileBytes;
     static constexpr uint32_t kSfb = 2 * kSf * kMxTileBytes;
     static constexpr uint32_t kStage = kA + kB + kSfa + kSfb;
-    static constexpr uint32_t kBar = kPairStages * kStage;
-    // full[S], empty[S], acc_full[2], acc_free, drain, then tmem slot + abort flag
-    static constexpr uint32_t kBarBytes = (2 * kPairStages + 4) * 8 + 16;
-    static constexpr uint32_t kEpi = (kBar + kBarBytes + 127) / 128 * 128;
-    static constexpr uint32_t kTotal = kEpi + 4 * 32 * 33 * 4;
-    static constexpr uint32_t kLaunch = kTotal + 1024;
-    // tensor memory: two accumulators of 256 columns that share 48 (the
-    // scales of a stage take the last 48 of the 512): accumulator 0 in
-    // columns 0-255, accumulator 1 in 208-463.  The epilogue reads the shared
-    // columns first, after which the next tile's MMAs may start.
-    static constexpr uint32_t kAcc1 = 208;
-    static constexpr uint32_t kSfCol = 464;
+    // epilogue staging: two boxes of 32 rows x 128 bytes per epilogue warp
+    static constexpr uint32_t kEpi = kPairStages * kStage;
+    static constexpr uint32_t kEpiWarp = 2 * 32 * 128;
+    static constexpr uint32_t kBar = kEpi + 4 * kEpiWarp;
+    // full[S], scales_full[S], empty[S], scales_ready[2], acc_full[2], acc_free, drain, tmem slot + abort flag
+    static constexpr uint32_t kBarBytes = (3 * kPairStages + 6) * 8 + 16;
+    static constexpr uint32_t kLaunch = kBar + kBarBytes + 1024;
+    // tensor memory: two stages' scales in the last columns, and before them
+    // two accumulators of 256 columns that share some (48 with MXFP4's scales,
+    // 96 with NVFP4's).  The epilogue reads the shared columns first, after
+    // which the next tile's MMAs may start.
     static constexpr uint32_t kSfCols = 12 * kSf;  // 4 for A and 8 for B per scale tile
+    static constexpr uint32_t kSfCol = 512 - 2 * kSfCols;
+    static constexpr uint32_t kAcc1 = kSfCol - 256;
+    static constexpr int kSharedUnits = (256 - kAcc1 + 63) / 64;  // 64-column units that hold them
     static_assert(kStage % 1024 == 0, "stages keep the swizzle atoms aligned");
-    static_assert(kSfCol + kSfCols <= 512, "scales fit behind the accumulators");
 };
 
 template <typename TOut>
@@ -135,11 +137,64 @@ __device__ __forceinline__ void tile_coords(uint32_t t, const MxParams& p, uint3
     tn = r / gm;
 }
 
+// A 32 x 64 unit of the tile, lane l its row l, through the staging boxes to C
+// by TMA: rows of 128 bytes, 16-byte pieces swizzled so that neither the
+// writes nor TMA's reads meet in a bank.  `turn` counts the boxes used.
+template <typename TOut>
+__device__ __forceinline__ void store_unit(const MxParams& p, const CUtensorMap* tmC, float alpha, uint8_t* boxes, int lane,
+                                           int32_t row, int32_t col, const uint32_t (&v)[64], uint32_t& turn) {
+    constexpr int kPer = 128 / sizeof(TOut);  // columns of a box
+#pragma unroll
+    for (int b = 0; b < 64 / kPer; ++b) {
+        uint8_t* box = boxes + (turn & 1) * (32 * 128);
+        if (lane == 0) bulk_wait_read<1>();  // the store before last has read this box
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (sizeof(TOut) == 4) {
+                    const int c = b * kPer + q * 4 + e;
+                    float x = alpha * __uint_as_float(v[c]);
+                    if (p.bias != nullptr && col + c < p.N) x += __ldg(static_cast<const float*>(p.bias) + col + c);
+                    w[e] = __float_as_uint(x);
+                } else {
+                    const int c = b * kPer + q * 8 + e * 2;
+                    TOut two[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float x = alpha * __uint_as_float(v[c + h]);
+                        if (p.bias != nullptr && col + c + h < p.N)
+                            x += OutT<TOut>::load(static_cast<const TOut*>(p.bias) + col + c + h);
+                        OutT<TOut>::store(&two[h], x);
+                    }
+                    memcpy(&w[e], two, 4);
+                }
+            }
+            *reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            if (row < p.M && col + b * kPer < p.N) tma_store_2d(tmC, box, col + b * kPer, row);
+            bulk_commit();
+        }
+        ++turn;
+    }
+}
+
+// Warps: TMA producer, MMA issuer, 4 epilogue, 4 that bring the scales to
+// tensor memory (tcgen05.cp would: measured 50 clocks of the tensor pipe per
+// 512-byte tile, in line with the MMAs, 72 (MXFP4) to 146 us (NVFP4) of
+// 283 to 359 us at 8192^3; tcgen05.st from these warps runs beside them).
+constexpr int kPairThreads = 320;
+
 template <int kFormat, typename TOut>
-__global__ void __launch_bounds__(192, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmSa, const __grid_constant__ CUtensorMap tmSb,
-                        MxParams p) {
+                        const __grid_constant__ CUtensorMap tmC, MxParams p) {
     using S = PairPlan<kFormat>;
     constexpr bool kE8M0 = kFormat == DGA_MXFP4;
     constexpr uint32_t kIdesc0 = idesc_mx(kE8M0, 256, 256, 0), kIdesc2 = idesc_mx(kE8M0, 256, 256, 2);
@@ -149,8 +204,10 @@ __global__ void __launch_bounds__(192, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBar);
-    uint64_t* empty = full + kPairStages;
-    uint64_t* acc_full = empty + kPairStages;
+    uint64_t* scales_full = full + kPairStages;
+    uint64_t* empty = scales_full + kPairStages;
+    uint64_t* scales_ready = empty + kPairStages;
+    uint64_t* acc_full = scales_ready + 2;
     uint64_t* acc_free = acc_full + 2;
     uint64_t* drain = acc_free + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -163,9 +220,13 @@ __global__ void __launch_bounds__(192, 1)
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kPairStages; ++s) {
             mbar_init(&full[s], 1);
+            mbar_init(&scales_full[s], 1);
             mbar_init(&empty[s], 1);
         }
-        for (int b = 0; b < 2; ++b) mbar_init(&acc_full[b], 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&scales_ready[b], 8);  // one lane of each scale warp of both CTAs
+            mbar_init(&acc_full[b], 1);
+        }
         mbar_init(acc_free, 8);  // one lane of each epilogue warp of both CTAs
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -204,15 +265,18 @@ __global__ void __launch_bounds__(192, 1)
                         break;
                     }
                     uint8_t* dst = smem + stage * S::kStage;
-                    if (leader) mbar_arrive_expect_tx(&full[stage], 2 * S::kStage);
+                    // the codes of both CTAs count on the leader's barrier, for
+                    // its MMA thread; each CTA's scales on its own
+                    if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (S::kA + S::kB));
+                    mbar_arrive_expect_tx(&scales_full[stage], S::kSfa + S::kSfb);
                     const uint32_t bar = map_to_cta(smem_u32(&full[stage]), 0);
                     const int32_t x = static_cast<int32_t>(kb * kRowBytes);
                     const int32_t sx = static_cast<int32_t>(kb * (S::kSf * kMxTileBytes / 8));
+                    tma_load_2d(dst + S::kA + S::kB, &tmSa, &scales_full[stage], sx, a_row / 128);
+                    // each CTA's MMA half reads all 256 of the tile's B scales
+                    tma_load_2d(dst + S::kA + S::kB + S::kSfa, &tmSb, &scales_full[stage], sx, static_cast<int32_t>(tn * 2));
                     tma_load_2d_pair(dst, &tmA, bar, x, a_row);
                     tma_load_2d_pair(dst + S::kA, &tmB, bar, x, b_row);
-                    tma_load_2d_pair(dst + S::kA + S::kB, &tmSa, bar, sx, a_row / 128);
-                    // each CTA's MMA half reads all 256 of the tile's B scales
-                    tma_load_2d_pair(dst + S::kA + S::kB + S::kSfa, &tmSb, bar, sx, static_cast<int32_t>(tn * 2));
                     if (++stage == kPairStages) { stage = 0; phase ^= 1; }
                 }
             }
@@ -227,27 +291,18 @@ __global__ void __launch_bounds__(192, 1)
                     record_failure(kRoleMma, abort_flag);
                     break;
                 }
-                tc_fence_after();
                 const uint32_t d = tmem + (i & 1 ? S::kAcc1 : 0u);
-                for (uint32_t kb = 0; kb < p.num_kb; ++kb) {
-                    if (!mbar_wait_bounded<true>(&full[stage], phase, abort_flag, kWaitLimitNs)) {
+                for (uint32_t kb = 0; kb < p.num_kb; ++kb, ++fill) {
+                    if (!mbar_wait_bounded<true>(&full[stage], phase, abort_flag, kWaitLimitNs) ||
+                        !mbar_wait_bounded<true>(&scales_ready[fill & 1], (fill >> 1) & 1, abort_flag, kWaitLimitNs)) {
                         record_failure(kRoleMma, abort_flag);
                         ok = false;
                         break;
                     }
                     tc_fence_after();
                     const uint32_t a_addr = smem_u32(smem + stage * S::kStage);
-                    const uint32_t sf_addr = a_addr + S::kA + S::kB;
-                    // MXFP4's scales of a stage take 24 columns: two stages' worth in turn
-                    const uint32_t sfa = tmem + S::kSfCol + (kE8M0 ? (fill & 1) * S::kSfCols : 0u);
+                    const uint32_t sfa = tmem + S::kSfCol + (fill & 1) * S::kSfCols;
                     const uint32_t sfb = sfa + 4 * S::kSf;
-                    ++fill;
-#pragma unroll
-                    for (int j = 0; j < S::kSf; ++j) {
-                        tc_cp_scales<true>(sfa + 4 * j, smem_desc_scales(sf_addr + j * kMxTileBytes));
-                        tc_cp_scales<true>(sfb + 8 * j, smem_desc_scales(sf_addr + S::kSfa + j * kMxTileBytes));
-                        tc_cp_scales<true>(sfb + 8 * j + 4, smem_desc_scales(sf_addr + S::kSfa + (S::kSf + j) * kMxTileBytes));
-                    }
                     const uint64_t a_desc = smem_desc_kmajor_sw128(a_addr);
                     const uint64_t b_desc = smem_desc_kmajor_sw128(a_addr + S::kA);
 #pragma unroll
@@ -267,12 +322,55 @@ __global__ void __launch_bounds__(192, 1)
             volatile int never = 0;
             mbar_wait_bounded(drain, 0, &never, kWaitLimitNs);
         }
+    } else if (warp >= 6) {
+        // ------------------------------------------------ scales to tensor memory
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        uint32_t stage = 0, phase = 0, fill = 0;
+        bool ok = true;
+        for (uint32_t t = cluster_id; ok && t < p.num_tiles; t += n_clusters) {
+            for (uint32_t kb = 0; kb < p.num_kb; ++kb, ++fill) {
+                // the columns are free when the MMAs of two stages ago are done
+                const uint32_t before = fill - 2;
+                if (!mbar_wait_bounded(&scales_full[stage], phase, abort_flag, kWaitLimitNs) ||
+                    (fill >= 2 && !mbar_wait_bounded<true>(&empty[before % kPairStages], (before / kPairStages) & 1,
+                                                           abort_flag, kWaitLimitNs))) {
+                    record_failure(kRoleScales, abort_flag);
+                    ok = false;
+                    break;
+                }
+                // a tile's lane l: the four scales of rows l, 32 + l, 64 + l, 96 + l
+                const uint8_t* src = smem + stage * S::kStage + S::kA + S::kB + lane * 16;
+                uint32_t r[S::kSfCols];
+#pragma unroll
+                for (int j = 0; j < S::kSf; ++j) {
+                    *reinterpret_cast<uint4*>(&r[4 * j]) = *reinterpret_cast<const uint4*>(src + j * kMxTileBytes);
+#pragma unroll
+                    for (int b = 0; b < 2; ++b)
+                        *reinterpret_cast<uint4*>(&r[4 * S::kSf + 8 * j + 4 * b]) =
+                            *reinterpret_cast<const uint4*>(src + S::kSfa + (b * S::kSf + j) * kMxTileBytes);
+                }
+                tc_fence_after();
+                const uint32_t dst = tmem + lane_base + S::kSfCol + (fill & 1) * S::kSfCols;
+                if constexpr (S::kSfCols == 24) {
+                    tmem_st_32x32b_x16(dst, r);
+                    tmem_st_32x32b_x8(dst + 16, r + 16);
+                } else {
+                    tmem_st_32x32b_x32(dst, r);
+                    tmem_st_32x32b_x16(dst + 32, r + 32);
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&scales_ready[fill & 1]), 0));
+                if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+            }
+        }
     } else {
         const int quarter = warp & 3;
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-        uint32_t* stage = reinterpret_cast<uint32_t*>(smem + S::kEpi + (warp - 2) * (32 * 33 * 4));
+        uint8_t* boxes = smem + S::kEpi + (warp - 2) * S::kEpiWarp;
         const float alpha = total_alpha(p);
-        uint32_t i = 0;
+        uint32_t i = 0, turn = 0;
         for (uint32_t t = cluster_id; t < p.num_tiles; t += n_clusters, ++i) {
             uint32_t tm, tn;
             tile_coords(t, p, tm, tn);
@@ -285,21 +383,30 @@ __global__ void __launch_bounds__(192, 1)
             tc_fence_after();
             const uint32_t d = tmem + lane_base + (i & 1 ? S::kAcc1 : 0u);
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < 4; ++c) {
                 // accumulator 0 from its end, 1 from its start: the columns
-                // they share are in the first two blocks
-                const int block = i & 1 ? c : 7 - c;
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(d + block * 32, r);
+                // they share are in the first units
+                const int unit = i & 1 ? c : 3 - c;
+                uint32_t r[64];
+                tmem_ld_32x32b_x32(d + unit * 64, reinterpret_cast<uint32_t(&)[32]>(r[0]));
+                tmem_ld_32x32b_x32(d + unit * 64 + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
                 tmem_ld_wait();
-                if (c == 1) {
+                if (c == S::kSharedUnits - 1) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(acc_free), 0));
+                    if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(acc_free), 0));
                 }
-                store_block<TOut>(p, alpha, stage, lane, row_base, col0 + block * 32, r);
+                if (p.tma_store) {
+                    store_unit<TOut>(p, &tmC, alpha, boxes, lane, static_cast<int32_t>(row_base),
+                                     static_cast<int32_t>(col0) + unit * 64, r, turn);
+                } else {
+                    uint32_t* square = reinterpret_cast<uint32_t*>(boxes);
+                    store_block<TOut>(p, alpha, square, lane, row_base, col0 + unit * 64, reinterpret_cast<uint32_t(&)[32]>(r[0]));
+                    store_block<TOut>(p, alpha, square, lane, row_base, col0 + unit * 64 + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
+                }
             }
         }
+        if (lane == 0) bulk_wait_all();  // shared memory outlives the stores that read it
     }
 
     tc_fence_before();
@@ -459,40 +566,57 @@ __global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
     const int64_t col = static_cast<int64_t>(tile) * 128 + w_in;  // a row of B: a column of C
     const int rows = static_cast<int>(p.M);
     float* red = reinterpret_cast<float*>(smem);
-    if (warp >= 2 && ok) {
-        const float alpha = total_alpha(p);
-        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-        constexpr int kStep = kN < 32 ? 16 : 32;
+    const float alpha = total_alpha(p);
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    constexpr int kStep = kN < 32 ? 16 : 32;
+    if (splits == 1) {
+        if (warp >= 2 && ok) {
 #pragma unroll 1
-        for (int c = 0; c < kN && c < rows; c += kStep) {
-            uint32_t r[kStep];
-            if constexpr (kStep == 16) tmem_ld_32x32b_x16(tmem + lane_base + c, r);
-            else tmem_ld_32x32b_x32(tmem + lane_base + c, r);
-            tmem_ld_wait();
-            if (splits == 1) {
+            for (int c = 0; c < kN && c < rows; c += kStep) {
+                uint32_t r[kStep];
+                if constexpr (kStep == 16) tmem_ld_32x32b_x16(tmem + lane_base + c, r);
+                else tmem_ld_32x32b_x32(tmem + lane_base + c, r);
+                tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < kStep; ++j)
                     if (c + j < rows && col < p.N) put<TOut>(p, alpha, c + j, col, __uint_as_float(r[j]));
-            } else {
-#pragma unroll
-                for (int j = 0; j < kStep; ++j) red[(c + j) * 128 + w_in] = __uint_as_float(r[j]);
             }
         }
-    }
-    if (splits > 1) {
+    } else {
+        // Row j of A is joined by CTA j % splits.  Each CTA sends its sums to
+        // the joining ones (stores, which nothing waits for) once every ring
+        // is done with, slot q of `red` coming from part q:
+        // red[(q * kN / splits + j / splits) * 128 + w].
+        const uint32_t per = kN / splits;
+        __syncwarp();
+        cluster_sync();
+        if (warp >= 2 && ok) {
+#pragma unroll 1
+            for (int c = 0; c < kN && c < rows; c += kStep) {
+                uint32_t r[kStep];
+                if constexpr (kStep == 16) tmem_ld_32x32b_x16(tmem + lane_base + c, r);
+                else tmem_ld_32x32b_x32(tmem + lane_base + c, r);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < kStep; ++j) {
+                    const uint32_t row = c + j;
+                    if (row < rows) {
+                        const uint32_t at = smem_u32(red + (part * per + row / splits) * 128 + w_in);
+                        st_shared_cluster_f32(map_to_cta(at, row % splits), __uint_as_float(r[j]));
+                    }
+                }
+            }
+        }
         __syncwarp();
         cluster_sync();
         if (warp >= 2 && col < p.N) {
-            const float alpha = total_alpha(p);
-            for (int j = static_cast<int>(part); j < rows; j += static_cast<int>(splits)) {
-                const uint32_t addr = smem_u32(red + j * 128 + w_in);
+            uint32_t slot = 0;
+            for (int j = static_cast<int>(part); j < rows; j += static_cast<int>(splits), ++slot) {
                 float sum = 0.0f;
-                for (uint32_t q = 0; q < splits; ++q) sum += ld_shared_cluster_f32(map_to_cta(addr, q));
+                for (uint32_t q = 0; q < splits; ++q) sum += red[(q * per + slot) * 128 + w_in];
                 put<TOut>(p, alpha, j, col, sum);
             }
         }
-        __syncwarp();
-        cluster_sync();  // no CTA leaves while another reads its sums
     }
     tc_fence_before();
     __syncthreads();
@@ -549,14 +673,14 @@ cudaError_t scales_map(CUtensorMap* map, int format, const MxMatrix& m, int64_t 
                     static_cast<uint32_t>(scale_tiles(format) * kMxTileBytes / 8), box_rows);
 }
 
-template <typename Kern>
-cudaError_t launch(Kern kern, unsigned grid, unsigned cluster, int smem, bool pdl, cudaStream_t s,
-                   const CUtensorMap* maps, const MxParams& p, uint32_t splits) {
+template <typename... P, typename... A>
+cudaError_t launch(void (*kern)(P...), unsigned grid, int threads, unsigned cluster, int smem, bool pdl,
+                   cudaStream_t s, const A&... args) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(192);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -568,10 +692,7 @@ cudaError_t launch(Kern kern, unsigned grid, unsigned cluster, int smem, bool pd
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
-    if constexpr (std::is_same_v<Kern, void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, MxParams)>)
-        return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p);
-    else
-        return cudaLaunchKernelEx(&cfg, kern, maps[0], maps[1], maps[2], maps[3], p, splits);
+    return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 template <int kFormat, int kN, typename TOut>
@@ -587,14 +708,14 @@ cudaError_t launch_skinny(const MxGemmArgs& a, MxParams p, const DeviceInfo& dev
     const int64_t tiles = (a.N + 127) / 128, slots = static_cast<int64_t>(dev.sm_count) * S::kCtas;
     uint32_t splits = 1;
     while (splits < 8 && tiles * splits * 2 <= slots && p.num_kb >= splits * 4) splits *= 2;
-    return launch(mx_gemm_skinny_kernel<kFormat, kN, TOut>, static_cast<unsigned>(tiles * splits), splits,
-                  static_cast<int>(S::kLaunch), a.after_quantize, a.stream, m, p, splits);
+    return launch(mx_gemm_skinny_kernel<kFormat, kN, TOut>, static_cast<unsigned>(tiles * splits), 192, splits,
+                  static_cast<int>(S::kLaunch), a.after_quantize, a.stream, m[0], m[1], m[2], m[3], p, splits);
 }
 
 template <int kFormat, typename TOut>
 cudaError_t launch_pair(const MxGemmArgs& a, MxParams p, const DeviceInfo& dev) {
     using S = PairPlan<kFormat>;
-    CUtensorMap m[4];
+    CUtensorMap m[5];
     cudaError_t e = codes_map(&m[0], a.A, a.M, a.K, 128);
     if (e == cudaSuccess) e = codes_map(&m[1], a.B, a.N, a.K, 128);
     if (e == cudaSuccess) e = scales_map(&m[2], kFormat, a.A, a.M, a.K, 1);
@@ -607,8 +728,17 @@ cudaError_t launch_pair(const MxGemmArgs& a, MxParams p, const DeviceInfo& dev) 
     const double panel = 256.0 * static_cast<double>(a.K) / 2;
     p.group_m = std::min(p.tiles_m, std::max(8u, std::min(64u, static_cast<uint32_t>(32.0 * 1024 * 1024 / panel))));
     const unsigned clusters = std::min<unsigned>(p.num_tiles, dev.sm_count / 2);
-    return launch(mx_gemm_pair_kernel<kFormat, TOut>, 2 * clusters, 2, static_cast<int>(S::kLaunch),
-                  a.after_quantize, a.stream, m, p, 1);
+    // C by TMA stores where its rows allow them and it is only written
+    constexpr int64_t kEs = sizeof(TOut);
+    p.tma_store = a.beta == 0.0f && aligned(a.C, 16) && a.ldc * kEs % 16 == 0;
+    if (p.tma_store)
+        e = make_map(&m[4], kEs == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
+                     CU_TENSOR_MAP_SWIZZLE_128B, a.C, a.N, a.M, a.ldc * kEs, 128 / kEs, 32);
+    else
+        m[4] = m[0];  // not used
+    if (e != cudaSuccess) return e;
+    return launch(mx_gemm_pair_kernel<kFormat, TOut>, 2 * clusters, kPairThreads, 2, static_cast<int>(S::kLaunch),
+                  a.after_quantize, a.stream, m[0], m[1], m[2], m[3], m[4], p);
 }
 
 template <int kFormat, typename TOut>

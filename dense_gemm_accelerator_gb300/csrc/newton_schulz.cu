@@ -43,6 +43,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "dga_internal.h"
 #include "epilogue.cuh"
@@ -75,7 +76,7 @@ struct NsParams {
     __half* out_l;  // null: hi alone
     int64_t rows, ld, stride;  // of old and out: padded rows, row and matrix strides
     void* result;
-    int result_type, transposed;
+    int result_type, transposed, result_vec;  // result_vec: its rows take 16-byte stores
     int64_t m, n, ldo, stride_o;
 };
 
@@ -108,6 +109,33 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// 32 columns of a row of X to the result: rows of m x n, or (transposed) of n x m.
+template <typename T>
+__device__ __forceinline__ void ns_result(const NsParams& p, uint32_t matrix, int64_t row, int64_t col, const float (&v)[32]) {
+    T* base = static_cast<T*>(p.result) + matrix * p.stride_o;
+    if (p.transposed) {
+        // element (col + j, row): consecutive lanes on consecutive columns
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (col + j < p.n) OutT<T>::store(base + (col + j) * p.ldo + row, v[j]);
+    } else if (p.result_vec && col + 32 <= p.n) {
+        constexpr int kPer = 16 / sizeof(T);
+#pragma unroll
+        for (int q = 0; q < 32 / kPer; ++q) {
+            T w[kPer];
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) OutT<T>::store(&w[e], v[q * kPer + e]);
+            uint4 x;
+            memcpy(&x, w, 16);
+            *reinterpret_cast<uint4*>(base + row * p.ldo + col + q * kPer) = x;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (col + j < p.n) OutT<T>::store(base + row * p.ldo + col + j, v[j]);
+    }
+}
+
 // 32 columns (col .. col+31) of one row per lane.  mirror: the tile is off the
 // diagonal of a symmetric product, so that its transpose is stored too.
 __device__ __forceinline__ void ns_store(const NsParams& p, uint32_t matrix, int64_t row, int64_t col, bool mirror,
@@ -137,18 +165,10 @@ __device__ __forceinline__ void ns_store(const NsParams& p, uint32_t matrix, int
         }
     }
     if (p.out_h == nullptr) {
-        // the result: rows of m x n, or (transposed) of n x m
-        auto put = [&](int64_t i, float x) {
-            if (p.result_type == DGA_F32) static_cast<float*>(p.result)[i] = x;
-            else if (p.result_type == DGA_BF16) static_cast<__nv_bfloat16*>(p.result)[i] = __float2bfloat16_rn(x);
-            else static_cast<__half*>(p.result)[i] = __float2half_rn(x);
-        };
-        const int64_t base = matrix * p.stride_o;
         if (row < p.m) {
-            const int64_t step = p.transposed ? p.ldo : 1, first = base + (p.transposed ? col * p.ldo + row : row * p.ldo + col);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-                if (col + j < p.n) put(first + j * step, v[j]);
+            if (p.result_type == DGA_F32) ns_result<float>(p, matrix, row, col, v);
+            else if (p.result_type == DGA_BF16) ns_result<__nv_bfloat16>(p, matrix, row, col, v);
+            else ns_result<__half>(p, matrix, row, col, v);
         }
         return;
     }
@@ -317,7 +337,15 @@ __global__ void __launch_bounds__(tile_threads(kChunked), 2)
     const int64_t row = static_cast<int64_t>(tm) * 128 + r_in, col0 = static_cast<int64_t>(tn) * 128;
     const bool mirror = p.sym && tm != tn;
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    // Column block c of 32 is joined by CTA c % splits.  Each CTA sends its sums
+    // to the joining ones (stores, which nothing waits for) once every CTA's
+    // ring is done with, slot q of `red` coming from part q:
+    // red[((q * 4 / splits + c / splits) * 32 + j) * 128 + row].
     float* red = reinterpret_cast<float*>(smem);
+    auto send = [&](uint32_t c, int j, float x) {
+        const uint32_t at = smem_u32(red + ((part * (4 / splits) + c / splits) * 32 + j) * 128 + r_in);
+        st_shared_cluster_f32(map_to_cta(at, c % splits), x);
+    };
     // the last commit: every MMA of this CTA, and with them every copy into the ring
     const uint32_t n_chunks = kChunked ? chunk_count(p, kb0, kb1) : 1;
     bool ok = true;
@@ -357,14 +385,23 @@ __global__ void __launch_bounds__(tile_threads(kChunked), 2)
                     }
                 }
             } else {
+                cluster_sync();
 #pragma unroll
-                for (int j = 0; j < 64; ++j) red[(half * 64 + j) * 128 + r_in] = sum[j];
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) send(half * 2 + c, j, sum[c * 32 + j]);
             }
+        } else if (splits > 1) {
+            cluster_sync();
         }
     } else {
         ok = mbar_wait_bounded(&acc_full[0], 0, abort_flag, kWaitLimitNs);
         if (!ok) record_failure(kRoleEpilogue, abort_flag);
         tc_fence_after();
+        if (splits > 1) {
+            __syncwarp();
+            cluster_sync();
+        }
         if (warp >= 2 && ok) {
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
@@ -378,7 +415,7 @@ __global__ void __launch_bounds__(tile_threads(kChunked), 2)
                     ns_store(p, matrix, row, col0 + c * 32, mirror, v);
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) red[(c * 32 + j) * 128 + r_in] = __uint_as_float(r[j]);
+                    for (int j = 0; j < 32; ++j) send(c, j, __uint_as_float(r[j]));
                 }
             }
         }
@@ -387,22 +424,20 @@ __global__ void __launch_bounds__(tile_threads(kChunked), 2)
         __syncwarp();
         cluster_sync();
         if (warp >= 2) {
-            // each CTA joins and stores its share of the columns, 32 at a time
-            const uint32_t first = part + (kChunked ? ((warp - 2) >> 2) * splits : 0u);
-            for (uint32_t c = first; c < 4; c += kChunked ? 2 * splits : splits) {
+            // this CTA's blocks, a warp quarter's rows; with eight warps each half takes every other one
+            const uint32_t per = 4 / splits;
+            for (uint32_t i = kChunked ? (warp - 2) >> 2 : 0; i < per; i += kChunked ? 2 : 1) {
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                 for (uint32_t q = 0; q < splits; ++q) {
-                    const uint32_t addr = map_to_cta(smem_u32(red + c * 32 * 128 + r_in), q);
+                    const float* src = red + ((q * per + i) * 32) * 128 + r_in;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] += ld_shared_cluster_f32(addr + j * 512);
+                    for (int j = 0; j < 32; ++j) v[j] += src[j * 128];
                 }
-                ns_store(p, matrix, row, col0 + c * 32, mirror, v);
+                ns_store(p, matrix, row, col0 + (i * splits + part) * 32, mirror, v);
             }
         }
-        __syncwarp();
-        cluster_sync();  // no CTA leaves while another reads its sums
     }
     tc_fence_before();
     __syncthreads();
@@ -583,7 +618,7 @@ __global__ void __launch_bounds__(pair_threads(kChunked), 1)
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
+                    if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
                     if (++acc == 2) { acc = 0; acc_phase ^= 1; }
                 }
                 if (!ok) break;
@@ -612,7 +647,7 @@ __global__ void __launch_bounds__(pair_threads(kChunked), 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
+                if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
                 if (++acc == 2) { acc = 0; acc_phase ^= 1; }
             }
         }
@@ -636,7 +671,7 @@ template <> __device__ __forceinline__ float ns_in<float>(float v) { return v; }
 template <> __device__ __forceinline__ float ns_in<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <> __device__ __forceinline__ float ns_in<__half>(__half v) { return __half2float(v); }
 
-// The block's sum in thread 0, in a fixed order.
+// The block's sum in every thread, in a fixed order.
 __device__ __forceinline__ float block_sum(float s) {
     __shared__ float part[8];
 #pragma unroll
@@ -649,82 +684,95 @@ __device__ __forceinline__ float block_sum(float s) {
     return s;
 }
 
-// Sums of squares: block (x, matrix) adds rows x, x + gridDim.x, ...
+constexpr int64_t kSegment = 2048;  // columns of a row that a warp takes at once
+
+// Eight consecutive values of a row from column c, zero from `cols` on.
+template <typename T>
+__device__ __forceinline__ void ns_load8(const T* row, int64_t c, int64_t cols, bool vec, float (&x)[8]) {
+    if (vec && c + 8 <= cols) {
+        T v[8];
+        uint4 w[sizeof(T) / 2];
+#pragma unroll
+        for (int q = 0; q < static_cast<int>(sizeof(T) / 2); ++q) w[q] = reinterpret_cast<const uint4*>(row + c)[q];
+        memcpy(v, w, sizeof v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = ns_in(v[q]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) x[q] = c + q < cols ? ns_in(row[c + q]) : 0.0f;
+    }
+}
+
+// Sums of squares of G (blockIdx.y: the matrix): each warp takes segments of
+// rows in turn, a lane eight values at a time; one partial sum per block.
 template <typename T>
 __global__ void __launch_bounds__(256) ns_squares_kernel(const T* __restrict__ G, int64_t rows, int64_t cols,
                                                          int64_t ldg, int64_t stride_g, bool vec,
                                                          float* __restrict__ partial) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    constexpr int kVec = 16 / sizeof(T);
     const T* base = G + blockIdx.y * stride_g;
-    float s = 0.0f;
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-        const T* row = base + r * ldg;
-        if (vec) {
-            for (int64_t c = threadIdx.x * kVec; c < cols; c += 256 * kVec) {
-                if (c + kVec <= cols) {
-                    T v[kVec];
-                    *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(row + c);
+    const int64_t segments = (cols + kSegment - 1) / kSegment, units = rows * segments;
+    float s[8];
 #pragma unroll
-                    for (int q = 0; q < kVec; ++q) s = fmaf(ns_in(v[q]), ns_in(v[q]), s);
-                } else {
-                    for (int64_t q = c; q < cols; ++q) s = fmaf(ns_in(row[q]), ns_in(row[q]), s);
-                }
-            }
-        } else {
-            for (int64_t c = threadIdx.x; c < cols; c += 256) s = fmaf(ns_in(row[c]), ns_in(row[c]), s);
+    for (int q = 0; q < 8; ++q) s[q] = 0.0f;
+    for (int64_t u = blockIdx.x * 8 + (threadIdx.x >> 5); u < units; u += gridDim.x * 8) {
+        const int64_t r = u / segments, c0 = (u - r * segments) * kSegment;
+        const int64_t end = min(cols, c0 + kSegment);
+#pragma unroll 4
+        for (int64_t c = c0 + (threadIdx.x & 31) * 8; c < end; c += 256) {
+            float x[8];
+            ns_load8(base + r * ldg, c, cols, vec, x);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) s[q] = fmaf(x[q], x[q], s[q]);
         }
     }
-    s = block_sum(s);
-    if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = s;
+    const float total = block_sum(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
+    if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = total;
 }
 
-// X = G / (|G| + eps) as hi and lo, zero in the padding; 64 x 64 tiles through
-// shared memory, transposed on the way for a tall G.
+// X = G / (|G| + eps) as hi and lo, zero in the padding: 64 x 64 tiles, a
+// thread 16 consecutive columns of a row; a tall G is transposed through
+// shared memory.
 template <typename T>
 __global__ void __launch_bounds__(256) ns_first_kernel(const T* __restrict__ G, int64_t rows, int64_t cols, int64_t ldg,
-                                                       int64_t stride_g, bool transposed,
+                                                       int64_t stride_g, bool vec, bool transposed,
                                                        const float* __restrict__ partial, int parts, float eps,
                                                        __half* __restrict__ xh, __half* __restrict__ xl, int64_t ld,
                                                        int64_t stride, uint32_t tiles_c) {
     __shared__ float tile[64][65];
-    __shared__ float unit;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t r0 = static_cast<int64_t>(blockIdx.x / tiles_c) * 64, c0 = static_cast<int64_t>(blockIdx.x % tiles_c) * 64;
+    const int tr = threadIdx.x >> 2, tc = (threadIdx.x & 3) * 16;
+    // X's rows r0.., columns c0..: G's rows from r0 (c0), columns from c0 (r0)
+    const int64_t gr = (transposed ? c0 : r0) + tr, gc = (transposed ? r0 : c0) + tc;
+    const T* row = G + blockIdx.y * stride_g + gr * ldg;
+    float x[2][8];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) ns_load8(row, gr < rows ? gc + q * 8 : cols, cols, vec, x[q]);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float s = 0.0f;
     for (int i = threadIdx.x; i < parts; i += 256) s += partial[blockIdx.y * parts + i];
-    s = block_sum(s);
-    if (threadIdx.x == 0) unit = kScale / (sqrtf(s) + eps);
-    __syncthreads();
-    const float u = unit;
-    const int64_t r0 = static_cast<int64_t>(blockIdx.x / tiles_c) * 64, c0 = static_cast<int64_t>(blockIdx.x % tiles_c) * 64;
-    // X's rows r0.., columns c0..: G's rows g0.., columns h0..
-    const int64_t g0 = transposed ? c0 : r0, h0 = transposed ? r0 : c0;
-    const T* base = G + blockIdx.y * stride_g;
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-#pragma unroll 4
-    for (int i = y; i < 64; i += 4) {
-        const int64_t r = g0 + i, c = h0 + x;
-        const float v = r < rows && c < cols ? ns_in(base[r * ldg + c]) * u : 0.0f;
-        if (transposed) tile[x][i] = v;
-        else tile[i][x] = v;
-    }
-    __syncthreads();
-    // 16 consecutive columns of a row per thread
-    const int tr = threadIdx.x >> 2, tc = (threadIdx.x & 3) * 16;
-    uint32_t h[8], l[8];
+    const float u = kScale / (sqrtf(block_sum(s)) + eps);
+    if (transposed) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float a = tile[tr][tc + 2 * j], b = tile[tr][tc + 2 * j + 1];
-        h[j] = pack2(a, b);
-        const float2 f = unpack2(h[j]);
-        l[j] = pack2(a - f.x, b - f.y);
+        for (int j = 0; j < 16; ++j) tile[tc + j][tr] = x[j / 8][j % 8];
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j / 8][j % 8] = tile[tr][tc + j];
     }
     const int64_t at = blockIdx.y * stride + (r0 + tr) * ld + c0 + tc;
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-        *reinterpret_cast<uint4*>(xh + at + q * 8) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
-        *reinterpret_cast<uint4*>(xl + at + q * 8) = make_uint4(l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]);
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float a = x[q][2 * j] * u, b = x[q][2 * j + 1] * u;
+            h[j] = pack2(a, b);
+            const float2 f = unpack2(h[j]);
+            l[j] = pack2(a - f.x, b - f.y);
+        }
+        *reinterpret_cast<uint4*>(xh + at + q * 8) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(xl + at + q * 8) = make_uint4(l[0], l[1], l[2], l[3]);
     }
 }
 
@@ -751,7 +799,7 @@ cudaError_t half_map(CUtensorMap* map, const __half* base, int64_t rows, int64_t
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
-constexpr int kMaxParts = 128;  // partial sums of squares per matrix
+constexpr int kMaxParts = 512;  // partial sums of squares per matrix
 
 struct NsPlan {
     int64_t m, n, mp, np;  // m <= n, and padded to the K block
@@ -830,17 +878,21 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
 }
 
 template <typename T>
-cudaError_t launch_first(const OrthoArgs& a, const NsPlan& pl, float* partial, __half* xh, __half* xl, cudaStream_t s) {
+cudaError_t launch_first(const OrthoArgs& a, const NsPlan& pl, float* partial, __half* xh, __half* xl,
+                         const DeviceInfo& dev, cudaStream_t s) {
     const T* G = static_cast<const T*>(a.G);
     constexpr int64_t kVec = 16 / sizeof(T);
     const bool vec = aligned(G, 16) && a.ldg % kVec == 0 && (a.batch == 1 || a.stride_g % kVec == 0);
-    const int parts = static_cast<int>(std::min<int64_t>(a.rows, kMaxParts));
+    // blocks of eight segments each, a few to an SM at most over all matrices
+    const int64_t units = a.rows * ((a.cols + kSegment - 1) / kSegment);
+    const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxParts, 4 * dev.sm_count / a.batch));
+    const int parts = static_cast<int>(std::min<int64_t>((units + 7) / 8, most));
     cudaError_t e = launch(ns_squares_kernel<T>, dim3(parts, static_cast<unsigned>(a.batch)), 256, 1, 0, false, s, G, a.rows,
                            a.cols, a.ldg, a.stride_g, vec, partial);
     if (e != cudaSuccess) return e;
     const uint32_t tiles_c = static_cast<uint32_t>(pl.np / 64);
     return launch(ns_first_kernel<T>, dim3(static_cast<unsigned>(pl.mp / 64 * tiles_c), static_cast<unsigned>(a.batch)), 256, 1, 0,
-                  true, s, G, a.rows, a.cols, a.ldg, a.stride_g, pl.transposed, static_cast<const float*>(partial), parts, a.eps,
+                  true, s, G, a.rows, a.cols, a.ldg, a.stride_g, vec, pl.transposed, static_cast<const float*>(partial), parts, a.eps,
                   xh, xl, pl.np, pl.mp * pl.np, tiles_c);
 }
 
@@ -876,9 +928,9 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
     al = pl.split ? take(pl.a_bytes) : nullptr;
     bl = pl.split ? take(pl.a_bytes) : nullptr;
 
-    cudaError_t e = a.in_dtype == DGA_F32    ? launch_first<float>(a, pl, partial, xh[0], xl[0], a.stream)
-                    : a.in_dtype == DGA_BF16 ? launch_first<__nv_bfloat16>(a, pl, partial, xh[0], xl[0], a.stream)
-                                             : launch_first<__half>(a, pl, partial, xh[0], xl[0], a.stream);
+    cudaError_t e = a.in_dtype == DGA_F32    ? launch_first<float>(a, pl, partial, xh[0], xl[0], dev, a.stream)
+                    : a.in_dtype == DGA_BF16 ? launch_first<__nv_bfloat16>(a, pl, partial, xh[0], xl[0], dev, a.stream)
+                                             : launch_first<__half>(a, pl, partial, xh[0], xl[0], dev, a.stream);
     if (e != cudaSuccess) return e;
     *launches += 2;
 
@@ -910,6 +962,8 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
     base.result = a.O;
     base.result_type = a.out_dtype;
     base.transposed = pl.transposed;
+    const int64_t per16 = a.out_dtype == DGA_F32 ? 4 : 8;
+    base.result_vec = aligned(a.O, 16) && a.ldo % per16 == 0 && (a.batch == 1 || a.stride_o % per16 == 0);
     base.ldo = a.ldo;
     base.stride_o = a.stride_o;
     for (int step = 0; step < a.steps; ++step) {
