@@ -445,7 +445,9 @@ int dga_orthogonalize(dga_dtype in_dtype, dga_dtype out_dtype, int64_t batch, in
     const uintptr_t g1 = g0 + static_cast<uintptr_t>(((batch - 1) * stride_g + (rows - 1) * ldg + cols) * gs);
     const uintptr_t o0 = reinterpret_cast<uintptr_t>(O);
     const uintptr_t o1 = o0 + static_cast<uintptr_t>(((batch - 1) * stride_o + (rows - 1) * ldo + cols) * os);
-    if (overlaps(w0, w1, g0, g1) || overlaps(w0, w1, o0, o1)) return DGA_ERR_OVERLAP;
+    const bool in_place = O == G && out_dtype == in_dtype && ldo == ldg && (batch == 1 || stride_o == stride_g);
+    if (overlaps(w0, w1, g0, g1) || overlaps(w0, w1, o0, o1) || (!in_place && overlaps(g0, g1, o0, o1)))
+        return DGA_ERR_OVERLAP;
     DeviceInfo dev;
     cudaError_t e = current_device_info(&dev);
     if (e != cudaSuccess) return fail_cuda(e);

@@ -223,12 +223,11 @@ constexpr uint32_t kTileBar = kTileStages * kTileStage;
 constexpr uint32_t kTileLaunch = kTileBar + (2 * kTileStages + 4) * 8 + 16 + 1024;
 static_assert(kTileBar >= 128 * 128 * 4, "the partial sums fit the ring");
 
-// Threads: producer warp, MMA warp, epilogue warps (4, or 8 with half the
-// columns each where they keep the chunks' sum in registers).
-constexpr int tile_threads(bool chunked) { return chunked ? 320 : 192; }
+// Producer warp, MMA warp, 8 epilogue warps with half of the columns each.
+constexpr int kTileThreads = 320;
 
 template <bool kChunked>
-__global__ void __launch_bounds__(tile_threads(kChunked), 2)
+__global__ void __launch_bounds__(kTileThreads, 2)
     ns_tile_kernel(const __grid_constant__ NsMaps maps, NsParams p, uint32_t splits) {
     constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 128, 128);
     extern __shared__ uint8_t smem_raw[];
@@ -403,8 +402,9 @@ __global__ void __launch_bounds__(tile_threads(kChunked), 2)
             cluster_sync();
         }
         if (warp >= 2 && ok) {
+            const int half = (warp - 2) >> 2;  // 64 columns
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = half * 2; c < half * 2 + 2; ++c) {
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(tmem + lane_base + c * 32, r);
                 tmem_ld_wait();
@@ -424,9 +424,9 @@ __global__ void __launch_bounds__(tile_threads(kChunked), 2)
         __syncwarp();
         cluster_sync();
         if (warp >= 2) {
-            // this CTA's blocks, a warp quarter's rows; with eight warps each half takes every other one
+            // this CTA's blocks, a warp quarter's rows; each half of the warps takes every other block
             const uint32_t per = 4 / splits;
-            for (uint32_t i = kChunked ? (warp - 2) >> 2 : 0; i < per; i += kChunked ? 2 : 1) {
+            for (uint32_t i = (warp - 2) >> 2; i < per; i += 2) {
                 float v[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 0.0f;
@@ -455,12 +455,11 @@ constexpr uint32_t kPairStage = 2 * 128 * 128;  // each CTA's half of both opera
 constexpr uint32_t kPairBar = kPairStages * kPairStage;
 constexpr uint32_t kPairLaunch = kPairBar + (2 * kPairStages + 5) * 8 + 16 + 1024;
 
-// Epilogue warps: 4, or 16 with 64 columns each where they keep the chunks'
-// sum in registers.
-constexpr int pair_threads(bool chunked) { return chunked ? 576 : 192; }
+// Producer warp, MMA warp, 16 epilogue warps with 64 columns each.
+constexpr int kPairThreads = 576;
 
 template <bool kChunked>
-__global__ void __launch_bounds__(pair_threads(kChunked), 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     ns_pair_kernel(const __grid_constant__ NsMaps maps, NsParams p) {
     constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 256, 256);
     constexpr uint16_t kBothCtas = 0x3;
@@ -485,7 +484,7 @@ __global__ void __launch_bounds__(pair_threads(kChunked), 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], kChunked ? 32 : 8);  // one lane of each epilogue warp of both CTAs
+            mbar_init(&acc_empty[b], 32);  // one lane of each epilogue warp of both CTAs
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -585,7 +584,7 @@ __global__ void __launch_bounds__(pair_threads(kChunked), 1)
             mbar_wait_bounded(drain, 0, &never, kWaitLimitNs);
         }
     } else {
-        const int quarter = warp & 3;
+        const int quarter = warp & 3, group = (warp - 2) >> 2;  // 64 columns
         const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
         uint32_t acc = 0, acc_phase = 0;
         bool ok = true;
@@ -596,7 +595,6 @@ __global__ void __launch_bounds__(pair_threads(kChunked), 1)
             const int64_t col0 = static_cast<int64_t>(tn) * 256;
             const bool mirror = p.sym && tm != tn;
             if constexpr (kChunked) {
-                const int group = (warp - 2) >> 2;  // 64 columns
                 float sum[64];
 #pragma unroll
                 for (int j = 0; j < 64; ++j) sum[j] = 0.0f;
@@ -636,7 +634,7 @@ __global__ void __launch_bounds__(pair_threads(kChunked), 1)
                 }
                 tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < 8; ++c) {
+                for (int c = group * 2; c < group * 2 + 2; ++c) {
                     uint32_t r[32];
                     float v[32];
                     tmem_ld_32x32b_x32(tmem + lane_base + acc * 256 + c * 32, r);
@@ -776,6 +774,364 @@ __global__ void __launch_bounds__(256) ns_first_kernel(const T* __restrict__ G, 
     }
 }
 
+// ---- the cluster kernel: up to 128 rows, all steps in one launch -------------------------
+//
+// One cluster of C CTAs per matrix; each CTA keeps a slab of X's columns (up
+// to 256) in its shared memory for all steps, as boxes of 64 columns x 128
+// rows (128-byte swizzle rows), which the MMA reads K-major for X X^T and
+// MN-major for B X.  A step is
+//   1. each CTA's share of X X^T (its columns are a part of K);
+//   2. the shares added up: CTA c receives columns [c 128/C, (c+1) 128/C) of
+//      all of them (stores into its `red`), adds them in the CTAs' order, and
+//      sends its columns of A as hi and lo to every CTA;
+//   3. A^2, B = b A + c A^2 and X <- a X + B X of the slab, in each CTA.
+// Only step 2 crosses CTAs: two cluster barriers (four where `red` has to
+// share A's memory).  With C = 1 nothing does.  Accumulators: the cross
+// products in one, each 128 values of K of the hi hi product in one of its own.
+// For m, n this small the time is latency: 15 products of 1 to 2 us; as
+// separate launches (2 + 3 a step) it was 85 us at 64 x 64 and 134 us at
+// 128 x 512.
+
+constexpr int kMaxBoxes = 4;                      // 64-column boxes of a slab
+constexpr uint32_t kXBox = 128 * 128;             // bytes of a box: 128 rows x 64 fp16
+constexpr uint32_t kABytes = 2 * kXBox;           // A or B, hi or lo
+constexpr uint32_t kRedBytes = 128 * 128 * 4;
+constexpr int kClusterThreads = 256;
+
+struct NsClusterParams {
+    const void* G;
+    int64_t ldg, stride_g;
+    int64_t m, n;
+    bool transposed, vec;
+    int boxes_all, boxes_each, cluster;  // boxes of X, of a CTA's slab; CTAs
+    bool own_red;                        // `red` has its own memory
+    float eps;
+    int steps;
+    float coefficients[3 * 32];
+};
+
+// Byte offset of 16-byte piece `piece` (8 columns) of a row in a box of 64 columns x 128 rows.
+__device__ __forceinline__ uint32_t box_at(int row, int piece) {
+    return static_cast<uint32_t>(row) * 128u + (static_cast<uint32_t>(piece ^ (row & 7)) << 4);
+}
+// Eight values as hi and lo.
+__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        h[j] = pack2(v[2 * j], v[2 * j + 1]);
+        const float2 f = unpack2(h[j]);
+        l[j] = pack2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// x[0..7] <- c_old * (hi + lo) + c_acc * x
+__device__ __forceinline__ void blend8(float* x, const uint4& hi, const uint4& lo, float c_old, float c_acc) {
+    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 a = unpack2(h[j]), b = unpack2(l[j]);
+        x[2 * j] = fmaf(c_old, a.x + b.x, c_acc * x[2 * j]);
+        x[2 * j + 1] = fmaf(c_old, a.y + b.y, c_acc * x[2 * j + 1]);
+    }
+}
+__device__ __forceinline__ void st_shared_cluster_v4(uint32_t cluster_addr, const uint4& v) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsClusterParams c, NsParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    __shared__ __align__(8) uint64_t done;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word;
+    __shared__ float norms[8];
+    volatile int* abort_flag = &abort_word;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int matrix = blockIdx.x / c.cluster, rank = blockIdx.x % c.cluster;
+    const int first_box = rank * c.boxes_each;
+    const int boxes = max(0, min(c.boxes_each, c.boxes_all - first_box));
+    uint8_t* xh = smem;
+    uint8_t* xl = xh + c.boxes_each * kXBox;
+    uint8_t* ah = xl + c.boxes_each * kXBox;
+    uint8_t* al = ah + kABytes;
+    float* red = reinterpret_cast<float*>(c.own_red ? al + kABytes : ah);
+
+    if (tid == 0) {
+        mbar_init(&done, 1);
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_slot, 512);
+        tmem_relinquish();
+    }
+
+    // ---- X = G / (|G| + eps): the slab in registers, its norm, then hi and lo
+    const T* G = static_cast<const T*>(c.G) + matrix * c.stride_g;
+    const int64_t col0 = static_cast<int64_t>(first_box) * 64;
+    float x[kMaxBoxes][4][8];
+    float s = 0.0f;
+    // not transposed: two threads to a row, 32 columns each; transposed: four
+    // to a column, 32 rows each
+    const int line = c.transposed ? tid >> 2 : tid >> 1, at32 = c.transposed ? (tid & 3) * 32 : (tid & 1) * 32;
+#pragma unroll
+    for (int b = 0; b < kMaxBoxes; ++b) {
+        if (b < boxes) {
+            const int64_t gr = c.transposed ? col0 + b * 64 + line : line;
+            const int64_t gc = c.transposed ? at32 : col0 + b * 64 + at32;
+            const int64_t rows = c.transposed ? c.n : c.m, cols = c.transposed ? c.m : c.n;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ns_load8(G + gr * c.ldg, gr < rows ? gc + q * 8 : cols, cols, c.vec, x[b][q]);
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < kMaxBoxes; ++b)
+        if (b < boxes)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s = fmaf(x[b][q][j], x[b][q][j], s);
+    s = block_sum(s);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    if (c.cluster > 1) {
+        cluster_sync();  // every CTA of the cluster runs
+        if (tid < c.cluster) st_shared_cluster_f32(map_to_cta(smem_u32(&norms[rank]), tid), s);
+        cluster_sync();
+        s = 0.0f;
+        for (int q = 0; q < c.cluster; ++q) s += norms[q];
+    }
+    const float unit = kScale / (sqrtf(s) + c.eps);
+#pragma unroll
+    for (int b = 0; b < kMaxBoxes; ++b) {
+        if (b < boxes) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) x[b][q][j] *= unit;
+                uint4 hi, lo;
+                split8(x[b][q], hi, lo);
+                if (!c.transposed) {
+                    const uint32_t at = b * kXBox + box_at(line, (at32 >> 3) + q);
+                    *reinterpret_cast<uint4*>(xh + at) = hi;
+                    *reinterpret_cast<uint4*>(xl + at) = lo;
+                } else {
+                    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t at = b * kXBox + box_at(at32 + q * 8 + j, line >> 3) + (line & 7) * 2;
+                        *reinterpret_cast<uint16_t*>(xh + at) = static_cast<uint16_t>(j & 1 ? h[j / 2] >> 16 : h[j / 2]);
+                        *reinterpret_cast<uint16_t*>(xl + at) = static_cast<uint16_t>(j & 1 ? l[j / 2] >> 16 : l[j / 2]);
+                    }
+                }
+            }
+        }
+    }
+    fence_async_shared();
+    __syncthreads();
+
+    const int quarter = warp & 3, half = warp >> 2;
+    const int row = quarter * 32 + lane;  // of A, B and X
+    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t xh_s = smem_u32(xh), xl_s = smem_u32(xl), ah_s = smem_u32(ah), al_s = smem_u32(al);
+    constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 128, 128);
+    uint32_t phase = 0;
+    auto wait_done = [&]() {
+        if (!mbar_wait_bounded(&done, phase, abort_flag, kWaitLimitNs)) record_failure(kRoleEpilogue, abort_flag);
+        phase ^= 1;
+        tc_fence_after();
+    };
+    // 32 columns of accumulator `acc` (at column `first` of tensor memory), added to v
+    auto add32 = [&](uint32_t first, float (&v)[32]) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tmem + lane_base + first, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
+    };
+    // D[128 x 128] (+)= P P'^T over `n` boxes of 64, both K-major
+    auto mma_kk = [&](uint32_t acc, uint32_t pa, uint32_t qa, int n, bool fresh) {
+        for (int b = 0; b < n; ++b) {
+            const uint64_t pd = smem_desc_kmajor_sw128(pa + b * kXBox), qd = smem_desc_kmajor_sw128(qa + b * kXBox);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tc_mma<kFmtF16>(tmem + acc, pd + 2 * k, qd + 2 * k, kIdesc, (fresh && b == 0 && k == 0) ? 0u : 1u);
+        }
+    };
+    const int per = 128 / c.cluster, mine = per / 2;  // columns of A a CTA joins; a thread's half of them
+    const int shift = 31 - __clz(per);
+    uint4 held[4][2];                                 // at most 32 of them, as hi and lo
+
+    for (int step = 0; step < c.steps; ++step) {
+        const float ca = c.coefficients[3 * step], cb = c.coefficients[3 * step + 1], cc = c.coefficients[3 * step + 2];
+        // ---- 1. this CTA's share of X X^T: columns 0-127 the cross products, then 128 per two boxes
+        if (tid == 0 && boxes > 0) {
+            mma_kk(0, xh_s, xl_s, boxes, true);
+            mma_kk(0, xl_s, xh_s, boxes, false);
+            for (int b = 0; b < boxes; b += 2) mma_kk(128 + 64 * b, xh_s + b * kXBox, xh_s + b * kXBox, min(2, boxes - b), true);
+            tc_commit(&done);
+        }
+        __syncwarp();
+        if (boxes > 0) wait_done();
+        // ---- 2. the shares joined
+        if (c.cluster > 1 && !c.own_red) cluster_sync();  // every CTA is done with B, whose memory `red` is
+#pragma unroll 1
+        for (int b32 = half * 2; b32 < half * 2 + 2; ++b32) {
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+            if (boxes > 0) {
+                add32(b32 * 32, v);
+                for (int b = 0; b < boxes; b += 2) add32(128 + 64 * b + b32 * 32, v);
+            }
+            if (c.cluster == 1) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] *= 1.0f / kScale;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint4 hi, lo;
+                    split8(&v[q * 8], hi, lo);
+                    const uint32_t at = (b32 >> 1) * kXBox + box_at(row, (b32 & 1) * 4 + q);
+                    *reinterpret_cast<uint4*>(ah + at) = hi;
+                    *reinterpret_cast<uint4*>(al + at) = lo;
+                }
+            } else {
+                // red[(share * per + column) * 128 + row] of the joining CTA
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int col = b32 * 32 + j;
+                    st_shared_cluster_f32(map_to_cta(smem_u32(red + (rank * per + (col & (per - 1))) * 128 + row), col >> shift), v[j]);
+                }
+            }
+        }
+        if (c.cluster > 1) {
+            cluster_sync();
+#pragma unroll
+            for (int q = 0; q < 32; q += 8) {
+                if (q >= mine) break;
+                float v[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+                for (int share = 0; share < c.cluster; ++share)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += red[(share * per + half * mine + q + j) * 128 + row];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= 1.0f / kScale;
+                split8(v, held[q / 8][0], held[q / 8][1]);
+            }
+            if (!c.own_red) cluster_sync();  // every CTA has read `red`, whose memory A is
+#pragma unroll
+            for (int q = 0; q < 32; q += 8) {
+                if (q >= mine) break;
+                const int col = rank * per + half * mine + q;
+                const uint32_t at = (col >> 6) * kXBox + box_at(row, (col & 63) >> 3);
+                for (int to = 0; to < c.cluster; ++to) {
+                    st_shared_cluster_v4(map_to_cta(ah_s + at, to), held[q / 8][0]);
+                    st_shared_cluster_v4(map_to_cta(al_s + at, to), held[q / 8][1]);
+                }
+            }
+            fence_async_all();
+            cluster_sync();
+        }
+        fence_async_shared();
+        __syncthreads();
+        // ---- 3. B = b A + c A^2, in A's place
+        if (tid == 0) {
+            mma_kk(0, ah_s, al_s, 2, true);
+            mma_kk(0, al_s, ah_s, 2, false);
+            mma_kk(128, ah_s, ah_s, 2, true);
+            tc_commit(&done);
+        }
+        __syncwarp();
+        wait_done();
+#pragma unroll 1
+        for (int b32 = half * 2; b32 < half * 2 + 2; ++b32) {
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+            add32(b32 * 32, v);
+            add32(128 + b32 * 32, v);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t at = (b32 >> 1) * kXBox + box_at(row, (b32 & 1) * 4 + q);
+                uint4 hi = *reinterpret_cast<const uint4*>(ah + at), lo = *reinterpret_cast<const uint4*>(al + at);
+                blend8(&v[q * 8], hi, lo, cb, cc / kScale);
+                split8(&v[q * 8], hi, lo);
+                *reinterpret_cast<uint4*>(ah + at) = hi;
+                *reinterpret_cast<uint4*>(al + at) = lo;
+            }
+        }
+        tc_fence_before();
+        fence_async_shared();
+        __syncthreads();
+        tc_fence_after();
+        // ---- X <- a X + B X: cross products in columns 0-255, hi hi in 256-511
+        if (boxes > 0) {
+            if (tid == 0) {
+                const uint32_t idesc = idesc_major(idesc_mma(kFmtF16, 128, static_cast<uint32_t>(boxes) * 64), 0, 1);
+                auto mma_kn = [&](uint32_t acc, uint32_t pa, uint32_t qa, bool fresh) {
+                    // K = 128 rows of X, 16 at a time: 32 bytes along B's rows, 16 rows of X's boxes
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t pd = smem_desc_kmajor_sw128(pa + (k >> 2) * kXBox) + 2 * (k & 3);
+                        const uint64_t qd = smem_desc_mnmajor_sw128(qa, kXBox) + 128 * k;
+                        tc_mma<kFmtF16>(tmem + acc, pd, qd, idesc, (fresh && k == 0) ? 0u : 1u);
+                    }
+                };
+                mma_kn(0, ah_s, xl_s, true);
+                mma_kn(0, al_s, xh_s, false);
+                mma_kn(256, ah_s, xh_s, true);
+                tc_commit(&done);
+            }
+            __syncwarp();
+            wait_done();
+            const bool last = step + 1 == c.steps;
+            for (int b32 = half * boxes; b32 < (half + 1) * boxes; ++b32) {
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                add32(b32 * 32, v);
+                add32(256 + b32 * 32, v);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t at = (b32 >> 1) * kXBox + box_at(row, (b32 & 1) * 4 + q);
+                    uint4 hi = *reinterpret_cast<const uint4*>(xh + at), lo = *reinterpret_cast<const uint4*>(xl + at);
+                    if (last) {
+                        blend8(&v[q * 8], hi, lo, ca / kScale, 1.0f / (kScale * kScale));
+                    } else {
+                        blend8(&v[q * 8], hi, lo, ca, 1.0f / kScale);
+                        split8(&v[q * 8], hi, lo);
+                        *reinterpret_cast<uint4*>(xh + at) = hi;
+                        *reinterpret_cast<uint4*>(xl + at) = lo;
+                    }
+                }
+                if (last && row < p.m) {
+                    const int64_t col = col0 + b32 * 32;
+                    if (p.result_type == DGA_F32) ns_result<float>(p, matrix, row, col, v);
+                    else if (p.result_type == DGA_BF16) ns_result<__nv_bfloat16>(p, matrix, row, col, v);
+                    else ns_result<__half>(p, matrix, row, col, v);
+                }
+            }
+        }
+        tc_fence_before();
+        fence_async_shared();
+        __syncthreads();
+        tc_fence_after();
+    }
+    if (c.cluster > 1) cluster_sync();  // no CTA leaves while another may still write to it
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // ---- host side ------------------------------------------------------------------------------
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -868,13 +1224,57 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
     const int64_t big = tiles(256);
     if (big >= pairs * 3 / 4)
         return launch(chunked ? ns_pair_kernel<true> : ns_pair_kernel<false>,
-                      dim3(static_cast<unsigned>(2 * std::min(big, pairs))), pair_threads(chunked), 2,
+                      dim3(static_cast<unsigned>(2 * std::min(big, pairs))), kPairThreads, 2,
                       static_cast<int>(kPairLaunch), true, s, maps, p);
     const int64_t small = tiles(128);
     uint32_t splits = 1;
     while (splits < 4 && small * splits * 2 <= 2 * dev.sm_count && p.num_kb * p.segs >= splits * 4) splits *= 2;
     return launch(chunked ? ns_tile_kernel<true> : ns_tile_kernel<false>, dim3(static_cast<unsigned>(small * splits)),
-                  tile_threads(chunked), splits, static_cast<int>(kTileLaunch), true, s, maps, p, splits);
+                  kTileThreads, splits, static_cast<int>(kTileLaunch), true, s, maps, p, splits);
+}
+
+// The cluster kernel's shape, or cluster = 0 where it does not apply: up to 128
+// rows and 8 slabs of 256 columns.  CTAs are added while a slab is over 128
+// columns (its products then take longer than the exchange) and the batch
+// leaves room for them, and as far as the slabs need them.
+struct ClusterShape {
+    int cluster, boxes_all, boxes_each;
+    bool own_red;
+    int smem;
+};
+ClusterShape cluster_shape(const OrthoArgs& a, const NsPlan& pl, const DeviceInfo& dev) {
+    ClusterShape c{};
+    if (pl.m > 128 || pl.np > 8 * 64 * kMaxBoxes || a.steps > 32) return c;
+    c.boxes_all = static_cast<int>(pl.np / 64);
+    int n = 1;
+    while (n < 8 && (c.boxes_all + n - 1) / n > 2 && (a.batch * n * 2 <= dev.sm_count || (c.boxes_all + n - 1) / n > kMaxBoxes)) n *= 2;
+    c.cluster = n;
+    c.boxes_each = (c.boxes_all + n - 1) / n;
+    c.own_red = n > 1 && c.boxes_each <= 3;
+    c.smem = static_cast<int>(2 * c.boxes_each * kXBox + 2 * kABytes + (c.own_red ? kRedBytes : 0) + 1024);
+    return c;
+}
+
+template <typename T>
+cudaError_t launch_cluster(const OrthoArgs& a, const NsPlan& pl, const ClusterShape& shape, const NsParams& p) {
+    constexpr int64_t kVec = 16 / sizeof(T);
+    NsClusterParams c{};
+    c.G = a.G;
+    c.ldg = a.ldg;
+    c.stride_g = a.stride_g;
+    c.m = pl.m;
+    c.n = pl.n;
+    c.transposed = pl.transposed;
+    c.vec = aligned(a.G, 16) && a.ldg % kVec == 0 && (a.batch == 1 || a.stride_g % kVec == 0);
+    c.boxes_all = shape.boxes_all;
+    c.boxes_each = shape.boxes_each;
+    c.cluster = shape.cluster;
+    c.own_red = shape.own_red;
+    c.eps = a.eps;
+    c.steps = a.steps;
+    for (int i = 0; i < 3 * a.steps; ++i) c.coefficients[i] = a.coefficients[i];
+    return launch(ns_cluster_kernel<T>, dim3(static_cast<unsigned>(a.batch * shape.cluster)), kClusterThreads, shape.cluster,
+                  shape.smem, false, a.stream, c, p);
 }
 
 template <typename T>
@@ -928,7 +1328,29 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
     al = pl.split ? take(pl.a_bytes) : nullptr;
     bl = pl.split ? take(pl.a_bytes) : nullptr;
 
-    cudaError_t e = a.in_dtype == DGA_F32    ? launch_first<float>(a, pl, partial, xh[0], xl[0], dev, a.stream)
+    NsParams base{};
+    base.segs = pl.split ? 3 : 1;
+    base.p_rows = base.q_rows = static_cast<uint32_t>(pl.mp);
+    base.rows = pl.mp;
+    base.m = pl.m;
+    base.n = pl.n;
+    base.result = a.O;
+    base.result_type = a.out_dtype;
+    base.transposed = pl.transposed;
+    const int64_t per16 = a.out_dtype == DGA_F32 ? 4 : 8;
+    base.result_vec = aligned(a.O, 16) && a.ldo % per16 == 0 && (a.batch == 1 || a.stride_o % per16 == 0);
+    base.ldo = a.ldo;
+    base.stride_o = a.stride_o;
+    cudaError_t e;
+    const ClusterShape shape = cluster_shape(a, pl, dev);
+    if (shape.cluster > 0) {
+        e = a.in_dtype == DGA_F32    ? launch_cluster<float>(a, pl, shape, base)
+            : a.in_dtype == DGA_BF16 ? launch_cluster<__nv_bfloat16>(a, pl, shape, base)
+                                     : launch_cluster<__half>(a, pl, shape, base);
+        if (e == cudaSuccess) ++*launches;
+        return e;
+    }
+    e = a.in_dtype == DGA_F32    ? launch_first<float>(a, pl, partial, xh[0], xl[0], dev, a.stream)
                     : a.in_dtype == DGA_BF16 ? launch_first<__nv_bfloat16>(a, pl, partial, xh[0], xl[0], dev, a.stream)
                                              : launch_first<__half>(a, pl, partial, xh[0], xl[0], dev, a.stream);
     if (e != cudaSuccess) return e;
@@ -953,19 +1375,6 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
         mb_l = mb_h;
     }
 
-    NsParams base{};
-    base.segs = pl.split ? 3 : 1;
-    base.p_rows = base.q_rows = static_cast<uint32_t>(pl.mp);
-    base.rows = pl.mp;
-    base.m = pl.m;
-    base.n = pl.n;
-    base.result = a.O;
-    base.result_type = a.out_dtype;
-    base.transposed = pl.transposed;
-    const int64_t per16 = a.out_dtype == DGA_F32 ? 4 : 8;
-    base.result_vec = aligned(a.O, 16) && a.ldo % per16 == 0 && (a.batch == 1 || a.stride_o % per16 == 0);
-    base.ldo = a.ldo;
-    base.stride_o = a.stride_o;
     for (int step = 0; step < a.steps; ++step) {
         const float ca = a.coefficients[3 * step], cb = a.coefficients[3 * step + 1], cc = a.coefficients[3 * step + 2];
         const int now = step & 1, next = now ^ 1;

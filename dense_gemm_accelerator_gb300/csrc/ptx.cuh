@@ -383,6 +383,8 @@ __device__ __forceinline__ void bulk_wait_read() {
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Orders this thread's shared-memory writes before later async-proxy reads.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// The same for writes to any memory, other CTAs' shared memory among it.
+__device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
 // Store a float to shared memory of a CTA of this cluster (address from map_to_cta).
 __device__ __forceinline__ void st_shared_cluster_f32(uint32_t cluster_addr, float v) {

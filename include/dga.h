@@ -496,7 +496,8 @@ size_t dga_mx_linear_workspace_size(dga_mx_format format, int64_t M, int64_t K);
  * being kept to 22 bits; intermediates of magnitude 16 or more overflow (the
  * quintic above stays below 4).  Results repeat bit for bit.
  *   coefficients  HOST, 3 * steps floats: a, b, c of each step
- *   O             may be G itself or overlap it
+ *   O             may be G itself (the same pointer, type and strides); must
+ *                 not overlap it otherwise
  *   workspace     device, 256-byte aligned, of
  *                 dga_orthogonalize_workspace_size(...) bytes; must not
  *                 overlap G or O
@@ -504,8 +505,9 @@ size_t dga_mx_linear_workspace_size(dga_mx_format format, int64_t M, int64_t K);
  * (over 65535), -4 rows, -5 cols, -6 G, -7 ldg, -8 stride_g < 0, -9 O, -10
  * ldo, -11 stride_o (outputs overlap), -12 steps (outside [1, 1000]), -13
  * coefficients, -14 eps < 0 or NaN, -15 workspace; DGA_ERR_WORKSPACE,
- * DGA_ERR_OVERLAP.  batch, rows or cols of 0 is a no-op.  2 + 3 * steps
- * launches.
+ * DGA_ERR_OVERLAP.  batch, rows or cols of 0 is a no-op.  One launch
+ * where min(rows, cols) <= 128, max(rows, cols) <= 2048 and steps <= 32, else
+ * 2 + 3 * steps.
  */
 int dga_orthogonalize(dga_dtype in_dtype, dga_dtype out_dtype, int64_t batch, int64_t rows,
                       int64_t cols, const void* G, int64_t ldg, int64_t stride_g, void* O,

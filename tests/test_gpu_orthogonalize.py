@@ -48,7 +48,8 @@ def _momentum(shape, seed, rank=4, noise=0.05):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("shape", [(1, 1), (1, 7), (9, 1), (64, 64), (65, 63), (100, 300), (300, 100), (256, 256),
                                    (257, 260), (513, 129), (515, 1030), (700, 640), (3, 100, 65), (5, 130, 257),
-                                   (40, 64, 64), (12, 300, 270), (1, 1100, 700)])
+                                   (40, 64, 64), (12, 300, 270), (1, 1100, 700), (128, 128), (127, 640), (1500, 100),
+                                   (120, 2048), (128, 2049), (80, 90, 200), (30, 500, 64), (3, 33, 1700)])
 def test_against_the_formula(dtype, shape):
     g = torch.Generator().manual_seed(sum(shape))
     for G, tol in ((torch.randn(*shape, generator=g), TOL), (1e-3 * _momentum(shape, 1), TOL),
