@@ -88,6 +88,8 @@ class DgaError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded libdga.so.  Raises if it has not been built."""
     global _lib_handle
+    if _lib_handle is not None:
+        return _lib_handle
     with _lock:
         if _lib_handle is None:
             if not os.path.exists(LIB_PATH):
@@ -101,6 +103,12 @@ def lib() -> ctypes.CDLL:
                 fn.argtypes = args
             _lib_handle = handle
         return _lib_handle
+
+
+def _raw_stream(device_index):
+    """The current CUDA stream of a device, as an integer."""
+    import torch
+    return torch.cuda.current_stream(device_index).cuda_stream
 
 
 # ---- the C entry points, same names and arguments ---------------------------
@@ -431,6 +439,10 @@ def linear_backward(X, W, G, need_bias=True):
     return dX, dW, db
 
 
+try:  # the same without building a Stream object (2 us less)
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream  # noqa: E402,F811
+except ImportError:  # a CPU build of PyTorch
+    pass
 from .mx import (MXFP4, NVFP4, MXTensor, mx_dequantize, mx_gemm, mx_linear_backward,  # noqa: E402,F401
                  mx_linear_forward, mx_quantize)
 from .muon import QUINTIC, orthogonalize  # noqa: E402,F401

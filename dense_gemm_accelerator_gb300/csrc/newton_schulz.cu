@@ -44,6 +44,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <mutex>
 
 #include "dga_internal.h"
 #include "epilogue.cuh"
@@ -109,19 +110,19 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// 32 columns of a row of X to the result: rows of m x n, or (transposed) of n x m.
-template <typename T>
-__device__ __forceinline__ void ns_result(const NsParams& p, uint32_t matrix, int64_t row, int64_t col, const float (&v)[32]) {
+// n columns of a row of X to the result: rows of m x n, or (transposed) of n x m.
+template <typename T, int n>
+__device__ __forceinline__ void ns_result(const NsParams& p, uint32_t matrix, int64_t row, int64_t col, const float (&v)[n]) {
     T* base = static_cast<T*>(p.result) + matrix * p.stride_o;
     if (p.transposed) {
         // element (col + j, row): consecutive lanes on consecutive columns
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < n; ++j)
             if (col + j < p.n) OutT<T>::store(base + (col + j) * p.ldo + row, v[j]);
-    } else if (p.result_vec && col + 32 <= p.n) {
+    } else if (p.result_vec && col + n <= p.n) {
         constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
-        for (int q = 0; q < 32 / kPer; ++q) {
+        for (int q = 0; q < n / kPer; ++q) {
             T w[kPer];
 #pragma unroll
             for (int e = 0; e < kPer; ++e) OutT<T>::store(&w[e], v[q * kPer + e]);
@@ -131,7 +132,7 @@ __device__ __forceinline__ void ns_result(const NsParams& p, uint32_t matrix, in
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
+        for (int j = 0; j < n; ++j)
             if (col + j < p.n) OutT<T>::store(base + row * p.ldo + col + j, v[j]);
     }
 }
@@ -670,15 +671,16 @@ template <> __device__ __forceinline__ float ns_in<__nv_bfloat16>(__nv_bfloat16 
 template <> __device__ __forceinline__ float ns_in<__half>(__half v) { return __half2float(v); }
 
 // The block's sum in every thread, in a fixed order.
+template <int kWarps>
 __device__ __forceinline__ float block_sum(float s) {
-    __shared__ float part[8];
+    __shared__ float part[kWarps];
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
     __syncthreads();
     s = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) s += part[w];
+    for (int w = 0; w < kWarps; ++w) s += part[w];
     return s;
 }
 
@@ -724,7 +726,7 @@ __global__ void __launch_bounds__(256) ns_squares_kernel(const T* __restrict__ G
             for (int q = 0; q < 8; ++q) s[q] = fmaf(x[q], x[q], s[q]);
         }
     }
-    const float total = block_sum(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
+    const float total = block_sum<8>(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
     if (threadIdx.x == 0) partial[blockIdx.y * gridDim.x + blockIdx.x] = total;
 }
 
@@ -750,7 +752,7 @@ __global__ void __launch_bounds__(256) ns_first_kernel(const T* __restrict__ G, 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float s = 0.0f;
     for (int i = threadIdx.x; i < parts; i += 256) s += partial[blockIdx.y * parts + i];
-    const float u = kScale / (sqrtf(block_sum(s)) + eps);
+    const float u = kScale / (sqrtf(block_sum<8>(s)) + eps);
     if (transposed) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) tile[tc + j][tr] = x[j / 8][j % 8];
@@ -777,26 +779,28 @@ __global__ void __launch_bounds__(256) ns_first_kernel(const T* __restrict__ G, 
 // ---- the cluster kernel: up to 128 rows, all steps in one launch -------------------------
 //
 // One cluster of C CTAs per matrix; each CTA keeps a slab of X's columns (up
-// to 256) in its shared memory for all steps, as boxes of 64 columns x 128
+// to 192) in its shared memory for all steps, as boxes of 64 columns x 128
 // rows (128-byte swizzle rows), which the MMA reads K-major for X X^T and
 // MN-major for B X.  A step is
 //   1. each CTA's share of X X^T (its columns are a part of K);
 //   2. the shares added up: CTA c receives columns [c 128/C, (c+1) 128/C) of
 //      all of them (stores into its `red`), adds them in the CTAs' order, and
-//      sends its columns of A as hi and lo to every CTA;
+//      has A's rows of the same numbers (A is symmetric), as hi and lo: rows
+//      of the boxes lie together, so that bulk copies hand them to the others;
 //   3. A^2, B = b A + c A^2 and X <- a X + B X of the slab, in each CTA.
-// Only step 2 crosses CTAs: two cluster barriers (four where `red` has to
-// share A's memory).  With C = 1 nothing does.  Accumulators: the cross
-// products in one, each 128 values of K of the hi hi product in one of its own.
+// Only step 2 crosses CTAs, with one full cluster barrier.  With C = 1 nothing
+// does.  Accumulators: the cross products in one, each 128 values of K of the
+// hi hi product in one of its own.
 // For m, n this small the time is latency: 15 products of 1 to 2 us; as
 // separate launches (2 + 3 a step) it was 85 us at 64 x 64 and 134 us at
 // 128 x 512.
 
-constexpr int kMaxBoxes = 4;                      // 64-column boxes of a slab
+constexpr int kMaxBoxes = 3;                      // 64-column boxes of a slab
+constexpr int kMaxCluster = 16;
 constexpr uint32_t kXBox = 128 * 128;             // bytes of a box: 128 rows x 64 fp16
 constexpr uint32_t kABytes = 2 * kXBox;           // A or B, hi or lo
-constexpr uint32_t kRedBytes = 128 * 128 * 4;
-constexpr int kClusterThreads = 256;
+constexpr int kClusterThreads = 512;
+static_assert(2 * kABytes == 128 * 128 * 4, "`red` has B's memory");
 
 struct NsClusterParams {
     const void* G;
@@ -804,7 +808,6 @@ struct NsClusterParams {
     int64_t m, n;
     bool transposed, vec;
     int boxes_all, boxes_each, cluster;  // boxes of X, of a CTA's slab; CTAs
-    bool own_red;                        // `red` has its own memory
     float eps;
     int steps;
     float coefficients[3 * 32];
@@ -836,20 +839,15 @@ __device__ __forceinline__ void blend8(float* x, const uint4& hi, const uint4& l
         x[2 * j + 1] = fmaf(c_old, a.y + b.y, c_acc * x[2 * j + 1]);
     }
 }
-__device__ __forceinline__ void st_shared_cluster_v4(uint32_t cluster_addr, const uint4& v) {
-    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsClusterParams c, NsParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    __shared__ __align__(8) uint64_t done;
+    __shared__ __align__(8) uint64_t done, gathered;
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
-    __shared__ float norms[8];
+    __shared__ float norms[kMaxCluster];
     volatile int* abort_flag = &abort_word;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int matrix = blockIdx.x / c.cluster, rank = blockIdx.x % c.cluster;
@@ -859,10 +857,13 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
     uint8_t* xl = xh + c.boxes_each * kXBox;
     uint8_t* ah = xl + c.boxes_each * kXBox;
     uint8_t* al = ah + kABytes;
-    float* red = reinterpret_cast<float*>(c.own_red ? al + kABytes : ah);
+    uint8_t* bh = al + kABytes;
+    uint8_t* bl = bh + kABytes;
+    float* red = reinterpret_cast<float*>(bh);
 
     if (tid == 0) {
         mbar_init(&done, 1);
+        mbar_init(&gathered, 1);
         abort_word = 0;
         fence_mbar_init();
     }
@@ -874,29 +875,29 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
     // ---- X = G / (|G| + eps): the slab in registers, its norm, then hi and lo
     const T* G = static_cast<const T*>(c.G) + matrix * c.stride_g;
     const int64_t col0 = static_cast<int64_t>(first_box) * 64;
-    float x[kMaxBoxes][4][8];
+    float x[kMaxBoxes][2][8];
     float s = 0.0f;
-    // not transposed: two threads to a row, 32 columns each; transposed: four
-    // to a column, 32 rows each
-    const int line = c.transposed ? tid >> 2 : tid >> 1, at32 = c.transposed ? (tid & 3) * 32 : (tid & 1) * 32;
+    // not transposed: four threads to a row, 16 columns each; transposed: eight
+    // to a column, 16 rows each
+    const int line = c.transposed ? tid >> 3 : tid >> 2, at16 = c.transposed ? (tid & 7) * 16 : (tid & 3) * 16;
 #pragma unroll
     for (int b = 0; b < kMaxBoxes; ++b) {
         if (b < boxes) {
             const int64_t gr = c.transposed ? col0 + b * 64 + line : line;
-            const int64_t gc = c.transposed ? at32 : col0 + b * 64 + at32;
+            const int64_t gc = c.transposed ? at16 : col0 + b * 64 + at16;
             const int64_t rows = c.transposed ? c.n : c.m, cols = c.transposed ? c.m : c.n;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) ns_load8(G + gr * c.ldg, gr < rows ? gc + q * 8 : cols, cols, c.vec, x[b][q]);
+            for (int q = 0; q < 2; ++q) ns_load8(G + gr * c.ldg, gr < rows ? gc + q * 8 : cols, cols, c.vec, x[b][q]);
         }
     }
 #pragma unroll
     for (int b = 0; b < kMaxBoxes; ++b)
         if (b < boxes)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s = fmaf(x[b][q][j], x[b][q][j], s);
-    s = block_sum(s);
+    s = block_sum<kClusterThreads / 32>(s);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -913,20 +914,20 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
     for (int b = 0; b < kMaxBoxes; ++b) {
         if (b < boxes) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) x[b][q][j] *= unit;
                 uint4 hi, lo;
                 split8(x[b][q], hi, lo);
                 if (!c.transposed) {
-                    const uint32_t at = b * kXBox + box_at(line, (at32 >> 3) + q);
+                    const uint32_t at = b * kXBox + box_at(line, (at16 >> 3) + q);
                     *reinterpret_cast<uint4*>(xh + at) = hi;
                     *reinterpret_cast<uint4*>(xl + at) = lo;
                 } else {
                     const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        const uint32_t at = b * kXBox + box_at(at32 + q * 8 + j, line >> 3) + (line & 7) * 2;
+                        const uint32_t at = b * kXBox + box_at(at16 + q * 8 + j, line >> 3) + (line & 7) * 2;
                         *reinterpret_cast<uint16_t*>(xh + at) = static_cast<uint16_t>(j & 1 ? h[j / 2] >> 16 : h[j / 2]);
                         *reinterpret_cast<uint16_t*>(xl + at) = static_cast<uint16_t>(j & 1 ? l[j / 2] >> 16 : l[j / 2]);
                     }
@@ -937,10 +938,11 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
     fence_async_shared();
     __syncthreads();
 
-    const int quarter = warp & 3, half = warp >> 2;
+    const int quarter = warp & 3, group = warp >> 2;  // of 4 groups of warps
     const int row = quarter * 32 + lane;  // of A, B and X
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t xh_s = smem_u32(xh), xl_s = smem_u32(xl), ah_s = smem_u32(ah), al_s = smem_u32(al);
+    const uint32_t bh_s = smem_u32(bh), bl_s = smem_u32(bl);
     constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 128, 128);
     uint32_t phase = 0;
     auto wait_done = [&]() {
@@ -948,13 +950,14 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
         phase ^= 1;
         tc_fence_after();
     };
-    // 32 columns of accumulator `acc` (at column `first` of tensor memory), added to v
-    auto add32 = [&](uint32_t first, float (&v)[32]) {
-        uint32_t r[32];
-        tmem_ld_32x32b_x32(tmem + lane_base + first, r);
+    // 16 columns of tensor memory from `a`, and from `b`, added up
+    auto add16 = [&](uint32_t a, uint32_t b, float (&v)[16]) {
+        uint32_t r[16], t[16];
+        tmem_ld_32x32b_x16(tmem + lane_base + a, r);
+        tmem_ld_32x32b_x16(tmem + lane_base + b, t);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
+        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]) + __uint_as_float(t[j]);
     };
     // D[128 x 128] (+)= P P'^T over `n` boxes of 64, both K-major
     auto mma_kk = [&](uint32_t acc, uint32_t pa, uint32_t qa, int n, bool fresh) {
@@ -965,9 +968,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
                 tc_mma<kFmtF16>(tmem + acc, pd + 2 * k, qd + 2 * k, kIdesc, (fresh && b == 0 && k == 0) ? 0u : 1u);
         }
     };
-    const int per = 128 / c.cluster, mine = per / 2;  // columns of A a CTA joins; a thread's half of them
-    const int shift = 31 - __clz(per);
-    uint4 held[4][2];                                 // at most 32 of them, as hi and lo
+    const int per = 128 / c.cluster, shift = 31 - __clz(per);  // columns of the shares, rows of A, that a CTA joins
 
     for (int step = 0; step < c.steps; ++step) {
         const float ca = c.coefficients[3 * step], cb = c.coefficients[3 * step + 1], cc = c.coefficients[3 * step + 2];
@@ -981,68 +982,90 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
         __syncwarp();
         if (boxes > 0) wait_done();
         // ---- 2. the shares joined
-        if (c.cluster > 1 && !c.own_red) cluster_sync();  // every CTA is done with B, whose memory `red` is
+        __syncwarp();
+        if (c.cluster > 1 && step > 0) cluster_wait();  // every CTA is done with B, whose memory `red` is
 #pragma unroll 1
-        for (int b32 = half * 2; b32 < half * 2 + 2; ++b32) {
-            float v[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+        for (int b16 = group * 2; b16 < group * 2 + 2; ++b16) {
+            float v[16];
             if (boxes > 0) {
-                add32(b32 * 32, v);
-                for (int b = 0; b < boxes; b += 2) add32(128 + 64 * b + b32 * 32, v);
+                add16(b16 * 16, 128 + b16 * 16, v);
+                if (boxes > 2) {
+                    uint32_t r[16];
+                    tmem_ld_32x32b_x16(tmem + lane_base + 256 + b16 * 16, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = 0.0f;
             }
             if (c.cluster == 1) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] *= 1.0f / kScale;
+                for (int j = 0; j < 16; ++j) v[j] *= 1.0f / kScale;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 2; ++q) {
                     uint4 hi, lo;
                     split8(&v[q * 8], hi, lo);
-                    const uint32_t at = (b32 >> 1) * kXBox + box_at(row, (b32 & 1) * 4 + q);
+                    const uint32_t at = (b16 >> 2) * kXBox + box_at(row, (b16 & 3) * 2 + q);
                     *reinterpret_cast<uint4*>(ah + at) = hi;
                     *reinterpret_cast<uint4*>(al + at) = lo;
                 }
             } else {
                 // red[(share * per + column) * 128 + row] of the joining CTA
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int col = b32 * 32 + j;
-                    st_shared_cluster_f32(map_to_cta(smem_u32(red + (rank * per + (col & (per - 1))) * 128 + row), col >> shift), v[j]);
+                for (int q = 0; q < 2; ++q) {
+                    const int col = b16 * 16 + q * 8;  // one CTA for 8 columns
+                    const uint32_t to = map_to_cta(smem_u32(red + (rank * per + (col & (per - 1))) * 128 + row), col >> shift);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) st_shared_cluster_f32(to + j * 512, v[q * 8 + j]);
                 }
             }
         }
         if (c.cluster > 1) {
+            __syncwarp();
             cluster_sync();
-#pragma unroll
-            for (int q = 0; q < 32; q += 8) {
-                if (q >= mine) break;
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-                for (int share = 0; share < c.cluster; ++share)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += red[(share * per + half * mine + q + j) * 128 + row];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) v[j] *= 1.0f / kScale;
-                split8(v, held[q / 8][0], held[q / 8][1]);
-            }
-            if (!c.own_red) cluster_sync();  // every CTA has read `red`, whose memory A is
-#pragma unroll
-            for (int q = 0; q < 32; q += 8) {
-                if (q >= mine) break;
-                const int col = rank * per + half * mine + q;
-                const uint32_t at = (col >> 6) * kXBox + box_at(row, (col & 63) >> 3);
-                for (int to = 0; to < c.cluster; ++to) {
-                    st_shared_cluster_v4(map_to_cta(ah_s + at, to), held[q / 8][0]);
-                    st_shared_cluster_v4(map_to_cta(al_s + at, to), held[q / 8][1]);
+            if (tid == 0) mbar_arrive_expect_tx(&gathered, static_cast<uint32_t>((c.cluster - 1) * per * 512));
+            // four columns of a row of A at a time
+            for (int u = tid; u < per * 32; u += kClusterThreads) {
+                const int r = u >> 5, col = (u & 31) * 4;
+                float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int share = 0; share < c.cluster; ++share) {
+                    const float4 x4 = *reinterpret_cast<const float4*>(red + (share * per + r) * 128 + col);
+                    v[0] += x4.x;
+                    v[1] += x4.y;
+                    v[2] += x4.z;
+                    v[3] += x4.w;
                 }
+                uint32_t h[2], l[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float a = v[2 * j] * (1.0f / kScale), b = v[2 * j + 1] * (1.0f / kScale);
+                    h[j] = pack2(a, b);
+                    const float2 f = unpack2(h[j]);
+                    l[j] = pack2(a - f.x, b - f.y);
+                }
+                const uint32_t at = (col >> 6) * kXBox + box_at(rank * per + r, (col & 63) >> 3) + (col & 4) * 2;
+                *reinterpret_cast<uint2*>(ah + at) = make_uint2(h[0], h[1]);
+                *reinterpret_cast<uint2*>(al + at) = make_uint2(l[0], l[1]);
             }
-            fence_async_all();
-            cluster_sync();
+            fence_async_shared();
+            __syncthreads();
+            // these rows, of both boxes of hi and lo (four runs of per * 128
+            // bytes), to every other CTA
+            if (tid < 4 * c.cluster && tid >> 2 != rank) {
+                const uint32_t at = ah_s + (tid & 3) * kXBox + rank * per * 128;
+                const uint32_t to = static_cast<uint32_t>(tid >> 2);
+                bulk_copy_to_cta(map_to_cta(at, to), at, per * 128, map_to_cta(smem_u32(&gathered), to));
+            }
+            __syncwarp();
+            if (!mbar_wait_bounded<true>(&gathered, step & 1, abort_flag, kWaitLimitNs)) record_failure(kRoleProducer, abort_flag);
         }
+        tc_fence_before();
         fence_async_shared();
         __syncthreads();
-        // ---- 3. B = b A + c A^2, in A's place
+        tc_fence_after();
+        // ---- 3. B = b A + c A^2
         if (tid == 0) {
             mma_kk(0, ah_s, al_s, 2, true);
             mma_kk(0, al_s, ah_s, 2, false);
@@ -1052,20 +1075,17 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
         __syncwarp();
         wait_done();
 #pragma unroll 1
-        for (int b32 = half * 2; b32 < half * 2 + 2; ++b32) {
-            float v[32];
+        for (int b16 = group * 2; b16 < group * 2 + 2; ++b16) {
+            float v[16];
+            add16(b16 * 16, 128 + b16 * 16, v);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-            add32(b32 * 32, v);
-            add32(128 + b32 * 32, v);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint32_t at = (b32 >> 1) * kXBox + box_at(row, (b32 & 1) * 4 + q);
+            for (int q = 0; q < 2; ++q) {
+                const uint32_t at = (b16 >> 2) * kXBox + box_at(row, (b16 & 3) * 2 + q);
                 uint4 hi = *reinterpret_cast<const uint4*>(ah + at), lo = *reinterpret_cast<const uint4*>(al + at);
                 blend8(&v[q * 8], hi, lo, cb, cc / kScale);
                 split8(&v[q * 8], hi, lo);
-                *reinterpret_cast<uint4*>(ah + at) = hi;
-                *reinterpret_cast<uint4*>(al + at) = lo;
+                *reinterpret_cast<uint4*>(bh + at) = hi;
+                *reinterpret_cast<uint4*>(bl + at) = lo;
             }
         }
         tc_fence_before();
@@ -1085,23 +1105,25 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
                         tc_mma<kFmtF16>(tmem + acc, pd, qd, idesc, (fresh && k == 0) ? 0u : 1u);
                     }
                 };
-                mma_kn(0, ah_s, xl_s, true);
-                mma_kn(0, al_s, xh_s, false);
-                mma_kn(256, ah_s, xh_s, true);
+                mma_kn(0, bh_s, xl_s, true);
+                mma_kn(0, bl_s, xh_s, false);
+                mma_kn(256, bh_s, xh_s, true);
                 tc_commit(&done);
             }
             __syncwarp();
             wait_done();
-            const bool last = step + 1 == c.steps;
-            for (int b32 = half * boxes; b32 < (half + 1) * boxes; ++b32) {
-                float v[32];
+        }
+        const bool last = step + 1 == c.steps;
+        __syncwarp();
+        if (c.cluster > 1 && !last) cluster_arrive_relaxed();  // this CTA is done with B
+        if (boxes > 0) {
+#pragma unroll 1
+            for (int b16 = group * boxes; b16 < (group + 1) * boxes; ++b16) {
+                float v[16];
+                add16(b16 * 16, 256 + b16 * 16, v);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                add32(b32 * 32, v);
-                add32(256 + b32 * 32, v);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t at = (b32 >> 1) * kXBox + box_at(row, (b32 & 1) * 4 + q);
+                for (int q = 0; q < 2; ++q) {
+                    const uint32_t at = (b16 >> 2) * kXBox + box_at(row, (b16 & 3) * 2 + q);
                     uint4 hi = *reinterpret_cast<const uint4*>(xh + at), lo = *reinterpret_cast<const uint4*>(xl + at);
                     if (last) {
                         blend8(&v[q * 8], hi, lo, ca / kScale, 1.0f / (kScale * kScale));
@@ -1113,7 +1135,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
                     }
                 }
                 if (last && row < p.m) {
-                    const int64_t col = col0 + b32 * 32;
+                    const int64_t col = col0 + b16 * 16;
                     if (p.result_type == DGA_F32) ns_result<float>(p, matrix, row, col, v);
                     else if (p.result_type == DGA_BF16) ns_result<__nv_bfloat16>(p, matrix, row, col, v);
                     else ns_result<__half>(p, matrix, row, col, v);
@@ -1125,6 +1147,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
         __syncthreads();
         tc_fence_after();
     }
+    __syncwarp();
     if (c.cluster > 1) cluster_sync();  // no CTA leaves while another may still write to it
     if (warp == 1) {
         __syncwarp();
@@ -1234,29 +1257,63 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
 }
 
 // The cluster kernel's shape, or cluster = 0 where it does not apply: up to 128
-// rows and 8 slabs of 256 columns.  CTAs are added while a slab is over 128
-// columns (its products then take longer than the exchange) and the batch
-// leaves room for them, and as far as the slabs need them.
+// rows and 16 slabs of 192 columns.  CTAs are added while a slab is over 128
+// columns and the batch leaves room for them, and as far as the slabs need
+// them; clusters of 16 only where the device can place one.
 struct ClusterShape {
-    int cluster, boxes_all, boxes_each;
-    bool own_red;
-    int smem;
+    int cluster, boxes_all, boxes_each, smem;
 };
+template <typename T>
+bool places_16(int smem, const DeviceInfo& dev) {
+    static int known[64] = {};  // 0 unknown, 1 no, 2 yes
+    static std::mutex mu;
+    std::lock_guard<std::mutex> lock(mu);
+    int& k = known[dev.ordinal & 63];
+    if (k == 0) {
+        k = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kMaxCluster);
+        cfg.blockDim = dim3(kClusterThreads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kMaxCluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(ns_cluster_kernel<T>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaFuncSetAttribute(ns_cluster_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&n, ns_cluster_kernel<T>, &cfg) == cudaSuccess && n > 0)
+            k = 2;
+        else
+            cudaGetLastError();
+    }
+    return k == 2;
+}
+constexpr int cluster_smem(int boxes) { return static_cast<int>(2 * boxes * kXBox + 4 * kABytes + 1024); }
+template <typename T>
 ClusterShape cluster_shape(const OrthoArgs& a, const NsPlan& pl, const DeviceInfo& dev) {
     ClusterShape c{};
-    if (pl.m > 128 || pl.np > 8 * 64 * kMaxBoxes || a.steps > 32) return c;
+    if (pl.m > 128 || pl.np > kMaxCluster * 64 * kMaxBoxes || a.steps > 32) return c;
     c.boxes_all = static_cast<int>(pl.np / 64);
+    auto each = [&](int n) { return (c.boxes_all + n - 1) / n; };
     int n = 1;
-    while (n < 8 && (c.boxes_all + n - 1) / n > 2 && (a.batch * n * 2 <= dev.sm_count || (c.boxes_all + n - 1) / n > kMaxBoxes)) n *= 2;
+    while (n < 8 && each(n) > 2 && (each(n) > kMaxBoxes || a.batch * n * 2 <= dev.sm_count)) n *= 2;
+    if (each(n) > kMaxBoxes) n = kMaxCluster;
+    if (n == kMaxCluster && !places_16<T>(cluster_smem(kMaxBoxes), dev)) return c;
     c.cluster = n;
-    c.boxes_each = (c.boxes_all + n - 1) / n;
-    c.own_red = n > 1 && c.boxes_each <= 3;
-    c.smem = static_cast<int>(2 * c.boxes_each * kXBox + 2 * kABytes + (c.own_red ? kRedBytes : 0) + 1024);
+    c.boxes_each = each(n);
+    c.smem = cluster_smem(c.boxes_each);
     return c;
 }
 
 template <typename T>
-cudaError_t launch_cluster(const OrthoArgs& a, const NsPlan& pl, const ClusterShape& shape, const NsParams& p) {
+cudaError_t launch_cluster(const OrthoArgs& a, const NsPlan& pl, const NsParams& p, const DeviceInfo& dev, bool* done) {
+    const ClusterShape shape = cluster_shape<T>(a, pl, dev);
+    *done = shape.cluster > 0;
+    if (!*done) return cudaSuccess;
     constexpr int64_t kVec = 16 / sizeof(T);
     NsClusterParams c{};
     c.G = a.G;
@@ -1269,7 +1326,6 @@ cudaError_t launch_cluster(const OrthoArgs& a, const NsPlan& pl, const ClusterSh
     c.boxes_all = shape.boxes_all;
     c.boxes_each = shape.boxes_each;
     c.cluster = shape.cluster;
-    c.own_red = shape.own_red;
     c.eps = a.eps;
     c.steps = a.steps;
     for (int i = 0; i < 3 * a.steps; ++i) c.coefficients[i] = a.coefficients[i];
@@ -1341,13 +1397,12 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
     base.result_vec = aligned(a.O, 16) && a.ldo % per16 == 0 && (a.batch == 1 || a.stride_o % per16 == 0);
     base.ldo = a.ldo;
     base.stride_o = a.stride_o;
-    cudaError_t e;
-    const ClusterShape shape = cluster_shape(a, pl, dev);
-    if (shape.cluster > 0) {
-        e = a.in_dtype == DGA_F32    ? launch_cluster<float>(a, pl, shape, base)
-            : a.in_dtype == DGA_BF16 ? launch_cluster<__nv_bfloat16>(a, pl, shape, base)
-                                     : launch_cluster<__half>(a, pl, shape, base);
-        if (e == cudaSuccess) ++*launches;
+    bool done = false;
+    cudaError_t e = a.in_dtype == DGA_F32    ? launch_cluster<float>(a, pl, base, dev, &done)
+                    : a.in_dtype == DGA_BF16 ? launch_cluster<__nv_bfloat16>(a, pl, base, dev, &done)
+                                             : launch_cluster<__half>(a, pl, base, dev, &done);
+    if (done) {
+        *launches = 1;
         return e;
     }
     e = a.in_dtype == DGA_F32    ? launch_first<float>(a, pl, partial, xh[0], xl[0], dev, a.stream)

@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from . import BF16, F16, F32, OK, DgaError, dga_orthogonalize_workspace_size, lib
+from . import BF16, F16, F32, DgaError, _raw_stream, lib
 
 _CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _TORCH = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
@@ -17,12 +17,14 @@ QUINTIC = (3.4445, -4.7750, 2.0315)
 
 
 def _layout(T, name):
-    """(batch, leading dimension, matrix stride) of a 2-D or 3-D tensor whose rows are contiguous."""
-    rows, cols = T.shape[-2:]
-    if T.stride(-1) != 1 and cols > 1:
+    """(batch, rows, columns, leading dimension, matrix stride) of a 2-D or 3-D
+    tensor whose rows are contiguous."""
+    shape, stride = T.shape, T.stride()
+    rows, cols = shape[-2], shape[-1]
+    if stride[-1] != 1 and cols > 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    ld = max(T.stride(-2), cols) if rows > 1 else max(cols, 1)
-    return (1, ld, 0) if T.dim() == 2 else (T.shape[0], ld, T.stride(0))
+    ld = max(stride[-2], cols) if rows > 1 else cols
+    return (1, rows, cols, ld, 0) if len(shape) == 2 else (shape[0], rows, cols, ld, stride[0])
 
 
 def orthogonalize(G, steps=5, coefficients=QUINTIC, eps=1e-7, out=None, out_dtype=None,
@@ -36,31 +38,37 @@ def orthogonalize(G, steps=5, coefficients=QUINTIC, eps=1e-7, out=None, out_dtyp
     allocator unless given (dga_orthogonalize_workspace_size bytes)."""
     if G.dim() not in (2, 3):
         raise ValueError("G must be a matrix or a batch of matrices")
-    if G.dtype not in _CODE:
+    code = _CODE.get(G.dtype)
+    if code is None:
         raise TypeError("G must be float32, bfloat16 or float16")
     if not G.is_cuda:
         raise ValueError("G must be a CUDA tensor")
+    dev = G.device
     if out is None:
-        out = torch.empty(G.shape, dtype=G.dtype if out_dtype is None else _TORCH[out_dtype], device=G.device)
-    elif out.shape != G.shape or out.dtype not in _CODE or out.device != G.device:
+        out_code = code if out_dtype is None else out_dtype
+        out = torch.empty(G.shape, dtype=_TORCH[out_code], device=dev)
+    elif out.shape != G.shape or out.dtype not in _CODE or out.device != dev:
         raise ValueError("out must be a float32, bfloat16 or float16 tensor of G's shape, on its device")
-    flat = [float(c) for t in coefficients for c in t] if hasattr(coefficients[0], "__len__") \
-        else [float(c) for c in coefficients] * steps
+    else:
+        out_code = _CODE[out.dtype]
+    if hasattr(coefficients[0], "__len__"):
+        flat = [c for t in coefficients for c in t]
+    else:
+        flat = list(coefficients) * max(steps, 0)
     if len(flat) != 3 * steps:
         raise ValueError(f"coefficients must be one (a, b, c), or {steps} of them")
-    batch, ldg, stride_g = _layout(G, "G")
-    _, ldo, stride_o = _layout(out, "out")
-    rows, cols = G.shape[-2:]
-    code = _CODE[out.dtype]
-    need = dga_orthogonalize_workspace_size(code, batch, rows, cols)
+    batch, rows, cols, ldg, stride_g = _layout(G, "G")
+    _, _, _, ldo, stride_o = _layout(out, "out")
+    L = lib()
+    need = L.dga_orthogonalize_workspace_size(out_code, batch, rows, cols)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=G.device)
-    if stream is None:
-        stream = torch.cuda.current_stream(G.device).cuda_stream
-    st = lib().dga_orthogonalize(_CODE[G.dtype], code, batch, rows, cols, G.data_ptr(), ldg, stride_g,
-                                 out.data_ptr(), ldo, stride_o, steps, (ctypes.c_float * len(flat))(*flat),
-                                 eps, workspace.data_ptr() if workspace.numel() else None,
-                                 workspace.numel() * workspace.element_size(), stream)
-    if st != OK:
+        workspace, have = torch.empty(need, dtype=torch.uint8, device=dev), need
+    else:
+        have = workspace.numel() * workspace.element_size()
+    st = L.dga_orthogonalize(code, out_code, batch, rows, cols, G.data_ptr(), ldg, stride_g, out.data_ptr(),
+                             ldo, stride_o, steps, (ctypes.c_float * len(flat))(*flat), eps,
+                             workspace.data_ptr() or None, have,
+                             _raw_stream(dev.index) if stream is None else stream)
+    if st:
         raise DgaError(st, "dga_orthogonalize")
     return out

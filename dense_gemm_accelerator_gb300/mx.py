@@ -10,8 +10,7 @@ import ctypes
 
 import torch
 
-from . import (BF16, F16, F32, OK, DgaError, dga_mx_linear_workspace_size, dga_mx_row_bytes,
-               dga_mx_scales_size, lib, sum_rows)
+from . import BF16, F16, F32, DgaError, _raw_stream, lib, sum_rows
 
 MXFP4, NVFP4 = 0, 1
 
@@ -44,12 +43,11 @@ class MXTensor:
 
 
 def _stream(device, stream):
-    return torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+    return _raw_stream(device.index) if stream is None else stream
 
 
-def _check(st, what):
-    if st != OK:
-        raise DgaError(st, what)
+def _raise(st, what):
+    raise DgaError(st, what)
 
 
 def _factor(t, format, device):
@@ -58,16 +56,19 @@ def _factor(t, format, device):
         return None
     if format != NVFP4:
         raise ValueError("tensor_scale needs the NVFP4 format")
-    if t.dtype != torch.float32 or t.numel() != 1 or t.device != device:
+    if t.dtype is not torch.float32 or t.numel() != 1 or t.device != device:
         raise ValueError("tensor_scale must be one float32 value on the tensor's device")
     return t.data_ptr()
 
 
 def _rows_of(T, name):
-    """(leading dimension) of a row-major 2-D tensor."""
-    if T.dim() != 2 or (T.stride(1) != 1 and T.shape[1] > 1):
-        raise ValueError(f"{name} must be 2-D and row-major")
-    return max(T.stride(0), T.shape[1], 1)
+    """(rows, columns, leading dimension) of a row-major 2-D tensor."""
+    if T.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    (rows, cols), (ld, step) = T.shape, T.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must be row-major")
+    return rows, cols, ld if ld > cols else (cols or 1)
 
 
 def mx_quantize(X, format=MXFP4, transpose=False, tensor_scale=None, stream=None):
@@ -76,49 +77,55 @@ def mx_quantize(X, format=MXFP4, transpose=False, tensor_scale=None, stream=None
     MXTensor of X's transpose (quantised along X's columns)."""
     if X.dim() != 2:
         raise ValueError("X must be 2-D")
-    if X.dtype not in _CODE:
+    code = _CODE.get(X.dtype)
+    if code is None:
         raise TypeError("X must be float32, bfloat16 or float16")
     if not X.is_cuda:
         raise ValueError("X must be a CUDA tensor")
     if X.stride(1) != 1 and X.shape[1] > 1 and X.stride(0) == 1:
         X, transpose = X.t(), not transpose  # a column-major X is its transpose, row-major
-    ldx = _rows_of(X, "X")
-    rows, cols = X.shape
+    rows, cols, ldx = _rows_of(X, "X")
     R, K = (cols, rows) if transpose else (rows, cols)
-    dev = X.device
-    row_bytes = dga_mx_row_bytes(K)
+    dev, L = X.device, lib()
+    row_bytes = (K + 31) // 32 * 16  # dga_mx_row_bytes
     codes = torch.empty((R, row_bytes), dtype=torch.uint8, device=dev)
-    scales = torch.empty(dga_mx_scales_size(format, R, K), dtype=torch.uint8, device=dev)
-    _check(lib().dga_mx_quantize(format, _CODE[X.dtype], int(transpose), rows, cols, X.data_ptr(), ldx,
-                                 _factor(tensor_scale, format, dev), codes.data_ptr(), row_bytes,
-                                 scales.data_ptr(), _stream(dev, stream)), "dga_mx_quantize")
+    scales = torch.empty(L.dga_mx_scales_size(format, R, K), dtype=torch.uint8, device=dev)
+    st = L.dga_mx_quantize(format, code, 1 if transpose else 0, rows, cols, X.data_ptr(), ldx,
+                           _factor(tensor_scale, format, dev), codes.data_ptr(), row_bytes,
+                           scales.data_ptr(), _stream(dev, stream))
+    if st:
+        _raise(st, "dga_mx_quantize")
     return MXTensor(format, R, K, codes, scales, tensor_scale)
 
 
 def mx_dequantize(Q, out_dtype=F32, stream=None):
     """The values an MXTensor stands for, rounded once to out_dtype."""
-    Y = torch.empty((Q.rows, Q.cols), dtype=_TORCH[out_dtype], device=Q.device)
-    _check(lib().dga_mx_dequantize(Q.format, out_dtype, Q.rows, Q.cols, Q.codes.data_ptr(),
-                                   Q.codes.stride(0), Q.scales.data_ptr(),
-                                   _factor(Q.tensor_scale, Q.format, Q.device), Y.data_ptr(),
-                                   max(Q.cols, 1), _stream(Q.device, stream)), "dga_mx_dequantize")
+    dev = Q.codes.device
+    Y = torch.empty((Q.rows, Q.cols), dtype=_TORCH[out_dtype], device=dev)
+    st = lib().dga_mx_dequantize(Q.format, out_dtype, Q.rows, Q.cols, Q.codes.data_ptr(),
+                                 Q.codes.stride(0), Q.scales.data_ptr(),
+                                 _factor(Q.tensor_scale, Q.format, dev), Y.data_ptr(), Q.cols or 1,
+                                 _stream(dev, stream))
+    if st:
+        _raise(st, "dga_mx_dequantize")
     return Y
 
 
 def _output(C, M, N, beta, out_dtype, device):
+    """(the output, its type's code, its leading dimension)."""
     if C is None:
         if beta != 0:
             raise ValueError("beta != 0 needs C")
-        return torch.empty((M, N), dtype=_TORCH[out_dtype], device=device), max(N, 1)
+        return torch.empty((M, N), dtype=_TORCH[out_dtype], device=device), out_dtype, N or 1
     if tuple(C.shape) != (M, N) or C.dtype not in _CODE or C.device != device:
         raise ValueError(f"the output must be a ({M}, {N}) float32, bfloat16 or float16 tensor on {device}")
-    return C, _rows_of(C, "the output")
+    return C, _CODE[C.dtype], _rows_of(C, "the output")[2]
 
 
 def _bias(bias, N, C):
     if bias is None:
         return None
-    if bias.dim() != 1 or bias.numel() != N or (N > 1 and bias.stride(0) != 1) or bias.dtype != C.dtype \
+    if bias.dim() != 1 or bias.numel() != N or (N > 1 and bias.stride(0) != 1) or bias.dtype is not C.dtype \
             or bias.device != C.device:
         raise ValueError("bias must be a contiguous vector of the output's length, type and device")
     return bias.data_ptr()
@@ -134,14 +141,15 @@ def mx_gemm(A, B, C=None, alpha=1.0, beta=0.0, out_dtype=BF16, bias=None, stream
     if A.device != B.device:
         raise ValueError("A and B must be on the same device")
     dev = A.codes.device
-    C, ldc = _output(C, A.rows, B.rows, beta, out_dtype, dev)
+    C, code, ldc = _output(C, A.rows, B.rows, beta, out_dtype, dev)
     a, b = ctypes.c_float(alpha), ctypes.c_float(beta)
-    _check(lib().dga_mx_gemm(A.format, _CODE[C.dtype], A.rows, B.rows, A.cols, ctypes.byref(a),
-                             A.codes.data_ptr(), A.codes.stride(0), A.scales.data_ptr(),
-                             _factor(A.tensor_scale, A.format, dev), B.codes.data_ptr(),
-                             B.codes.stride(0), B.scales.data_ptr(),
-                             _factor(B.tensor_scale, B.format, dev), ctypes.byref(b), C.data_ptr(),
-                             ldc, _bias(bias, B.rows, C), _stream(dev, stream)), "dga_mx_gemm")
+    st = lib().dga_mx_gemm(A.format, code, A.rows, B.rows, A.cols, ctypes.byref(a), A.codes.data_ptr(),
+                           A.codes.stride(0), A.scales.data_ptr(), _factor(A.tensor_scale, A.format, dev),
+                           B.codes.data_ptr(), B.codes.stride(0), B.scales.data_ptr(),
+                           _factor(B.tensor_scale, B.format, dev), ctypes.byref(b), C.data_ptr(), ldc,
+                           _bias(bias, B.rows, C), _stream(dev, stream))
+    if st:
+        _raise(st, "dga_mx_gemm")
     return C
 
 
@@ -149,25 +157,27 @@ def mx_linear_forward(X, W, bias=None, Y=None, tensor_scale=None, workspace=None
     """Y = X @ W^T + bias for X [batch, in] (float32, bfloat16 or float16) and a
     4-bit weight W, an MXTensor [out, in]: X is quantised in W's format
     (tensor_scale: its factor) and multiplied.  Y, of X's type unless given."""
-    if X.dtype not in _CODE:
+    code = _CODE.get(X.dtype)
+    if code is None:
         raise TypeError("X must be float32, bfloat16 or float16")
-    ldx = _rows_of(X, "X")
-    M, K = X.shape
+    M, K, ldx = _rows_of(X, "X")
     if K != W.cols:
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {W.shape}")
-    dev = X.device
+    dev, fmt, N, L = X.device, W.format, W.rows, lib()
     if W.codes.device != dev:
         raise ValueError("X and W must be on the same device")
-    N = W.rows
-    Y, ldy = _output(Y, M, N, 0, _CODE[X.dtype], dev)
+    Y, out, ldy = _output(Y, M, N, 0, code, dev)
+    need = L.dga_mx_linear_workspace_size(fmt, M, K)
     if workspace is None:
-        workspace = torch.empty(dga_mx_linear_workspace_size(W.format, M, K), dtype=torch.uint8, device=dev)
-    _check(lib().dga_mx_linear(W.format, _CODE[X.dtype], _CODE[Y.dtype], M, N, K, X.data_ptr(), ldx,
-                               _factor(tensor_scale, W.format, dev), W.codes.data_ptr(),
-                               W.codes.stride(0), W.scales.data_ptr(),
-                               _factor(W.tensor_scale, W.format, dev), _bias(bias, N, Y), Y.data_ptr(),
-                               ldy, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                               _stream(dev, stream)), "dga_mx_linear")
+        workspace, have = torch.empty(need, dtype=torch.uint8, device=dev), need
+    else:
+        have = workspace.numel() * workspace.element_size()
+    st = L.dga_mx_linear(fmt, code, out, M, N, K, X.data_ptr(), ldx, _factor(tensor_scale, fmt, dev),
+                         W.codes.data_ptr(), W.codes.stride(0), W.scales.data_ptr(),
+                         _factor(W.tensor_scale, fmt, dev), _bias(bias, N, Y), Y.data_ptr(), ldy,
+                         workspace.data_ptr(), have, _stream(dev, stream))
+    if st:
+        _raise(st, "dga_mx_linear")
     return Y
 
 

@@ -506,7 +506,7 @@ size_t dga_mx_linear_workspace_size(dga_mx_format format, int64_t M, int64_t K);
  * ldo, -11 stride_o (outputs overlap), -12 steps (outside [1, 1000]), -13
  * coefficients, -14 eps < 0 or NaN, -15 workspace; DGA_ERR_WORKSPACE,
  * DGA_ERR_OVERLAP.  batch, rows or cols of 0 is a no-op.  One launch
- * where min(rows, cols) <= 128, max(rows, cols) <= 2048 and steps <= 32, else
+ * where min(rows, cols) <= 128, max(rows, cols) <= 3072 and steps <= 32, else
  * 2 + 3 * steps.
  */
 int dga_orthogonalize(dga_dtype in_dtype, dga_dtype out_dtype, int64_t batch, int64_t rows,
