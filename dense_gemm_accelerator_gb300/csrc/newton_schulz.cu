@@ -69,15 +69,15 @@ struct NsParams {
     uint32_t num_kb, segs;  // K blocks of 64; 1 product (hi hi), or 3 (hi lo, lo hi, hi hi)
     uint32_t q_mn;          // the second operand is read MN-major (rows along K)
     uint32_t p_rows, q_rows;  // rows of one matrix in each operand's map
-    // value = c_old * (old_h + old_l) + c_acc * sum; old_* may be null
+    int32_t rows, ld;         // padded rows and columns of the value
+    // value = c_old * (old hi + lo) + c_acc * sum
     float c_old, c_acc;
-    const __half* old_h;
-    const __half* old_l;
-    __half* out_h;  // null: the last step, to `result`
-    __half* out_l;  // null: hi alone
-    int64_t rows, ld, stride;  // of old and out: padded rows, row and matrix strides
+    uint32_t has_old, old_lo;  // there is an old value; it has a lo word
+    uint32_t out_lo;           // the value is stored with its lo word
+    uint32_t last;             // the value is the result
     void* result;
-    int result_type, transposed, result_vec;  // result_vec: its rows take 16-byte stores
+    int result_type, transposed;
+    uint32_t result_tma, result_vec;  // its rows can be stored by TMA; by 16-byte stores
     int64_t m, n, ldo, stride_o;
 };
 
@@ -137,65 +137,180 @@ __device__ __forceinline__ void ns_result(const NsParams& p, uint32_t matrix, in
     }
 }
 
-// 32 columns (col .. col+31) of one row per lane.  mirror: the tile is off the
-// diagonal of a symmetric product, so that its transpose is stored too.
-__device__ __forceinline__ void ns_store(const NsParams& p, uint32_t matrix, int64_t row, int64_t col, bool mirror,
-                                         float (&v)[32]) {
-    const bool in = row < p.rows && col < p.ld;  // padded sizes are multiples of 64
-    const int64_t at = matrix * p.stride + row * p.ld + col;
-    if (in) {
-        if (p.old_h != nullptr) {
+// The tensor maps of one product.  Operands: boxes of one 128-byte row of K
+// (64 fp16) x 128 rows, or, MN-major, 64 columns x 64 rows of K.  Values: 64
+// columns x 32 rows of one matrix (and mirrored, 32 x 64), so that what lies
+// past a matrix' padded rows is neither read nor written.
+struct NsMaps {
+    CUtensorMap p_h, p_l, q_h, q_l, old_h, old_l, out_h, out_l, mirror_h, mirror_l, result;
+};
+
+// Byte offset of 16-byte piece `piece` (8 fp16) of a row in a box of 128-byte rows.
+__device__ __forceinline__ uint32_t box_at(int row, int piece) {
+    return static_cast<uint32_t>(row) * 128u + (static_cast<uint32_t>(piece ^ (row & 7)) << 4);
+}
+// Eight values as hi and lo.
+__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
+    uint32_t h[4], l[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const uint4 h = *reinterpret_cast<const uint4*>(p.old_h + at + q * 8);
-                uint4 l = make_uint4(0, 0, 0, 0);
-                if (p.old_l != nullptr) l = *reinterpret_cast<const uint4*>(p.old_l + at + q * 8);
-                const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const float2 a = unpack2(hw[w]), b = unpack2(lw[w]);
-                    float& x = v[q * 8 + w * 2];
-                    float& y = v[q * 8 + w * 2 + 1];
-                    x = fmaf(p.c_old, a.x + b.x, p.c_acc * x);
-                    y = fmaf(p.c_old, a.y + b.y, p.c_acc * y);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= p.c_acc;
-        }
-    }
-    if (p.out_h == nullptr) {
-        if (row < p.m) {
-            if (p.result_type == DGA_F32) ns_result<float>(p, matrix, row, col, v);
-            else if (p.result_type == DGA_BF16) ns_result<__nv_bfloat16>(p, matrix, row, col, v);
-            else ns_result<__half>(p, matrix, row, col, v);
-        }
-        return;
-    }
-    if (!in) return;
-    uint32_t h[16], l[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < 4; ++j) {
         h[j] = pack2(v[2 * j], v[2 * j + 1]);
         const float2 f = unpack2(h[j]);
         l[j] = pack2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
     }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// x[0..7] <- c_old * (hi + lo) + c_acc * x
+__device__ __forceinline__ void blend8(float* x, const uint4& hi, const uint4& lo, float c_old, float c_acc) {
+    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        *reinterpret_cast<uint4*>(p.out_h + at + q * 8) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
-        if (p.out_l != nullptr)
-            *reinterpret_cast<uint4*>(p.out_l + at + q * 8) = make_uint4(l[4 * q], l[4 * q + 1], l[4 * q + 2], l[4 * q + 3]);
+    for (int j = 0; j < 4; ++j) {
+        const float2 a = unpack2(h[j]), b = unpack2(l[j]);
+        x[2 * j] = fmaf(c_old, a.x + b.x, c_acc * x[2 * j]);
+        x[2 * j + 1] = fmaf(c_old, a.y + b.y, c_acc * x[2 * j + 1]);
+    }
+}
+
+// ---- the epilogue: units of 32 rows x 64 columns, one warp each ----------------------------
+//
+// A warp has two boxes of 32 rows x 128 bytes.  The old values come into them
+// by TMA while the products run (hi, lo); lane l then takes row l's, in
+// swizzled 16-byte pieces, and puts the new ones there, which TMA stores.
+// (With a lane's own 16-byte loads and stores, one row per lane, the epilogue
+// was bound by the L1's one line per cycle: 8,000 to 20,000 clocks a tile.)
+constexpr uint32_t kBox32 = 32 * 128;
+constexpr uint32_t kUnitBytes = 2 * kBox32;
+
+// Starts the loads of a unit's old values (one lane).
+__device__ __forceinline__ void unit_prefetch(const NsParams& p, const NsMaps& maps, uint8_t* boxes, uint64_t* bar,
+                                              uint32_t matrix, int32_t row0, int32_t col0) {
+    mbar_arrive_expect_tx(bar, p.old_lo ? 2 * kBox32 : kBox32);
+    tma_load_3d(boxes, &maps.old_h, bar, col0, row0, static_cast<int32_t>(matrix));
+    if (p.old_lo) tma_load_3d(boxes + kBox32, &maps.old_l, bar, col0, row0, static_cast<int32_t>(matrix));
+}
+
+// The result's part of ns_unit: v to rows of m x n, or (transposed) of n x m.
+template <typename T>
+__device__ __forceinline__ void unit_result(const NsParams& p, const NsMaps& maps, uint8_t* boxes, uint32_t matrix,
+                                            int32_t row0, int32_t col0, int lane, const float (&v)[64]) {
+    constexpr int kPer = 16 / sizeof(T), kBoxCols = 128 / sizeof(T);
+    if (p.transposed) {
+        // column j of the unit becomes a row of 32
+#pragma unroll
+        for (int j = 0; j < 64; ++j) OutT<T>::store(reinterpret_cast<T*>(boxes) + j * 32 + lane, v[j]);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 64 / kPer; ++q) {
+            T w[kPer];
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) OutT<T>::store(&w[e], v[q * kPer + e]);
+            uint4 x;
+            memcpy(&x, w, 16);
+            *reinterpret_cast<uint4*>(boxes + (q / 8) * kBox32 + box_at(lane, q % 8)) = x;
+        }
+    }
+    if (p.result_tma) {
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0 && row0 < p.m && col0 < p.n) {
+            if (p.transposed) {
+                tma_store_3d(&maps.result, boxes, row0, col0, static_cast<int32_t>(matrix));
+            } else {
+#pragma unroll
+                for (int b = 0; b < 64 / kBoxCols; ++b)
+                    if (col0 + b * kBoxCols < p.n)
+                        tma_store_3d(&maps.result, boxes + b * kBox32, col0 + b * kBoxCols, row0, static_cast<int32_t>(matrix));
+            }
+        }
+        if (lane == 0) bulk_commit();
+        return;
+    }
+    __syncwarp();
+    T* base = static_cast<T*>(p.result) + matrix * p.stride_o;
+    if (p.transposed) {
+        if (row0 + lane < p.m)
+            for (int j = 0; j < 64 && col0 + j < p.n; ++j)
+                base[static_cast<int64_t>(col0 + j) * p.ldo + row0 + lane] = reinterpret_cast<const T*>(boxes)[j * 32 + lane];
+    } else {
+        for (int i = 0; i < 32 && row0 + i < p.m; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int c = h * 32 + lane, in = c % kBoxCols;
+                if (col0 + c < p.n)
+                    base[static_cast<int64_t>(row0 + i) * p.ldo + col0 + c] = *reinterpret_cast<const T*>(
+                        boxes + (c / kBoxCols) * kBox32 + box_at(i, in / kPer) + (in % kPer) * sizeof(T));
+            }
+    }
+    __syncwarp();
+}
+
+// One unit of a tile, v its sums: lane l has row row0 + l, columns col0 ..
+// col0 + 63.  mirror: the tile is off the diagonal of a symmetric product, so
+// that its transpose is stored too.  On return the boxes' stores are under way.
+__device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, uint8_t* boxes, uint64_t* bar, uint32_t phase,
+                                        volatile int* abort_flag, uint32_t matrix, int32_t row0, int32_t col0, int lane,
+                                        bool mirror, float (&v)[64]) {
+    if (p.has_old) {
+        if (!mbar_wait_bounded(bar, phase, abort_flag, kWaitLimitNs)) record_failure(kRoleEpilogue, abort_flag);
+        uint4 lo = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            const uint4 hi = *reinterpret_cast<const uint4*>(boxes + box_at(lane, q));
+            if (p.old_lo) lo = *reinterpret_cast<const uint4*>(boxes + kBox32 + box_at(lane, q));
+            blend8(&v[q * 8], hi, lo, p.c_old, p.c_acc);
+        }
+    } else {
+        // the boxes may still be read by the last unit's stores
+        if (lane == 0) bulk_wait_read<0>();
+#pragma unroll
+        for (int j = 0; j < 64; ++j) v[j] *= p.c_acc;
+    }
+    __syncwarp();
+    if (p.last) {
+        if (p.result_type == DGA_F32) unit_result<float>(p, maps, boxes, matrix, row0, col0, lane, v);
+        else if (p.result_type == DGA_BF16) unit_result<__nv_bfloat16>(p, maps, boxes, matrix, row0, col0, lane, v);
+        else unit_result<__half>(p, maps, boxes, matrix, row0, col0, lane, v);
+        return;
+    }
+    uint32_t h[32], l[32];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        uint4 hi, lo;
+        split8(&v[q * 8], hi, lo);
+        *reinterpret_cast<uint4*>(boxes + box_at(lane, q)) = hi;
+        if (p.out_lo) *reinterpret_cast<uint4*>(boxes + kBox32 + box_at(lane, q)) = lo;
+        h[4 * q] = hi.x, h[4 * q + 1] = hi.y, h[4 * q + 2] = hi.z, h[4 * q + 3] = hi.w;
+        l[4 * q] = lo.x, l[4 * q + 1] = lo.y, l[4 * q + 2] = lo.z, l[4 * q + 3] = lo.w;
+    }
+    fence_async_shared();
+    __syncwarp();
+    const bool in = row0 < p.rows && col0 < p.ld;
+    if (lane == 0) {
+        if (in) tma_store_3d(&maps.out_h, boxes, col0, row0, static_cast<int32_t>(matrix));
+        if (in && p.out_lo) tma_store_3d(&maps.out_l, boxes + kBox32, col0, row0, static_cast<int32_t>(matrix));
+        bulk_commit();
     }
     if (mirror) {
-        // element (col + j, row): consecutive lanes on consecutive columns
-        const int64_t mt = matrix * p.stride + col * p.ld + row;
-        uint16_t* oh = reinterpret_cast<uint16_t*>(p.out_h) + mt;
-        uint16_t* ol = reinterpret_cast<uint16_t*>(p.out_l) + mt;
+        // column j of the unit becomes a row of 32: 64 rows of 64 bytes, hi in
+        // the second box if there is no lo
+        uint16_t* mh = reinterpret_cast<uint16_t*>(p.out_lo ? boxes : boxes + kBox32);
+        uint16_t* ml = reinterpret_cast<uint16_t*>(boxes + kBox32);
+        if (p.out_lo) {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+        }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            oh[j * p.ld] = static_cast<uint16_t>(j & 1 ? h[j / 2] >> 16 : h[j / 2]);
-            if (p.out_l != nullptr) ol[j * p.ld] = static_cast<uint16_t>(j & 1 ? l[j / 2] >> 16 : l[j / 2]);
+        for (int j = 0; j < 64; ++j) {
+            mh[j * 32 + lane] = static_cast<uint16_t>(j & 1 ? h[j / 2] >> 16 : h[j / 2]);
+            if (p.out_lo) ml[j * 32 + lane] = static_cast<uint16_t>(j & 1 ? l[j / 2] >> 16 : l[j / 2]);
+        }
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            if (in) tma_store_3d(&maps.mirror_h, mh, row0, col0, static_cast<int32_t>(matrix));
+            if (in && p.out_lo) tma_store_3d(&maps.mirror_l, ml, row0, col0, static_cast<int32_t>(matrix));
+            bulk_commit();
         }
     }
 }
@@ -212,23 +327,20 @@ __device__ __forceinline__ uint32_t chunk_count(const NsParams& p, uint32_t kb0,
     return n;
 }
 
-struct NsMaps {
-    CUtensorMap p_h, p_l, q_h, q_l;
-};
-
 // ---- the tile kernel: 128 x 128, K parts in a cluster ---------------------------------
 
-constexpr int kTileStages = 3;  // two CTAs to an SM: a launch's start overlaps the last one's end
+constexpr int kTileStages = 4;
 constexpr uint32_t kTileStage = 2 * 128 * 128;
-constexpr uint32_t kTileBar = kTileStages * kTileStage;
-constexpr uint32_t kTileLaunch = kTileBar + (2 * kTileStages + 4) * 8 + 16 + 1024;
-static_assert(kTileBar >= 128 * 128 * 4, "the partial sums fit the ring");
+constexpr uint32_t kTileEpi = kTileStages * kTileStage;
+constexpr uint32_t kTileBar = kTileEpi + 8 * kUnitBytes;
+constexpr uint32_t kTileLaunch = kTileBar + (2 * kTileStages + 4 + 8) * 8 + 16 + 1024;
+static_assert(kTileEpi >= 128 * 128 * 4, "the partial sums fit the ring");
 
-// Producer warp, MMA warp, 8 epilogue warps with half of the columns each.
+// Producer warp, MMA warp, 8 epilogue warps with a unit of the tile each.
 constexpr int kTileThreads = 320;
 
 template <bool kChunked>
-__global__ void __launch_bounds__(kTileThreads, 2)
+__global__ void __launch_bounds__(kTileThreads, 1)
     ns_tile_kernel(const __grid_constant__ NsMaps maps, NsParams p, uint32_t splits) {
     constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 128, 128);
     extern __shared__ uint8_t smem_raw[];
@@ -238,7 +350,8 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     uint64_t* empty = full + kTileStages;
     uint64_t* acc_full = empty + kTileStages;
     uint64_t* acc_empty = acc_full + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    uint64_t* old_full = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     constexpr uint32_t kCols = kChunked ? 256 : 128;  // two accumulators, or one
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -258,8 +371,11 @@ __global__ void __launch_bounds__(kTileThreads, 2)
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 8);
         }
+        for (int w = 0; w < 8; ++w) mbar_init(&old_full[w], 1);
         *abort_flag = 0;
         fence_mbar_init();
+        tma_prefetch_desc(&maps.p_h);
+        tma_prefetch_desc(&maps.q_h);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, kCols);
@@ -333,112 +449,82 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         }
     }
     __syncwarp();
-    const int quarter = warp & 3, r_in = quarter * 32 + lane;
-    const int64_t row = static_cast<int64_t>(tm) * 128 + r_in, col0 = static_cast<int64_t>(tn) * 128;
-    const bool mirror = p.sym && tm != tn;
-    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    // Column block c of 32 is joined by CTA c % splits.  Each CTA sends its sums
-    // to the joining ones (stores, which nothing waits for) once every CTA's
-    // ring is done with, slot q of `red` coming from part q:
-    // red[((q * 4 / splits + c / splits) * 32 + j) * 128 + row].
-    float* red = reinterpret_cast<float*>(smem);
-    auto send = [&](uint32_t c, int j, float x) {
-        const uint32_t at = smem_u32(red + ((part * (4 / splits) + c / splits) * 32 + j) * 128 + r_in);
-        st_shared_cluster_f32(map_to_cta(at, c % splits), x);
-    };
-    // the last commit: every MMA of this CTA, and with them every copy into the ring
-    const uint32_t n_chunks = kChunked ? chunk_count(p, kb0, kb1) : 1;
-    bool ok = true;
-    if constexpr (kChunked) {
-        if (warp >= 2) {
-            const int half = (warp - 2) >> 2;  // 64 columns
-            float sum[64];
+    if (warp >= 2) {
+        // Unit (quarter, half): 32 rows, 64 columns.  With K in parts, CTA c
+        // joins the quarters q % splits == c, `units` of them; slot i there is
+        // half i % 2 of quarter c + i / 2 * splits, and warp 2 + i's.  Each CTA
+        // sends its sums to the joining ones (stores, which nothing waits for)
+        // once every CTA's ring is done with: share q's slot i, column j at
+        // red[((q * units + i) * 64 + j) * 32 + lane].
+        const uint32_t e = warp - 2, quarter = warp & 3, half = e >> 2;
+        const uint32_t lane_base = (quarter * 32) << 16;
+        const uint32_t units = 8 / splits;
+        const uint32_t my_half = splits == 1 ? half : e & 1, my_quarter = splits == 1 ? quarter : part + (e >> 1) * splits;
+        const int32_t row0 = static_cast<int32_t>(tm * 128 + my_quarter * 32), col0 = static_cast<int32_t>(tn * 128 + my_half * 64);
+        uint8_t* boxes = smem + kTileEpi + e * kUnitBytes;
+        if (p.has_old && e < units && lane == 0) unit_prefetch(p, maps, boxes, &old_full[e], matrix, row0, col0);
+        __syncwarp();
+        float v[64];
+        if constexpr (kChunked) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) sum[j] = 0.0f;
+            for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+            const uint32_t n_chunks = chunk_count(p, kb0, kb1);
             for (uint32_t ch = 0; ch < n_chunks; ++ch) {
                 if (!mbar_wait_bounded(&acc_full[ch & 1], ch >> 1 & 1, abort_flag, kWaitLimitNs)) {
                     record_failure(kRoleEpilogue, abort_flag);
-                    ok = false;
                     break;
                 }
                 tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t r[16];
-                    tmem_ld_32x32b_x16(tmem + lane_base + (ch & 1) * 128 + half * 64 + c * 16, r);
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tmem + lane_base + (ch & 1) * 128 + half * 64 + c * 32, r);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(r[j]);
+                    for (int j = 0; j < 32; ++j) v[c * 32 + j] += __uint_as_float(r[j]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[ch & 1]);
             }
-            if (splits == 1) {
-                if (ok) {
+        } else {
+            if (!mbar_wait_bounded(&acc_full[0], 0, abort_flag, kWaitLimitNs)) record_failure(kRoleEpilogue, abort_flag);
+            tc_fence_after();
+            uint32_t r[64];
+            tmem_ld_32x32b_x32(tmem + lane_base + half * 64, reinterpret_cast<uint32_t(&)[32]>(r[0]));
+            tmem_ld_32x32b_x32(tmem + lane_base + half * 64 + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
+            tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float v[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = sum[c * 32 + j];
-                        ns_store(p, matrix, row, col0 + half * 64 + c * 32, mirror, v);
-                    }
-                }
-            } else {
-                cluster_sync();
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) send(half * 2 + c, j, sum[c * 32 + j]);
-            }
-        } else if (splits > 1) {
-            cluster_sync();
+            for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(r[j]);
         }
-    } else {
-        ok = mbar_wait_bounded(&acc_full[0], 0, abort_flag, kWaitLimitNs);
-        if (!ok) record_failure(kRoleEpilogue, abort_flag);
-        tc_fence_after();
         if (splits > 1) {
+            float* red = reinterpret_cast<float*>(smem);
             __syncwarp();
             cluster_sync();
-        }
-        if (warp >= 2 && ok) {
-            const int half = (warp - 2) >> 2;  // 64 columns
-#pragma unroll 1
-            for (int c = half * 2; c < half * 2 + 2; ++c) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tmem + lane_base + c * 32, r);
-                tmem_ld_wait();
-                if (splits == 1) {
-                    float v[32];
+            const uint32_t slot = half + 2 * (quarter / splits);
+            const uint32_t to = map_to_cta(smem_u32(red + (part * units + slot) * 2048 + lane), quarter % splits);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-                    ns_store(p, matrix, row, col0 + c * 32, mirror, v);
-                } else {
+            for (int j = 0; j < 64; ++j) st_shared_cluster_f32(to + j * 128, v[j]);
+            __syncwarp();
+            cluster_sync();
+            if (e < units) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) send(c, j, __uint_as_float(r[j]));
+                for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+                for (uint32_t q = 0; q < splits; ++q) {
+                    const float* src = red + (q * units + e) * 2048 + lane;
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) v[j] += src[j * 32];
                 }
             }
         }
-    }
-    if (splits > 1) {
+        if (e < units) {
+            ns_unit(p, maps, boxes, &old_full[e], 0, abort_flag, matrix, row0, col0, lane, p.sym && tm != tn, v);
+            if (lane == 0) bulk_wait_all();  // shared memory outlives the stores that read it
+        }
+    } else if (splits > 1) {
+        cluster_sync();
         __syncwarp();
         cluster_sync();
-        if (warp >= 2) {
-            // this CTA's blocks, a warp quarter's rows; each half of the warps takes every other block
-            const uint32_t per = 4 / splits;
-            for (uint32_t i = (warp - 2) >> 2; i < per; i += 2) {
-                float v[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                for (uint32_t q = 0; q < splits; ++q) {
-                    const float* src = red + ((q * per + i) * 32) * 128 + r_in;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] += src[j * 128];
-                }
-                ns_store(p, matrix, row, col0 + (i * splits + part) * 32, mirror, v);
-            }
-        }
     }
     tc_fence_before();
     __syncthreads();
@@ -451,13 +537,14 @@ __global__ void __launch_bounds__(kTileThreads, 2)
 
 // ---- the pair kernel: 256 x 256 on two CTAs, persistent --------------------------------
 
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
 constexpr uint32_t kPairStage = 2 * 128 * 128;  // each CTA's half of both operands
-constexpr uint32_t kPairBar = kPairStages * kPairStage;
-constexpr uint32_t kPairLaunch = kPairBar + (2 * kPairStages + 5) * 8 + 16 + 1024;
+constexpr uint32_t kPairEpi = kPairStages * kPairStage;
+constexpr uint32_t kPairBar = kPairEpi + 8 * kUnitBytes;
+constexpr uint32_t kPairLaunch = kPairBar + (2 * kPairStages + 5 + 8) * 8 + 16 + 1024;
 
-// Producer warp, MMA warp, 16 epilogue warps with 64 columns each.
-constexpr int kPairThreads = 576;
+// Producer warp, MMA warp, 8 epilogue warps with 128 columns (two units) each.
+constexpr int kPairThreads = 320;
 
 template <bool kChunked>
 __global__ void __launch_bounds__(kPairThreads, 1)
@@ -472,7 +559,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint64_t* acc_full = empty + kPairStages;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* old_full = drain + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -485,11 +573,14 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 32);  // one lane of each epilogue warp of both CTAs
+            mbar_init(&acc_empty[b], 16);  // one lane of each epilogue warp of both CTAs
         }
         mbar_init(drain, 1);
+        for (int w = 0; w < 8; ++w) mbar_init(&old_full[w], 1);
         *abort_flag = 0;
         fence_mbar_init();
+        tma_prefetch_desc(&maps.p_h);
+        tma_prefetch_desc(&maps.q_h);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
@@ -585,20 +676,32 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_wait_bounded(drain, 0, &never, kWaitLimitNs);
         }
     } else {
-        const int quarter = warp & 3, group = (warp - 2) >> 2;  // 64 columns
-        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-        uint32_t acc = 0, acc_phase = 0;
+        const uint32_t e = warp - 2, quarter = warp & 3, half = e >> 2;  // 128 columns
+        const uint32_t lane_base = (quarter * 32) << 16;
+        uint8_t* boxes = smem + kPairEpi + e * kUnitBytes;
+        uint32_t acc = 0, acc_phase = 0, old_phase = 0;
         bool ok = true;
+        // unit u (0, 1) of tile t
+        auto rows_of = [&](uint32_t tm) { return static_cast<int32_t>(tm * 256 + rank * 128 + quarter * 32); };
+        auto cols_of = [&](uint32_t tn, uint32_t u) { return static_cast<int32_t>(tn * 256 + half * 128 + u * 64); };
+        auto prefetch = [&](uint32_t t, uint32_t u) {
+            if (p.has_old && t < p.num_tiles && lane == 0) {
+                uint32_t matrix, tm, tn;
+                ns_tile(p, t, matrix, tm, tn);
+                bulk_wait_read<0>();  // the boxes' last stores
+                unit_prefetch(p, maps, boxes, &old_full[e], matrix, rows_of(tm), cols_of(tn, u));
+            }
+            __syncwarp();
+        };
+        prefetch(cluster_id, 0);
         for (uint32_t t = cluster_id; ok && t < p.num_tiles; t += n_clusters) {
             uint32_t matrix, tm, tn;
             ns_tile(p, t, matrix, tm, tn);
-            const int64_t row = static_cast<int64_t>(tm) * 256 + rank * 128 + quarter * 32 + lane;
-            const int64_t col0 = static_cast<int64_t>(tn) * 256;
             const bool mirror = p.sym && tm != tn;
+            float sum[kChunked ? 128 : 1];
             if constexpr (kChunked) {
-                float sum[64];
 #pragma unroll
-                for (int j = 0; j < 64; ++j) sum[j] = 0.0f;
+                for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
                 const uint32_t n_chunks = chunk_count(p, 0, total_kb);
                 for (uint32_t ch = 0; ch < n_chunks; ++ch) {
                     if (!mbar_wait_bounded<true>(&acc_full[acc], acc_phase, abort_flag, kWaitLimitNs)) {
@@ -609,47 +712,52 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t r[16];
-                        tmem_ld_32x32b_x16(tmem + lane_base + acc * 256 + group * 64 + c * 16, r);
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(tmem + lane_base + acc * 256 + half * 128 + c * 32, r);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) sum[c * 16 + j] += __uint_as_float(r[j]);
+                        for (int j = 0; j < 32; ++j) sum[c * 32 + j] += __uint_as_float(r[j]);
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
                     if (++acc == 2) { acc = 0; acc_phase ^= 1; }
                 }
-                if (!ok) break;
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float v[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = sum[c * 32 + j];
-                    ns_store(p, matrix, row, col0 + group * 64 + c * 32, mirror, v);
-                }
             } else {
                 if (!mbar_wait_bounded<true>(&acc_full[acc], acc_phase, abort_flag, kWaitLimitNs)) {
                     record_failure(kRoleEpilogue, abort_flag);
-                    break;
+                    ok = false;
                 }
                 tc_fence_after();
-#pragma unroll 1
-                for (int c = group * 2; c < group * 2 + 2; ++c) {
-                    uint32_t r[32];
-                    float v[32];
-                    tmem_ld_32x32b_x32(tmem + lane_base + acc * 256 + c * 32, r);
+            }
+            if (!ok) break;
+#pragma unroll
+            for (uint32_t u = 0; u < 2; ++u) {
+                float v[64];
+                if constexpr (kChunked) {
+#pragma unroll
+                    for (int j = 0; j < 64; ++j) v[j] = sum[u * 64 + j];
+                } else {
+                    uint32_t r[64];
+                    const uint32_t at = tmem + lane_base + acc * 256 + half * 128 + u * 64;
+                    tmem_ld_32x32b_x32(at, reinterpret_cast<uint32_t(&)[32]>(r[0]));
+                    tmem_ld_32x32b_x32(at + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-                    ns_store(p, matrix, row, col0 + c * 32, mirror, v);
+                    for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(r[j]);
+                    if (u == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
+                        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                    }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
-                if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                ns_unit(p, maps, boxes, &old_full[e], old_phase, abort_flag, matrix, rows_of(tm), cols_of(tn, u), lane, mirror, v);
+                old_phase ^= 1;
+                prefetch(u == 0 ? t : t + n_clusters, u ^ 1);
             }
         }
+        if (lane == 0) bulk_wait_all();  // shared memory outlives the stores that read it
     }
 
     tc_fence_before();
@@ -813,32 +921,6 @@ struct NsClusterParams {
     float coefficients[3 * 32];
 };
 
-// Byte offset of 16-byte piece `piece` (8 columns) of a row in a box of 64 columns x 128 rows.
-__device__ __forceinline__ uint32_t box_at(int row, int piece) {
-    return static_cast<uint32_t>(row) * 128u + (static_cast<uint32_t>(piece ^ (row & 7)) << 4);
-}
-// Eight values as hi and lo.
-__device__ __forceinline__ void split8(const float* v, uint4& hi, uint4& lo) {
-    uint32_t h[4], l[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        h[j] = pack2(v[2 * j], v[2 * j + 1]);
-        const float2 f = unpack2(h[j]);
-        l[j] = pack2(v[2 * j] - f.x, v[2 * j + 1] - f.y);
-    }
-    hi = make_uint4(h[0], h[1], h[2], h[3]);
-    lo = make_uint4(l[0], l[1], l[2], l[3]);
-}
-// x[0..7] <- c_old * (hi + lo) + c_acc * x
-__device__ __forceinline__ void blend8(float* x, const uint4& hi, const uint4& lo, float c_old, float c_acc) {
-    const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 a = unpack2(h[j]), b = unpack2(l[j]);
-        x[2 * j] = fmaf(c_old, a.x + b.x, c_acc * x[2 * j]);
-        x[2 * j + 1] = fmaf(c_old, a.y + b.y, c_acc * x[2 * j + 1]);
-    }
-}
 template <typename T>
 __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsClusterParams c, NsParams p) {
     extern __shared__ uint8_t smem_raw[];
@@ -1162,6 +1244,25 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
+// batch matrices of rows x cols values, boxes of box_cols x box_rows of one of
+// them: 128-byte rows swizzled, narrower ones not.
+cudaError_t value_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld,
+                      int64_t stride, uint32_t box_cols, uint32_t box_rows, bool swizzle) {
+    auto fn = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t es = type == DGA_F32 ? 4 : 2;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
+    // a single matrix has no stride to speak of: any multiple of 16 bytes
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * es, batch > 1 ? static_cast<cuuint64_t>(stride) * es : static_cast<cuuint64_t>(ld) * es};
+    cuuint32_t box[3] = {box_cols, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, type == DGA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
+                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // rows x ld fp16, boxes of 64 columns (one 128-byte row) x box_rows
 cudaError_t half_map(CUtensorMap* map, const __half* base, int64_t rows, int64_t ld, uint32_t box_rows) {
     auto fn = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
@@ -1202,7 +1303,8 @@ NsPlan plan_of(int out_dtype, int64_t batch, int64_t rows, int64_t cols) {
 }
 
 template <typename... P, typename... A>
-cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, unsigned cluster, int smem, bool pdl, cudaStream_t s, A... args) {
+cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, unsigned cluster, int smem, bool pdl, cudaStream_t s,
+                   const A&... args) {
     if (smem > 0) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
@@ -1231,7 +1333,7 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, unsigned cluster,
 
 // One product: pair kernel where its tiles can occupy most of the machine's
 // CTA pairs, else the tile kernel with K in as many parts as there are idle
-// CTA slots.
+// SMs, each at least 16 K blocks (2 us: joining the parts takes as long).
 cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_t rows, int64_t cols,
                            const DeviceInfo& dev, cudaStream_t s) {
     auto tiles = [&](int64_t size) {
@@ -1251,7 +1353,7 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
                       static_cast<int>(kPairLaunch), true, s, maps, p);
     const int64_t small = tiles(128);
     uint32_t splits = 1;
-    while (splits < 4 && small * splits * 2 <= 2 * dev.sm_count && p.num_kb * p.segs >= splits * 4) splits *= 2;
+    while (splits < 4 && small * splits * 2 <= dev.sm_count && p.num_kb * p.segs >= splits * 32) splits *= 2;
     return launch(chunked ? ns_tile_kernel<true> : ns_tile_kernel<false>, dim3(static_cast<unsigned>(small * splits)),
                   kTileThreads, splits, static_cast<int>(kTileLaunch), true, s, maps, p, splits);
 }
@@ -1387,7 +1489,6 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
     NsParams base{};
     base.segs = pl.split ? 3 : 1;
     base.p_rows = base.q_rows = static_cast<uint32_t>(pl.mp);
-    base.rows = pl.mp;
     base.m = pl.m;
     base.n = pl.n;
     base.result = a.O;
@@ -1395,6 +1496,7 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
     base.transposed = pl.transposed;
     const int64_t per16 = a.out_dtype == DGA_F32 ? 4 : 8;
     base.result_vec = aligned(a.O, 16) && a.ldo % per16 == 0 && (a.batch == 1 || a.stride_o % per16 == 0);
+    base.result_tma = base.result_vec;
     base.ldo = a.ldo;
     base.stride_o = a.stride_o;
     bool done = false;
@@ -1411,62 +1513,91 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
     if (e != cudaSuccess) return e;
     *launches += 2;
 
-    // maps: rows of 64-column boxes; 128-row boxes serve K-major operands, 64-row ones the MN-major X
+    // operand maps (128-row boxes K-major, 64-row ones the MN-major X) and value maps
     const int64_t all_rows = a.batch * pl.mp;
-    CUtensorMap x_h[2], x_l[2], xk_h[2], xk_l[2], ma_h, ma_l, mb_h, mb_l;
-    for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
-        e = half_map(&x_h[i], xh[i], all_rows, pl.np, 128);
-        if (e == cudaSuccess) e = half_map(&x_l[i], xl[i], all_rows, pl.np, 128);
-        if (e == cudaSuccess) e = half_map(&xk_h[i], xh[i], all_rows, pl.np, 64);
-        if (e == cudaSuccess) e = half_map(&xk_l[i], xl[i], all_rows, pl.np, 64);
+    struct Maps {
+        CUtensorMap op, mn, value, mirror;
+    } mx_h[2], mx_l[2], ma_h, ma_l, mb_h, mb_l;
+    auto make = [&](Maps* m, const __half* base, int64_t ld, bool square) {
+        if (e == cudaSuccess) e = half_map(&m->op, base, all_rows, ld, 128);
+        if (e == cudaSuccess) e = value_map(&m->value, DGA_F16, base, ld, pl.mp, a.batch, ld, pl.mp * ld, 64, 32, true);
+        if (e == cudaSuccess && square) e = value_map(&m->mirror, DGA_F16, base, ld, pl.mp, a.batch, ld, pl.mp * ld, 32, 64, false);
+        if (e == cudaSuccess && !square) e = half_map(&m->mn, base, all_rows, ld, 64);
+    };
+    for (int i = 0; i < 2; ++i) {
+        make(&mx_h[i], xh[i], pl.np, false);
+        make(&mx_l[i], xl[i], pl.np, false);
     }
-    if (e == cudaSuccess) e = half_map(&ma_h, ah, all_rows, pl.mp, 128);
-    if (e == cudaSuccess) e = half_map(&mb_h, bh, all_rows, pl.mp, 128);
-    if (e == cudaSuccess && pl.split) e = half_map(&ma_l, al, all_rows, pl.mp, 128);
-    if (e == cudaSuccess && pl.split) e = half_map(&mb_l, bl, all_rows, pl.mp, 128);
-    if (e != cudaSuccess) return e;
-    if (!pl.split) {
+    make(&ma_h, ah, pl.mp, true);
+    make(&mb_h, bh, pl.mp, true);
+    if (pl.split) {
+        make(&ma_l, al, pl.mp, true);
+        make(&mb_l, bl, pl.mp, true);
+    } else {
         ma_l = ma_h;
         mb_l = mb_h;
     }
+    CUtensorMap result = ma_h.value;  // not used without result_tma
+    if (base.result_tma && e == cudaSuccess) {
+        const uint32_t box_cols = a.out_dtype == DGA_F32 ? 32 : 64;
+        e = pl.transposed ? value_map(&result, a.out_dtype, a.O, a.cols, a.rows, a.batch, a.ldo, a.stride_o, 32, 64, false)
+                          : value_map(&result, a.out_dtype, a.O, a.cols, a.rows, a.batch, a.ldo, a.stride_o, box_cols, 32, true);
+    }
+    if (e != cudaSuccess) return e;
 
     for (int step = 0; step < a.steps; ++step) {
         const float ca = a.coefficients[3 * step], cb = a.coefficients[3 * step + 1], cc = a.coefficients[3 * step + 2];
         const int now = step & 1, next = now ^ 1;
         NsParams p = base;
         p.sym = 1;
-        p.ld = pl.mp;
-        p.stride = pl.mp * pl.mp;
+        p.rows = p.ld = static_cast<int32_t>(pl.mp);
+        p.out_lo = pl.split;
+        NsMaps m;
         // A = X X^T
         p.num_kb = static_cast<uint32_t>(pl.np / 64);
         p.c_acc = 1.0f / kScale;
-        p.out_h = ah;
-        p.out_l = al;
-        e = launch_product(p, NsMaps{x_h[now], x_l[now], x_h[now], x_l[now]}, a.batch, pl.mp, pl.mp, dev, a.stream);
+        m.p_h = m.q_h = mx_h[now].op;
+        m.p_l = m.q_l = mx_l[now].op;
+        m.old_h = m.old_l = ma_h.value;  // not used
+        m.out_h = ma_h.value;
+        m.out_l = ma_l.value;
+        m.mirror_h = ma_h.mirror;
+        m.mirror_l = ma_l.mirror;
+        m.result = result;
+        e = launch_product(p, m, a.batch, pl.mp, pl.mp, dev, a.stream);
         if (e != cudaSuccess) return e;
         // B = b A + c A^2
         p.num_kb = static_cast<uint32_t>(pl.mp / 64);
         p.c_old = cb;
         p.c_acc = cc / kScale;
-        p.old_h = ah;
-        p.old_l = al;
-        p.out_h = bh;
-        p.out_l = bl;
-        e = launch_product(p, NsMaps{ma_h, ma_l, ma_h, ma_l}, a.batch, pl.mp, pl.mp, dev, a.stream);
+        p.has_old = 1;
+        p.old_lo = pl.split;
+        m.p_h = m.q_h = ma_h.op;
+        m.p_l = m.q_l = ma_l.op;
+        m.old_l = ma_l.value;
+        m.out_h = mb_h.value;
+        m.out_l = mb_l.value;
+        m.mirror_h = mb_h.mirror;
+        m.mirror_l = mb_l.mirror;
+        e = launch_product(p, m, a.batch, pl.mp, pl.mp, dev, a.stream);
         if (e != cudaSuccess) return e;
         // X <- a X + B X
-        const bool last = step + 1 == a.steps;
+        p.last = step + 1 == a.steps;
         p.sym = 0;
         p.q_mn = 1;
-        p.ld = pl.np;
-        p.stride = pl.mp * pl.np;
-        p.c_old = last ? ca / kScale : ca;
-        p.c_acc = last ? 1.0f / (kScale * kScale) : 1.0f / kScale;
-        p.old_h = xh[now];
-        p.old_l = xl[now];
-        p.out_h = last ? nullptr : xh[next];
-        p.out_l = last ? nullptr : xl[next];
-        e = launch_product(p, NsMaps{mb_h, mb_l, xk_h[now], xk_l[now]}, a.batch, pl.mp, pl.np, dev, a.stream);
+        p.ld = static_cast<int32_t>(pl.np);
+        p.c_old = p.last ? ca / kScale : ca;
+        p.c_acc = p.last ? 1.0f / (kScale * kScale) : 1.0f / kScale;
+        p.old_lo = p.out_lo = 1;
+        m.p_h = mb_h.op;
+        m.p_l = mb_l.op;
+        m.q_h = mx_h[now].mn;
+        m.q_l = mx_l[now].mn;
+        m.old_h = mx_h[now].value;
+        m.old_l = mx_l[now].value;
+        m.out_h = mx_h[next].value;
+        m.out_l = mx_l[next].value;
+        e = launch_product(p, m, a.batch, pl.mp, pl.np, dev, a.stream);
         if (e != cudaSuccess) return e;
         *launches += 3;
     }
