@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
             }
         }
-        if (lane == 0) bulk_wait_all();  // shared memory outlives the stores that read it
+        if (lane == 0) bulk_wait_read<0>();  // shared memory outlives the stores that read it
     }
 
     tc_fence_before();

@@ -28,8 +28,8 @@
 //     unit of the sum lost per MMA on average (2.2e-5 off the result at K =
 //     4099 x 3), so the hi hi products are accumulated in chunks of 128 values
 //     of K, added up in registers with rounding: as exact as fp32 products of
-//     the same formula.  The cross products, 2^-11 of the sum, come first and
-//     make one chunk.
+//     the same formula.  The cross products, 2^-11 of the sum, have an
+//     accumulator of their own.
 //
 // Two product kernels share one epilogue, value = c_old * old + c_acc * sum,
 // stored as hi (and lo), at its mirror place too for the symmetric products,
@@ -59,14 +59,15 @@ namespace {
 constexpr uint64_t kWaitLimitNs = 4000000000ull;  // 4 s
 constexpr float kScale = 4096.0f;                 // stored = kScale * value
 constexpr int kSmallRows = 256;
-constexpr uint32_t kChunk = 2;  // K blocks of one chunk of the hi hi product where sums are chunked
+constexpr uint32_t kChunk = 2;  // K blocks of one chunk of the hi hi product where operands are split
 constexpr uint32_t kBoxBytes = 64 * 64 * 2;  // an MN-major box: 64 columns x 64 k
 enum : int { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3 };
 
 struct NsParams {
     // tiles: of each matrix, all tiles_m x tiles_n or, sym, those with tm <= tn
     uint32_t tiles_m, tiles_n, sym, per_matrix, num_tiles;
-    uint32_t num_kb, segs;  // K blocks of 64; 1 product (hi hi), or 3 (hi lo, lo hi, hi hi)
+    uint32_t num_kb;        // K blocks of 64
+    uint32_t split;         // hi hi + hi lo + lo hi, else hi hi alone
     uint32_t q_mn;          // the second operand is read MN-major (rows along K)
     uint32_t p_rows, q_rows;  // rows of one matrix in each operand's map
     int32_t rows, ld;         // padded rows and columns of the value
@@ -315,31 +316,25 @@ __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, u
     }
 }
 
-// Chunked sums: whether K block kb (of the three segments in a row) begins a
-// chunk of the range that starts at kb0, and how many chunks kb0 .. kb1 has.
-__device__ __forceinline__ bool chunk_begins(const NsParams& p, uint32_t kb, uint32_t kb0) {
-    return kb == kb0 || (kb >= 2 * p.num_kb && (kb - 2 * p.num_kb) % kChunk == 0);
-}
-__device__ __forceinline__ uint32_t chunk_count(const NsParams& p, uint32_t kb0, uint32_t kb1) {
-    const uint32_t lo = 2 * p.num_kb, h0 = max(kb0, lo) - lo;
-    uint32_t n = kb0 < lo ? 1 : 0;
-    if (kb1 > lo) n += (kb1 - lo - 1) / kChunk - h0 / kChunk + 1;
-    return n;
-}
-
 // ---- the tile kernel: 128 x 128, K parts in a cluster ---------------------------------
 
-constexpr int kTileStages = 4;
+// A ring slot holds the P and the Q box of a K block; split operands take two
+// slots for it, the hi boxes and the lo boxes (each loaded once for the three
+// products).  A CTA takes in 46 to 60 bytes a clock, which bounds these tiles:
+// 512 clocks or more for a slot, whose MMAs take 256.
+constexpr int kTileStages = 5;
 constexpr uint32_t kTileStage = 2 * 128 * 128;
 constexpr uint32_t kTileEpi = kTileStages * kTileStage;
 constexpr uint32_t kTileBar = kTileEpi + 8 * kUnitBytes;
-constexpr uint32_t kTileLaunch = kTileBar + (2 * kTileStages + 4 + 8) * 8 + 16 + 1024;
-static_assert(kTileEpi >= 128 * 128 * 4, "the partial sums fit the ring");
+// full[S], empty[S], acc_full[2], acc_empty[2], joined, old_full[8], then tmem slot + abort flag
+constexpr uint32_t kTileLaunch = kTileBar + (2 * kTileStages + 5 + 8) * 8 + 16 + 1024;
+constexpr uint32_t kUnitSums = 64 * 32 * 4;  // a unit's sums
+static_assert(kTileEpi >= 2 * 8 * kUnitSums, "the parts' sums fit the ring twice");
 
 // Producer warp, MMA warp, 8 epilogue warps with a unit of the tile each.
 constexpr int kTileThreads = 320;
 
-template <bool kChunked>
+template <bool kSplit>
 __global__ void __launch_bounds__(kTileThreads, 1)
     ns_tile_kernel(const __grid_constant__ NsMaps maps, NsParams p, uint32_t splits) {
     constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 128, 128);
@@ -350,15 +345,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint64_t* empty = full + kTileStages;
     uint64_t* acc_full = empty + kTileStages;
     uint64_t* acc_empty = acc_full + 2;
-    uint64_t* old_full = acc_empty + 2;
+    uint64_t* joined = acc_empty + 2;
+    uint64_t* old_full = joined + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + 8);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    constexpr uint32_t kCols = kChunked ? 256 : 128;  // two accumulators, or one
+    // accumulators: one, or the cross products' and two for the chunks in turn
+    constexpr uint32_t kCols = kSplit ? 512 : 128;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t t = blockIdx.x / splits, part = blockIdx.x % splits;
-    // this part's K blocks, of all segments in a row
-    const uint32_t total_kb = p.num_kb * p.segs;
-    const uint32_t kb0 = part * total_kb / splits, kb1 = (part + 1) * total_kb / splits;
+    const uint32_t kb0 = part * p.num_kb / splits, kb1 = (part + 1) * p.num_kb / splits;
+    const uint32_t units = 8 / splits;  // of the tile's 8, what this CTA joins and stores
     uint32_t matrix, tm, tn;
     ns_tile(p, t, matrix, tm, tn);
 
@@ -372,8 +368,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             mbar_init(&acc_empty[b], 8);
         }
         for (int w = 0; w < 8; ++w) mbar_init(&old_full[w], 1);
+        mbar_init(joined, 1);
         *abort_flag = 0;
         fence_mbar_init();
+        if (splits > 1) mbar_arrive_expect_tx(joined, splits * units * kUnitSums);
         tma_prefetch_desc(&maps.p_h);
         tma_prefetch_desc(&maps.q_h);
     }
@@ -392,7 +390,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (lane == 0) {
             uint32_t stage = 0, phase = 0;
             const int32_t p_row = static_cast<int32_t>(matrix * p.p_rows + tm * 128);
-            for (uint32_t kb = kb0; kb < kb1; ++kb) {
+            const uint32_t per = kSplit ? 2 : 1;  // slots of a K block
+            for (uint32_t i = kb0 * per; i < kb1 * per; ++i) {
                 if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
                     record_failure(kRoleProducer, abort_flag);
                     __nanosleep(20000);  // let copies already issued land
@@ -400,10 +399,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 }
                 uint8_t* dst = smem + stage * kTileStage;
                 mbar_arrive_expect_tx(&full[stage], kTileStage);
-                const uint32_t seg = kb / p.num_kb + (kChunked ? 0 : 2);
-                const int32_t k = static_cast<int32_t>((kChunked ? kb - seg * p.num_kb : kb) * 64);
-                tma_load_2d(dst, seg == 1 ? &maps.p_l : &maps.p_h, &full[stage], k, p_row);
-                const CUtensorMap* q = seg == 0 ? &maps.q_l : &maps.q_h;
+                const bool lo = kSplit && (i & 1);
+                const int32_t k = static_cast<int32_t>((kSplit ? i >> 1 : i) * 64);
+                tma_load_2d(dst, lo ? &maps.p_l : &maps.p_h, &full[stage], k, p_row);
+                const CUtensorMap* q = lo ? &maps.q_l : &maps.q_h;
                 if (p.q_mn) {
                     const int32_t row = static_cast<int32_t>(matrix * p.q_rows) + k;
                     tma_load_2d(dst + 128 * 128, q, &full[stage], static_cast<int32_t>(tn * 128), row);
@@ -419,112 +418,133 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             uint32_t stage = 0, phase = 0, chunk = 0;
             const uint32_t idesc = idesc_major(kIdesc, 0, p.q_mn);
             const uint32_t q_step = p.q_mn ? (16 * 128) >> 4 : 32 >> 4;
-            for (uint32_t kb = kb0; kb < kb1; ++kb) {
-                const bool first = kChunked ? chunk_begins(p, kb, kb0) : kb == kb0;
-                if (kChunked && first && !mbar_wait_bounded(&acc_empty[chunk & 1], (chunk >> 1 & 1) ^ 1, abort_flag, kWaitLimitNs)) {
-                    record_failure(kRoleMma, abort_flag);
-                    break;
-                }
-                if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs)) {
-                    record_failure(kRoleMma, abort_flag);
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t addr = smem_u32(smem + stage * kTileStage);
-                const uint64_t pd = smem_desc_kmajor_sw128(addr);
-                const uint64_t qd = p.q_mn ? smem_desc_mnmajor_sw128(addr + 128 * 128, kBoxBytes)
-                                           : smem_desc_kmajor_sw128(addr + 128 * 128);
-                const uint32_t d = tmem + (kChunked ? (chunk & 1) * 128 : 0);
+            auto mma = [&](uint32_t acc, uint32_t ps, uint32_t qs, bool fresh) {
+                const uint32_t pa = smem_u32(smem + ps * kTileStage), qa = smem_u32(smem + qs * kTileStage) + 128 * 128;
+                const uint64_t pd = smem_desc_kmajor_sw128(pa);
+                const uint64_t qd = p.q_mn ? smem_desc_mnmajor_sw128(qa, kBoxBytes) : smem_desc_kmajor_sw128(qa);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    tc_mma<kFmtF16>(d, pd + 2 * k, qd + q_step * k, idesc, (!first || k > 0) ? 1u : 0u);
-                tc_commit(&empty[stage]);
+                    tc_mma<kFmtF16>(tmem + acc, pd + 2 * k, qd + q_step * k, idesc, (fresh && k == 0) ? 0u : 1u);
+            };
+            auto next_full = [&](uint32_t& slot) {
+                slot = stage;
+                const bool ok = mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs);
                 if (++stage == kTileStages) { stage = 0; phase ^= 1; }
-                if (kChunked && (kb + 1 == kb1 || chunk_begins(p, kb + 1, kb0))) {
-                    tc_commit(&acc_full[chunk & 1]);
-                    ++chunk;
+                return ok;
+            };
+            for (uint32_t kb = kb0; kb < kb1; ++kb) {
+                uint32_t hi = 0, lo = 0;
+                if constexpr (kSplit) {
+                    const bool begins = (kb - kb0) % kChunk == 0;
+                    if (!next_full(hi) || !next_full(lo) ||
+                        (begins && !mbar_wait_bounded(&acc_empty[chunk & 1], (chunk >> 1 & 1) ^ 1, abort_flag, kWaitLimitNs))) {
+                        record_failure(kRoleMma, abort_flag);
+                        break;
+                    }
+                    tc_fence_after();
+                    mma(0, hi, lo, kb == kb0);
+                    mma(0, lo, hi, false);
+                    mma(128 + (chunk & 1) * 128, hi, hi, begins);
+                    tc_commit(&empty[hi]);
+                    tc_commit(&empty[lo]);
+                    if ((kb - kb0) % kChunk == kChunk - 1 || kb + 1 == kb1) {
+                        tc_commit(&acc_full[chunk & 1]);
+                        ++chunk;
+                    }
+                } else {
+                    if (!next_full(hi)) {
+                        record_failure(kRoleMma, abort_flag);
+                        break;
+                    }
+                    tc_fence_after();
+                    mma(0, hi, hi, kb == kb0);
+                    tc_commit(&empty[hi]);
                 }
             }
-            if (!kChunked) tc_commit(&acc_full[0]);
+            if (!kSplit) tc_commit(&acc_full[0]);
         }
     }
     __syncwarp();
     if (warp >= 2) {
         // Unit (quarter, half): 32 rows, 64 columns.  With K in parts, CTA c
         // joins the quarters q % splits == c, `units` of them; slot i there is
-        // half i % 2 of quarter c + i / 2 * splits, and warp 2 + i's.  Each CTA
-        // sends its sums to the joining ones (stores, which nothing waits for)
-        // once every CTA's ring is done with: share q's slot i, column j at
-        // red[((q * units + i) * 64 + j) * 32 + lane].
+        // half i % 2 of quarter c + i / 2 * splits, and warp 2 + i's.  Once
+        // every CTA's ring is done with, each sends its sums by bulk copies
+        // from the ring's first half to the second halves of the joining CTAs,
+        // which add them up in the parts' order.
         const uint32_t e = warp - 2, quarter = warp & 3, half = e >> 2;
         const uint32_t lane_base = (quarter * 32) << 16;
-        const uint32_t units = 8 / splits;
         const uint32_t my_half = splits == 1 ? half : e & 1, my_quarter = splits == 1 ? quarter : part + (e >> 1) * splits;
         const int32_t row0 = static_cast<int32_t>(tm * 128 + my_quarter * 32), col0 = static_cast<int32_t>(tn * 128 + my_half * 64);
         uint8_t* boxes = smem + kTileEpi + e * kUnitBytes;
         if (p.has_old && e < units && lane == 0) unit_prefetch(p, maps, boxes, &old_full[e], matrix, row0, col0);
         __syncwarp();
         float v[64];
-        if constexpr (kChunked) {
+        auto add = [&](uint32_t column) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] = 0.0f;
-            const uint32_t n_chunks = chunk_count(p, kb0, kb1);
-            for (uint32_t ch = 0; ch < n_chunks; ++ch) {
-                if (!mbar_wait_bounded(&acc_full[ch & 1], ch >> 1 & 1, abort_flag, kWaitLimitNs)) {
-                    record_failure(kRoleEpilogue, abort_flag);
-                    break;
-                }
-                tc_fence_after();
+            for (int c = 0; c < 2; ++c) {
+                uint32_t r[32];
+                tmem_ld_32x32b_x32(tmem + lane_base + column + half * 64 + c * 32, r);
+                tmem_ld_wait();
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t r[32];
-                    tmem_ld_32x32b_x32(tmem + lane_base + (ch & 1) * 128 + half * 64 + c * 32, r);
-                    tmem_ld_wait();
+                for (int j = 0; j < 32; ++j) v[c * 32 + j] += __uint_as_float(r[j]);
+            }
+        };
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[c * 32 + j] += __uint_as_float(r[j]);
-                }
+        for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+        const uint32_t n_chunks = kSplit ? (kb1 - kb0 + kChunk - 1) / kChunk : 1;
+        for (uint32_t ch = 0; ch < n_chunks; ++ch) {
+            if (!mbar_wait_bounded(&acc_full[ch & 1], ch >> 1 & 1, abort_flag, kWaitLimitNs)) {
+                record_failure(kRoleEpilogue, abort_flag);
+                break;
+            }
+            tc_fence_after();
+            if constexpr (kSplit) {
+                add(128 + (ch & 1) * 128);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[ch & 1]);
             }
-        } else {
-            if (!mbar_wait_bounded(&acc_full[0], 0, abort_flag, kWaitLimitNs)) record_failure(kRoleEpilogue, abort_flag);
-            tc_fence_after();
-            uint32_t r[64];
-            tmem_ld_32x32b_x32(tmem + lane_base + half * 64, reinterpret_cast<uint32_t(&)[32]>(r[0]));
-            tmem_ld_32x32b_x32(tmem + lane_base + half * 64 + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(r[j]);
         }
+        add(0);
         if (splits > 1) {
-            float* red = reinterpret_cast<float*>(smem);
-            __syncwarp();
-            cluster_sync();
-            const uint32_t slot = half + 2 * (quarter / splits);
-            const uint32_t to = map_to_cta(smem_u32(red + (part * units + slot) * 2048 + lane), quarter % splits);
+            uint8_t* sent = smem + e * kUnitSums;
 #pragma unroll
-            for (int j = 0; j < 64; ++j) st_shared_cluster_f32(to + j * 128, v[j]);
+            for (int j = 0; j < 64; ++j) reinterpret_cast<float*>(sent)[j * 32 + lane] = v[j];
+            fence_async_shared();
             __syncwarp();
-            cluster_sync();
+            cluster_arrive_relaxed();
+            cluster_wait();
+            if (lane == 0) {
+                const uint32_t slot = half + 2 * (quarter / splits), to = quarter % splits;
+                const uint32_t at = smem_u32(smem + (8 + part * units + slot) * kUnitSums);
+                bulk_copy_to_cta(map_to_cta(at, to), smem_u32(sent), kUnitSums, map_to_cta(smem_u32(joined), to));
+            }
+            __syncwarp();
             if (e < units) {
+                if (!mbar_wait_bounded<true>(joined, 0, abort_flag, kWaitLimitNs)) record_failure(kRoleEpilogue, abort_flag);
 #pragma unroll
                 for (int j = 0; j < 64; ++j) v[j] = 0.0f;
                 for (uint32_t q = 0; q < splits; ++q) {
-                    const float* src = red + (q * units + e) * 2048 + lane;
+                    const float* src = reinterpret_cast<const float*>(smem + (8 + q * units + e) * kUnitSums) + lane;
 #pragma unroll
                     for (int j = 0; j < 64; ++j) v[j] += src[j * 32];
                 }
             }
+            __syncwarp();
+            cluster_arrive_relaxed();  // what was sent here has arrived
         }
         if (e < units) {
             ns_unit(p, maps, boxes, &old_full[e], 0, abort_flag, matrix, row0, col0, lane, p.sym && tm != tn, v);
-            if (lane == 0) bulk_wait_all();  // shared memory outlives the stores that read it
+            if (lane == 0) bulk_wait_read<0>();  // shared memory outlives the stores that read it
         }
-    } else if (splits > 1) {
-        cluster_sync();
         __syncwarp();
-        cluster_sync();
+        if (splits > 1) cluster_wait();  // and what this CTA sent, at the others
+    } else if (splits > 1) {
+        cluster_arrive_relaxed();
+        cluster_wait();
+        cluster_arrive_relaxed();
+        cluster_wait();
     }
     tc_fence_before();
     __syncthreads();
@@ -546,7 +566,7 @@ constexpr uint32_t kPairLaunch = kPairBar + (2 * kPairStages + 5 + 8) * 8 + 16 +
 // Producer warp, MMA warp, 8 epilogue warps with 128 columns (two units) each.
 constexpr int kPairThreads = 320;
 
-template <bool kChunked>
+template <bool kSplit>
 __global__ void __launch_bounds__(kPairThreads, 1)
     ns_pair_kernel(const __grid_constant__ NsMaps maps, NsParams p) {
     constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 256, 256);
@@ -595,7 +615,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t cluster_id = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
-    const uint32_t total_kb = p.num_kb * p.segs;
+    // accumulators of 256 columns: two in turn, or the cross products' and the chunks'
 
     if (warp == 0) {
         if (lane == 0) {
@@ -607,8 +627,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const int32_t p_row = static_cast<int32_t>(matrix * p.p_rows + tm * 256 + rank * 128);
                 const int32_t q_at = static_cast<int32_t>(tn * 256 + rank * 128);
                 const int32_t q_row = static_cast<int32_t>(matrix * p.q_rows);
-                uint32_t seg = kChunked ? 0 : 2, k = 0;
-                for (uint32_t kb = 0; kb < total_kb; ++kb) {
+                const uint32_t per = kSplit ? 2 : 1;  // slots of a K block: the hi boxes, the lo boxes
+                for (uint32_t i = 0; i < p.num_kb * per; ++i) {
                     if (!mbar_wait_bounded<true>(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
                         record_failure(kRoleProducer, abort_flag);
                         ok = false;
@@ -617,16 +637,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     uint8_t* dst = smem + stage * kPairStage;
                     if (leader) mbar_arrive_expect_tx(&full[stage], 2 * kPairStage);
                     const uint32_t bar = map_to_cta(smem_u32(&full[stage]), 0);
-                    tma_load_2d_pair(dst, seg == 1 ? &maps.p_l : &maps.p_h, bar, static_cast<int32_t>(k * 64), p_row);
-                    const CUtensorMap* q = seg == 0 ? &maps.q_l : &maps.q_h;
+                    const bool lo = kSplit && (i & 1);
+                    const int32_t k = static_cast<int32_t>((kSplit ? i >> 1 : i) * 64);
+                    tma_load_2d_pair(dst, lo ? &maps.p_l : &maps.p_h, bar, k, p_row);
+                    const CUtensorMap* q = lo ? &maps.q_l : &maps.q_h;
                     if (p.q_mn) {
-                        const int32_t row = q_row + static_cast<int32_t>(k * 64);
-                        tma_load_2d_pair(dst + 128 * 128, q, bar, q_at, row);
-                        tma_load_2d_pair(dst + 128 * 128 + kBoxBytes, q, bar, q_at + 64, row);
+                        tma_load_2d_pair(dst + 128 * 128, q, bar, q_at, q_row + k);
+                        tma_load_2d_pair(dst + 128 * 128 + kBoxBytes, q, bar, q_at + 64, q_row + k);
                     } else {
-                        tma_load_2d_pair(dst + 128 * 128, q, bar, static_cast<int32_t>(k * 64), q_row + q_at);
+                        tma_load_2d_pair(dst + 128 * 128, q, bar, k, q_row + q_at);
                     }
-                    if (++k == p.num_kb) { k = 0; ++seg; }
                     if (++stage == kPairStages) { stage = 0; phase ^= 1; }
                 }
             }
@@ -637,40 +657,60 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
             const uint32_t idesc = idesc_major(kIdesc, 0, p.q_mn);
             const uint32_t q_step = p.q_mn ? (16 * 128) >> 4 : 32 >> 4;
+            auto mma = [&](uint32_t d, uint32_t ps, uint32_t qs, bool fresh) {
+                const uint32_t pa = smem_u32(smem + ps * kPairStage), qa = smem_u32(smem + qs * kPairStage) + 128 * 128;
+                const uint64_t pd = smem_desc_kmajor_sw128(pa);
+                const uint64_t qd = p.q_mn ? smem_desc_mnmajor_sw128(qa, kBoxBytes) : smem_desc_kmajor_sw128(qa);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    tc_mma_pair<kFmtF16>(tmem + d, pd + 2 * k, qd + q_step * k, idesc, (fresh && k == 0) ? 0u : 1u);
+            };
+            auto next_full = [&](uint32_t& slot) {
+                slot = stage;
+                const bool done = mbar_wait_bounded<true>(&full[stage], phase, abort_flag, kWaitLimitNs);
+                if (++stage == kPairStages) { stage = 0; phase ^= 1; }
+                return done;
+            };
+            auto acc_ready = [&]() { return mbar_wait_bounded<true>(&acc_empty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs); };
             bool ok = true;
             for (uint32_t t = cluster_id; ok && t < p.num_tiles; t += n_clusters) {
-                uint32_t d = 0;
-                for (uint32_t kb = 0; kb < total_kb; ++kb) {
-                    const bool first = kChunked ? chunk_begins(p, kb, 0) : kb == 0;
-                    if (first) {
-                        if (!mbar_wait_bounded<true>(&acc_empty[acc], acc_phase ^ 1, abort_flag, kWaitLimitNs)) {
-                            record_failure(kRoleMma, abort_flag);
-                            ok = false;
-                            break;
+                for (uint32_t kb = 0; ok && kb < p.num_kb; ++kb) {
+                    uint32_t hi = 0, lo = 0;
+                    if constexpr (kSplit) {
+                        // the chunks' accumulator is read while the next chunk's
+                        // first cross products run; both are free at a tile's start
+                        const bool begins = kb % kChunk == 0;
+                        ok = next_full(hi) && next_full(lo) && (kb > 0 || acc_ready());
+                        if (!ok) break;
+                        tc_fence_after();
+                        mma(0, hi, lo, kb == 0);
+                        mma(0, lo, hi, false);
+                        if (begins && kb > 0) {
+                            ok = acc_ready();
+                            if (!ok) break;
+                            tc_fence_after();
                         }
-                        d = tmem + acc * 256;
-                    }
-                    if (!mbar_wait_bounded<true>(&full[stage], phase, abort_flag, kWaitLimitNs)) {
-                        record_failure(kRoleMma, abort_flag);
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t addr = smem_u32(smem + stage * kPairStage);
-                    const uint64_t pd = smem_desc_kmajor_sw128(addr);
-                    const uint64_t qd = p.q_mn ? smem_desc_mnmajor_sw128(addr + 128 * 128, kBoxBytes)
-                                               : smem_desc_kmajor_sw128(addr + 128 * 128);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        tc_mma_pair<kFmtF16>(d, pd + 2 * k, qd + q_step * k, idesc, (!first || k > 0) ? 1u : 0u);
-                    tc_commit_pair_multicast(&empty[stage], kBothCtas);
-                    if (++stage == kPairStages) { stage = 0; phase ^= 1; }
-                    if (kb + 1 == total_kb || (kChunked && chunk_begins(p, kb + 1, 0))) {
-                        tc_commit_pair_multicast(&acc_full[acc], kBothCtas);
-                        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                        mma(256, hi, hi, begins);
+                        tc_commit_pair_multicast(&empty[hi], kBothCtas);
+                        tc_commit_pair_multicast(&empty[lo], kBothCtas);
+                        if (kb % kChunk == kChunk - 1 || kb + 1 == p.num_kb) {
+                            tc_commit_pair_multicast(&acc_full[0], kBothCtas);
+                            acc_phase ^= 1;
+                        }
+                    } else {
+                        ok = (kb > 0 || acc_ready()) && next_full(hi);
+                        if (!ok) break;
+                        tc_fence_after();
+                        mma(acc * 256, hi, hi, kb == 0);
+                        tc_commit_pair_multicast(&empty[hi], kBothCtas);
+                        if (kb + 1 == p.num_kb) {
+                            tc_commit_pair_multicast(&acc_full[acc], kBothCtas);
+                            if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                        }
                     }
                 }
             }
+            if (!ok) record_failure(kRoleMma, abort_flag);
             tc_commit_pair_multicast(drain, 0x1);
             volatile int never = 0;
             mbar_wait_bounded(drain, 0, &never, kWaitLimitNs);
@@ -698,30 +738,34 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             uint32_t matrix, tm, tn;
             ns_tile(p, t, matrix, tm, tn);
             const bool mirror = p.sym && tm != tn;
-            float sum[kChunked ? 128 : 1];
-            if constexpr (kChunked) {
+            float sum[kSplit ? 128 : 1];
+            if constexpr (kSplit) {
+                auto add = [&](uint32_t column) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t r[32];
+                        tmem_ld_32x32b_x32(tmem + lane_base + column + half * 128 + c * 32, r);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[c * 32 + j] += __uint_as_float(r[j]);
+                    }
+                };
 #pragma unroll
                 for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
-                const uint32_t n_chunks = chunk_count(p, 0, total_kb);
+                const uint32_t n_chunks = (p.num_kb + kChunk - 1) / kChunk;
                 for (uint32_t ch = 0; ch < n_chunks; ++ch) {
-                    if (!mbar_wait_bounded<true>(&acc_full[acc], acc_phase, abort_flag, kWaitLimitNs)) {
+                    if (!mbar_wait_bounded<true>(&acc_full[0], acc_phase, abort_flag, kWaitLimitNs)) {
                         record_failure(kRoleEpilogue, abort_flag);
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t r[32];
-                        tmem_ld_32x32b_x32(tmem + lane_base + acc * 256 + half * 128 + c * 32, r);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[c * 32 + j] += __uint_as_float(r[j]);
-                    }
+                    add(256);
+                    if (ch + 1 == n_chunks) add(0);
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
-                    if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+                    if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&acc_empty[0]), 0));
+                    acc_phase ^= 1;
                 }
             } else {
                 if (!mbar_wait_bounded<true>(&acc_full[acc], acc_phase, abort_flag, kWaitLimitNs)) {
@@ -734,7 +778,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (uint32_t u = 0; u < 2; ++u) {
                 float v[64];
-                if constexpr (kChunked) {
+                if constexpr (kSplit) {
 #pragma unroll
                     for (int j = 0; j < 64; ++j) v[j] = sum[u * 64 + j];
                 } else {
@@ -757,7 +801,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 prefetch(u == 0 ? t : t + n_clusters, u ^ 1);
             }
         }
-        if (lane == 0) bulk_wait_all();  // shared memory outlives the stores that read it
+        if (lane == 0) bulk_wait_read<0>();  // shared memory outlives the stores that read it
     }
 
     tc_fence_before();
@@ -1333,7 +1377,7 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, unsigned cluster,
 
 // One product: pair kernel where its tiles can occupy most of the machine's
 // CTA pairs, else the tile kernel with K in as many parts as there are idle
-// SMs, each at least 16 K blocks (2 us: joining the parts takes as long).
+// SMs, each at least 8 slots long (2 us: joining the parts takes as long).
 cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_t rows, int64_t cols,
                            const DeviceInfo& dev, cudaStream_t s) {
     auto tiles = [&](int64_t size) {
@@ -1344,17 +1388,16 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
         p.num_tiles = static_cast<uint32_t>(all);
         return all;
     };
-    const bool chunked = p.segs == 3;
     const int64_t pairs = dev.sm_count / 2;
     const int64_t big = tiles(256);
     if (big >= pairs * 3 / 4)
-        return launch(chunked ? ns_pair_kernel<true> : ns_pair_kernel<false>,
+        return launch(p.split ? ns_pair_kernel<true> : ns_pair_kernel<false>,
                       dim3(static_cast<unsigned>(2 * std::min(big, pairs))), kPairThreads, 2,
                       static_cast<int>(kPairLaunch), true, s, maps, p);
     const int64_t small = tiles(128);
     uint32_t splits = 1;
-    while (splits < 4 && small * splits * 2 <= dev.sm_count && p.num_kb * p.segs >= splits * 32) splits *= 2;
-    return launch(chunked ? ns_tile_kernel<true> : ns_tile_kernel<false>, dim3(static_cast<unsigned>(small * splits)),
+    while (splits < 4 && small * splits * 2 <= dev.sm_count && p.num_kb * (p.split ? 2 : 1) >= splits * 16) splits *= 2;
+    return launch(p.split ? ns_tile_kernel<true> : ns_tile_kernel<false>, dim3(static_cast<unsigned>(small * splits)),
                   kTileThreads, splits, static_cast<int>(kTileLaunch), true, s, maps, p, splits);
 }
 
@@ -1487,7 +1530,7 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
     bl = pl.split ? take(pl.a_bytes) : nullptr;
 
     NsParams base{};
-    base.segs = pl.split ? 3 : 1;
+    base.split = pl.split;
     base.p_rows = base.q_rows = static_cast<uint32_t>(pl.mp);
     base.m = pl.m;
     base.n = pl.n;

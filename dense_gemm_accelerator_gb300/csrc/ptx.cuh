@@ -394,8 +394,6 @@ template <int n>
 __device__ __forceinline__ void bulk_wait_read() {
     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(n) : "memory");
 }
-// Waits until all bulk groups of this thread are complete.
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 // Orders this thread's shared-memory writes before later async-proxy reads.
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // Copies `bytes` (a multiple of 16, both ends 16-byte aligned) of this CTA's
