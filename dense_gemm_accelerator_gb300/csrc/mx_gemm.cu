@@ -437,13 +437,15 @@ struct SkinnyPlan {
     static constexpr uint32_t kBudget = (kCtas == 2 ? 110u : 220u) * 1024;
     static constexpr int kStages = kBudget / kStage;
     static constexpr uint32_t kBar = kStages * kStage;
-    // full[S], empty[S], acc_full, then tmem slot + abort flag
-    static constexpr uint32_t kLaunch = kBar + (2 * kStages + 1) * 8 + 16 + 1024;
+    // full[S], empty[S], acc_full, joined, then tmem slot + abort flag
+    static constexpr uint32_t kLaunch = kBar + (2 * kStages + 2) * 8 + 16 + 1024;
     static constexpr uint32_t kSfCol = kN;  // the scales behind the accumulator
     static constexpr uint32_t kUsed = kN + 4 * kSf * (1 + kSfRows);
     static constexpr uint32_t kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
     static_assert(kStage % 1024 == 0, "stages keep the swizzle atoms aligned");
-    static_assert(kBar >= kN * 128 * 4, "the partial sums fit the ring");
+    // K parts: the sums, and those of the other parts, fit the ring
+    static constexpr uint32_t kMaxSplits = kN > 128 ? 2 : 8;
+    static_assert(kBar >= kN * 512 + kN * 512 * (kMaxSplits - 1) / kMaxSplits, "the partial sums fit the ring");
     static_assert(kStages >= 3, "a ring");
 };
 
@@ -462,7 +464,8 @@ __global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBar);
     uint64_t* empty = full + S::kStages;
     uint64_t* acc_full = empty + S::kStages;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_full + 1);
+    uint64_t* joined = acc_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(joined + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -476,8 +479,14 @@ __global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
+        mbar_init(joined, 1);
         *abort_flag = 0;
         fence_mbar_init();
+        if (splits > 1) {
+            const int per = kN / static_cast<int>(splits);
+            const int mine = max(0, min(per, static_cast<int>(p.M) - static_cast<int>(part) * per));
+            if (mine > 0) mbar_arrive_expect_tx(joined, (splits - 1) * mine * 512);
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, S::kTmem);
@@ -557,66 +566,86 @@ __global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
         }
     }
     __syncwarp();
-    // every MMA of this CTA is done, and with them every copy into the ring
-    const bool ok = mbar_wait_bounded(acc_full, 0, abort_flag, kWaitLimitNs);
-    if (!ok) record_failure(kRoleEpilogue, abort_flag);
-    tc_fence_after();
-    const int quarter = warp & 3;
-    const int w_in = quarter * 32 + lane;  // this thread's row of the tile
-    const int64_t col = static_cast<int64_t>(tile) * 128 + w_in;  // a row of B: a column of C
-    const int rows = static_cast<int>(p.M);
-    float* red = reinterpret_cast<float*>(smem);
-    const float alpha = total_alpha(p);
-    const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
-    constexpr int kStep = kN < 32 ? 16 : 32;
-    if (splits == 1) {
-        if (warp >= 2 && ok) {
+    if (warp >= 2) {
+        // Lane: a row of B, that is a column of C; accumulator columns: rows of A
+        // ("tokens").  With K in parts, CTA q joins tokens [q per, (q + 1) per).
+        // Every CTA puts its sums into the ring, token by token, 128 floats each,
+        // and sends each other CTA its tokens by one bulk copy, to a slot of
+        // its own behind them; the parts are added up in their order.
+        const bool ok = mbar_wait_bounded(acc_full, 0, abort_flag, kWaitLimitNs);
+        if (!ok) record_failure(kRoleEpilogue, abort_flag);
+        tc_fence_after();
+        const int quarter = warp & 3, w = quarter * 32 + lane;
+        const int64_t col = static_cast<int64_t>(tile) * 128 + w;
+        const int rows = static_cast<int>(p.M), per = kN / static_cast<int>(splits);
+        const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
+        const float alpha = total_alpha(p);
+        const float bias = (p.bias != nullptr && col < p.N) ? OutT<TOut>::load(static_cast<const TOut*>(p.bias) + col) : 0.0f;
+        TOut* const C = static_cast<TOut*>(p.C) + col;
+        auto store = [&](int token, float sum) {
+            TOut* dst = C + token * p.ldc;
+            const float old = p.beta != 0.0f ? OutT<TOut>::load(dst) : 0.0f;
+            OutT<TOut>::store(dst, axpby(alpha, sum, p.beta, old) + bias);
+        };
+        float* sums = reinterpret_cast<float*>(smem);
+        constexpr int kStep = kN < 32 ? 16 : 32;
 #pragma unroll 1
-            for (int c = 0; c < kN && c < rows; c += kStep) {
-                uint32_t r[kStep];
-                if constexpr (kStep == 16) tmem_ld_32x32b_x16(tmem + lane_base + c, r);
-                else tmem_ld_32x32b_x32(tmem + lane_base + c, r);
-                tmem_ld_wait();
+        for (int c = 0; c < kN && c < rows; c += kStep) {
+            uint32_t r[kStep];
+            if constexpr (kStep == 16) tmem_ld_32x32b_x16(tmem + lane_base + c, r);
+            else tmem_ld_32x32b_x32(tmem + lane_base + c, r);
+            tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < kStep; ++j)
-                    if (c + j < rows && col < p.N) put<TOut>(p, alpha, c + j, col, __uint_as_float(r[j]));
+            for (int j = 0; j < kStep; ++j) {
+                if (splits > 1) sums[(c + j) * 128 + w] = __uint_as_float(r[j]);
+                else if (c + j < rows && col < p.N) store(c + j, __uint_as_float(r[j]));
             }
         }
-    } else {
-        // Row j of A is joined by CTA j % splits.  Each CTA sends its sums to
-        // the joining ones (stores, which nothing waits for) once every ring
-        // is done with, slot q of `red` coming from part q:
-        // red[(q * kN / splits + j / splits) * 128 + w].
-        const uint32_t per = kN / splits;
-        __syncwarp();
-        cluster_sync();
-        if (warp >= 2 && ok) {
-#pragma unroll 1
-            for (int c = 0; c < kN && c < rows; c += kStep) {
-                uint32_t r[kStep];
-                if constexpr (kStep == 16) tmem_ld_32x32b_x16(tmem + lane_base + c, r);
-                else tmem_ld_32x32b_x32(tmem + lane_base + c, r);
-                tmem_ld_wait();
+        if (splits > 1) {
+            fence_async_shared();
+            asm volatile("bar.sync 1, 128;" ::: "memory");  // the four epilogue warps
+            cluster_arrive_relaxed();
+            cluster_wait();  // every ring is done with
+            const int first = static_cast<int>(part) * per, mine = max(0, min(per, rows - first));
+            const float* received = sums + kN * 128;  // part q's slot: q, or q - 1 past this CTA's own
+            if (warp == 2 && lane < static_cast<int>(splits) && lane != static_cast<int>(part)) {
+                const int theirs = max(0, min(per, rows - lane * per));
+                const uint32_t slot = part - (static_cast<int>(part) > lane ? 1 : 0);
+                if (theirs > 0)
+                    bulk_copy_to_cta(map_to_cta(smem_u32(received + slot * per * 128), lane), smem_u32(sums + lane * per * 128),
+                                     theirs * 512, map_to_cta(smem_u32(joined), lane));
+            }
+            __syncwarp();
+            if (mine > 0 && !mbar_wait_bounded<true>(joined, 0, abort_flag, kWaitLimitNs)) record_failure(kRoleEpilogue, abort_flag);
+            __syncwarp();
+            cluster_arrive_relaxed();  // what was sent here has arrived
+            if (col < p.N) {
+                // eight tokens at a time: their loads are issued together
+                for (int j0 = 0; j0 < mine; j0 += 8) {
+                    float sum[8];
 #pragma unroll
-                for (int j = 0; j < kStep; ++j) {
-                    const uint32_t row = c + j;
-                    if (row < rows) {
-                        const uint32_t at = smem_u32(red + (part * per + row / splits) * 128 + w_in);
-                        st_shared_cluster_f32(map_to_cta(at, row % splits), __uint_as_float(r[j]));
+                    for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+                    for (int q = 0; q < static_cast<int>(splits); ++q) {
+                        const float* src = q == static_cast<int>(part)
+                                               ? sums + first * 128
+                                               : received + (q - (q > static_cast<int>(part) ? 1 : 0)) * per * 128;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j0 + j < mine) sum[j] += src[(j0 + j) * 128 + w];
                     }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j0 + j < mine) store(first + j0 + j, sum[j]);
                 }
             }
+            __syncwarp();
+            cluster_wait();  // and what this CTA sent, at the others
         }
-        __syncwarp();
-        cluster_sync();
-        if (warp >= 2 && col < p.N) {
-            uint32_t slot = 0;
-            for (int j = static_cast<int>(part); j < rows; j += static_cast<int>(splits), ++slot) {
-                float sum = 0.0f;
-                for (uint32_t q = 0; q < splits; ++q) sum += red[(q * per + slot) * 128 + w_in];
-                put<TOut>(p, alpha, j, col, sum);
-            }
-        }
+    } else if (splits > 1) {
+        cluster_arrive_relaxed();
+        cluster_wait();
+        cluster_arrive_relaxed();
+        cluster_wait();
     }
     tc_fence_before();
     __syncthreads();
@@ -707,7 +736,7 @@ cudaError_t launch_skinny(const MxGemmArgs& a, MxParams p, const DeviceInfo& dev
     // parts of K: as many as fill the machine's CTA slots, each at least two stages
     const int64_t tiles = (a.N + 127) / 128, slots = static_cast<int64_t>(dev.sm_count) * S::kCtas;
     uint32_t splits = 1;
-    while (splits < 8 && tiles * splits * 2 <= slots && p.num_kb >= splits * 4) splits *= 2;
+    while (splits < S::kMaxSplits && tiles * splits * 2 <= slots && p.num_kb >= splits * 4) splits *= 2;
     return launch(mx_gemm_skinny_kernel<kFormat, kN, TOut>, static_cast<unsigned>(tiles * splits), 192, splits,
                   static_cast<int>(S::kLaunch), a.after_quantize, a.stream, m[0], m[1], m[2], m[3], p, splits);
 }

@@ -557,30 +557,43 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // ---- the pair kernel: 256 x 256 on two CTAs, persistent --------------------------------
 
-constexpr int kPairStages = 5;
+// Warps: producer, MMA, epilogue: 8 epilogue warps of 128 columns and 5 ring
+// slots, or, kDeep, 4 warps of 256 columns, whose smaller staging leaves room
+// for a sixth slot.  A long K is bound by the bytes in flight, a short one by
+// the epilogue (bf16, deep against not: 4096^2 1107 / 1135 us, 2048^2 261 / 277
+// us, 12 x 1030 x 515 309 / 265 us); split operands keep their sums in
+// registers, so that they need the 8 warps.
 constexpr uint32_t kPairStage = 2 * 128 * 128;  // each CTA's half of both operands
-constexpr uint32_t kPairEpi = kPairStages * kPairStage;
-constexpr uint32_t kPairBar = kPairEpi + 8 * kUnitBytes;
-constexpr uint32_t kPairLaunch = kPairBar + (2 * kPairStages + 5 + 8) * 8 + 16 + 1024;
+constexpr uint32_t kDeepBlocks = 32;  // K blocks from which the deep ring is taken
+template <bool kDeep>
+struct PairPlan {
+    static constexpr int kStages = kDeep ? 6 : 5;
+    static constexpr int kWarps = kDeep ? 4 : 8;
+    static constexpr uint32_t kUnits = 8 / kWarps * 2;  // units of a warp: 32 rows x 256 columns are 4 of them
+    static constexpr int kThreads = 64 + 32 * kWarps;
+    static constexpr uint32_t kEpi = kStages * kPairStage;
+    static constexpr uint32_t kBar = kEpi + kWarps * kUnitBytes;
+    // full[S], empty[S], acc_full[2], acc_empty[2], drain, old_full[W], tmem slot + abort flag
+    static constexpr uint32_t kLaunch = kBar + (2 * kStages + 5 + kWarps) * 8 + 16 + 1024;
+};
 
-// Producer warp, MMA warp, 8 epilogue warps with 128 columns (two units) each.
-constexpr int kPairThreads = 320;
-
-template <bool kSplit>
-__global__ void __launch_bounds__(kPairThreads, 1)
+template <bool kSplit, bool kDeep>
+__global__ void __launch_bounds__(PairPlan<kDeep>::kThreads, 1)
     ns_pair_kernel(const __grid_constant__ NsMaps maps, NsParams p) {
+    using S = PairPlan<kDeep>;
+    constexpr int kPairStages = S::kStages;
     constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 256, 256);
     constexpr uint16_t kBothCtas = 0x3;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairBar);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBar);
     uint64_t* empty = full + kPairStages;
     uint64_t* acc_full = empty + kPairStages;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
     uint64_t* old_full = drain + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + 8);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + S::kWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -593,10 +606,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 16);  // one lane of each epilogue warp of both CTAs
+            mbar_init(&acc_empty[b], 2 * S::kWarps);  // one lane of each epilogue warp of both CTAs
         }
         mbar_init(drain, 1);
-        for (int w = 0; w < 8; ++w) mbar_init(&old_full[w], 1);
+        for (int w = 0; w < S::kWarps; ++w) mbar_init(&old_full[w], 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&maps.p_h);
@@ -716,12 +729,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_wait_bounded(drain, 0, &never, kWaitLimitNs);
         }
     } else {
-        const uint32_t e = warp - 2, quarter = warp & 3, half = e >> 2;  // 128 columns
+        const uint32_t e = warp - 2, quarter = warp & 3, half = e >> 2;  // 128 columns, or all 256
         const uint32_t lane_base = (quarter * 32) << 16;
-        uint8_t* boxes = smem + kPairEpi + e * kUnitBytes;
+        uint8_t* boxes = smem + S::kEpi + e * kUnitBytes;
         uint32_t acc = 0, acc_phase = 0, old_phase = 0;
         bool ok = true;
-        // unit u (0, 1) of tile t
+        // unit u of tile t
         auto rows_of = [&](uint32_t tm) { return static_cast<int32_t>(tm * 256 + rank * 128 + quarter * 32); };
         auto cols_of = [&](uint32_t tn, uint32_t u) { return static_cast<int32_t>(tn * 256 + half * 128 + u * 64); };
         auto prefetch = [&](uint32_t t, uint32_t u) {
@@ -775,8 +788,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 tc_fence_after();
             }
             if (!ok) break;
-#pragma unroll
-            for (uint32_t u = 0; u < 2; ++u) {
+#pragma unroll(kDeep ? 1 : 2)
+            for (uint32_t u = 0; u < S::kUnits; ++u) {
                 float v[64];
                 if constexpr (kSplit) {
 #pragma unroll
@@ -789,7 +802,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(r[j]);
-                    if (u == 1) {
+                    if (u == S::kUnits - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
@@ -798,7 +811,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
                 ns_unit(p, maps, boxes, &old_full[e], old_phase, abort_flag, matrix, rows_of(tm), cols_of(tn, u), lane, mirror, v);
                 old_phase ^= 1;
-                prefetch(u == 0 ? t : t + n_clusters, u ^ 1);
+                if (u + 1 < S::kUnits) prefetch(t, u + 1);
+                else prefetch(t + n_clusters, 0);
             }
         }
         if (lane == 0) bulk_wait_read<0>();  // shared memory outlives the stores that read it
@@ -1390,10 +1404,15 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
     };
     const int64_t pairs = dev.sm_count / 2;
     const int64_t big = tiles(256);
-    if (big >= pairs * 3 / 4)
-        return launch(p.split ? ns_pair_kernel<true> : ns_pair_kernel<false>,
-                      dim3(static_cast<unsigned>(2 * std::min(big, pairs))), kPairThreads, 2,
-                      static_cast<int>(kPairLaunch), true, s, maps, p);
+    if (big >= pairs * 3 / 4) {
+        auto run = [&](auto kernel, int threads, uint32_t smem) {
+            return launch(kernel, dim3(static_cast<unsigned>(2 * std::min(big, pairs))), threads, 2, static_cast<int>(smem), true, s,
+                          maps, p);
+        };
+        if (p.split) return run(ns_pair_kernel<true, false>, PairPlan<false>::kThreads, PairPlan<false>::kLaunch);
+        if (p.num_kb < kDeepBlocks) return run(ns_pair_kernel<false, false>, PairPlan<false>::kThreads, PairPlan<false>::kLaunch);
+        return run(ns_pair_kernel<false, true>, PairPlan<true>::kThreads, PairPlan<true>::kLaunch);
+    }
     const int64_t small = tiles(128);
     uint32_t splits = 1;
     while (splits < 4 && small * splits * 2 <= dev.sm_count && p.num_kb * (p.split ? 2 : 1) >= splits * 16) splits *= 2;

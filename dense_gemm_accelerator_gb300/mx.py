@@ -160,22 +160,32 @@ def mx_linear_forward(X, W, bias=None, Y=None, tensor_scale=None, workspace=None
     code = _CODE.get(X.dtype)
     if code is None:
         raise TypeError("X must be float32, bfloat16 or float16")
-    M, K, ldx = _rows_of(X, "X")
-    if K != W.cols:
-        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {W.shape}")
-    dev, fmt, N, L = X.device, W.format, W.rows, lib()
-    if W.codes.device != dev:
+    shape = X.shape
+    if len(shape) != 2 or shape[1] != W.cols:
+        raise ValueError(f"shape mismatch: X {tuple(shape)}, W {W.shape}")
+    M, K = shape
+    ldx, step = X.stride()
+    if step != 1 and K > 1:
+        raise ValueError("X must be row-major")
+    dev, fmt, N, codes = X.device, W.format, W.rows, W.codes
+    if codes.device != dev:
         raise ValueError("X and W must be on the same device")
-    Y, out, ldy = _output(Y, M, N, 0, code, dev)
-    need = L.dga_mx_linear_workspace_size(fmt, M, K)
+    if Y is None:
+        Y, out, ldy = torch.empty((M, N), dtype=X.dtype, device=dev), code, N or 1
+    else:
+        Y, out, ldy = _output(Y, M, N, 0, code, dev)
+    L = lib()
     if workspace is None:
-        workspace, have = torch.empty(need, dtype=torch.uint8, device=dev), need
+        have = L.dga_mx_linear_workspace_size(fmt, M, K)
+        workspace = torch.empty(have, dtype=torch.uint8, device=dev)
     else:
         have = workspace.numel() * workspace.element_size()
-    st = L.dga_mx_linear(fmt, code, out, M, N, K, X.data_ptr(), ldx, _factor(tensor_scale, fmt, dev),
-                         W.codes.data_ptr(), W.codes.stride(0), W.scales.data_ptr(),
-                         _factor(W.tensor_scale, fmt, dev), _bias(bias, N, Y), Y.data_ptr(), ldy,
-                         workspace.data_ptr(), have, _stream(dev, stream))
+    st = L.dga_mx_linear(fmt, code, out, M, N, K, X.data_ptr(), ldx if ldx > K else K or 1,
+                         None if tensor_scale is None else _factor(tensor_scale, fmt, dev),
+                         codes.data_ptr(), codes.stride(0), W.scales.data_ptr(),
+                         None if W.tensor_scale is None else _factor(W.tensor_scale, fmt, dev),
+                         None if bias is None else _bias(bias, N, Y), Y.data_ptr(), ldy,
+                         workspace.data_ptr(), have, _raw_stream(dev.index) if stream is None else stream)
     if st:
         _raise(st, "dga_mx_linear")
     return Y
