@@ -126,7 +126,13 @@ struct MxGemmArgs {
     const void* bias;  // N values of the output type, or null
     bool after_quantize;  // launched right behind the quantisation of A
     cudaStream_t stream;
+    // A as values the product quantises itself (M <= kMxFusedRows; A then holds
+    // its factor alone), or null
+    const void* X;
+    int64_t ldx;
+    int x_dtype;
 };
+constexpr int64_t kMxFusedRows = 16;
 
 cudaError_t mx_quantize_launch(const MxQuantArgs& a, const DeviceInfo& dev);
 cudaError_t mx_dequantize_launch(int format, int out_dtype, const MxMatrix& q, int64_t rows, int64_t K,

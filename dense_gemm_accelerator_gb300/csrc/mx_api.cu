@@ -148,7 +148,7 @@ int dga_mx_gemm(dga_mx_format format, dga_dtype out_dtype, int64_t M, int64_t N,
     if (st != DGA_OK) return st;
     MxGemmArgs a{format, out_dtype, M, N, K, *alpha, *beta, {A_codes, lda, A_scales, A_tensor_scale},
                  {B_codes, ldb, B_scales, B_tensor_scale}, C, ldc, bias, false,
-                 reinterpret_cast<cudaStream_t>(stream)};
+                 reinterpret_cast<cudaStream_t>(stream), nullptr, 0, 0};
     int launches = 0;
     const cudaError_t e = mx_gemm_launch(a, dev, &launches);
     if (e != cudaSuccess) return note_cuda_error(e);
@@ -157,7 +157,7 @@ int dga_mx_gemm(dga_mx_format format, dga_dtype out_dtype, int64_t M, int64_t N,
 }
 
 size_t dga_mx_linear_workspace_size(dga_mx_format format, int64_t M, int64_t K) {
-    if (!format_ok(format) || M <= 0 || K <= 0) return 0;
+    if (!format_ok(format) || M <= kMxFusedRows || K <= 0) return 0;
     return static_cast<size_t>(round_up(M * mx_row_bytes(K), 256) + scales_bytes(format, M, K));
 }
 
@@ -194,21 +194,28 @@ int dga_mx_linear(dga_mx_format format, dga_dtype x_dtype, dga_dtype out_dtype, 
     const Span w = span(workspace, 1, 0, static_cast<int64_t>(need));
     const Span wc = span(W_codes, N, ldw, mx_row_bytes(K)), wsc = span(W_scales, 1, 0, scales_bytes(format, N, K));
     const Span x = span(X, M, ldx * type_size(x_dtype), K * type_size(x_dtype));
-    if (meet(y, x) || meet(y, w) || meet(w, x) || meet(y, wc) || meet(y, wsc) || meet(w, wc) || meet(w, wsc) ||
-        (bias && meet(w, span(bias, 1, 0, N * es))))
+    if (meet(y, x) || meet(y, wc) || meet(y, wsc) ||
+        (need > 0 && (meet(y, w) || meet(w, x) || meet(w, wc) || meet(w, wsc) || (bias && meet(w, span(bias, 1, 0, N * es))))))
         return DGA_ERR_OVERLAP;
     DeviceInfo dev;
     const int st = device(&dev);
     if (st != DGA_OK) return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    uint8_t* codes = static_cast<uint8_t*>(workspace);
-    uint8_t* scales = codes + round_up(M * mx_row_bytes(K), 256);
-    MxQuantArgs q{format, x_dtype, false, M, K, X, ldx, x_tensor_scale, codes, mx_row_bytes(K), scales, s};
-    cudaError_t e = mx_quantize_launch(q, dev);
-    if (e != cudaSuccess) return note_cuda_error(e);
-    MxGemmArgs a{format, out_dtype, M, N, K, 1.0f, 0.0f, {codes, mx_row_bytes(K), scales, x_tensor_scale},
-                 {W_codes, ldw, W_scales, W_tensor_scale}, Y, ldy, bias, true, s};
-    int launches = 1;
+    MxGemmArgs a{format, out_dtype, M, N, K, 1.0f, 0.0f, {nullptr, 0, nullptr, x_tensor_scale},
+                 {W_codes, ldw, W_scales, W_tensor_scale}, Y, ldy, bias, false, s, X, ldx, x_dtype};
+    cudaError_t e;
+    int launches = 0;
+    if (M > kMxFusedRows) {
+        uint8_t* codes = static_cast<uint8_t*>(workspace);
+        uint8_t* scales = codes + round_up(M * mx_row_bytes(K), 256);
+        MxQuantArgs q{format, x_dtype, false, M, K, X, ldx, x_tensor_scale, codes, mx_row_bytes(K), scales, s};
+        e = mx_quantize_launch(q, dev);
+        if (e != cudaSuccess) return note_cuda_error(e);
+        launches = 1;
+        a.A = {codes, mx_row_bytes(K), scales, x_tensor_scale};
+        a.after_quantize = true;
+        a.X = nullptr;
+    }
     e = mx_gemm_launch(a, dev, &launches);
     if (e != cudaSuccess) return note_cuda_error(e);
     set_last_launches(launches);

@@ -30,6 +30,7 @@
 #include "dga_internal.h"
 #include "epilogue.cuh"
 #include "mx_common.cuh"
+#include "mx_quant.cuh"
 #include "ptx.cuh"
 
 namespace dga {
@@ -437,8 +438,8 @@ struct SkinnyPlan {
     static constexpr uint32_t kBudget = (kCtas == 2 ? 110u : 220u) * 1024;
     static constexpr int kStages = kBudget / kStage;
     static constexpr uint32_t kBar = kStages * kStage;
-    // full[S], empty[S], acc_full, joined, then tmem slot + abort flag
-    static constexpr uint32_t kLaunch = kBar + (2 * kStages + 2) * 8 + 16 + 1024;
+    // full[S], empty[S], acc_full, joined, x_full[S], then tmem slot + abort flag
+    static constexpr uint32_t kLaunch = kBar + (3 * kStages + 2) * 8 + 16 + 1024;
     static constexpr uint32_t kSfCol = kN;  // the scales behind the accumulator
     static constexpr uint32_t kUsed = kN + 4 * kSf * (1 + kSfRows);
     static constexpr uint32_t kTmem = kUsed <= 64 ? 64 : kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
@@ -449,11 +450,22 @@ struct SkinnyPlan {
     static_assert(kStages >= 3, "a ring");
 };
 
-template <int kFormat, int kN, typename TOut>
-__global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
+// A's values, where the kernel quantises them itself.
+struct MxSource {
+    const void* X;
+    int64_t ldx, K;
+    int type, vec;  // vec: rows take 16-byte loads
+};
+
+// kFused: A comes as values of up to 16 rows and four more warps quantise it,
+// a thread 32 values of a stage, while B's codes are under way: one launch, no
+// workspace (a token through 4096 x 4096: 8.4 us as two kernels).
+template <int kFormat, int kN, bool kFused, typename TOut>
+__global__ void __launch_bounds__(kFused ? 320 : 192, (SkinnyPlan<kFormat, kN>::kCtas))
     mx_gemm_skinny_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                           const __grid_constant__ CUtensorMap tmSw, const __grid_constant__ CUtensorMap tmSx,
-                          MxParams p, uint32_t splits) {
+                          MxParams p, MxSource src, uint32_t splits) {
+    static_assert(!kFused || kN == 16, "a stage of 16 rows is one run of 32 values for each of 128 threads");
     using S = SkinnyPlan<kFormat, kN>;
     constexpr bool kE8M0 = kFormat == DGA_MXFP4;
     constexpr uint32_t kIdesc0 = idesc_mx(kE8M0, 128, kN, 0), kIdesc2 = idesc_mx(kE8M0, 128, kN, 2);
@@ -465,7 +477,8 @@ __global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
     uint64_t* empty = full + S::kStages;
     uint64_t* acc_full = empty + S::kStages;
     uint64_t* joined = acc_full + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(joined + 1);
+    uint64_t* x_full = joined + 1;  // kFused: A's codes and scales of a stage
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(x_full + S::kStages);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -477,6 +490,7 @@ __global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
         for (int s = 0; s < S::kStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&x_full[s], 4);  // one lane of each quantising warp
         }
         mbar_init(acc_full, 1);
         mbar_init(joined, 1);
@@ -502,7 +516,7 @@ __global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
             const int32_t w_row = static_cast<int32_t>(tile * 128);
             auto load_w = [&](uint32_t stage, uint32_t kb) {
                 uint8_t* dst = smem + stage * S::kStage;
-                mbar_arrive_expect_tx(&full[stage], S::kStage);
+                mbar_arrive_expect_tx(&full[stage], kFused ? S::kW + S::kSw : S::kStage);
                 tma_load_2d(dst, &tmW, &full[stage], static_cast<int32_t>(kb * kRowBytes), w_row);
                 tma_load_2d(dst + S::kW + S::kX, &tmSw, &full[stage], static_cast<int32_t>(kb * (S::kSf * kMxTileBytes / 8)),
                             static_cast<int32_t>(tile));
@@ -518,7 +532,8 @@ __global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
             const uint32_t first = min(kb1 - kb0, static_cast<uint32_t>(S::kStages));
             for (uint32_t s = 0; s < first; ++s) load_w(s, kb0 + s);
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            for (uint32_t s = 0; s < first; ++s) load_x(s, kb0 + s);
+            if (!kFused)
+                for (uint32_t s = 0; s < first; ++s) load_x(s, kb0 + s);
             uint32_t stage = 0, phase = 0;
             for (uint32_t kb = kb0 + first; kb < kb1; ++kb) {
                 if (!mbar_wait_bounded(&empty[stage], phase, abort_flag, kWaitLimitNs)) {
@@ -526,7 +541,7 @@ __global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
                     break;
                 }
                 load_w(stage, kb);
-                load_x(stage, kb);
+                if (!kFused) load_x(stage, kb);
                 if (++stage == S::kStages) { stage = 0; phase ^= 1; }
             }
         }
@@ -534,7 +549,8 @@ __global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
         if (lane == 0) {
             uint32_t stage = 0, phase = 0;
             for (uint32_t kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs)) {
+                if (!mbar_wait_bounded(&full[stage], phase, abort_flag, kWaitLimitNs) ||
+                    (kFused && !mbar_wait_bounded(&x_full[stage], phase, abort_flag, kWaitLimitNs))) {
                     record_failure(kRoleMma, abort_flag);
                     break;
                 }
@@ -566,7 +582,40 @@ __global__ void __launch_bounds__(192, (SkinnyPlan<kFormat, kN>::kCtas))
         }
     }
     __syncwarp();
-    if (warp >= 2) {
+    if (kFused && warp >= 6) {
+        const int row = (warp & 1) * 8 + (lane & 7), run = ((warp - 6) >> 1) * 4 + (lane >> 3);  // of 16 and 8
+        const TensorFactor g((kFormat == DGA_NVFP4 && p.fa != nullptr) ? __ldg(p.fa) : 1.0f);
+        const int64_t es = src.type == DGA_F32 ? 4 : 2;
+        const uint8_t* const X = static_cast<const uint8_t*>(src.X) + row * src.ldx * es;
+        uint32_t raw[32] = {};
+        auto load = [&](uint32_t kb) {
+            const int64_t k = static_cast<int64_t>(kb) * kStageK + run * 32;
+            if (row < p.M && kb < kb1) load_run(src.type, X + k * es, src.K - k, src.vec, raw);
+        };
+        load(kb0);
+        uint32_t stage = 0, phase = 0;
+        for (uint32_t kb = kb0; kb < kb1; ++kb) {
+            uint4 codes;
+            uint32_t bytes;
+            quantize_run<kFormat>(src.type, raw, g, codes, bytes);
+            load(kb + 1);
+            if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, kWaitLimitNs)) {
+                record_failure(kRoleScales, abort_flag);
+                break;
+            }
+            uint8_t* x = smem + stage * S::kStage + S::kW;
+            *reinterpret_cast<uint4*>(x + row * 128 + ((run ^ (row & 7)) << 4)) = codes;
+            uint8_t* scale = x + S::kX + S::kSw + row * 16;  // block b: byte b % 4 of tile b / 4
+            if constexpr (kFormat == DGA_MXFP4) scale[(run >> 2) * kMxTileBytes + (run & 3)] = static_cast<uint8_t>(bytes);
+            else *reinterpret_cast<uint16_t*>(scale + (run >> 1) * kMxTileBytes + (run & 1) * 2) = static_cast<uint16_t>(bytes);
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&x_full[stage]);
+            if (++stage == S::kStages) { stage = 0; phase ^= 1; }
+        }
+        __syncwarp();
+    }
+    if (warp >= 2 && warp < 6) {
         // Lane: a row of B, that is a column of C; accumulator columns: rows of A
         // ("tokens").  With K in parts, CTA q joins tokens [q per, (q + 1) per).
         // Every CTA puts its sums into the ring, token by token, 128 floats each,
@@ -724,21 +773,26 @@ cudaError_t launch(void (*kern)(P...), unsigned grid, int threads, unsigned clus
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-template <int kFormat, int kN, typename TOut>
+template <int kFormat, int kN, bool kFused, typename TOut>
 cudaError_t launch_skinny(const MxGemmArgs& a, MxParams p, const DeviceInfo& dev) {
     using S = SkinnyPlan<kFormat, kN>;
     CUtensorMap m[4];
     cudaError_t e = codes_map(&m[0], a.B, a.N, a.K, 128);
-    if (e == cudaSuccess) e = codes_map(&m[1], a.A, a.M, a.K, kN);
     if (e == cudaSuccess) e = scales_map(&m[2], kFormat, a.B, a.N, a.K, 1);
-    if (e == cudaSuccess) e = scales_map(&m[3], kFormat, a.A, a.M, a.K, S::kSfRows);
+    if (kFused) {
+        m[1] = m[0], m[3] = m[2];  // not used
+    } else {
+        if (e == cudaSuccess) e = codes_map(&m[1], a.A, a.M, a.K, kN);
+        if (e == cudaSuccess) e = scales_map(&m[3], kFormat, a.A, a.M, a.K, S::kSfRows);
+    }
     if (e != cudaSuccess) return e;
+    const MxSource src{a.X, a.ldx, a.K, a.x_dtype, aligned(a.X, 16) && a.ldx % (a.x_dtype == DGA_F32 ? 4 : 8) == 0};
     // parts of K: as many as fill the machine's CTA slots, each at least two stages
     const int64_t tiles = (a.N + 127) / 128, slots = static_cast<int64_t>(dev.sm_count) * S::kCtas;
     uint32_t splits = 1;
     while (splits < S::kMaxSplits && tiles * splits * 2 <= slots && p.num_kb >= splits * 4) splits *= 2;
-    return launch(mx_gemm_skinny_kernel<kFormat, kN, TOut>, static_cast<unsigned>(tiles * splits), 192, splits,
-                  static_cast<int>(S::kLaunch), a.after_quantize, a.stream, m[0], m[1], m[2], m[3], p, splits);
+    return launch(mx_gemm_skinny_kernel<kFormat, kN, kFused, TOut>, static_cast<unsigned>(tiles * splits), kFused ? 320 : 192,
+                  splits, static_cast<int>(S::kLaunch), a.after_quantize, a.stream, m[0], m[1], m[2], m[3], p, src, splits);
 }
 
 template <int kFormat, typename TOut>
@@ -788,11 +842,12 @@ cudaError_t launch_as(const MxGemmArgs& a, const DeviceInfo& dev) {
         return cudaGetLastError();
     }
     p.num_kb = static_cast<uint32_t>((a.K + kStageK - 1) / kStageK);
-    if (a.M <= 16) return launch_skinny<kFormat, 16, TOut>(a, p, dev);
-    if (a.M <= 32) return launch_skinny<kFormat, 32, TOut>(a, p, dev);
-    if (a.M <= 64) return launch_skinny<kFormat, 64, TOut>(a, p, dev);
-    if (a.M <= 128) return launch_skinny<kFormat, 128, TOut>(a, p, dev);
-    if (a.M <= 256) return launch_skinny<kFormat, 256, TOut>(a, p, dev);
+    if (a.X != nullptr) return launch_skinny<kFormat, 16, true, TOut>(a, p, dev);
+    if (a.M <= 16) return launch_skinny<kFormat, 16, false, TOut>(a, p, dev);
+    if (a.M <= 32) return launch_skinny<kFormat, 32, false, TOut>(a, p, dev);
+    if (a.M <= 64) return launch_skinny<kFormat, 64, false, TOut>(a, p, dev);
+    if (a.M <= 128) return launch_skinny<kFormat, 128, false, TOut>(a, p, dev);
+    if (a.M <= 256) return launch_skinny<kFormat, 256, false, TOut>(a, p, dev);
     return launch_pair<kFormat, TOut>(a, p, dev);
 }
 

@@ -22,6 +22,7 @@
 
 #include "dga_internal.h"
 #include "mx_common.cuh"
+#include "mx_quant.cuh"
 
 namespace dga {
 namespace {
@@ -36,74 +37,6 @@ template <> struct MxIn<__nv_bfloat16> {
 template <> struct MxIn<__half> {
     __device__ __forceinline__ static float f(__half v) { return __half2float(v); }
 };
-
-// Magnitude bits of x: ordered like |x|, with infinity and NaN on top.
-__device__ __forceinline__ uint32_t mag_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-
-// One block's scale byte and what its values are divided by: MXFP4
-// multiplies by `inv`, the exact 2^-e; NVFP4 divides by `unit`.
-struct BlockScale {
-    uint8_t byte;
-    float unit, inv;
-};
-
-template <int kFormat>
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float g) {
-    BlockScale b;
-    const bool finite = amax_bits < 0x7f800000u;
-    if constexpr (kFormat == DGA_MXFP4) {
-        // biased exponent of the scale: floor(log2 m) + 127 - 2, at least 0
-        // (a subnormal m has exponent field 0); at most 252
-        const uint32_t e = amax_bits >> 23;
-        const uint32_t s = e > 2 ? e - 2 : 0;
-        b.byte = finite ? static_cast<uint8_t>(s) : uint8_t(0xff);
-        b.inv = finite ? __uint_as_float((254u - s) << 23) : 0.0f;
-        b.unit = 0.0f;  // not used
-    } else {
-        const float r = __fdiv_rn(__uint_as_float(amax_bits), __fmul_rn(6.0f, g));
-        uint16_t two;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(r));
-        b.byte = finite ? static_cast<uint8_t>(two & 0xff) : uint8_t(0x7f);
-        uint32_t h2;  // the scale back as fp16 (exact)
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(two));
-        const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(h2 & 0xffff)));
-        b.unit = finite ? __fmul_rn(s, g) : 0.0f;
-        b.inv = b.unit > 0.0f ? __frcp_rn(b.unit) : 0.0f;
-    }
-    return b;
-}
-
-// x over the block's unit.  NVFP4: the correctly rounded quotient from the
-// correctly rounded reciprocal, one residual and one correction (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor",
-// 1990); units so small or large that the residual would leave fp32's range
-// take the plain division.  A zero unit gives a zero of x's sign.
-template <int kFormat>
-__device__ __forceinline__ float over_unit(float x, const BlockScale& b) {
-    if constexpr (kFormat == DGA_MXFP4) {
-        return x * b.inv;
-    } else {
-        if (b.unit >= 0x1p-90f && b.unit <= 0x1p90f) {
-            const float q = x * b.inv;
-            return copysignf(fmaf(fmaf(-q, b.unit, x), b.inv, q), x);  // the sign of a zero too
-        }
-        return b.unit > 0.0f ? __fdiv_rn(x, b.unit) : copysignf(0.0f, x);
-    }
-}
-
-// Eight values to eight codes, value i in bits 4i..4i+3.
-__device__ __forceinline__ uint32_t codes8(const float (&t)[8]) {
-    uint32_t out;
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
-        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
-        : "=r"(out)
-        : "f"(t[0]), "f"(t[1]), "f"(t[2]), "f"(t[3]), "f"(t[4]), "f"(t[5]), "f"(t[6]), "f"(t[7]));
-    return out;
-}
 
 // Eight codes to their values.
 __device__ __forceinline__ void values8(uint32_t c, float (&v)[8]) {
@@ -155,21 +88,6 @@ __device__ __forceinline__ void load8(const T* __restrict__ row, int64_t k, int6
 // fp32 sources: eight values to a lane as just described, since 128 bytes to a
 // lane would be bound by the L1's lines.
 
-// Larger of the magnitudes (bits, ordered like the values) in each half.
-__device__ __forceinline__ uint32_t max_mag2(uint32_t a, uint32_t b) {
-    return __vmaxu2(a & 0x7fff7fffu, b & 0x7fff7fffu);
-}
-template <typename T>
-__device__ __forceinline__ float half_value(uint32_t word, int h);
-template <>
-__device__ __forceinline__ float half_value<__nv_bfloat16>(uint32_t word, int h) {
-    return __uint_as_float(h ? word & 0xffff0000u : word << 16);
-}
-template <>
-__device__ __forceinline__ float half_value<__half>(uint32_t word, int h) {
-    return __half2float(__ushort_as_half(static_cast<uint16_t>(h ? word >> 16 : word)));
-}
-
 template <int kFormat, typename T>
 __global__ void __launch_bounds__(256) mx_quant_rows16_kernel(const T* __restrict__ X, int64_t ldx, uint32_t rows, int64_t K,
                                                               bool vec, const float* __restrict__ factor,
@@ -179,7 +97,7 @@ __global__ void __launch_bounds__(256) mx_quant_rows16_kernel(const T* __restric
     // a product launched behind this kernel may start now: it waits for this
     // grid's end before it reads what is written here
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const float g = (kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f;
+    const TensorFactor g((kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f);
     // 2^log_x threads along a row, the block's others on the rows below
     const uint32_t run = (blockIdx.x << log_x) + (threadIdx.x & ((1u << log_x) - 1));
     const int64_t k = static_cast<int64_t>(run) * 32;
@@ -216,7 +134,8 @@ __global__ void __launch_bounds__(256) mx_quant_rows16_kernel(const T* __restric
             for (int o = 0; o < kB / 8; ++o) {
                 float t[8];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) t[q] = over_unit<kFormat>(half_value<T>(w[p * (kB / 2) + o * 4 + q / 2], q & 1), b);
+                for (int q = 0; q < 8; ++q) t[q] = half_value<T>(w[p * (kB / 2) + o * 4 + q / 2], q & 1);
+                over_unit8<kFormat>(t, b);
                 out[p * (kB / 8) + o] = codes8(t);
             }
             bytes |= (k + p * kB < K ? static_cast<uint32_t>(b.byte) : 0u) << (8 * p);
@@ -239,7 +158,7 @@ __global__ void __launch_bounds__(256) mx_quant_rows_kernel(const T* __restrict_
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // as above
     constexpr int kLanes = mx_block(kFormat) / 8;  // lanes of a block
     const int lane = threadIdx.x & 31;
-    const float g = (kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f;
+    const TensorFactor g((kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f);
     const int64_t total = rows * chunks;
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); u < total;
          u += static_cast<int64_t>(gridDim.x) * 8) {
@@ -252,8 +171,7 @@ __global__ void __launch_bounds__(256) mx_quant_rows_kernel(const T* __restrict_
 #pragma unroll
         for (int d = 1; d < kLanes; d *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
         const BlockScale b = block_scale<kFormat>(m, g);
-#pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = over_unit<kFormat>(x[q], b);
+        over_unit8<kFormat>(x, b);
         if ((k >> 1) < row_bytes) *reinterpret_cast<uint32_t*>(codes + r * ldc + (k >> 1)) = codes8(x);
         // four blocks' scales to the first lane of the four; a block past the
         // row's end has scale 0 (its codes are 0 too)
@@ -288,7 +206,7 @@ __global__ void __launch_bounds__(256) mx_quant_cols_kernel(const T* __restrict_
     __shared__ __align__(16) uint32_t out[64][16 + 4];
     const int t = threadIdx.x;
     const int64_t k0 = (blockIdx.x % blocks_k) * 128, c0 = (blockIdx.x / blocks_k) * 64;
-    const float g = (kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f;
+    const TensorFactor g((kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f);
     constexpr int kVec = 16 / sizeof(T);       // values of one 16-byte load
     constexpr int kPerRow = 64 / kVec;         // loads of a tile row
 #pragma unroll
@@ -323,7 +241,8 @@ __global__ void __launch_bounds__(256) mx_quant_cols_kernel(const T* __restrict_
         for (int o = 0; o < kB / 8; ++o) {
             float y[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] = over_unit<kFormat>(x[o * 8 + q], b);
+            for (int q = 0; q < 8; ++q) y[q] = x[o * 8 + q];
+            over_unit8<kFormat>(y, b);
             four[p * (kB / 8) + o] = codes8(y);
         }
         const int64_t k = k0 + quarter * 32 + p * kB;
@@ -360,7 +279,7 @@ __global__ void __launch_bounds__(256) mx_quant_cols16_kernel(const T* __restric
     __shared__ __align__(16) uint32_t out[128][16 + 4];
     const int t = threadIdx.x;
     const int64_t k0 = (blockIdx.x % blocks_k) * 128, c0 = (blockIdx.x / blocks_k) * 128;
-    const float g = (kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f;
+    const TensorFactor g((kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int idx = i * 256 + t, kk = idx >> 4, cc = (idx & 15) * 8;
@@ -399,7 +318,8 @@ __global__ void __launch_bounds__(256) mx_quant_cols16_kernel(const T* __restric
             for (int o = 0; o < kB / 8; ++o) {
                 float y[8];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) y[q] = over_unit<kFormat>(half_value<T>(w[o * 8 + q], h), b);
+                for (int q = 0; q < 8; ++q) y[q] = half_value<T>(w[o * 8 + q], h);
+                over_unit8<kFormat>(y, b);
                 four[h][p * (kB / 8) + o] = codes8(y);
             }
             word[h] |= (k < K ? static_cast<uint32_t>(b.byte) : 0u) << (8 * p);

@@ -176,8 +176,9 @@ def mx_linear_forward(X, W, bias=None, Y=None, tensor_scale=None, workspace=None
         Y, out, ldy = _output(Y, M, N, 0, code, dev)
     L = lib()
     if workspace is None:
-        have = L.dga_mx_linear_workspace_size(fmt, M, K)
-        workspace = torch.empty(have, dtype=torch.uint8, device=dev)
+        have = L.dga_mx_linear_workspace_size(fmt, M, K)  # 0 for a few rows
+        if have:
+            workspace = torch.empty(have, dtype=torch.uint8, device=dev)
     else:
         have = workspace.numel() * workspace.element_size()
     st = L.dga_mx_linear(fmt, code, out, M, N, K, X.data_ptr(), ldx if ldx > K else K or 1,
@@ -185,7 +186,7 @@ def mx_linear_forward(X, W, bias=None, Y=None, tensor_scale=None, workspace=None
                          codes.data_ptr(), codes.stride(0), W.scales.data_ptr(),
                          None if W.tensor_scale is None else _factor(W.tensor_scale, fmt, dev),
                          None if bias is None else _bias(bias, N, Y), Y.data_ptr(), ldy,
-                         workspace.data_ptr(), have, _raw_stream(dev.index) if stream is None else stream)
+                         workspace.data_ptr() if have else None, have, _raw_stream(dev.index) if stream is None else stream)
     if st:
         _raise(st, "dga_mx_linear")
     return Y

@@ -465,7 +465,9 @@ int dga_mx_gemm(dga_mx_format format, dga_dtype out_dtype, int64_t M, int64_t N,
  * Y <- X W^T + bias (M x N, row-major, out_dtype; types DGA_F32, DGA_BF16 or
  * DGA_F16).  The same result as dga_mx_quantize and dga_mx_gemm; the product
  * starts loading W while X is being quantised.
+ * Up to 16 rows are quantised by the product itself: one launch, no workspace.
  *   workspace   device, 16-byte aligned, dga_mx_linear_workspace_size bytes
+ *               (0 for M <= 16)
  * Errors: DGA_ERR_UNSUPPORTED; -4 M, -5 N, -6 K, -7 X, -8 ldx,
  * -9 x_tensor_scale, -10..-13 W's codes, ldw, scales, tensor_scale, -15 Y,
  * -16 ldy, -17 workspace; DGA_ERR_WORKSPACE, DGA_ERR_OVERLAP.

@@ -221,7 +221,8 @@ def test_nan_blocks_stay_in_their_rows(fmt, M):
 
 @pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("T,N,K", [(1, 1, 1), (1, 1000, 2048), (7, 513, 1111), (90, 300, 700), (400, 300, 520)])
+@pytest.mark.parametrize("T,N,K", [(1, 1, 1), (1, 1000, 2048), (7, 513, 1111), (16, 300, 5000), (17, 300, 800), (90, 300, 700),
+                                   (400, 300, 520)])
 def test_linear_forward(fmt, dtype, T, N, K):
     """The layer equals quantisation and product called apart, bit for bit."""
     x, w = _values(T, K, 3, dtype), _values(N, K, 4) / K ** 0.5
@@ -313,4 +314,5 @@ def test_refusals():
     with pytest.raises(ValueError):
         dga.mx_linear_forward(torch.ones(2, 63, device="cuda"), q)
     with pytest.raises(dga.DgaError):
-        dga.mx_linear_forward(x, q, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        dga.mx_linear_forward(torch.ones(17, 64, device="cuda"), q,
+                              workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
