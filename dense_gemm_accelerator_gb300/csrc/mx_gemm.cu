@@ -109,27 +109,6 @@ struct PairPlan {
     static_assert(kStage % 1024 == 0, "stages keep the swizzle atoms aligned");
 };
 
-template <typename TOut>
-__device__ __forceinline__ void store_block(const MxParams& p, float alpha, uint32_t* stage, int lane,
-                                            int64_t row_base, int64_t col_base, const uint32_t (&v)[32]) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) stage[lane * 33 + j] = v[j];
-    __syncwarp();
-    const int64_t col = col_base + lane;
-    const bool col_ok = col < p.N;
-    const float bv = (p.bias != nullptr && col_ok) ? OutT<TOut>::load(static_cast<const TOut*>(p.bias) + col) : 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < 32; ++i) {
-        const int64_t row = row_base + i;
-        if (col_ok && row < p.M) {
-            TOut* dst = static_cast<TOut*>(p.C) + row * p.ldc + col;
-            const float old = p.beta != 0.0f ? OutT<TOut>::load(dst) : 0.0f;
-            OutT<TOut>::store(dst, axpby(alpha, __uint_as_float(stage[i * 33 + lane]), p.beta, old) + bv);
-        }
-    }
-    __syncwarp();  // the next block reuses the square
-}
-
 __device__ __forceinline__ void tile_coords(uint32_t t, const MxParams& p, uint32_t& tm, uint32_t& tn) {
     const uint32_t group_size = p.group_m * p.tiles_n;
     const uint32_t group = t / group_size, first_m = group * p.group_m;
@@ -182,6 +161,69 @@ __device__ __forceinline__ void store_unit(const MxParams& p, const CUtensorMap*
             bulk_commit();
         }
         ++turn;
+    }
+}
+
+// The same where TMA cannot store (C's rows not 16-byte aligned) or C is read
+// (beta): the unit, transposed through the boxes.  Element (row, c) lies at word
+// row * 64 + (c + turn * row) % 64: an odd turn keeps the writes (a row to a
+// lane) apart, and one 2 past an odd ldc the reads, whose rows begin ldc
+// further on each time (at the same bank, else).
+// A row's 64 columns go out as the aligned 16-byte pieces inside them and one
+// piece's worth of single elements at the two ends.  (Single elements all along,
+// 64 bytes a store, 143 us at 8192 x 8192 x 2048; these 131, being bound by instructions;
+// TMA stores 60.)
+template <typename TOut>
+__device__ __forceinline__ void store_unit_plain(const MxParams& p, float alpha, uint8_t* boxes, int lane, int64_t row, int64_t col,
+                                                 const uint32_t (&v)[64]) {
+    float* words = reinterpret_cast<float*>(boxes);
+    const int turn = p.ldc & 1 ? static_cast<int>((p.ldc + 2) & 7) : 1;
+    __syncwarp();  // the last unit's rows have been read
+#pragma unroll
+    for (int c = 0; c < 64; ++c) words[lane * 64 + ((c + turn * lane) & 63)] = __uint_as_float(v[c]);
+    __syncwarp();
+    const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.M - row));
+    TOut* const C = static_cast<TOut*>(p.C) + row * p.ldc + col;
+    const TOut* const bias = p.bias != nullptr ? static_cast<const TOut*>(p.bias) + col : nullptr;
+    auto value = [&](int i, int c) {
+        const float b = bias != nullptr ? OutT<TOut>::load(bias + c) : 0.0f;
+        return fmaf(alpha, words[i * 64 + ((c + turn * i) & 63)], b);
+    };
+    if (p.beta == 0.0f && col + 64 <= p.N) {
+        constexpr int kE = 16 / sizeof(TOut), kL = 64 / kE;  // elements of a piece; lanes of a row
+        const int q = lane % kL;
+        for (int i0 = 0; i0 < rows; i0 += 32 / kL) {
+            const int i = i0 + lane / kL;
+            TOut* dst = C + i * p.ldc;
+            // elements before the first aligned piece; at the ends, kE in all
+            const int head = static_cast<int>((0 - reinterpret_cast<uintptr_t>(dst)) & 15) / static_cast<int>(sizeof(TOut));
+            const bool full = i < rows && (head == 0 || q < kL - 1);
+            const int c = head + q * kE;
+            TOut piece[kE];
+#pragma unroll
+            for (int e = 0; e < kE; ++e) OutT<TOut>::store(&piece[e], full ? value(i, c + e) : 0.0f);
+            uint4 w;
+            memcpy(&w, piece, 16);
+            if (full) *reinterpret_cast<uint4*>(dst + c) = w;
+            if (i < rows && head != 0 && q < kE) {
+                const int e = q < head ? q : (kL - 1) * kE + q;
+                OutT<TOut>::store(dst + e, value(i, e));
+            }
+        }
+        return;
+    }
+#pragma unroll 2
+    for (int i = 0; i < rows; ++i) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = h * 32 + lane;
+            if (col + c < p.N) {
+                TOut* dst = C + i * p.ldc + c;
+                const float b = bias != nullptr ? OutT<TOut>::load(bias + c) : 0.0f;
+                const float old = p.beta != 0.0f ? OutT<TOut>::load(dst) : 0.0f;
+                OutT<TOut>::store(dst, axpby(alpha, words[i * 64 + ((c + turn * i) & 63)], p.beta, old) + b);
+            }
+        }
     }
 }
 
@@ -401,9 +443,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     store_unit<TOut>(p, &tmC, alpha, boxes, lane, static_cast<int32_t>(row_base),
                                      static_cast<int32_t>(col0) + unit * 64, r, turn);
                 } else {
-                    uint32_t* square = reinterpret_cast<uint32_t*>(boxes);
-                    store_block<TOut>(p, alpha, square, lane, row_base, col0 + unit * 64, reinterpret_cast<uint32_t(&)[32]>(r[0]));
-                    store_block<TOut>(p, alpha, square, lane, row_base, col0 + unit * 64 + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
+                    store_unit_plain<TOut>(p, alpha, boxes, lane, row_base, col0 + unit * 64, r);
                 }
             }
         }

@@ -277,6 +277,9 @@ __global__ void __launch_bounds__(256) mx_quant_cols16_kernel(const T* __restric
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ __align__(16) uint32_t tile[128][64 + 4];
     __shared__ __align__(16) uint32_t out[128][16 + 4];
+    // the scales of 128 rows and 128 k: one tile (MXFP4) or two, which lie together
+    constexpr int kTiles = 32 / mx_block(kFormat);
+    __shared__ __align__(16) uint8_t tiles[kTiles * kMxTileBytes];
     const int t = threadIdx.x;
     const int64_t k0 = (blockIdx.x % blocks_k) * 128, c0 = (blockIdx.x / blocks_k) * 128;
     const TensorFactor g((kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f);
@@ -325,18 +328,19 @@ __global__ void __launch_bounds__(256) mx_quant_cols16_kernel(const T* __restric
             word[h] |= (k < K ? static_cast<uint32_t>(b.byte) : 0u) << (8 * p);
         }
     }
-    const int64_t s = (k0 + quarter * 32) / kB;
+    const int s = quarter * kPer;  // of the blocks in these 128 k
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int64_t c = c0 + 2 * pair + h;
-        *reinterpret_cast<uint4*>(&out[2 * pair + h][quarter * 4]) = make_uint4(four[h][0], four[h][1], four[h][2], four[h][3]);
-        if (c < cols && (s >> 2) < tiles_k) {
-            uint8_t* dst = scales + mx_scale_offset(c, s, tiles_k);
-            if constexpr (kPer == 1) *dst = static_cast<uint8_t>(word[h]);
-            else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(word[h]);
-        }
+        const int c = 2 * pair + h;
+        *reinterpret_cast<uint4*>(&out[c][quarter * 4]) = make_uint4(four[h][0], four[h][1], four[h][2], four[h][3]);
+        uint8_t* dst = tiles + mx_scale_offset(c, s, kTiles);
+        if constexpr (kPer == 1) *dst = static_cast<uint8_t>(word[h]);
+        else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(word[h]);
     }
     __syncthreads();
+    const int64_t first_tile = k0 / 128 * kTiles;
+    if (t < kTiles * (kMxTileBytes / 16) && first_tile + t / (kMxTileBytes / 16) < tiles_k)
+        reinterpret_cast<uint4*>(scales + mx_scale_offset(c0, first_tile * 4, tiles_k))[t] = reinterpret_cast<const uint4*>(tiles)[t];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int idx = i * 256 + t, orow = idx >> 2, ow = (idx & 3) * 4;  // 16 bytes of a result row

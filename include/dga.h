@@ -414,7 +414,7 @@ typedef enum { DGA_MXFP4 = 0, DGA_NVFP4 = 1 } dga_mx_format;
  *                 tiles of 128 rows x 4 blocks, the scale of row r and block s
  *                 at byte (r%32)*16 + (r/32%4)*4 + s%4 of tile
  *                 (r/128)*ceil(blocks/4) + s/4; blocks past K are written as
- *                 0, rows past R are not written (and never used)
+ *                 0, what rows past R hold is never used
  * codes and scales must be 16-byte aligned.  Errors: DGA_ERR_UNSUPPORTED for a
  * format or type; -3 transpose, -4 rows, -5 cols (outside [0, 2^31)), -6 X,
  * -7 ldx, -8 tensor_scale with DGA_MXFP4, -9 codes, -10 ld_codes, -11 scales;
