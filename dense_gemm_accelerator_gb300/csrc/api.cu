@@ -560,7 +560,7 @@ const char* dga_status_string(int status) {
     }
 }
 
-int dga_version(void) { return 310; }  // 0.3.1: split last waves on the tensor cores (INT8 included)
+int dga_version(void) { return 400; }  // 0.4.0: 4-bit microscaled matrices, Newton-Schulz orthogonalisation
 
 }  // extern "C"
 

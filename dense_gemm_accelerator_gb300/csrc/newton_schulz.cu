@@ -1390,8 +1390,7 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, unsigned cluster,
 }
 
 // One product: pair kernel where its tiles can occupy most of the machine's
-// CTA pairs, else the tile kernel with K in as many parts as there are idle
-// SMs, each at least 8 slots long (2 us: joining the parts takes as long).
+// CTA pairs, else the tile kernel with K in parts.
 cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_t rows, int64_t cols,
                            const DeviceInfo& dev, cudaStream_t s) {
     auto tiles = [&](int64_t size) {
@@ -1414,8 +1413,14 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
         return run(ns_pair_kernel<false, true>, PairPlan<true>::kThreads, PairPlan<true>::kLaunch);
     }
     const int64_t small = tiles(128);
+    // Parts of K while there are idle SMs: joining them takes 2 to 3 us, a slot
+    // 0.3 us.  Split operands with 8 slots or more gain from 4 parts (256^2 fp32
+    // 133 -> 123 us, 400 x 1000 fp32 166 -> 147 us, but 150^2, 6 slots, 109 ->
+    // 129 us); single ones from 16 slots to a part (700^2 bf16 119 us with, 132
+    // us from 4 slots to a part).
+    const uint32_t slots = p.num_kb * (p.split ? 2 : 1);
     uint32_t splits = 1;
-    while (splits < 4 && small * splits * 2 <= dev.sm_count && p.num_kb * (p.split ? 2 : 1) >= splits * 16) splits *= 2;
+    while (splits < 4 && small * splits * 2 <= dev.sm_count && slots >= (p.split ? std::max(8u, splits * 4) : splits * 16)) splits *= 2;
     return launch(p.split ? ns_tile_kernel<true> : ns_tile_kernel<false>, dim3(static_cast<unsigned>(small * splits)),
                   kTileThreads, splits, static_cast<int>(kTileLaunch), true, s, maps, p, splits);
 }
