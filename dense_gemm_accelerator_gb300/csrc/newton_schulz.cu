@@ -139,9 +139,9 @@ __device__ __forceinline__ void ns_result(const NsParams& p, uint32_t matrix, in
 }
 
 // The tensor maps of one product.  Operands: boxes of one 128-byte row of K
-// (64 fp16) x 128 rows, or, MN-major, 64 columns x 64 rows of K.  Values: 64
-// columns x 32 rows of one matrix (and mirrored, 32 x 64), so that what lies
-// past a matrix' padded rows is neither read nor written.
+// (64 fp16) x 128 rows, or, MN-major, 64 columns x 64 rows of K.  Values: 32 x
+// 32 of one matrix, so that what lies past a matrix' padded rows is neither
+// read nor written.
 struct NsMaps {
     CUtensorMap p_h, p_l, q_h, q_l, old_h, old_l, out_h, out_l, mirror_h, mirror_l, result;
 };
@@ -173,15 +173,20 @@ __device__ __forceinline__ void blend8(float* x, const uint4& hi, const uint4& l
     }
 }
 
-// ---- the epilogue: units of 32 rows x 64 columns, one warp each ----------------------------
+// ---- the epilogue: units of 32 rows x 32 columns, one warp each ----------------------------
 //
-// A warp has two boxes of 32 rows x 128 bytes.  The old values come into them
+// A warp has two boxes of 32 rows x 64 bytes.  The old values come into them
 // by TMA while the products run (hi, lo); lane l then takes row l's, in
 // swizzled 16-byte pieces, and puts the new ones there, which TMA stores.
 // (With a lane's own 16-byte loads and stores, one row per lane, the epilogue
 // was bound by the L1's one line per cycle: 8,000 to 20,000 clocks a tile.)
-constexpr uint32_t kBox32 = 32 * 128;
+constexpr uint32_t kBox32 = 32 * 64;
 constexpr uint32_t kUnitBytes = 2 * kBox32;
+
+// Byte offset of 16-byte piece `piece` (8 fp16) of a row in a box of 64-byte rows.
+__device__ __forceinline__ uint32_t unit_at(int row, int piece) {
+    return static_cast<uint32_t>(row) * 64u + (static_cast<uint32_t>(piece ^ ((row >> 1) & 3)) << 4);
+}
 
 // Starts the loads of a unit's old values (one lane).
 __device__ __forceinline__ void unit_prefetch(const NsParams& p, const NsMaps& maps, uint8_t* boxes, uint64_t* bar,
@@ -194,78 +199,69 @@ __device__ __forceinline__ void unit_prefetch(const NsParams& p, const NsMaps& m
 // The result's part of ns_unit: v to rows of m x n, or (transposed) of n x m.
 template <typename T>
 __device__ __forceinline__ void unit_result(const NsParams& p, const NsMaps& maps, uint8_t* boxes, uint32_t matrix,
-                                            int32_t row0, int32_t col0, int lane, const float (&v)[64]) {
-    constexpr int kPer = 16 / sizeof(T), kBoxCols = 128 / sizeof(T);
+                                            int32_t row0, int32_t col0, int lane, const float (&v)[32]) {
+    constexpr int kPer = 16 / sizeof(T);
+    // fp32 rows are 128 bytes and take both boxes
+    auto at = [](int row, int piece) { return sizeof(T) == 4 ? box_at(row, piece) : unit_at(row, piece); };
     if (p.transposed) {
         // column j of the unit becomes a row of 32
 #pragma unroll
-        for (int j = 0; j < 64; ++j) OutT<T>::store(reinterpret_cast<T*>(boxes) + j * 32 + lane, v[j]);
+        for (int j = 0; j < 32; ++j) OutT<T>::store(reinterpret_cast<T*>(boxes) + j * 32 + lane, v[j]);
     } else {
 #pragma unroll
-        for (int q = 0; q < 64 / kPer; ++q) {
+        for (int q = 0; q < 32 / kPer; ++q) {
             T w[kPer];
 #pragma unroll
             for (int e = 0; e < kPer; ++e) OutT<T>::store(&w[e], v[q * kPer + e]);
             uint4 x;
             memcpy(&x, w, 16);
-            *reinterpret_cast<uint4*>(boxes + (q / 8) * kBox32 + box_at(lane, q % 8)) = x;
+            *reinterpret_cast<uint4*>(boxes + at(lane, q)) = x;
         }
     }
     if (p.result_tma) {
         fence_async_shared();
         __syncwarp();
-        if (lane == 0 && row0 < p.m && col0 < p.n) {
-            if (p.transposed) {
-                tma_store_3d(&maps.result, boxes, row0, col0, static_cast<int32_t>(matrix));
-            } else {
-#pragma unroll
-                for (int b = 0; b < 64 / kBoxCols; ++b)
-                    if (col0 + b * kBoxCols < p.n)
-                        tma_store_3d(&maps.result, boxes + b * kBox32, col0 + b * kBoxCols, row0, static_cast<int32_t>(matrix));
-            }
+        if (lane == 0) {
+            if (row0 < p.m && col0 < p.n)
+                tma_store_3d(&maps.result, boxes, p.transposed ? row0 : col0, p.transposed ? col0 : row0, static_cast<int32_t>(matrix));
+            bulk_commit();
         }
-        if (lane == 0) bulk_commit();
         return;
     }
     __syncwarp();
     T* base = static_cast<T*>(p.result) + matrix * p.stride_o;
     if (p.transposed) {
         if (row0 + lane < p.m)
-            for (int j = 0; j < 64 && col0 + j < p.n; ++j)
+            for (int j = 0; j < 32 && col0 + j < p.n; ++j)
                 base[static_cast<int64_t>(col0 + j) * p.ldo + row0 + lane] = reinterpret_cast<const T*>(boxes)[j * 32 + lane];
-    } else {
+    } else if (col0 + lane < p.n) {
         for (int i = 0; i < 32 && row0 + i < p.m; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int c = h * 32 + lane, in = c % kBoxCols;
-                if (col0 + c < p.n)
-                    base[static_cast<int64_t>(row0 + i) * p.ldo + col0 + c] = *reinterpret_cast<const T*>(
-                        boxes + (c / kBoxCols) * kBox32 + box_at(i, in / kPer) + (in % kPer) * sizeof(T));
-            }
+            base[static_cast<int64_t>(row0 + i) * p.ldo + col0 + lane] =
+                *reinterpret_cast<const T*>(boxes + at(i, lane / kPer) + (lane % kPer) * sizeof(T));
     }
     __syncwarp();
 }
 
 // One unit of a tile, v its sums: lane l has row row0 + l, columns col0 ..
-// col0 + 63.  mirror: the tile is off the diagonal of a symmetric product, so
+// col0 + 31.  mirror: the tile is off the diagonal of a symmetric product, so
 // that its transpose is stored too.  On return the boxes' stores are under way.
 __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, uint8_t* boxes, uint64_t* bar, uint32_t phase,
                                         volatile int* abort_flag, uint32_t matrix, int32_t row0, int32_t col0, int lane,
-                                        bool mirror, float (&v)[64]) {
+                                        bool mirror, float (&v)[32]) {
     if (p.has_old) {
         if (!mbar_wait_bounded(bar, phase, abort_flag, kWaitLimitNs)) record_failure(kRoleEpilogue, abort_flag);
         uint4 lo = make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-            const uint4 hi = *reinterpret_cast<const uint4*>(boxes + box_at(lane, q));
-            if (p.old_lo) lo = *reinterpret_cast<const uint4*>(boxes + kBox32 + box_at(lane, q));
+        for (int q = 0; q < 4; ++q) {
+            const uint4 hi = *reinterpret_cast<const uint4*>(boxes + unit_at(lane, q));
+            if (p.old_lo) lo = *reinterpret_cast<const uint4*>(boxes + kBox32 + unit_at(lane, q));
             blend8(&v[q * 8], hi, lo, p.c_old, p.c_acc);
         }
     } else {
         // the boxes may still be read by the last unit's stores
         if (lane == 0) bulk_wait_read<0>();
 #pragma unroll
-        for (int j = 0; j < 64; ++j) v[j] *= p.c_acc;
+        for (int j = 0; j < 32; ++j) v[j] *= p.c_acc;
     }
     __syncwarp();
     if (p.last) {
@@ -274,13 +270,13 @@ __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, u
         else unit_result<__half>(p, maps, boxes, matrix, row0, col0, lane, v);
         return;
     }
-    uint32_t h[32], l[32];
+    uint32_t h[16], l[16];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < 4; ++q) {
         uint4 hi, lo;
         split8(&v[q * 8], hi, lo);
-        *reinterpret_cast<uint4*>(boxes + box_at(lane, q)) = hi;
-        if (p.out_lo) *reinterpret_cast<uint4*>(boxes + kBox32 + box_at(lane, q)) = lo;
+        *reinterpret_cast<uint4*>(boxes + unit_at(lane, q)) = hi;
+        if (p.out_lo) *reinterpret_cast<uint4*>(boxes + kBox32 + unit_at(lane, q)) = lo;
         h[4 * q] = hi.x, h[4 * q + 1] = hi.y, h[4 * q + 2] = hi.z, h[4 * q + 3] = hi.w;
         l[4 * q] = lo.x, l[4 * q + 1] = lo.y, l[4 * q + 2] = lo.z, l[4 * q + 3] = lo.w;
     }
@@ -293,8 +289,8 @@ __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, u
         bulk_commit();
     }
     if (mirror) {
-        // column j of the unit becomes a row of 32: 64 rows of 64 bytes, hi in
-        // the second box if there is no lo
+        // column j of the unit becomes a row of 32, hi in the second box if
+        // there is no lo
         uint16_t* mh = reinterpret_cast<uint16_t*>(p.out_lo ? boxes : boxes + kBox32);
         uint16_t* ml = reinterpret_cast<uint16_t*>(boxes + kBox32);
         if (p.out_lo) {
@@ -302,7 +298,7 @@ __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, u
             __syncwarp();
         }
 #pragma unroll
-        for (int j = 0; j < 64; ++j) {
+        for (int j = 0; j < 32; ++j) {
             mh[j * 32 + lane] = static_cast<uint16_t>(j & 1 ? h[j / 2] >> 16 : h[j / 2]);
             if (p.out_lo) ml[j * 32 + lane] = static_cast<uint16_t>(j & 1 ? l[j / 2] >> 16 : l[j / 2]);
         }
@@ -325,14 +321,15 @@ __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, u
 constexpr int kTileStages = 5;
 constexpr uint32_t kTileStage = 2 * 128 * 128;
 constexpr uint32_t kTileEpi = kTileStages * kTileStage;
-constexpr uint32_t kTileBar = kTileEpi + 8 * kUnitBytes;
-// full[S], empty[S], acc_full[2], acc_empty[2], joined, old_full[8], then tmem slot + abort flag
-constexpr uint32_t kTileLaunch = kTileBar + (2 * kTileStages + 5 + 8) * 8 + 16 + 1024;
-constexpr uint32_t kUnitSums = 64 * 32 * 4;  // a unit's sums
-static_assert(kTileEpi >= 2 * 8 * kUnitSums, "the parts' sums fit the ring twice");
+constexpr int kTileUnits = 16;  // of 32 x 32, one to an epilogue warp
+constexpr uint32_t kTileBar = kTileEpi + kTileUnits * kUnitBytes;
+// full[S], empty[S], acc_full[2], acc_empty[2], joined, old_full[U], then tmem slot + abort flag
+constexpr uint32_t kTileLaunch = kTileBar + (2 * kTileStages + 5 + kTileUnits) * 8 + 16 + 1024;
+constexpr uint32_t kUnitSums = 32 * 32 * 4;  // a unit's sums
+static_assert(kTileEpi >= 2 * kTileUnits * kUnitSums, "the parts' sums fit the ring twice");
 
-// Producer warp, MMA warp, 8 epilogue warps with a unit of the tile each.
-constexpr int kTileThreads = 320;
+// Producer warp, MMA warp, 16 epilogue warps with a unit of the tile each.
+constexpr int kTileThreads = 64 + 32 * kTileUnits;
 
 template <bool kSplit>
 __global__ void __launch_bounds__(kTileThreads, 1)
@@ -347,14 +344,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* joined = acc_empty + 2;
     uint64_t* old_full = joined + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + 8);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + kTileUnits);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     // accumulators: one, or the cross products' and two for the chunks in turn
     constexpr uint32_t kCols = kSplit ? 512 : 128;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t t = blockIdx.x / splits, part = blockIdx.x % splits;
     const uint32_t kb0 = part * p.num_kb / splits, kb1 = (part + 1) * p.num_kb / splits;
-    const uint32_t units = 8 / splits;  // of the tile's 8, what this CTA joins and stores
+    const uint32_t units = kTileUnits / splits;  // of the tile's, what this CTA joins and stores
     uint32_t matrix, tm, tn;
     ns_tile(p, t, matrix, tm, tn);
 
@@ -365,9 +362,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 8);
+            mbar_init(&acc_empty[b], kTileUnits);
         }
-        for (int w = 0; w < 8; ++w) mbar_init(&old_full[w], 1);
+        for (int w = 0; w < kTileUnits; ++w) mbar_init(&old_full[w], 1);
         mbar_init(joined, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -466,32 +463,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     }
     __syncwarp();
     if (warp >= 2) {
-        // Unit (quarter, half): 32 rows, 64 columns.  With K in parts, CTA c
+        // Unit (quarter, block): 32 rows, 32 columns.  With K in parts, CTA c
         // joins the quarters q % splits == c, `units` of them; slot i there is
-        // half i % 2 of quarter c + i / 2 * splits, and warp 2 + i's.  Once
+        // block i % 4 of quarter c + i / 4 * splits, and warp 2 + i's.  Once
         // every CTA's ring is done with, each sends its sums by bulk copies
         // from the ring's first half to the second halves of the joining CTAs,
         // which add them up in the parts' order.
-        const uint32_t e = warp - 2, quarter = warp & 3, half = e >> 2;
+        const uint32_t e = warp - 2, quarter = warp & 3, block = e >> 2;
         const uint32_t lane_base = (quarter * 32) << 16;
-        const uint32_t my_half = splits == 1 ? half : e & 1, my_quarter = splits == 1 ? quarter : part + (e >> 1) * splits;
-        const int32_t row0 = static_cast<int32_t>(tm * 128 + my_quarter * 32), col0 = static_cast<int32_t>(tn * 128 + my_half * 64);
+        const uint32_t my_block = splits == 1 ? block : e & 3, my_quarter = splits == 1 ? quarter : part + (e >> 2) * splits;
+        const int32_t row0 = static_cast<int32_t>(tm * 128 + my_quarter * 32), col0 = static_cast<int32_t>(tn * 128 + my_block * 32);
         uint8_t* boxes = smem + kTileEpi + e * kUnitBytes;
         if (p.has_old && e < units && lane == 0) unit_prefetch(p, maps, boxes, &old_full[e], matrix, row0, col0);
         __syncwarp();
-        float v[64];
+        float v[32];
         auto add = [&](uint32_t column) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(tmem + lane_base + column + block * 32, r);
+            tmem_ld_wait();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(tmem + lane_base + column + half * 64 + c * 32, r);
-                tmem_ld_wait();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[c * 32 + j] += __uint_as_float(r[j]);
-            }
+            for (int j = 0; j < 32; ++j) v[j] += __uint_as_float(r[j]);
         };
 #pragma unroll
-        for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
         const uint32_t n_chunks = kSplit ? (kb1 - kb0 + kChunk - 1) / kChunk : 1;
         for (uint32_t ch = 0; ch < n_chunks; ++ch) {
             if (!mbar_wait_bounded(&acc_full[ch & 1], ch >> 1 & 1, abort_flag, kWaitLimitNs)) {
@@ -510,25 +504,25 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (splits > 1) {
             uint8_t* sent = smem + e * kUnitSums;
 #pragma unroll
-            for (int j = 0; j < 64; ++j) reinterpret_cast<float*>(sent)[j * 32 + lane] = v[j];
+            for (int j = 0; j < 32; ++j) reinterpret_cast<float*>(sent)[j * 32 + lane] = v[j];
             fence_async_shared();
             __syncwarp();
             cluster_arrive_relaxed();
             cluster_wait();
             if (lane == 0) {
-                const uint32_t slot = half + 2 * (quarter / splits), to = quarter % splits;
-                const uint32_t at = smem_u32(smem + (8 + part * units + slot) * kUnitSums);
+                const uint32_t slot = block + 4 * (quarter / splits), to = quarter % splits;
+                const uint32_t at = smem_u32(smem + (kTileUnits + part * units + slot) * kUnitSums);
                 bulk_copy_to_cta(map_to_cta(at, to), smem_u32(sent), kUnitSums, map_to_cta(smem_u32(joined), to));
             }
             __syncwarp();
             if (e < units) {
                 if (!mbar_wait_bounded<true>(joined, 0, abort_flag, kWaitLimitNs)) record_failure(kRoleEpilogue, abort_flag);
 #pragma unroll
-                for (int j = 0; j < 64; ++j) v[j] = 0.0f;
+                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                 for (uint32_t q = 0; q < splits; ++q) {
-                    const float* src = reinterpret_cast<const float*>(smem + (8 + q * units + e) * kUnitSums) + lane;
+                    const float* src = reinterpret_cast<const float*>(smem + (kTileUnits + q * units + e) * kUnitSums) + lane;
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] += src[j * 32];
+                    for (int j = 0; j < 32; ++j) v[j] += src[j * 32];
                 }
             }
             __syncwarp();
@@ -557,43 +551,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // ---- the pair kernel: 256 x 256 on two CTAs, persistent --------------------------------
 
-// Warps: producer, MMA, epilogue: 8 epilogue warps of 128 columns and 5 ring
-// slots, or, kDeep, 4 warps of 256 columns, whose smaller staging leaves room
-// for a sixth slot.  A long K is bound by the bytes in flight, a short one by
-// the epilogue (bf16, deep against not: 4096^2 1107 / 1135 us, 2048^2 261 / 277
-// us, 12 x 1030 x 515 309 / 265 us); split operands keep their sums in
-// registers, so that they need the 8 warps.
+// Warps: producer, MMA, 8 epilogue warps of 128 columns (four units) each.
 constexpr uint32_t kPairStage = 2 * 128 * 128;  // each CTA's half of both operands
-constexpr uint32_t kDeepBlocks = 32;  // K blocks from which the deep ring is taken
-template <bool kDeep>
-struct PairPlan {
-    static constexpr int kStages = kDeep ? 6 : 5;
-    static constexpr int kWarps = kDeep ? 4 : 8;
-    static constexpr uint32_t kUnits = 8 / kWarps * 2;  // units of a warp: 32 rows x 256 columns are 4 of them
-    static constexpr int kThreads = 64 + 32 * kWarps;
-    static constexpr uint32_t kEpi = kStages * kPairStage;
-    static constexpr uint32_t kBar = kEpi + kWarps * kUnitBytes;
-    // full[S], empty[S], acc_full[2], acc_empty[2], drain, old_full[W], tmem slot + abort flag
-    static constexpr uint32_t kLaunch = kBar + (2 * kStages + 5 + kWarps) * 8 + 16 + 1024;
-};
+constexpr int kPairStages = 6;
+constexpr int kPairWarps = 8;
+constexpr uint32_t kPairUnits = 4;
+constexpr int kPairThreads = 64 + 32 * kPairWarps;
+constexpr uint32_t kPairEpi = kPairStages * kPairStage;
+constexpr uint32_t kPairBar = kPairEpi + kPairWarps * kUnitBytes;
+// full[S], empty[S], acc_full[2], acc_empty[2], drain, old_full[W], tmem slot + abort flag
+constexpr uint32_t kPairLaunch = kPairBar + (2 * kPairStages + 5 + kPairWarps) * 8 + 16 + 1024;
 
-template <bool kSplit, bool kDeep>
-__global__ void __launch_bounds__(PairPlan<kDeep>::kThreads, 1)
+template <bool kSplit>
+__global__ void __launch_bounds__(kPairThreads, 1)
     ns_pair_kernel(const __grid_constant__ NsMaps maps, NsParams p) {
-    using S = PairPlan<kDeep>;
-    constexpr int kPairStages = S::kStages;
     constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 256, 256);
     constexpr uint16_t kBothCtas = 0x3;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBar);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kPairBar);
     uint64_t* empty = full + kPairStages;
     uint64_t* acc_full = empty + kPairStages;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
     uint64_t* old_full = drain + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + S::kWarps);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + kPairWarps);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -606,10 +589,10 @@ __global__ void __launch_bounds__(PairPlan<kDeep>::kThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 2 * S::kWarps);  // one lane of each epilogue warp of both CTAs
+            mbar_init(&acc_empty[b], 2 * kPairWarps);  // one lane of each epilogue warp of both CTAs
         }
         mbar_init(drain, 1);
-        for (int w = 0; w < S::kWarps; ++w) mbar_init(&old_full[w], 1);
+        for (int w = 0; w < kPairWarps; ++w) mbar_init(&old_full[w], 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&maps.p_h);
@@ -729,14 +712,14 @@ __global__ void __launch_bounds__(PairPlan<kDeep>::kThreads, 1)
             mbar_wait_bounded(drain, 0, &never, kWaitLimitNs);
         }
     } else {
-        const uint32_t e = warp - 2, quarter = warp & 3, half = e >> 2;  // 128 columns, or all 256
+        const uint32_t e = warp - 2, quarter = warp & 3, half = e >> 2;  // 128 columns
         const uint32_t lane_base = (quarter * 32) << 16;
-        uint8_t* boxes = smem + S::kEpi + e * kUnitBytes;
+        uint8_t* boxes = smem + kPairEpi + e * kUnitBytes;
         uint32_t acc = 0, acc_phase = 0, old_phase = 0;
         bool ok = true;
         // unit u of tile t
         auto rows_of = [&](uint32_t tm) { return static_cast<int32_t>(tm * 256 + rank * 128 + quarter * 32); };
-        auto cols_of = [&](uint32_t tn, uint32_t u) { return static_cast<int32_t>(tn * 256 + half * 128 + u * 64); };
+        auto cols_of = [&](uint32_t tn, uint32_t u) { return static_cast<int32_t>(tn * 256 + half * 128 + u * 32); };
         auto prefetch = [&](uint32_t t, uint32_t u) {
             if (p.has_old && t < p.num_tiles && lane == 0) {
                 uint32_t matrix, tm, tn;
@@ -788,21 +771,19 @@ __global__ void __launch_bounds__(PairPlan<kDeep>::kThreads, 1)
                 tc_fence_after();
             }
             if (!ok) break;
-#pragma unroll(kDeep ? 1 : 2)
-            for (uint32_t u = 0; u < S::kUnits; ++u) {
-                float v[64];
+#pragma unroll(kSplit ? 4 : 1)
+            for (uint32_t u = 0; u < kPairUnits; ++u) {
+                float v[32];
                 if constexpr (kSplit) {
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] = sum[u * 64 + j];
+                    for (int j = 0; j < 32; ++j) v[j] = sum[u * 32 + j];
                 } else {
-                    uint32_t r[64];
-                    const uint32_t at = tmem + lane_base + acc * 256 + half * 128 + u * 64;
-                    tmem_ld_32x32b_x32(at, reinterpret_cast<uint32_t(&)[32]>(r[0]));
-                    tmem_ld_32x32b_x32(at + 32, reinterpret_cast<uint32_t(&)[32]>(r[32]));
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tmem + lane_base + acc * 256 + half * 128 + u * 32, r);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) v[j] = __uint_as_float(r[j]);
-                    if (u == S::kUnits - 1) {
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                    if (u == kPairUnits - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
@@ -811,7 +792,7 @@ __global__ void __launch_bounds__(PairPlan<kDeep>::kThreads, 1)
                 }
                 ns_unit(p, maps, boxes, &old_full[e], old_phase, abort_flag, matrix, rows_of(tm), cols_of(tn, u), lane, mirror, v);
                 old_phase ^= 1;
-                if (u + 1 < S::kUnits) prefetch(t, u + 1);
+                if (u + 1 < kPairUnits) prefetch(t, u + 1);
                 else prefetch(t + n_clusters, 0);
             }
         }
@@ -1302,21 +1283,22 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                    CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// batch matrices of rows x cols values, boxes of box_cols x box_rows of one of
-// them: 128-byte rows swizzled, narrower ones not.
+// batch matrices of rows x cols values, boxes of 32 x 32 of one of them, whose
+// rows in shared memory are swizzled or not.
 cudaError_t value_map(CUtensorMap* map, int type, const void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld,
-                      int64_t stride, uint32_t box_cols, uint32_t box_rows, bool swizzle) {
+                      int64_t stride, bool swizzle) {
     auto fn = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t es = type == DGA_F32 ? 4 : 2;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
     // a single matrix has no stride to speak of: any multiple of 16 bytes
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * es, batch > 1 ? static_cast<cuuint64_t>(stride) * es : static_cast<cuuint64_t>(ld) * es};
-    cuuint32_t box[3] = {box_cols, box_rows, 1};
+    cuuint32_t box[3] = {32, 32, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(map, type == DGA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
                     const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : type == DGA_F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -1404,13 +1386,9 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
     const int64_t pairs = dev.sm_count / 2;
     const int64_t big = tiles(256);
     if (big >= pairs * 3 / 4) {
-        auto run = [&](auto kernel, int threads, uint32_t smem) {
-            return launch(kernel, dim3(static_cast<unsigned>(2 * std::min(big, pairs))), threads, 2, static_cast<int>(smem), true, s,
-                          maps, p);
-        };
-        if (p.split) return run(ns_pair_kernel<true, false>, PairPlan<false>::kThreads, PairPlan<false>::kLaunch);
-        if (p.num_kb < kDeepBlocks) return run(ns_pair_kernel<false, false>, PairPlan<false>::kThreads, PairPlan<false>::kLaunch);
-        return run(ns_pair_kernel<false, true>, PairPlan<true>::kThreads, PairPlan<true>::kLaunch);
+        return launch(p.split ? ns_pair_kernel<true> : ns_pair_kernel<false>,
+                      dim3(static_cast<unsigned>(2 * std::min(big, pairs))), kPairThreads, 2, static_cast<int>(kPairLaunch), true,
+                      s, maps, p);
     }
     const int64_t small = tiles(128);
     // Parts of K while there are idle SMs: joining them takes 2 to 3 us, a slot
@@ -1587,8 +1565,8 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
     } mx_h[2], mx_l[2], ma_h, ma_l, mb_h, mb_l;
     auto make = [&](Maps* m, const __half* base, int64_t ld, bool square) {
         if (e == cudaSuccess) e = half_map(&m->op, base, all_rows, ld, 128);
-        if (e == cudaSuccess) e = value_map(&m->value, DGA_F16, base, ld, pl.mp, a.batch, ld, pl.mp * ld, 64, 32, true);
-        if (e == cudaSuccess && square) e = value_map(&m->mirror, DGA_F16, base, ld, pl.mp, a.batch, ld, pl.mp * ld, 32, 64, false);
+        if (e == cudaSuccess) e = value_map(&m->value, DGA_F16, base, ld, pl.mp, a.batch, ld, pl.mp * ld, true);
+        if (e == cudaSuccess && square) e = value_map(&m->mirror, DGA_F16, base, ld, pl.mp, a.batch, ld, pl.mp * ld, false);
         if (e == cudaSuccess && !square) e = half_map(&m->mn, base, all_rows, ld, 64);
     };
     for (int i = 0; i < 2; ++i) {
@@ -1606,9 +1584,7 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
     }
     CUtensorMap result = ma_h.value;  // not used without result_tma
     if (base.result_tma && e == cudaSuccess) {
-        const uint32_t box_cols = a.out_dtype == DGA_F32 ? 32 : 64;
-        e = pl.transposed ? value_map(&result, a.out_dtype, a.O, a.cols, a.rows, a.batch, a.ldo, a.stride_o, 32, 64, false)
-                          : value_map(&result, a.out_dtype, a.O, a.cols, a.rows, a.batch, a.ldo, a.stride_o, box_cols, 32, true);
+        e = value_map(&result, a.out_dtype, a.O, a.cols, a.rows, a.batch, a.ldo, a.stride_o, !pl.transposed);
     }
     if (e != cudaSuccess) return e;
 
