@@ -120,27 +120,11 @@ __global__ void __launch_bounds__(256) mx_quant_rows16_kernel(const T* __restric
                 w[q] = (k + 2 * q < K ? static_cast<uint32_t>(bits[2 * q]) : 0u) |
                        (k + 2 * q + 1 < K ? static_cast<uint32_t>(bits[2 * q + 1]) << 16 : 0u);
         }
-        constexpr int kB = mx_block(kFormat), kPer = 32 / kB;  // blocks of a thread
-        uint32_t out[4], bytes = 0;
-#pragma unroll
-        for (int p = 0; p < kPer; ++p) {
-            uint32_t m2 = 0;
-#pragma unroll
-            for (int q = 0; q < kB / 2; ++q) m2 = max_mag2(m2, w[p * (kB / 2) + q]);
-            // the larger half as fp32 bits (infinity and NaN stay what they are)
-            const uint32_t m16 = max(m2 & 0xffffu, m2 >> 16);
-            const BlockScale b = block_scale<kFormat>(mag_bits(half_value<T>(m16, 0)), g);
-#pragma unroll
-            for (int o = 0; o < kB / 8; ++o) {
-                float t[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) t[q] = half_value<T>(w[p * (kB / 2) + o * 4 + q / 2], q & 1);
-                over_unit8<kFormat>(t, b);
-                out[p * (kB / 8) + o] = codes8(t);
-            }
-            bytes |= (k + p * kB < K ? static_cast<uint32_t>(b.byte) : 0u) << (8 * p);
-        }
-        if (k < K) *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(r) * ldc + (k >> 1)) = make_uint4(out[0], out[1], out[2], out[3]);
+        constexpr int kPer = 32 / mx_block(kFormat);  // blocks of a thread
+        uint4 out;
+        uint32_t bytes;
+        quantize_run16<kFormat, T>(w, g, out, bytes);  // past the last value: zero codes and scales
+        if (k < K) *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(r) * ldc + (k >> 1)) = out;
         uint8_t* dst = scales + mx_scale_offset(r, static_cast<int64_t>(run) * kPer, tiles_k);
         if constexpr (kPer == 1) *dst = static_cast<uint8_t>(bytes);
         else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(bytes);

@@ -145,19 +145,36 @@ __device__ __forceinline__ void load_run(int type, const void* src, int64_t left
 }
 
 // Their 16 bytes of codes, and scale bytes (one block or two).
-template <int kFormat>
-__device__ __forceinline__ void quantize_run(int type, const uint32_t (&raw)[32], const TensorFactor& g, uint4& codes, uint32_t& bytes) {
-    float x[32];
-    if (type == DGA_F32) {
+template <int kFormat, typename T>
+__device__ __forceinline__ void quantize_run16(const uint32_t* w, const TensorFactor& g, uint4& codes, uint32_t& bytes) {
+    constexpr int kB = mx_block(kFormat);
+    uint32_t out[4];
+    bytes = 0;
 #pragma unroll
-        for (int q = 0; q < 32; ++q) x[q] = __uint_as_float(raw[q]);
-    } else if (type == DGA_BF16) {
+    for (int p = 0; p < 32 / kB; ++p) {
+        uint32_t m2 = 0;
 #pragma unroll
-        for (int q = 0; q < 32; ++q) x[q] = half_value<__nv_bfloat16>(raw[q / 2], q & 1);
-    } else {
+        for (int q = 0; q < kB / 2; ++q) m2 = max_mag2(m2, w[p * (kB / 2) + q]);
+        // the larger half as fp32 bits (infinity and NaN stay what they are)
+        const uint32_t m16 = max(m2 & 0xffffu, m2 >> 16);
+        const BlockScale b = block_scale<kFormat>(mag_bits(half_value<T>(m16, 0)), g);
 #pragma unroll
-        for (int q = 0; q < 32; ++q) x[q] = half_value<__half>(raw[q / 2], q & 1);
+        for (int o = 0; o < kB / 8; ++o) {
+            float t[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) t[q] = half_value<T>(w[p * (kB / 2) + o * 4 + q / 2], q & 1);
+            over_unit8<kFormat>(t, b);
+            out[p * (kB / 8) + o] = codes8(t);
+        }
+        bytes |= static_cast<uint32_t>(b.byte) << (8 * p);
     }
+    codes = make_uint4(out[0], out[1], out[2], out[3]);
+}
+template <int kFormat>
+__device__ __forceinline__ void quantize_run(int type, const uint32_t (&raw)[32], const TensorFactor& g, uint4& codes,
+                                             uint32_t& bytes) {
+    if (type == DGA_BF16) return quantize_run16<kFormat, __nv_bfloat16>(raw, g, codes, bytes);
+    if (type == DGA_F16) return quantize_run16<kFormat, __half>(raw, g, codes, bytes);
     constexpr int kB = mx_block(kFormat);
     uint32_t out[4];
     bytes = 0;
@@ -165,13 +182,13 @@ __device__ __forceinline__ void quantize_run(int type, const uint32_t (&raw)[32]
     for (int p = 0; p < 32 / kB; ++p) {
         uint32_t m = 0;
 #pragma unroll
-        for (int q = 0; q < kB; ++q) m = max(m, mag_bits(x[p * kB + q]));
+        for (int q = 0; q < kB; ++q) m = max(m, raw[p * kB + q] & 0x7fffffffu);
         const BlockScale b = block_scale<kFormat>(m, g);
 #pragma unroll
         for (int o = 0; o < kB / 8; ++o) {
             float t[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) t[q] = x[p * kB + o * 8 + q];
+            for (int q = 0; q < 8; ++q) t[q] = __uint_as_float(raw[p * kB + o * 8 + q]);
             over_unit8<kFormat>(t, b);
             out[p * (kB / 8) + o] = codes8(t);
         }
