@@ -10,7 +10,7 @@ using namespace dga;
 
 namespace {
 
-constexpr int64_t kMaxDim = int64_t{1} << 31;  // tensor maps count rows and bytes in 32 bits
+constexpr int64_t kMaxDim = int64_t{1} << 30;  // the kernels count rows, bytes and scales in 31 bits
 
 bool format_ok(int format) { return format == DGA_MXFP4 || format == DGA_NVFP4; }
 bool float_type(int t) { return t == DGA_F32 || t == DGA_BF16 || t == DGA_F16; }

@@ -152,7 +152,7 @@ __device__ __forceinline__ void store_unit(const MxParams& p, const CUtensorMap*
                     memcpy(&w[e], two, 4);
                 }
             }
-            *reinterpret_cast<uint4*>(box + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            st_shared_v4(smem_u32(box) + lane * 128 + ((q ^ (lane & 7)) << 4), make_uint4(w[0], w[1], w[2], w[3]));
         }
         fence_async_shared();
         __syncwarp();
@@ -165,64 +165,44 @@ __device__ __forceinline__ void store_unit(const MxParams& p, const CUtensorMap*
 }
 
 // The same where TMA cannot store (C's rows not 16-byte aligned) or C is read
-// (beta): the unit, transposed through the boxes.  Element (row, c) lies at word
-// row * 64 + (c + turn * row) % 64: an odd turn keeps the writes (a row to a
-// lane) apart, and one 2 past an odd ldc the reads, whose rows begin ldc
-// further on each time (at the same bank, else).
-// A row's 64 columns go out as the aligned 16-byte pieces inside them and one
-// piece's worth of single elements at the two ends.  (Single elements all along,
-// 64 bytes a store, 143 us at 8192 x 8192 x 2048; these 131, being bound by instructions;
-// TMA stores 60.)
+// (beta): the unit, transposed through the boxes, row by row with a lane on
+// columns l and 32 + l.  Element (row, c) lies at word row * 64 + (c + row) % 64,
+// so that neither direction meets in a bank.
 template <typename TOut>
 __device__ __forceinline__ void store_unit_plain(const MxParams& p, float alpha, uint8_t* boxes, int lane, int64_t row, int64_t col,
                                                  const uint32_t (&v)[64]) {
-    float* words = reinterpret_cast<float*>(boxes);
-    const int turn = p.ldc & 1 ? static_cast<int>((p.ldc + 2) & 7) : 1;
+    const uint32_t words = smem_u32(boxes);
     __syncwarp();  // the last unit's rows have been read
 #pragma unroll
-    for (int c = 0; c < 64; ++c) words[lane * 64 + ((c + turn * lane) & 63)] = __uint_as_float(v[c]);
+    for (int c = 0; c < 64; ++c) st_shared_u32(words + (lane * 64 + ((c + lane) & 63)) * 4, v[c]);
     __syncwarp();
-    const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.M - row));
-    TOut* const C = static_cast<TOut*>(p.C) + row * p.ldc + col;
-    const TOut* const bias = p.bias != nullptr ? static_cast<const TOut*>(p.bias) + col : nullptr;
-    auto value = [&](int i, int c) {
-        const float b = bias != nullptr ? OutT<TOut>::load(bias + c) : 0.0f;
-        return fmaf(alpha, words[i * 64 + ((c + turn * i) & 63)], b);
-    };
-    if (p.beta == 0.0f && col + 64 <= p.N) {
-        constexpr int kE = 16 / sizeof(TOut), kL = 64 / kE;  // elements of a piece; lanes of a row
-        const int q = lane % kL;
-        for (int i0 = 0; i0 < rows; i0 += 32 / kL) {
-            const int i = i0 + lane / kL;
-            TOut* dst = C + i * p.ldc;
-            // elements before the first aligned piece; at the ends, kE in all
-            const int head = static_cast<int>((0 - reinterpret_cast<uintptr_t>(dst)) & 15) / static_cast<int>(sizeof(TOut));
-            const bool full = i < rows && (head == 0 || q < kL - 1);
-            const int c = head + q * kE;
-            TOut piece[kE];
-#pragma unroll
-            for (int e = 0; e < kE; ++e) OutT<TOut>::store(&piece[e], full ? value(i, c + e) : 0.0f);
-            uint4 w;
-            memcpy(&w, piece, 16);
-            if (full) *reinterpret_cast<uint4*>(dst + c) = w;
-            if (i < rows && head != 0 && q < kE) {
-                const int e = q < head ? q : (kL - 1) * kE + q;
-                OutT<TOut>::store(dst + e, value(i, e));
-            }
-        }
-        return;
+    const bool in0 = col + lane < p.N, in1 = col + 32 + lane < p.N;
+    float b0 = 0.0f, b1 = 0.0f;
+    if (p.bias != nullptr) {
+        const TOut* bias = static_cast<const TOut*>(p.bias) + col + lane;
+        if (in0) b0 = OutT<TOut>::load(bias);
+        if (in1) b1 = OutT<TOut>::load(bias + 32);
     }
-#pragma unroll 2
-    for (int i = 0; i < rows; ++i) {
+    TOut* dst = static_cast<TOut*>(p.C) + row * p.ldc + col + lane;
+    const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.M - row));
+    for (int i0 = 0; i0 < rows; i0 += 8) {
+        float x[8][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int c = h * 32 + lane;
-            if (col + c < p.N) {
-                TOut* dst = C + i * p.ldc + c;
-                const float b = bias != nullptr ? OutT<TOut>::load(bias + c) : 0.0f;
-                const float old = p.beta != 0.0f ? OutT<TOut>::load(dst) : 0.0f;
-                OutT<TOut>::store(dst, axpby(alpha, words[i * 64 + ((c + turn * i) & 63)], p.beta, old) + b);
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t line = words + (i0 + i) * 256;
+            x[i][0] = ld_shared_f32(line + ((lane + i0 + i) & 63) * 4);
+            x[i][1] = ld_shared_f32(line + ((lane + 32 + i0 + i) & 63) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i, dst += p.ldc) {
+            const bool in = i0 + i < rows;
+            float old0 = 0.0f, old1 = 0.0f;
+            if (p.beta != 0.0f) {
+                if (in && in0) old0 = OutT<TOut>::load(dst);
+                if (in && in1) old1 = OutT<TOut>::load(dst + 32);
             }
+            if (in && in0) OutT<TOut>::store(dst, axpby(alpha, x[i][0], p.beta, old0) + b0);
+            if (in && in1) OutT<TOut>::store(dst + 32, axpby(alpha, x[i][1], p.beta, old1) + b1);
         }
     }
 }
@@ -382,15 +362,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     break;
                 }
                 // a tile's lane l: the four scales of rows l, 32 + l, 64 + l, 96 + l
-                const uint8_t* src = smem + stage * S::kStage + S::kA + S::kB + lane * 16;
+                const uint32_t src = smem_u32(smem + stage * S::kStage + S::kA + S::kB) + lane * 16;
                 uint32_t r[S::kSfCols];
+                auto take = [&](int at, uint32_t from) {
+                    const uint4 v = ld_shared_v4(from);
+                    r[at] = v.x, r[at + 1] = v.y, r[at + 2] = v.z, r[at + 3] = v.w;
+                };
 #pragma unroll
                 for (int j = 0; j < S::kSf; ++j) {
-                    *reinterpret_cast<uint4*>(&r[4 * j]) = *reinterpret_cast<const uint4*>(src + j * kMxTileBytes);
+                    take(4 * j, src + j * kMxTileBytes);
 #pragma unroll
                     for (int b = 0; b < 2; ++b)
-                        *reinterpret_cast<uint4*>(&r[4 * S::kSf + 8 * j + 4 * b]) =
-                            *reinterpret_cast<const uint4*>(src + S::kSfa + (b * S::kSf + j) * kMxTileBytes);
+                        take(4 * S::kSf + 8 * j + 4 * b, src + S::kSfa + (b * S::kSf + j) * kMxTileBytes);
                 }
                 tc_fence_after();
                 const uint32_t dst = tmem + lane_base + S::kSfCol + (fill & 1) * S::kSfCols;
@@ -578,6 +561,7 @@ __global__ void __launch_bounds__(kFused ? 320 : 192, (SkinnyPlan<kFormat, kN>::
             for (uint32_t kb = kb0 + first; kb < kb1; ++kb) {
                 if (!mbar_wait_bounded(&empty[stage], phase, abort_flag, kWaitLimitNs)) {
                     record_failure(kRoleProducer, abort_flag);
+                    __nanosleep(20000);  // let copies already issued land before teardown
                     break;
                 }
                 load_w(stage, kb);
@@ -644,7 +628,7 @@ __global__ void __launch_bounds__(kFused ? 320 : 192, (SkinnyPlan<kFormat, kN>::
                 break;
             }
             uint8_t* x = smem + stage * S::kStage + S::kW;
-            *reinterpret_cast<uint4*>(x + row * 128 + ((run ^ (row & 7)) << 4)) = codes;
+            st_shared_v4(smem_u32(x) + row * 128 + ((run ^ (row & 7)) << 4), codes);
             uint8_t* scale = x + S::kX + S::kSw + row * 16;  // block b: byte b % 4 of tile b / 4
             if constexpr (kFormat == DGA_MXFP4) scale[(run >> 2) * kMxTileBytes + (run & 3)] = static_cast<uint8_t>(bytes);
             else *reinterpret_cast<uint16_t*>(scale + (run >> 1) * kMxTileBytes + (run & 1) * 2) = static_cast<uint16_t>(bytes);

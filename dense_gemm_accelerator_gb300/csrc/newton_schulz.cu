@@ -2,7 +2,7 @@
 //
 // G (one matrix or a batch) is scaled to X = G / (|G|_F + eps), transposed
 // where it has more rows than columns (m <= n from here on), and each step
-// replaces X by a odd quintic of it,
+// replaces X by an odd quintic of it,
 //
 //     A = X X^T,   B = b A + c A^2,   X <- a X + B X,
 //
@@ -18,12 +18,12 @@
 //     X would round every step's a X, an error in all directions, which the
 //     following steps amplify by up to a per step where X's singular values
 //     are small (simulated: 1e-2 to 4e-2 off for momentum of low rank).
-//   * 16-bit output: the products take hi alone.  Their roundings multiply A,
-//     B or X by 1 + O(2^-12) on either side and so stay within X's own
-//     singular subspaces: 1e-4 to 1.7e-3 off, at or below the output's own
-//     rounding (1.7e-3).
-//   * fp32 output, and matrices of up to kSmallRows rows, whose time goes to
-//     launches and not to products: hi lo + lo hi + hi hi, 22-bit operands.
+//   * bf16 output: the products take hi alone.  Their roundings multiply A, B
+//     or X by 1 + O(2^-12) on either side and so stay within X's own singular
+//     subspaces: 1e-4 to 1.7e-3 off, at or below the output's own rounding
+//     (1.7e-3).
+//   * fp32 and fp16 output, and matrices of up to kSmallRows rows, whose time
+//     goes to latency and not to products: hi lo + lo hi + hi hi, 22 bits.
 //     The tensor cores' fp32 accumulation cuts off instead of rounding, half a
 //     unit of the sum lost per MMA on average (2.2e-5 off the result at K =
 //     4099 x 3), so the hi hi products are accumulated in chunks of 128 values
@@ -36,7 +36,8 @@
 // or as the result: `pair` (256 x 256 tiles on CTA pairs, persistent) where
 // there are enough tiles to fill the machine, `tile` (128 x 128 tiles, K shared
 // by a cluster and joined through distributed shared memory in a fixed order)
-// below.  Every launch is a programmatic dependent of the one before.
+// below; every launch is a programmatic dependent of the one before.  Up to 128
+// rows one launch of a third kernel does all of it on chip.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -206,7 +207,18 @@ __device__ __forceinline__ void unit_result(const NsParams& p, const NsMaps& map
     if (p.transposed) {
         // column j of the unit becomes a row of 32
 #pragma unroll
-        for (int j = 0; j < 32; ++j) OutT<T>::store(reinterpret_cast<T*>(boxes) + j * 32 + lane, v[j]);
+        for (int j = 0; j < 32; ++j) {
+            const uint32_t to = smem_u32(boxes) + (j * 32 + lane) * sizeof(T);
+            T x;
+            OutT<T>::store(&x, v[j]);
+            if constexpr (sizeof(T) == 4) {
+                st_shared_u32(to, __float_as_uint(x));
+            } else {
+                uint16_t bits;
+                memcpy(&bits, &x, 2);
+                st_shared_u16(to, bits);
+            }
+        }
     } else {
 #pragma unroll
         for (int q = 0; q < 32 / kPer; ++q) {
@@ -215,7 +227,7 @@ __device__ __forceinline__ void unit_result(const NsParams& p, const NsMaps& map
             for (int e = 0; e < kPer; ++e) OutT<T>::store(&w[e], v[q * kPer + e]);
             uint4 x;
             memcpy(&x, w, 16);
-            *reinterpret_cast<uint4*>(boxes + at(lane, q)) = x;
+            st_shared_v4(smem_u32(boxes) + at(lane, q), x);
         }
     }
     if (p.result_tma) {
@@ -248,13 +260,14 @@ __device__ __forceinline__ void unit_result(const NsParams& p, const NsMaps& map
 __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, uint8_t* boxes, uint64_t* bar, uint32_t phase,
                                         volatile int* abort_flag, uint32_t matrix, int32_t row0, int32_t col0, int lane,
                                         bool mirror, float (&v)[32]) {
+    const uint32_t box = smem_u32(boxes);
     if (p.has_old) {
         if (!mbar_wait_bounded(bar, phase, abort_flag, kWaitLimitNs)) record_failure(kRoleEpilogue, abort_flag);
         uint4 lo = make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const uint4 hi = *reinterpret_cast<const uint4*>(boxes + unit_at(lane, q));
-            if (p.old_lo) lo = *reinterpret_cast<const uint4*>(boxes + kBox32 + unit_at(lane, q));
+            const uint4 hi = ld_shared_v4(box + unit_at(lane, q));
+            if (p.old_lo) lo = ld_shared_v4(box + kBox32 + unit_at(lane, q));
             blend8(&v[q * 8], hi, lo, p.c_old, p.c_acc);
         }
     } else {
@@ -275,8 +288,8 @@ __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, u
     for (int q = 0; q < 4; ++q) {
         uint4 hi, lo;
         split8(&v[q * 8], hi, lo);
-        *reinterpret_cast<uint4*>(boxes + unit_at(lane, q)) = hi;
-        if (p.out_lo) *reinterpret_cast<uint4*>(boxes + kBox32 + unit_at(lane, q)) = lo;
+        st_shared_v4(box + unit_at(lane, q), hi);
+        if (p.out_lo) st_shared_v4(box + kBox32 + unit_at(lane, q), lo);
         h[4 * q] = hi.x, h[4 * q + 1] = hi.y, h[4 * q + 2] = hi.z, h[4 * q + 3] = hi.w;
         l[4 * q] = lo.x, l[4 * q + 1] = lo.y, l[4 * q + 2] = lo.z, l[4 * q + 3] = lo.w;
     }
@@ -291,16 +304,17 @@ __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, u
     if (mirror) {
         // column j of the unit becomes a row of 32, hi in the second box if
         // there is no lo
-        uint16_t* mh = reinterpret_cast<uint16_t*>(p.out_lo ? boxes : boxes + kBox32);
-        uint16_t* ml = reinterpret_cast<uint16_t*>(boxes + kBox32);
+        uint8_t* mh = p.out_lo ? boxes : boxes + kBox32;
+        uint8_t* ml = boxes + kBox32;
+        const uint32_t mh_s = smem_u32(mh) + lane * 2, ml_s = smem_u32(ml) + lane * 2;
         if (p.out_lo) {
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
         }
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-            mh[j * 32 + lane] = static_cast<uint16_t>(j & 1 ? h[j / 2] >> 16 : h[j / 2]);
-            if (p.out_lo) ml[j * 32 + lane] = static_cast<uint16_t>(j & 1 ? l[j / 2] >> 16 : l[j / 2]);
+            st_shared_u16(mh_s + j * 64, j & 1 ? h[j / 2] >> 16 : h[j / 2]);
+            if (p.out_lo) st_shared_u16(ml_s + j * 64, j & 1 ? l[j / 2] >> 16 : l[j / 2]);
         }
         fence_async_shared();
         __syncwarp();
@@ -436,6 +450,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     if (!next_full(hi) || !next_full(lo) ||
                         (begins && !mbar_wait_bounded(&acc_empty[chunk & 1], (chunk >> 1 & 1) ^ 1, abort_flag, kWaitLimitNs))) {
                         record_failure(kRoleMma, abort_flag);
+                        __nanosleep(200000);  // let the MMAs issued finish
                         break;
                     }
                     tc_fence_after();
@@ -504,7 +519,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (splits > 1) {
             uint8_t* sent = smem + e * kUnitSums;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) reinterpret_cast<float*>(sent)[j * 32 + lane] = v[j];
+            for (int j = 0; j < 32; ++j) st_shared_u32(smem_u32(sent) + (j * 32 + lane) * 4, __float_as_uint(v[j]));
             fence_async_shared();
             __syncwarp();
             cluster_arrive_relaxed();
@@ -520,9 +535,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                 for (uint32_t q = 0; q < splits; ++q) {
-                    const float* src = reinterpret_cast<const float*>(smem + (kTileUnits + q * units + e) * kUnitSums) + lane;
+                    const uint32_t src = smem_u32(smem + (kTileUnits + q * units + e) * kUnitSums) + lane * 4;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] += src[j * 32];
+                    for (int j = 0; j < 32; ++j) v[j] += ld_shared_f32(src + j * 128);
                 }
             }
             __syncwarp();
@@ -980,7 +995,6 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
     uint8_t* al = ah + kABytes;
     uint8_t* bh = al + kABytes;
     uint8_t* bl = bh + kABytes;
-    float* red = reinterpret_cast<float*>(bh);
 
     if (tid == 0) {
         mbar_init(&done, 1);
@@ -1042,15 +1056,15 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
                 split8(x[b][q], hi, lo);
                 if (!c.transposed) {
                     const uint32_t at = b * kXBox + box_at(line, (at16 >> 3) + q);
-                    *reinterpret_cast<uint4*>(xh + at) = hi;
-                    *reinterpret_cast<uint4*>(xl + at) = lo;
+                    st_shared_v4(smem_u32(xh) + at, hi);
+                    st_shared_v4(smem_u32(xl) + at, lo);
                 } else {
                     const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const uint32_t at = b * kXBox + box_at(at16 + q * 8 + j, line >> 3) + (line & 7) * 2;
-                        *reinterpret_cast<uint16_t*>(xh + at) = static_cast<uint16_t>(j & 1 ? h[j / 2] >> 16 : h[j / 2]);
-                        *reinterpret_cast<uint16_t*>(xl + at) = static_cast<uint16_t>(j & 1 ? l[j / 2] >> 16 : l[j / 2]);
+                        st_shared_u16(smem_u32(xh) + at, j & 1 ? h[j / 2] >> 16 : h[j / 2]);
+                        st_shared_u16(smem_u32(xl) + at, j & 1 ? l[j / 2] >> 16 : l[j / 2]);
                     }
                 }
             }
@@ -1063,7 +1077,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
     const int row = quarter * 32 + lane;  // of A, B and X
     const uint32_t lane_base = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t xh_s = smem_u32(xh), xl_s = smem_u32(xl), ah_s = smem_u32(ah), al_s = smem_u32(al);
-    const uint32_t bh_s = smem_u32(bh), bl_s = smem_u32(bl);
+    const uint32_t bh_s = smem_u32(bh), bl_s = smem_u32(bl), red_s = bh_s;  // `red`: floats
     constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 128, 128);
     uint32_t phase = 0;
     auto wait_done = [&]() {
@@ -1129,15 +1143,15 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
                     uint4 hi, lo;
                     split8(&v[q * 8], hi, lo);
                     const uint32_t at = (b16 >> 2) * kXBox + box_at(row, (b16 & 3) * 2 + q);
-                    *reinterpret_cast<uint4*>(ah + at) = hi;
-                    *reinterpret_cast<uint4*>(al + at) = lo;
+                    st_shared_v4(ah_s + at, hi);
+                    st_shared_v4(al_s + at, lo);
                 }
             } else {
                 // red[(share * per + column) * 128 + row] of the joining CTA
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int col = b16 * 16 + q * 8;  // one CTA for 8 columns
-                    const uint32_t to = map_to_cta(smem_u32(red + (rank * per + (col & (per - 1))) * 128 + row), col >> shift);
+                    const uint32_t to = map_to_cta(red_s + ((rank * per + (col & (per - 1))) * 128 + row) * 4, col >> shift);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) st_shared_cluster_f32(to + j * 512, v[q * 8 + j]);
                 }
@@ -1152,11 +1166,11 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
                 const int r = u >> 5, col = (u & 31) * 4;
                 float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 for (int share = 0; share < c.cluster; ++share) {
-                    const float4 x4 = *reinterpret_cast<const float4*>(red + (share * per + r) * 128 + col);
-                    v[0] += x4.x;
-                    v[1] += x4.y;
-                    v[2] += x4.z;
-                    v[3] += x4.w;
+                    const uint4 x4 = ld_shared_v4(red_s + ((share * per + r) * 128 + col) * 4);
+                    v[0] += __uint_as_float(x4.x);
+                    v[1] += __uint_as_float(x4.y);
+                    v[2] += __uint_as_float(x4.z);
+                    v[3] += __uint_as_float(x4.w);
                 }
                 uint32_t h[2], l[2];
 #pragma unroll
@@ -1167,8 +1181,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
                     l[j] = pack2(a - f.x, b - f.y);
                 }
                 const uint32_t at = (col >> 6) * kXBox + box_at(rank * per + r, (col & 63) >> 3) + (col & 4) * 2;
-                *reinterpret_cast<uint2*>(ah + at) = make_uint2(h[0], h[1]);
-                *reinterpret_cast<uint2*>(al + at) = make_uint2(l[0], l[1]);
+                st_shared_v2(ah_s + at, h[0], h[1]);
+                st_shared_v2(al_s + at, l[0], l[1]);
             }
             fence_async_shared();
             __syncthreads();
@@ -1202,11 +1216,11 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const uint32_t at = (b16 >> 2) * kXBox + box_at(row, (b16 & 3) * 2 + q);
-                uint4 hi = *reinterpret_cast<const uint4*>(ah + at), lo = *reinterpret_cast<const uint4*>(al + at);
+                uint4 hi = ld_shared_v4(ah_s + at), lo = ld_shared_v4(al_s + at);
                 blend8(&v[q * 8], hi, lo, cb, cc / kScale);
                 split8(&v[q * 8], hi, lo);
-                *reinterpret_cast<uint4*>(bh + at) = hi;
-                *reinterpret_cast<uint4*>(bl + at) = lo;
+                st_shared_v4(bh_s + at, hi);
+                st_shared_v4(bl_s + at, lo);
             }
         }
         tc_fence_before();
@@ -1245,14 +1259,14 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const uint32_t at = (b16 >> 2) * kXBox + box_at(row, (b16 & 3) * 2 + q);
-                    uint4 hi = *reinterpret_cast<const uint4*>(xh + at), lo = *reinterpret_cast<const uint4*>(xl + at);
+                    uint4 hi = ld_shared_v4(xh_s + at), lo = ld_shared_v4(xl_s + at);
                     if (last) {
                         blend8(&v[q * 8], hi, lo, ca / kScale, 1.0f / (kScale * kScale));
                     } else {
                         blend8(&v[q * 8], hi, lo, ca, 1.0f / kScale);
                         split8(&v[q * 8], hi, lo);
-                        *reinterpret_cast<uint4*>(xh + at) = hi;
-                        *reinterpret_cast<uint4*>(xl + at) = lo;
+                        st_shared_v4(xh_s + at, hi);
+                        st_shared_v4(xl_s + at, lo);
                     }
                 }
                 if (last && row < p.m) {
@@ -1334,7 +1348,7 @@ NsPlan plan_of(int out_dtype, int64_t batch, int64_t rows, int64_t cols) {
     pl.n = std::max(rows, cols);
     pl.mp = round_up(pl.m, 64);
     pl.np = round_up(pl.n, 64);
-    pl.split = out_dtype == DGA_F32 || pl.m <= kSmallRows;
+    pl.split = out_dtype != DGA_BF16 || pl.m <= kSmallRows;
     pl.x_bytes = static_cast<size_t>(batch * pl.mp * pl.np) * 2;
     pl.a_bytes = static_cast<size_t>(batch * pl.mp * pl.mp) * 2;
     // partial sums; X now and next, hi and lo; A and B, hi and (split) lo

@@ -416,7 +416,8 @@ typedef enum { DGA_MXFP4 = 0, DGA_NVFP4 = 1 } dga_mx_format;
  *                 (r/128)*ceil(blocks/4) + s/4; blocks past K are written as
  *                 0, what rows past R hold is never used
  * codes and scales must be 16-byte aligned.  Errors: DGA_ERR_UNSUPPORTED for a
- * format or type; -3 transpose, -4 rows, -5 cols (outside [0, 2^31)), -6 X,
+ * format or type; -3 transpose, -4 rows, -5 cols (outside [0, 2^30), as every
+ * size of the dga_mx_* calls), -6 X,
  * -7 ldx, -8 tensor_scale with DGA_MXFP4, -9 codes, -10 ld_codes, -11 scales;
  * DGA_ERR_OVERLAP.  rows == 0 or cols == 0 is a no-op.  One launch.
  */
@@ -493,10 +494,12 @@ size_t dga_mx_linear_workspace_size(dga_mx_format format, int64_t M, int64_t K);
  * anywhere in a matrix makes that matrix's O NaN (or, with infinities, 0).
  *
  * G and O: DGA_F32, DGA_BF16 or DGA_F16, each its own.  All products run on
- * the tensor cores with fp32 accumulation from operands of 22 bits for
- * DGA_F32 output (as exact as fp32 products) and 11 bits otherwise, X itself
- * being kept to 22 bits; intermediates of magnitude 16 or more overflow (the
- * quintic above stays below 4).  Results repeat bit for bit.
+ * the tensor cores with fp32 accumulation from operands of 22 bits (as exact
+ * as fp32 products), or, for DGA_BF16 output of matrices with more than 256
+ * rows and columns, of 11 bits, X itself being kept to 22 (1e-4 to 1.7e-3 off
+ * in all, bf16's own rounding being 1.7e-3).  Intermediates of magnitude 16 or
+ * more overflow (the quintic above stays below 4), as do squares of G past
+ * fp32's range in the norm.  Results repeat bit for bit.
  *   coefficients  HOST, 3 * steps floats: a, b, c of each step
  *   O             may be G itself (the same pointer, type and strides); must
  *                 not overlap it otherwise

@@ -81,7 +81,7 @@ def _quantize(**over):
 
 @pytest.mark.parametrize("over,code", [
     (dict(format=2), dga.ERR_UNSUPPORTED), (dict(in_dtype=gen.I8), dga.ERR_UNSUPPORTED), (dict(transpose=2), -3),
-    (dict(rows=-1), -4), (dict(rows=1 << 31), -4), (dict(cols=-1), -5), (dict(X=None), -6), (dict(ldx=63), -7),
+    (dict(rows=-1), -4), (dict(rows=1 << 30), -4), (dict(cols=-1), -5), (dict(X=None), -6), (dict(ldx=63), -7),
     (dict(format=dga.MXFP4, tensor_scale=D), -8), (dict(codes=None), -9), (dict(codes=B + 8), -9),
     (dict(ld_codes=16), -10), (dict(ld_codes=40), -10), (dict(transpose=1, ld_codes=8), -10), (dict(scales=None), -11),
     (dict(scales=C + 4), -11), (dict(codes=A), dga.ERR_OVERLAP), (dict(scales=A), dga.ERR_OVERLAP),
