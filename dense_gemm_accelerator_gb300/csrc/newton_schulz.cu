@@ -251,15 +251,20 @@ __device__ __forceinline__ void unit_result(const NsParams& p, const NsMaps& map
             base[static_cast<int64_t>(row0 + i) * p.ldo + col0 + lane] =
                 *reinterpret_cast<const T*>(boxes + at(i, lane / kPer) + (lane % kPer) * sizeof(T));
     }
+    fence_async_shared();  // loads of old values may follow into these boxes
     __syncwarp();
 }
 
 // One unit of a tile, v its sums: lane l has row row0 + l, columns col0 ..
 // col0 + 31.  mirror: the tile is off the diagonal of a symmetric product, so
-// that its transpose is stored too.  On return the boxes' stores are under way.
+// that its transpose is stored too.  free_groups: of this thread's bulk groups,
+// the latest that do not use these boxes (2: none does).  `loaded` is called once the old values
+// have been taken (by every lane).  On return the boxes' stores are under way,
+// at most one bulk group of them (an earlier one has been waited for).
+template <typename F>
 __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, uint8_t* boxes, uint64_t* bar, uint32_t phase,
                                         volatile int* abort_flag, uint32_t matrix, int32_t row0, int32_t col0, int lane,
-                                        bool mirror, float (&v)[32]) {
+                                        bool mirror, int free_groups, float (&v)[32], F loaded) {
     const uint32_t box = smem_u32(boxes);
     if (p.has_old) {
         if (!mbar_wait_bounded(bar, phase, abort_flag, kWaitLimitNs)) record_failure(kRoleEpilogue, abort_flag);
@@ -271,12 +276,14 @@ __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, u
             blend8(&v[q * 8], hi, lo, p.c_old, p.c_acc);
         }
     } else {
-        // the boxes may still be read by the last unit's stores
-        if (lane == 0) bulk_wait_read<0>();
+        // the boxes may still be read by earlier stores
+        if (lane == 0 && free_groups == 0) bulk_wait_read<0>();
+        if (lane == 0 && free_groups == 1) bulk_wait_read<1>();
 #pragma unroll
         for (int j = 0; j < 32; ++j) v[j] *= p.c_acc;
     }
     __syncwarp();
+    loaded();
     if (p.last) {
         if (p.result_type == DGA_F32) unit_result<float>(p, maps, boxes, matrix, row0, col0, lane, v);
         else if (p.result_type == DGA_BF16) unit_result<__nv_bfloat16>(p, maps, boxes, matrix, row0, col0, lane, v);
@@ -299,7 +306,7 @@ __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, u
     if (lane == 0) {
         if (in) tma_store_3d(&maps.out_h, boxes, col0, row0, static_cast<int32_t>(matrix));
         if (in && p.out_lo) tma_store_3d(&maps.out_l, boxes + kBox32, col0, row0, static_cast<int32_t>(matrix));
-        bulk_commit();
+        if (!mirror || p.out_lo) bulk_commit();
     }
     if (mirror) {
         // column j of the unit becomes a row of 32, hi in the second box if
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             cluster_arrive_relaxed();  // what was sent here has arrived
         }
         if (e < units) {
-            ns_unit(p, maps, boxes, &old_full[e], 0, abort_flag, matrix, row0, col0, lane, p.sym && tm != tn, v);
+            ns_unit(p, maps, boxes, &old_full[e], 0, abort_flag, matrix, row0, col0, lane, p.sym && tm != tn, 2, v, [] {});
             if (lane == 0) bulk_wait_read<0>();  // shared memory outlives the stores that read it
         }
         __syncwarp();
@@ -566,22 +573,32 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 
 // ---- the pair kernel: 256 x 256 on two CTAs, persistent --------------------------------
 
-// Warps: producer, MMA, 8 epilogue warps of 128 columns (four units) each.
+// Warps: producer, MMA, 16 epilogue warps of 64 columns (two units) each, or,
+// where each keeps its sums in registers, 8 of 128 (four units).  A unit's time
+// is latency more than instructions, so warps count: PAIRFIG.
+// Their 16 pairs of boxes make one for a warp, or two, so that one unit's old
+// values arrive while another is computed; in a CTA's last tile, whose epilogue
+// nothing hides, the remaining units take the ring's space, done with by then.
 constexpr uint32_t kPairStage = 2 * 128 * 128;  // each CTA's half of both operands
-constexpr int kPairStages = 6;
-constexpr int kPairWarps = 8;
-constexpr uint32_t kPairUnits = 4;
-constexpr int kPairThreads = 64 + 32 * kPairWarps;
+constexpr int kPairStages = 5;
+constexpr uint32_t kPairBoxes = 16;  // pairs of boxes
+template <bool kSplit>
+constexpr uint32_t kPairWarps = kSplit ? 8 : 16;
+template <bool kSplit>
+constexpr int kPairThreads = 64 + 32 * kPairWarps<kSplit>;
 constexpr uint32_t kPairEpi = kPairStages * kPairStage;
-constexpr uint32_t kPairBar = kPairEpi + kPairWarps * kUnitBytes;
-// full[S], empty[S], acc_full[2], acc_empty[2], drain, old_full[W], tmem slot + abort flag
-constexpr uint32_t kPairLaunch = kPairBar + (2 * kPairStages + 5 + kPairWarps) * 8 + 16 + 1024;
+constexpr uint32_t kPairBar = kPairEpi + kPairBoxes * kUnitBytes;
+constexpr uint32_t kPairAllUnits = 32;  // of a CTA's 128 x 256
+static_assert(kPairEpi >= kPairBoxes * kUnitBytes, "the last tile's boxes fit the ring");
+// full[S], empty[S], acc_full[2], acc_empty[2], drain, old_full[units], tmem slot + abort flag
+constexpr uint32_t kPairLaunch = kPairBar + (2 * kPairStages + 5 + kPairAllUnits) * 8 + 16 + 1024;
 
 template <bool kSplit>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kPairThreads<kSplit>, 1)
     ns_pair_kernel(const __grid_constant__ NsMaps maps, NsParams p) {
     constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 256, 256);
     constexpr uint16_t kBothCtas = 0x3;
+    constexpr uint32_t kWarps = kPairWarps<kSplit>, kUnits = kPairAllUnits / kWarps, kSets = kPairBoxes / kWarps;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -591,7 +608,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
     uint64_t* old_full = drain + 1;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + kPairWarps);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + kPairAllUnits);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -604,10 +621,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 2 * kPairWarps);  // one lane of each epilogue warp of both CTAs
+            mbar_init(&acc_empty[b], 2 * kWarps);  // one lane of each epilogue warp of both CTAs
         }
         mbar_init(drain, 1);
-        for (int w = 0; w < kPairWarps; ++w) mbar_init(&old_full[w], 1);
+        for (uint32_t w = 0; w < kPairAllUnits; ++w) mbar_init(&old_full[w], 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&maps.p_h);
@@ -727,42 +744,53 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_wait_bounded(drain, 0, &never, kWaitLimitNs);
         }
     } else {
-        const uint32_t e = warp - 2, quarter = warp & 3, half = e >> 2;  // 128 columns
+        const uint32_t e = warp - 2, quarter = warp & 3, share = e >> 2;  // kUnits * 32 columns
         const uint32_t lane_base = (quarter * 32) << 16;
-        uint8_t* boxes = smem + kPairEpi + e * kUnitBytes;
         uint32_t acc = 0, acc_phase = 0, old_phase = 0;
         bool ok = true;
+        auto boxes_of = [&](uint32_t u, bool last_tile) {
+            return smem + (last_tile && u >= kSets ? 0 : kPairEpi) + (e * kSets + u % kSets) * kUnitBytes;
+        };
         // unit u of tile t
         auto rows_of = [&](uint32_t tm) { return static_cast<int32_t>(tm * 256 + rank * 128 + quarter * 32); };
-        auto cols_of = [&](uint32_t tn, uint32_t u) { return static_cast<int32_t>(tn * 256 + half * 128 + u * 32); };
-        auto prefetch = [&](uint32_t t, uint32_t u) {
-            if (p.has_old && t < p.num_tiles && lane == 0) {
-                uint32_t matrix, tm, tn;
-                ns_tile(p, t, matrix, tm, tn);
-                bulk_wait_read<0>();  // the boxes' last stores
-                unit_prefetch(p, maps, boxes, &old_full[e], matrix, rows_of(tm), cols_of(tn, u));
+        auto cols_of = [&](uint32_t tn, uint32_t u) { return static_cast<int32_t>(tn * 256 + share * kUnits * 32 + u * 32); };
+        auto in_range = [&](uint32_t tm, uint32_t tn, uint32_t u) {
+            return rows_of(tm) < p.rows && cols_of(tn, u) < p.ld;
+        };
+        // the old values of unit u, once the boxes' last stores have been read
+        auto prefetch = [&](uint32_t matrix, uint32_t tm, uint32_t tn, bool last_tile, uint32_t u) {
+            if (p.has_old && lane == 0 && in_range(tm, tn, u)) {
+                bulk_wait_read<0>();
+                unit_prefetch(p, maps, boxes_of(u, last_tile), &old_full[e * kUnits + u], matrix, rows_of(tm), cols_of(tn, u));
             }
             __syncwarp();
         };
-        prefetch(cluster_id, 0);
+        auto prefetch_tile = [&](uint32_t t, uint32_t u) {
+            if (p.has_old && t < p.num_tiles) {
+                uint32_t matrix, tm, tn;
+                ns_tile(p, t, matrix, tm, tn);
+                prefetch(matrix, tm, tn, t + n_clusters >= p.num_tiles, u);
+            }
+        };
+        for (uint32_t u = 0; u < kSets; ++u) prefetch_tile(cluster_id, u);
         for (uint32_t t = cluster_id; ok && t < p.num_tiles; t += n_clusters) {
             uint32_t matrix, tm, tn;
             ns_tile(p, t, matrix, tm, tn);
-            const bool mirror = p.sym && tm != tn;
-            float sum[kSplit ? 128 : 1];
+            const bool mirror = p.sym && tm != tn, last_tile = t + n_clusters >= p.num_tiles;
+            float sum[kSplit ? kUnits : 1][32];
             if constexpr (kSplit) {
                 auto add = [&](uint32_t column) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (uint32_t c = 0; c < kUnits; ++c) {
                         uint32_t r[32];
-                        tmem_ld_32x32b_x32(tmem + lane_base + column + half * 128 + c * 32, r);
+                        tmem_ld_32x32b_x32(tmem + lane_base + column + share * kUnits * 32 + c * 32, r);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[c * 32 + j] += __uint_as_float(r[j]);
+                        for (int j = 0; j < 32; ++j) sum[c][j] += __uint_as_float(r[j]);
                     }
                 };
 #pragma unroll
-                for (int j = 0; j < 128; ++j) sum[j] = 0.0f;
+                for (uint32_t j = 0; j < kUnits * 32; ++j) sum[j / 32][j % 32] = 0.0f;
                 const uint32_t n_chunks = (p.num_kb + kChunk - 1) / kChunk;
                 for (uint32_t ch = 0; ch < n_chunks; ++ch) {
                     if (!mbar_wait_bounded<true>(&acc_full[0], acc_phase, abort_flag, kWaitLimitNs)) {
@@ -786,30 +814,55 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 tc_fence_after();
             }
             if (!ok) break;
-#pragma unroll(kSplit ? 4 : 1)
-            for (uint32_t u = 0; u < kPairUnits; ++u) {
+            if (last_tile)
+                for (uint32_t u = kSets; u < kUnits; ++u) prefetch(matrix, tm, tn, true, u);
+            // (one copy of the unit's code: unrolled, each would run once in a
+            // launch and wait for its instructions)
+#pragma unroll 1
+            for (uint32_t u = 0; u < kUnits; ++u) {
                 float v[32];
                 if constexpr (kSplit) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = sum[u * 32 + j];
+                    for (int j = 0; j < 32; ++j) {
+                        v[j] = sum[0][j];
+#pragma unroll
+                        for (uint32_t c = 1; c < kUnits; ++c) sum[c - 1][j] = sum[c][j];
+                    }
                 } else {
                     uint32_t r[32];
-                    tmem_ld_32x32b_x32(tmem + lane_base + acc * 256 + half * 128 + u * 32, r);
+                    tmem_ld_32x32b_x32(tmem + lane_base + acc * 256 + share * kUnits * 32 + u * 32, r);
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-                    if (u == kPairUnits - 1) {
+                    if (u == kUnits - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
                         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
                     }
                 }
-                ns_unit(p, maps, boxes, &old_full[e], old_phase, abort_flag, matrix, rows_of(tm), cols_of(tn, u), lane, mirror, v);
-                old_phase ^= 1;
-                if (u + 1 < kPairUnits) prefetch(t, u + 1);
-                else prefetch(t + n_clusters, 0);
+                // the next unit to load: into this one's boxes after it, or, of
+                // two sets, into the other while this one is computed
+                auto next = [&] {
+                    if (last_tile) return;
+                    if (u + 1 < kUnits) {
+                        if (kSets == 1 || u > 0) prefetch(matrix, tm, tn, false, u + 1);
+                    } else {
+                        prefetch_tile(t + n_clusters, 0);
+                    }
+                };
+                // a unit all of whose values lie past the matrix has nothing to do
+                if (in_range(tm, tn, u)) {
+                    ns_unit(p, maps, boxes_of(u, last_tile), &old_full[e * kUnits + u], old_phase >> u & 1, abort_flag, matrix,
+                            rows_of(tm), cols_of(tn, u), lane, mirror, last_tile && u >= kSets ? 2 : static_cast<int>(kSets) - 1, v,
+                            [&] { if (kSets > 1) next(); });
+                    old_phase ^= 1u << u;
+                    if (kSets == 1) next();
+                } else {
+                    next();
+                }
             }
+            if (kSets > 1) prefetch_tile(t + n_clusters, 1);
         }
         if (lane == 0) bulk_wait_read<0>();  // shared memory outlives the stores that read it
     }
@@ -1401,7 +1454,7 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
     const int64_t big = tiles(256);
     if (big >= pairs * 3 / 4) {
         return launch(p.split ? ns_pair_kernel<true> : ns_pair_kernel<false>,
-                      dim3(static_cast<unsigned>(2 * std::min(big, pairs))), kPairThreads, 2, static_cast<int>(kPairLaunch), true,
+                      dim3(static_cast<unsigned>(2 * std::min(big, pairs))), p.split ? kPairThreads<true> : kPairThreads<false>, 2, static_cast<int>(kPairLaunch), true,
                       s, maps, p);
     }
     const int64_t small = tiles(128);
