@@ -19,6 +19,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cstring>
 
 #include "dga_internal.h"
 #include "mx_common.cuh"
@@ -85,8 +86,30 @@ __device__ __forceinline__ void load8(const T* __restrict__ row, int64_t k, int6
 // lanes and nothing computed twice; with eight values to a lane and a block's
 // maximum and scale found by 2 or 4 lanes it was bound by instructions (8192 x
 // 8192 bf16: 51 us MXFP4, 70 us NVFP4).
+// Rows that do not start on 16 bytes are read by the aligned pieces that cover
+// them, shifted in registers (4093 x 4099 bf16, MXFP4:
+// 16 us, element by element 35 us).
 // fp32 sources: eight values to a lane as just described, since 128 bytes to a
 // lane would be bound by the L1's lines.
+
+// 16 words from `src`, an address of 16-bit values: the five aligned 16-byte
+// pieces around them, shifted by 8, 4 and 2 bytes as the address asks.
+__device__ __forceinline__ void load_words_shifted(const void* src, uint32_t (&w)[16]) {
+    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src)) & 15;
+    const uint4* at = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(src) - off);
+    uint32_t x[20];
+#pragma unroll
+    for (int q = 0; q < 5; ++q) {
+        const uint4 v = __ldg(at + q);
+        x[4 * q] = v.x, x[4 * q + 1] = v.y, x[4 * q + 2] = v.z, x[4 * q + 3] = v.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 18; ++j) x[j] = off & 8 ? x[j + 2] : x[j];
+#pragma unroll
+    for (int j = 0; j < 17; ++j) x[j] = off & 4 ? x[j + 1] : x[j];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = __funnelshift_r(x[j], x[j + 1], (off & 2) * 8);
+}
 
 template <int kFormat, typename T>
 __global__ void __launch_bounds__(256) mx_quant_rows16_kernel(const T* __restrict__ X, int64_t ldx, uint32_t rows, int64_t K,
@@ -104,6 +127,7 @@ __global__ void __launch_bounds__(256) mx_quant_rows16_kernel(const T* __restric
     // runs past the last value, up to the end of its scale tile: scales of 0
     if (run >= runs) return;
     const uint32_t rows_per_block = 256u >> log_x;
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(X), end = begin + ((rows - 1) * ldx + K) * sizeof(T);
     for (uint32_t r = blockIdx.y * rows_per_block + (threadIdx.x >> log_x); r < rows; r += gridDim.y * rows_per_block) {
         const T* src = X + static_cast<int64_t>(r) * ldx + k;
         uint32_t w[16];
@@ -112,6 +136,14 @@ __global__ void __launch_bounds__(256) mx_quant_rows16_kernel(const T* __restric
             for (int q = 0; q < 4; ++q) {
                 const uint4 v = __ldg(reinterpret_cast<const uint4*>(src) + q);
                 w[4 * q] = v.x, w[4 * q + 1] = v.y, w[4 * q + 2] = v.z, w[4 * q + 3] = v.w;
+            }
+        } else if (reinterpret_cast<uintptr_t>(src) - begin >= 16 && reinterpret_cast<uintptr_t>(src) + 80 <= end) {
+            // (begin, end: of X's bytes; a piece may hold neighbours of the row)
+            load_words_shifted(src, w);
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+                if (k + 2 * q >= K) w[q] = 0;
+                else if (k + 2 * q + 1 >= K) w[q] &= 0xffffu;
             }
         } else {
             const uint16_t* bits = reinterpret_cast<const uint16_t*>(src);
@@ -344,39 +376,77 @@ __device__ __forceinline__ float scale_value(int format, uint8_t byte) {
     return __half2float(__ushort_as_half(static_cast<uint16_t>(h2 & 0xffff)));
 }
 
-// A lane reads eight codes (4 bytes) and writes eight values: code times
-// (scale times factor), rounded once to the output type.
-template <int kFormat, typename T>
-__global__ void __launch_bounds__(256) mx_dequant_kernel(int64_t rows, int64_t K,
-                                                         const uint8_t* __restrict__ codes, int64_t ldc,
-                                                         const uint8_t* __restrict__ scales,
-                                                         int64_t tiles_k,
-                                                         const float* __restrict__ factor,
-                                                         T* __restrict__ Y, int64_t ldy, bool vec,
-                                                         int64_t groups) {
+// A lane makes 16 bytes of a row, code times (scale times factor)
+// rounded once to the output type, for several rows of the same columns.  Bound
+// by memory (0.53 bytes in, 2 or 4 out a value), so four rows' loads go out
+// before the first is used: 8192 x 8192 in 31 us to bf16 (5.5 TB/s), 51 us to
+// fp32 (5.9 TB/s; 54 us with a 64-bit division and one row at a time, 65 us with
+// eight values, two separate stores, to a lane).
+// kShifted: rows do not start on 16 bytes; the pieces, of eight values, begin
+// at the first aligned address at or before a row's start, and their codes lie
+// across two words and maybe two blocks (4093 x 4099:
+// bf16 17 us against 51 us with element stores, fp32 21 us against 25 us).
+constexpr int kDequantRows = 4;
+template <int kFormat, typename T, bool kShifted>
+__global__ void __launch_bounds__(256) mx_dequant_kernel(uint32_t rows, int32_t K, const uint8_t* __restrict__ codes, int64_t ldc,
+                                                         const uint8_t* __restrict__ scales, int64_t tiles_k,
+                                                         const float* __restrict__ factor, T* __restrict__ Y, int64_t ldy,
+                                                         int log_x) {
+    constexpr int kAlign = 16 / sizeof(T), kPer = kShifted ? 8 : kAlign, kBlock = mx_block(kFormat);
     const float g = (kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f;
-    const int64_t total = rows * groups;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; u < total;
-         u += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = u / groups, k = (u - r * groups) * 8;
-        float v[8];
-        values8(__ldg(reinterpret_cast<const uint32_t*>(codes + r * ldc + (k >> 1))), v);
-        const float s = scale_value(kFormat, __ldg(scales + mx_scale_offset(r, k / mx_block(kFormat), tiles_k))) * g;
-        T y[8];
+    // 2^log_x threads along a row, the block's others on the rows below
+    const int32_t piece = static_cast<int32_t>((blockIdx.x << log_x) + (threadIdx.x & ((1u << log_x) - 1))) * kPer;
+    const uint32_t step = gridDim.y * (256u >> log_x);
+    for (uint32_t r0 = blockIdx.y * (256u >> log_x) + (threadIdx.x >> log_x); r0 < rows; r0 += step * kDequantRows) {
+        int32_t k[kDequantRows];  // the piece's first column, below 0 or past K where it is not a whole one
+        uint32_t c[kDequantRows];
+        uint8_t scale[kDequantRows], scale2[kDequantRows];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) y[q] = mx_out<T>(v[q] * s);
-        T* dst = Y + r * ldy + k;
-        if (vec && k + 8 <= K) {
-            if constexpr (sizeof(T) == 2) {
-                *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(y);
+        for (int i = 0; i < kDequantRows; ++i) {
+            const uint32_t r = r0 + i * step;
+            k[i] = piece;
+            if constexpr (kShifted)
+                k[i] -= static_cast<int32_t>(reinterpret_cast<uintptr_t>(Y + static_cast<int64_t>(r) * ldy) / sizeof(T) & (kAlign - 1));
+            if (r >= rows || k[i] >= K) continue;
+            const uint32_t first = max(k[i], 0), last = min(k[i] + kPer, K) - 1;
+            const uint8_t* src = codes + static_cast<int64_t>(r) * ldc;
+            if constexpr (kShifted) {
+                // nibbles k .. k + kPer - 1, the first at bit 0 (those below 0 or past K are not used)
+                const uint32_t w0 = first >> 3, w1 = last >> 3;
+                const uint32_t* words = reinterpret_cast<const uint32_t*>(src);
+                const uint32_t lo = __ldg(words + w0), hi = w1 > w0 ? __ldg(words + w1) : 0;
+                c[i] = k[i] < 0 ? lo << (static_cast<uint32_t>(-k[i]) * 4) : __funnelshift_r(lo, hi, (static_cast<uint32_t>(k[i]) & 7) * 4);
+            } else if constexpr (kPer == 8) {
+                c[i] = __ldg(reinterpret_cast<const uint32_t*>(src + (first >> 1)));
             } else {
-                reinterpret_cast<uint4*>(dst)[0] = reinterpret_cast<const uint4*>(y)[0];
-                reinterpret_cast<uint4*>(dst)[1] = reinterpret_cast<const uint4*>(y)[1];
+                c[i] = __ldg(reinterpret_cast<const uint16_t*>(src + (first >> 1)));
             }
-        } else {
+            scale[i] = __ldg(scales + mx_scale_offset(r, first / kBlock, tiles_k));
+            if constexpr (kShifted) scale2[i] = __ldg(scales + mx_scale_offset(r, last / kBlock, tiles_k));
+        }
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (k + q < K) dst[q] = y[q];
+        for (int i = 0; i < kDequantRows; ++i) {
+            const uint32_t r = r0 + i * step;
+            if (r >= rows || k[i] >= K) continue;
+            float v[8];
+            values8(c[i], v);
+            const float s = scale_value(kFormat, scale[i]) * g, s2 = kShifted ? scale_value(kFormat, scale2[i]) * g : s;
+            // values from this one on belong to the second block
+            const int turn = (k[i] + kPer - 1) / kBlock * kBlock - k[i];
+            T y[kPer];
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) y[q] = mx_out<T>(v[q] * (kShifted && turn > 0 && q >= turn && k[i] >= 0 ? s2 : s));
+            T* dst = Y + static_cast<int64_t>(r) * ldy + k[i];
+            if (k[i] >= 0 && k[i] + kPer <= K) {
+                uint4 x[kPer / kAlign];
+                memcpy(x, y, sizeof x);
+#pragma unroll
+                for (int q = 0; q < kPer / kAlign; ++q) reinterpret_cast<uint4*>(dst)[q] = x[q];
+            } else {
+#pragma unroll
+                for (int q = 0; q < kPer; ++q)
+                    if (k[i] + q >= 0 && k[i] + q < K) dst[q] = y[q];
+            }
         }
     }
 }
@@ -427,11 +497,18 @@ cudaError_t dequantize_as(const MxMatrix& q, int64_t rows, int64_t K, void* Y, i
                           const DeviceInfo& dev, cudaStream_t stream) {
     constexpr int64_t kVec = 16 / sizeof(T);
     const bool vec = aligned(Y, 16) && ldy % kVec == 0;
-    const int64_t groups = (K + 7) / 8, total = rows * groups;
-    const int64_t blocks = std::min<int64_t>((total + 255) / 256, static_cast<int64_t>(dev.sm_count) * 64);
-    mx_dequant_kernel<kFormat, T><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(
-        rows, K, static_cast<const uint8_t*>(q.codes), q.ld, static_cast<const uint8_t*>(q.scales),
-        mx_tiles_k(kFormat, K), q.factor, static_cast<T*>(Y), ldy, vec, groups);
+    const int64_t groups = vec ? (K + kVec - 1) / kVec : (K + 7) / 8 + 1;
+    int log_x = 0;
+    while (log_x < 8 && (int64_t{1} << log_x) < groups) ++log_x;
+    const int64_t per_block = 256 >> log_x, cols = (groups + (int64_t{1} << log_x) - 1) >> log_x;
+    const int64_t all = (rows + per_block - 1) / per_block;  // blocks that a column of them needs, a row to a thread
+    // several rows to a thread once the machine is full
+    const int64_t down = cols * all >= static_cast<int64_t>(dev.sm_count) * 8 * kDequantRows ? (all + kDequantRows - 1) / kDequantRows : all;
+    const dim3 grid(static_cast<unsigned>(cols), static_cast<unsigned>(std::min<int64_t>(down, 65535)));
+    const auto kernel = vec ? mx_dequant_kernel<kFormat, T, false> : mx_dequant_kernel<kFormat, T, true>;
+    kernel<<<grid, 256, 0, stream>>>(static_cast<uint32_t>(rows), static_cast<int32_t>(K), static_cast<const uint8_t*>(q.codes), q.ld,
+                                     static_cast<const uint8_t*>(q.scales), mx_tiles_k(kFormat, K), q.factor, static_cast<T*>(Y),
+                                     ldy, log_x);
     return cudaGetLastError();
 }
 

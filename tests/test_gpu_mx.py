@@ -138,6 +138,34 @@ def test_strided_and_column_major_inputs():
             assert np.array_equal(got_c, want_c) and np.array_equal(got_s, want_s)
 
 
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols,ld", [(1, 70, 70), (3, 5, 7), (9, 95, 95), (33, 257, 259), (5, 1030, 1037)])
+@pytest.mark.parametrize("offset", range(8))
+def test_rows_at_any_alignment(fmt, dtype, rows, cols, ld, offset):
+    """Sources and results whose rows start on any element, at the ends of their
+    memory, between neighbours that must not be taken in or changed."""
+    x = _values(rows, cols, 7 * rows + cols + offset, dtype)
+    f, fv = _factor(x, fmt)
+    memory = torch.full((offset + (rows - 1) * ld + cols,), 3e4, dtype=dtype, device="cuda")
+    X = memory.as_strided((rows, cols), (ld, 1), offset)
+    X.copy_(x)
+    q = dga.mx_quantize(X, fmt, tensor_scale=f)
+    want_c, want_s = ref.quantize(_np(x), fmt, fv)
+    got_c, got_s = _parts(q)
+    assert np.array_equal(got_s, want_s)
+    assert np.array_equal(got_c, want_c)
+    plain = dga.mx_dequantize(q, out_dtype=OUT[dtype])
+    memory.fill_(5.0)
+    st = dga.dga_mx_dequantize(fmt, OUT[dtype], rows, cols, q.codes.data_ptr(), q.codes.stride(0), q.scales.data_ptr(),
+                               f.data_ptr() if f is not None else None, X.data_ptr(), ld, torch.cuda.current_stream().cuda_stream)
+    assert st == dga.OK
+    assert torch.equal(X, plain)
+    assert torch.equal(X.cpu(), torch.from_numpy(ref.dequantize(want_c, want_s, fmt, fv)).to(dtype))
+    X.fill_(5.0)
+    assert bool((memory == 5.0).all())
+
+
 def _pair(M, N, K, fmt, seed=0):
     a, b = _values(M, K, seed + 1), _values(N, K, seed + 2)
     fa, va = _factor(a, fmt)
