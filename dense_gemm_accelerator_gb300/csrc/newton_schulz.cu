@@ -88,16 +88,20 @@ __device__ __forceinline__ void record_failure(int role, volatile int* abort_fla
     *abort_flag = 1;
 }
 
+// kPer: tiles' columns to one tile's rows
+template <uint32_t kPer = 1>
 __device__ __forceinline__ void ns_tile(const NsParams& p, uint32_t t, uint32_t& matrix, uint32_t& tm, uint32_t& tn) {
     matrix = t / p.per_matrix;
     const uint32_t r = t - matrix * p.per_matrix;
     if (p.sym) {
-        // column by column of the upper triangle: r = tn (tn + 1) / 2 + tm
-        uint32_t c = static_cast<uint32_t>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
-        while (c * (c + 1) / 2 > r) --c;
-        while ((c + 1) * (c + 2) / 2 <= r) ++c;
-        tn = c;
-        tm = r - c * (c + 1) / 2;
+        // column by column of the upper triangle of squares: square column c
+        // has c + 1 of them, and begins at kPer c (c + 1) / 2
+        uint32_t c = static_cast<uint32_t>((sqrtf(8.0f / kPer * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+        while (kPer * c * (c + 1) / 2 > r) --c;
+        while (kPer * (c + 1) * (c + 2) / 2 <= r) ++c;
+        const uint32_t at = r - kPer * c * (c + 1) / 2;
+        tn = kPer * c + at / (c + 1);
+        tm = at % (c + 1);
     } else {
         tm = r % p.tiles_m;
         tn = r / p.tiles_m;
@@ -144,7 +148,7 @@ __device__ __forceinline__ void ns_result(const NsParams& p, uint32_t matrix, in
 // 32 of one matrix, so that what lies past a matrix' padded rows is neither
 // read nor written.
 struct NsMaps {
-    CUtensorMap p_h, p_l, q_h, q_l, old_h, old_l, out_h, out_l, mirror_h, mirror_l, result;
+    CUtensorMap p_h, p_l, q_h, q_l, q64_h, q64_l, old_h, old_l, out_h, out_l, mirror_h, mirror_l, result;
 };
 
 // Byte offset of 16-byte piece `piece` (8 fp16) of a row in a box of 128-byte rows.
@@ -339,27 +343,35 @@ __device__ __forceinline__ void ns_unit(const NsParams& p, const NsMaps& maps, u
 // slots for it, the hi boxes and the lo boxes (each loaded once for the three
 // products).  A CTA takes in 46 to 60 bytes a clock, which bounds these tiles:
 // 512 clocks or more for a slot, whose MMAs take 256.
-constexpr int kTileStages = 5;
-constexpr uint32_t kTileStage = 2 * 128 * 128;
-constexpr uint32_t kTileEpi = kTileStages * kTileStage;
-constexpr int kTileUnits = 16;  // of 32 x 32, one to an epilogue warp
-constexpr uint32_t kTileBar = kTileEpi + kTileUnits * kUnitBytes;
-// full[S], empty[S], acc_full[2], acc_empty[2], joined, old_full[U], then tmem slot + abort flag
-constexpr uint32_t kTileLaunch = kTileBar + (2 * kTileStages + 5 + kTileUnits) * 8 + 16 + 1024;
+// kN: the tile's columns, 128 or, where K is short, 64: more tiles instead of
+// parts of K, whose joining costs more than what is loaded twice then (2.8 us of a
+// product's 7).
+template <uint32_t kN>
+struct TileShape {
+    static constexpr int kStages = kN == 128 ? 5 : 8;
+    static constexpr uint32_t kQ = kN * 128, kStage = 128 * 128 + kQ;
+    static constexpr int kUnits = 4 * kN / 32;  // of 32 x 32, one to an epilogue warp
+    static constexpr int kThreads = 64 + 32 * kUnits;  // and a producer and an MMA warp
+    static constexpr uint32_t kEpi = kStages * kStage;
+    static constexpr uint32_t kBar = kEpi + kUnits * kUnitBytes;
+    // full[S], empty[S], acc_full[2], acc_empty[2], joined, old_full[U], then tmem slot + abort flag
+    static constexpr uint32_t kLaunch = kBar + (2 * kStages + 5 + kUnits) * 8 + 16 + 1024;
+};
 constexpr uint32_t kUnitSums = 32 * 32 * 4;  // a unit's sums
-static_assert(kTileEpi >= 2 * kTileUnits * kUnitSums, "the parts' sums fit the ring twice");
+static_assert(TileShape<128>::kEpi >= 2 * TileShape<128>::kUnits * kUnitSums, "the parts' sums fit the ring twice");
 
-// Producer warp, MMA warp, 16 epilogue warps with a unit of the tile each.
-constexpr int kTileThreads = 64 + 32 * kTileUnits;
-
-template <bool kSplit>
-__global__ void __launch_bounds__(kTileThreads, 1)
-    ns_tile_kernel(const __grid_constant__ NsMaps maps, NsParams p, uint32_t splits) {
-    constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 128, 128);
+template <bool kSplit, uint32_t kN>
+__global__ void __launch_bounds__(TileShape<kN>::kThreads, 1)
+    ns_tile_kernel(const __grid_constant__ NsMaps maps, NsParams p, uint32_t k_parts) {
+    const uint32_t splits = kN == 128 ? k_parts : 1;
+    using S = TileShape<kN>;
+    constexpr int kTileStages = S::kStages, kTileUnits = S::kUnits;
+    constexpr uint32_t kTileStage = S::kStage, kTileEpi = S::kEpi;
+    constexpr uint32_t kIdesc = idesc_mma(kFmtF16, 128, kN);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kTileBar);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S::kBar);
     uint64_t* empty = full + kTileStages;
     uint64_t* acc_full = empty + kTileStages;
     uint64_t* acc_empty = acc_full + 2;
@@ -368,13 +380,13 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(old_full + kTileUnits);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     // accumulators: one, or the cross products' and two for the chunks in turn
-    constexpr uint32_t kCols = kSplit ? 512 : 128;
+    constexpr uint32_t kCols = kSplit ? 4 * kN : kN;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t t = blockIdx.x / splits, part = blockIdx.x % splits;
     const uint32_t kb0 = part * p.num_kb / splits, kb1 = (part + 1) * p.num_kb / splits;
     const uint32_t units = kTileUnits / splits;  // of the tile's, what this CTA joins and stores
     uint32_t matrix, tm, tn;
-    ns_tile(p, t, matrix, tm, tn);
+    ns_tile<128 / kN>(p, t, matrix, tm, tn);
 
     if (warp == 0 && lane == 0) {
         for (int s = 0; s < kTileStages; ++s) {
@@ -421,7 +433,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 const int32_t k = static_cast<int32_t>((kSplit ? i >> 1 : i) * 64);
                 tma_load_2d(dst, lo ? &maps.p_l : &maps.p_h, &full[stage], k, p_row);
                 const CUtensorMap* q = lo ? &maps.q_l : &maps.q_h;
-                if (p.q_mn) {
+                if constexpr (kN == 64) {  // one box of 64 x 64 either way
+                    const int32_t row = static_cast<int32_t>(matrix * p.q_rows);
+                    const int32_t col = static_cast<int32_t>(tn * 64);
+                    tma_load_2d(dst + 128 * 128, lo ? &maps.q64_l : &maps.q64_h, &full[stage], p.q_mn ? col : k, p.q_mn ? row + k : row + col);
+                } else if (p.q_mn) {
                     const int32_t row = static_cast<int32_t>(matrix * p.q_rows) + k;
                     tma_load_2d(dst + 128 * 128, q, &full[stage], static_cast<int32_t>(tn * 128), row);
                     tma_load_2d(dst + 128 * 128 + kBoxBytes, q, &full[stage], static_cast<int32_t>(tn * 128 + 64), row);
@@ -463,7 +479,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                     tc_fence_after();
                     mma(0, hi, lo, kb == kb0);
                     mma(0, lo, hi, false);
-                    mma(128 + (chunk & 1) * 128, hi, hi, begins);
+                    mma(kN + (chunk & 1) * kN, hi, hi, begins);
                     tc_commit(&empty[hi]);
                     tc_commit(&empty[lo]);
                     if ((kb - kb0) % kChunk == kChunk - 1 || kb + 1 == kb1) {
@@ -494,7 +510,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const uint32_t e = warp - 2, quarter = warp & 3, block = e >> 2;
         const uint32_t lane_base = (quarter * 32) << 16;
         const uint32_t my_block = splits == 1 ? block : e & 3, my_quarter = splits == 1 ? quarter : part + (e >> 2) * splits;
-        const int32_t row0 = static_cast<int32_t>(tm * 128 + my_quarter * 32), col0 = static_cast<int32_t>(tn * 128 + my_block * 32);
+        const int32_t row0 = static_cast<int32_t>(tm * 128 + my_quarter * 32), col0 = static_cast<int32_t>(tn * kN + my_block * 32);
         uint8_t* boxes = smem + kTileEpi + e * kUnitBytes;
         if (p.has_old && e < units && lane == 0) unit_prefetch(p, maps, boxes, &old_full[e], matrix, row0, col0);
         __syncwarp();
@@ -516,7 +532,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             }
             tc_fence_after();
             if constexpr (kSplit) {
-                add(128 + (ch & 1) * 128);
+                add(kN + (ch & 1) * kN);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&acc_empty[ch & 1]);
@@ -551,7 +567,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             cluster_arrive_relaxed();  // what was sent here has arrived
         }
         if (e < units) {
-            ns_unit(p, maps, boxes, &old_full[e], 0, abort_flag, matrix, row0, col0, lane, p.sym && tm != tn, 2, v, [] {});
+            ns_unit(p, maps, boxes, &old_full[e], 0, abort_flag, matrix, row0, col0, lane, p.sym && tm != tn / (128 / kN), 2, v, [] {});
             if (lane == 0) bulk_wait_read<0>();  // shared memory outlives the stores that read it
         }
         __syncwarp();
@@ -1443,10 +1459,17 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, unsigned cluster,
 // CTA pairs, else the tile kernel with K in parts.
 cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_t rows, int64_t cols,
                            const DeviceInfo& dev, cudaStream_t s) {
+    // tiles of 256 or 128 squared, or 128 x 64
     auto tiles = [&](int64_t size) {
-        p.tiles_m = static_cast<uint32_t>((rows + size - 1) / size);
+        const int64_t high = std::max<int64_t>(size, 128);
+        p.tiles_m = static_cast<uint32_t>((rows + high - 1) / high);
         p.tiles_n = static_cast<uint32_t>((cols + size - 1) / size);
-        p.per_matrix = p.sym ? p.tiles_m * (p.tiles_m + 1) / 2 : p.tiles_m * p.tiles_n;
+        if (p.sym) {
+            const uint32_t per = static_cast<uint32_t>(high / size), whole = p.tiles_n / per;  // columns of squares
+            p.per_matrix = per * whole * (whole + 1) / 2 + p.tiles_n % per * (whole + 1);
+        } else {
+            p.per_matrix = p.tiles_m * p.tiles_n;
+        }
         const int64_t all = batch * p.per_matrix;
         p.num_tiles = static_cast<uint32_t>(all);
         return all;
@@ -1458,17 +1481,26 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
                       dim3(static_cast<unsigned>(2 * std::min(big, pairs))), p.split ? kPairThreads<true> : kPairThreads<false>, 2, static_cast<int>(kPairLaunch), true,
                       s, maps, p);
     }
-    const int64_t small = tiles(128);
+    // Tiles of 64 columns where K is short and even they leave half of the SMs
+    // idle (700^2 bf16 115 -> 101 us, 400 x 1000 bf16 109 -> 96 us, 150^2 fp32
+    // 105 -> 92 us); split operands with more slots do better with parts of K
+    // (256 x 512 fp32 111 us against 116 to 119).
+    const uint32_t slots = p.num_kb * (p.split ? 2 : 1);
+    if (slots <= (p.split ? 6u : 16u)) {
+        const int64_t narrow = tiles(64);
+        if (narrow * 2 <= dev.sm_count)
+            return launch(p.split ? ns_tile_kernel<true, 64> : ns_tile_kernel<false, 64>, dim3(static_cast<unsigned>(narrow)),
+                          TileShape<64>::kThreads, 1, static_cast<int>(TileShape<64>::kLaunch), true, s, maps, p, 1u);
+    }
     // Parts of K while there are idle SMs: joining them takes 2 to 3 us, a slot
     // 0.3 us.  Split operands with 8 slots or more gain from 4 parts (256^2 fp32
-    // 133 -> 123 us, 400 x 1000 fp32 166 -> 147 us, but 150^2, 6 slots, 109 ->
-    // 129 us); single ones from 16 slots to a part (700^2 bf16 119 us with, 132
-    // us from 4 slots to a part).
-    const uint32_t slots = p.num_kb * (p.split ? 2 : 1);
+    // 133 -> 123 us, 400 x 1000 fp32 166 -> 147 us); single ones from 16 slots
+    // to a part (700^2 bf16 119 us with, 132 us from 4 slots to a part).
+    const int64_t small = tiles(128);
     uint32_t splits = 1;
-    while (splits < 4 && small * splits * 2 <= dev.sm_count && slots >= (p.split ? std::max(8u, splits * 4) : splits * 16)) splits *= 2;
-    return launch(p.split ? ns_tile_kernel<true> : ns_tile_kernel<false>, dim3(static_cast<unsigned>(small * splits)),
-                  kTileThreads, splits, static_cast<int>(kTileLaunch), true, s, maps, p, splits);
+    while (splits < 4 && small * splits * 2 <= dev.sm_count && slots >= (p.split ? 8u : splits * 16)) splits *= 2;
+    return launch(p.split ? ns_tile_kernel<true, 128> : ns_tile_kernel<false, 128>, dim3(static_cast<unsigned>(small * splits)),
+                  TileShape<128>::kThreads, splits, static_cast<int>(TileShape<128>::kLaunch), true, s, maps, p, splits);
 }
 
 // The cluster kernel's shape, or cluster = 0 where it does not apply: up to 128
@@ -1635,7 +1667,7 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
         if (e == cudaSuccess) e = half_map(&m->op, base, all_rows, ld, 128);
         if (e == cudaSuccess) e = value_map(&m->value, DGA_F16, base, ld, pl.mp, a.batch, ld, pl.mp * ld, true);
         if (e == cudaSuccess && square) e = value_map(&m->mirror, DGA_F16, base, ld, pl.mp, a.batch, ld, pl.mp * ld, false);
-        if (e == cudaSuccess && !square) e = half_map(&m->mn, base, all_rows, ld, 64);
+        if (e == cudaSuccess) e = half_map(&m->mn, base, all_rows, ld, 64);
     };
     for (int i = 0; i < 2; ++i) {
         make(&mx_h[i], xh[i], pl.np, false);
@@ -1669,6 +1701,8 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
         p.c_acc = 1.0f / kScale;
         m.p_h = m.q_h = mx_h[now].op;
         m.p_l = m.q_l = mx_l[now].op;
+        m.q64_h = mx_h[now].mn;
+        m.q64_l = mx_l[now].mn;
         m.old_h = m.old_l = ma_h.value;  // not used
         m.out_h = ma_h.value;
         m.out_l = ma_l.value;
@@ -1685,6 +1719,8 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
         p.old_lo = pl.split;
         m.p_h = m.q_h = ma_h.op;
         m.p_l = m.q_l = ma_l.op;
+        m.q64_h = ma_h.mn;
+        m.q64_l = ma_l.mn;
         m.old_l = ma_l.value;
         m.out_h = mb_h.value;
         m.out_l = mb_l.value;
@@ -1702,8 +1738,8 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
         p.old_lo = p.out_lo = 1;
         m.p_h = mb_h.op;
         m.p_l = mb_l.op;
-        m.q_h = mx_h[now].mn;
-        m.q_l = mx_l[now].mn;
+        m.q_h = m.q64_h = mx_h[now].mn;
+        m.q_l = m.q64_l = mx_l[now].mn;
         m.old_h = mx_h[now].value;
         m.old_l = mx_l[now].value;
         m.out_h = mx_h[next].value;
