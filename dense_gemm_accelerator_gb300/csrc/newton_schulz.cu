@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(TileShape<kN>::kThreads, 1)
         mbar_init(joined, 1);
         *abort_flag = 0;
         fence_mbar_init();
-        if (splits > 1) mbar_arrive_expect_tx(joined, splits * units * kUnitSums);
+        if (splits > 1) mbar_arrive_expect_tx(joined, (splits - 1) * units * kUnitSums);
         tma_prefetch_desc(&maps.p_h);
         tma_prefetch_desc(&maps.q_h);
     }
@@ -502,17 +502,17 @@ __global__ void __launch_bounds__(TileShape<kN>::kThreads, 1)
     __syncwarp();
     if (warp >= 2) {
         // Unit (quarter, block): 32 rows, 32 columns.  With K in parts, CTA c
-        // joins the quarters q % splits == c, `units` of them; slot i there is
-        // block i % 4 of quarter c + i / 4 * splits, and warp 2 + i's.  Once
-        // every CTA's ring is done with, each sends its sums by bulk copies
-        // from the ring's first half to the second halves of the joining CTAs,
-        // which add them up in the parts' order.
+        // joins the blocks q % splits == c, whose warps keep their own sums;
+        // once every CTA's ring is done with, the other warps send theirs by
+        // bulk copies from the ring's first half to the second halves of the
+        // joining CTAs, which add them up in the parts' order.
         const uint32_t e = warp - 2, quarter = warp & 3, block = e >> 2;
         const uint32_t lane_base = (quarter * 32) << 16;
-        const uint32_t my_block = splits == 1 ? block : e & 3, my_quarter = splits == 1 ? quarter : part + (e >> 2) * splits;
-        const int32_t row0 = static_cast<int32_t>(tm * 128 + my_quarter * 32), col0 = static_cast<int32_t>(tn * kN + my_block * 32);
+        const bool joins = block % splits == part;
+        const uint32_t slot = block / splits * 4 + quarter;  // at the joining CTA
+        const int32_t row0 = static_cast<int32_t>(tm * 128 + quarter * 32), col0 = static_cast<int32_t>(tn * kN + block * 32);
         uint8_t* boxes = smem + kTileEpi + e * kUnitBytes;
-        if (p.has_old && e < units && lane == 0) unit_prefetch(p, maps, boxes, &old_full[e], matrix, row0, col0);
+        if (p.has_old && joins && lane == 0) unit_prefetch(p, maps, boxes, &old_full[e], matrix, row0, col0);
         __syncwarp();
         float v[32];
         auto add = [&](uint32_t column) {
@@ -541,32 +541,36 @@ __global__ void __launch_bounds__(TileShape<kN>::kThreads, 1)
         add(0);
         if (splits > 1) {
             uint8_t* sent = smem + e * kUnitSums;
+            if (!joins) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) st_shared_u32(smem_u32(sent) + (j * 32 + lane) * 4, __float_as_uint(v[j]));
-            fence_async_shared();
+                for (int j = 0; j < 32; ++j) st_shared_u32(smem_u32(sent) + (j * 32 + lane) * 4, __float_as_uint(v[j]));
+                fence_async_shared();
+            }
             __syncwarp();
             cluster_arrive_relaxed();
             cluster_wait();
-            if (lane == 0) {
-                const uint32_t slot = block + 4 * (quarter / splits), to = quarter % splits;
-                const uint32_t at = smem_u32(smem + (kTileUnits + part * units + slot) * kUnitSums);
+            if (!joins && lane == 0) {
+                const uint32_t to = block % splits, at = smem_u32(smem + (kTileUnits + part * units + slot) * kUnitSums);
                 bulk_copy_to_cta(map_to_cta(at, to), smem_u32(sent), kUnitSums, map_to_cta(smem_u32(joined), to));
             }
             __syncwarp();
-            if (e < units) {
+            if (joins) {
                 if (!mbar_wait_bounded<true>(joined, 0, abort_flag, kWaitLimitNs)) record_failure(kRoleEpilogue, abort_flag);
+                float sum[32];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                for (int j = 0; j < 32; ++j) sum[j] = 0.0f;
                 for (uint32_t q = 0; q < splits; ++q) {
-                    const uint32_t src = smem_u32(smem + (kTileUnits + q * units + e) * kUnitSums) + lane * 4;
+                    const uint32_t src = smem_u32(smem + (kTileUnits + q * units + slot) * kUnitSums) + lane * 4;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] += ld_shared_f32(src + j * 128);
+                    for (int j = 0; j < 32; ++j) sum[j] += q == part ? v[j] : ld_shared_f32(src + j * 128);
                 }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = sum[j];
             }
             __syncwarp();
             cluster_arrive_relaxed();  // what was sent here has arrived
         }
-        if (e < units) {
+        if (joins) {
             ns_unit(p, maps, boxes, &old_full[e], 0, abort_flag, matrix, row0, col0, lane, p.sym && tm != tn / (128 / kN), 2, v, [] {});
             if (lane == 0) bulk_wait_read<0>();  // shared memory outlives the stores that read it
         }
