@@ -20,6 +20,12 @@
 //           by a cluster and its parts joined through distributed shared
 //           memory in a fixed order.  For few rows the bytes of B are the
 //           bound.
+//
+// Measured: 8192^3 to bf16 172 us MXFP4 (6.4 PFLOP/s), 193 us NVFP4, where the
+// operands' way into shared memory alone takes 138 us (46 to 60 bytes a clock
+// and SM).  8192 x 8192 weights: 100 rows 18.6 us, 256 rows 24.8 us (MXFP4);
+// 13 rows of values 12.5 us MXFP4, 16.6 us NVFP4, of which the weight's 36 MB
+// take 5.3 us at the copy rate.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -167,7 +173,9 @@ __device__ __forceinline__ void store_unit(const MxParams& p, const CUtensorMap*
 // The same where TMA cannot store (C's rows not 16-byte aligned) or C is read
 // (beta): the unit, transposed through the boxes, row by row with a lane on
 // columns l and 32 + l.  Element (row, c) lies at word row * 64 + (c + row) % 64,
-// so that neither direction meets in a bank.
+// so that neither direction meets in a bank.  (8192 x 8192 x 2048 to bf16 with
+// an odd leading dimension: 107 us, by TMA into an even one 60 us; 4093 x 4099 x
+// 4097 NVFP4 to fp32 47 us.)
 template <typename TOut>
 __device__ __forceinline__ void store_unit_plain(const MxParams& p, float alpha, uint8_t* boxes, int lane, int64_t row, int64_t col,
                                                  const uint32_t (&v)[64]) {
