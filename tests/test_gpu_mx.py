@@ -302,6 +302,38 @@ def test_on_another_stream_and_in_a_graph():
     assert torch.equal(out, dga.mx_linear_forward(x * 2, W))
 
 
+@pytest.mark.parametrize("fmt", FMT)
+def test_offsets_past_32_bits(fmt):
+    """Sources, values and products of more than 2^31 elements: their last rows
+    and columns are those of the same rows alone."""
+    rows, cols = 65536 + 128, 33000
+    X = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for r in range(0, rows, 8208):
+        X[r:r + 8208] = torch.randn(8208, cols, device="cuda", generator=g)
+    tail = X[-128:].contiguous()
+    q, alone = dga.mx_quantize(X, fmt), dga.mx_quantize(tail, fmt)
+    assert torch.equal(q.codes[-128:], alone.codes)
+    per = alone.scales.numel()
+    assert torch.equal(q.scales.flatten()[-per:], alone.scales.flatten())
+    assert torch.equal(dga.mx_dequantize(q, out_dtype=dga.BF16)[-128:], dga.mx_dequantize(alone, out_dtype=dga.BF16))
+    t = dga.mx_quantize(X, fmt, transpose=True)
+    t_alone = dga.mx_quantize(X[:, -104:].contiguous(), fmt, transpose=True)
+    assert torch.equal(t.codes[-104:], t_alone.codes)
+    del X, q, t
+    # one-hot rows: C's last rows and columns are entries of A and B
+    M, N, K = 66000, 33000, 64
+    A = torch.zeros(M, K, device="cuda")
+    A[torch.arange(M, device="cuda"), torch.arange(M, device="cuda") % K] = 6.0
+    B = torch.randint(-3, 4, (N, K), device="cuda", generator=g).float()
+    B[:, ::16] = 6.0  # every block's largest, so that the scales are exact
+    C = dga.mx_gemm(dga.mx_quantize(A, fmt), dga.mx_quantize(B, fmt), out_dtype=dga.BF16)
+    _sync_ok()
+    for r in (0, M - 300):
+        want = B[:, (torch.arange(r, r + 300, device="cuda") % K)].mT
+        assert torch.equal(C[r:r + 300].float(), 6.0 * want)
+
+
 def test_empty():
     e = torch.empty(0, 40, device="cuda")
     q = dga.mx_quantize(e)

@@ -72,6 +72,44 @@ def test_large_enough_for_cta_pairs(shape):
         assert _rel(got, want) <= TOL[dtype]
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(12, 515, 1030), (12, 1030, 515), (20, 259, 270), (9, 770, 580)])
+def test_batches_on_cta_pairs_with_thin_last_tiles(dtype, shape):
+    """256 x 256 tiles of which the last hold a few rows or columns, several
+    rounds of them, into results whose rows TMA can and cannot store."""
+    G = _momentum(shape, 11).to(dtype).cuda()
+    want = _formula(G).cpu()
+    got = dga.orthogonalize(G)
+    frame = torch.full((shape[0], shape[1] + 2, shape[2] + 5), 7.0, dtype=dtype, device="cuda")
+    dga.orthogonalize(G, out=frame[:, 1:-1, 3:-2])
+    _ok()
+    assert _rel(got, want) <= TOL[dtype]
+    assert torch.equal(frame[:, 1:-1, 3:-2], got)
+    frame[:, 1:-1, 3:-2] = 7.0
+    assert (frame == 7.0).all(), "written outside the result"
+
+
+def test_offsets_past_32_bits():
+    """A 140 x 16,000,000 update (2.24e9 values): the columns at both ends, from
+    fp64 products."""
+    m, n = 140, 16_000_000
+    g = torch.Generator(device="cuda").manual_seed(12)
+    G = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+    for c in range(0, n, 1_000_000):
+        G[:, c:c + 1_000_000] = torch.randn(m, 1_000_000, device="cuda", generator=g)
+    got = dga.orthogonalize(G, steps=1, coefficients=(1.5, -0.5, 0.0))
+    _ok()
+    A = torch.zeros(m, m, dtype=torch.float64, device="cuda")
+    for c in range(0, n, 1_000_000):
+        x = G[:, c:c + 1_000_000].double()
+        A += x @ x.mT
+    norm2 = float(A.diagonal().sum())
+    for c in (0, n // 2 - 50, n - 100):
+        x = G[:, c:c + 100].double() / norm2 ** 0.5
+        want = 1.5 * x - 0.5 * (A / norm2) @ x
+        assert float((got[:, c:c + 100].double() - want).norm() / want.norm()) <= TOL[torch.bfloat16]
+
+
 def test_types_steps_and_coefficients():
     G = _momentum((90, 200), 4)
     cases = [(3, dga.QUINTIC), (1, (1.5, -0.5, 0.0)), (4, [(3.0, -4.0, 1.6), (2.5, -3.0, 1.2), (2.0, -1.6, 0.6), (1.875, -1.25, 0.375)])]
