@@ -852,8 +852,9 @@ cudaError_t launch_pair(const MxGemmArgs& a, MxParams p, const DeviceInfo& dev) 
     else
         m[4] = m[0];  // not used
     if (e != cudaSuccess) return e;
-    return launch(mx_gemm_pair_kernel<kFormat, TOut>, 2 * clusters, kPairThreads, 2, static_cast<int>(S::kLaunch),
-                  a.after_quantize, a.stream, m[0], m[1], m[2], m[3], m[4], p);
+    // (it waits for the grid before it ahead of its first load)
+    return launch(mx_gemm_pair_kernel<kFormat, TOut>, 2 * clusters, kPairThreads, 2, static_cast<int>(S::kLaunch), true,
+                  a.stream, m[0], m[1], m[2], m[3], m[4], p);
 }
 
 template <int kFormat, typename TOut>

@@ -78,6 +78,16 @@ __device__ __forceinline__ void load8(const T* __restrict__ row, int64_t k, int6
     }
 }
 
+// These kernels are launched as programmatic dependents: their blocks may be
+// placed while the kernel before still runs, and wait here for its end.  Then a
+// product launched behind this one may be placed: it reads its weight at once,
+// which was complete before this grid's start, and waits for this grid's end
+// before it reads what is written here.  (BWDFIG)
+__device__ __forceinline__ void begin_after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---- along rows ------------------------------------------------------------
 //
 // 16-bit sources: a thread takes 32 consecutive values of a row, one block
@@ -117,9 +127,7 @@ __global__ void __launch_bounds__(256) mx_quant_rows16_kernel(const T* __restric
                                                               uint8_t* __restrict__ codes, int64_t ldc,
                                                               uint8_t* __restrict__ scales, int64_t tiles_k, uint32_t runs,
                                                               int log_x) {
-    // a product launched behind this kernel may start now: it waits for this
-    // grid's end before it reads what is written here
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_after_previous();
     const TensorFactor g((kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f);
     // 2^log_x threads along a row, the block's others on the rows below
     const uint32_t run = (blockIdx.x << log_x) + (threadIdx.x & ((1u << log_x) - 1));
@@ -171,7 +179,7 @@ __global__ void __launch_bounds__(256) mx_quant_rows_kernel(const T* __restrict_
                                                             int64_t ldc, uint8_t* __restrict__ scales,
                                                             int64_t tiles_k, int64_t chunks,
                                                             int64_t row_bytes) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // as above
+    begin_after_previous();
     constexpr int kLanes = mx_block(kFormat) / 8;  // lanes of a block
     const int lane = threadIdx.x & 31;
     const TensorFactor g((kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f);
@@ -216,7 +224,7 @@ __global__ void __launch_bounds__(256) mx_quant_cols_kernel(const T* __restrict_
                                                             int64_t ldc, uint8_t* __restrict__ scales,
                                                             int64_t tiles_k, int64_t blocks_k,
                                                             int64_t row_bytes) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_after_previous();
     constexpr int kPad = 16 / sizeof(T);
     __shared__ __align__(16) T tile[128][64 + kPad];
     __shared__ __align__(16) uint32_t out[64][16 + 4];
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(256) mx_quant_cols16_kernel(const T* __restric
                                                               int64_t ldc, uint8_t* __restrict__ scales,
                                                               int64_t tiles_k, int64_t blocks_k,
                                                               int64_t row_bytes) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_after_previous();
     __shared__ __align__(16) uint32_t out[128][16 + 4];
     // the scales of 128 rows and 128 k: one tile (MXFP4) or two, which lie together
     constexpr int kTiles = 32 / mx_block(kFormat);
@@ -393,6 +401,7 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(uint32_t rows, int32_t 
                                                          const float* __restrict__ factor, T* __restrict__ Y, int64_t ldy,
                                                          int log_x) {
     constexpr int kAlign = 16 / sizeof(T), kPer = kShifted ? 8 : kAlign, kBlock = mx_block(kFormat);
+    begin_after_previous();
     const float g = (kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f;
     // 2^log_x threads along a row, the block's others on the rows below
     const int32_t piece = static_cast<int32_t>((blockIdx.x << log_x) + (threadIdx.x & ((1u << log_x) - 1))) * kPer;
@@ -451,6 +460,20 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(uint32_t rows, int32_t 
     }
 }
 
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 template <int kFormat, typename T>
 cudaError_t quantize_as(const MxQuantArgs& a, const DeviceInfo& dev) {
     const T* X = static_cast<const T*>(a.X);
@@ -467,14 +490,14 @@ cudaError_t quantize_as(const MxQuantArgs& a, const DeviceInfo& dev) {
             const int64_t rows_per_block = 256 >> log_x;
             const dim3 grid(static_cast<unsigned>((runs + (1 << log_x) - 1) >> log_x),
                             static_cast<unsigned>(std::min<int64_t>((a.rows + rows_per_block - 1) / rows_per_block, 65535)));
-            mx_quant_rows16_kernel<kFormat, T><<<grid, 256, 0, a.stream>>>(
-                X, a.ldx, static_cast<uint32_t>(a.rows), K, vec, a.factor, a.codes, a.ld_codes, a.scales, tiles_k,
+            return launch_behind(
+                mx_quant_rows16_kernel<kFormat, T>, grid, a.stream, X, a.ldx, static_cast<uint32_t>(a.rows), K, vec, a.factor, a.codes, a.ld_codes, a.scales, tiles_k,
                 static_cast<uint32_t>(runs), log_x);
         } else {
             const int64_t chunks = (K + 255) / 256, units = a.rows * chunks;
             const int64_t blocks = std::min<int64_t>((units + 7) / 8, static_cast<int64_t>(dev.sm_count) * 64);
-            mx_quant_rows_kernel<kFormat, T><<<static_cast<unsigned>(blocks), 256, 0, a.stream>>>(
-                X, a.ldx, a.rows, K, vec, a.factor, a.codes, a.ld_codes, a.scales, tiles_k, chunks, row_bytes);
+            return launch_behind(
+                mx_quant_rows_kernel<kFormat, T>, dim3(static_cast<unsigned>(blocks)), a.stream, X, a.ldx, a.rows, K, vec, a.factor, a.codes, a.ld_codes, a.scales, tiles_k, chunks, row_bytes);
         }
     } else {
         constexpr int64_t kWide = sizeof(T) == 2 ? 128 : 64;
@@ -483,13 +506,12 @@ cudaError_t quantize_as(const MxQuantArgs& a, const DeviceInfo& dev) {
         // two 16-bit values of a row at once
         const bool pairs = aligned(a.X, 4) && a.ldx % 2 == 0;
         auto run = [&](auto kernel) {
-            kernel<<<static_cast<unsigned>(blocks), 256, 0, a.stream>>>(X, a.ldx, K, a.cols, sizeof(T) == 2 ? pairs : vec, a.factor, a.codes, a.ld_codes,
+            return launch_behind(kernel, dim3(static_cast<unsigned>(blocks)), a.stream, X, a.ldx, K, a.cols, sizeof(T) == 2 ? pairs : vec, a.factor, a.codes, a.ld_codes,
                                                                         a.scales, tiles_k, blocks_k, row_bytes);
         };
-        if constexpr (sizeof(T) == 2) run(mx_quant_cols16_kernel<kFormat, T>);
-        else run(mx_quant_cols_kernel<kFormat, T>);
+        if constexpr (sizeof(T) == 2) return run(mx_quant_cols16_kernel<kFormat, T>);
+        else return run(mx_quant_cols_kernel<kFormat, T>);
     }
-    return cudaGetLastError();
 }
 
 template <int kFormat, typename T>
@@ -506,10 +528,9 @@ cudaError_t dequantize_as(const MxMatrix& q, int64_t rows, int64_t K, void* Y, i
     const int64_t down = cols * all >= static_cast<int64_t>(dev.sm_count) * 8 * kDequantRows ? (all + kDequantRows - 1) / kDequantRows : all;
     const dim3 grid(static_cast<unsigned>(cols), static_cast<unsigned>(std::min<int64_t>(down, 65535)));
     const auto kernel = vec ? mx_dequant_kernel<kFormat, T, false> : mx_dequant_kernel<kFormat, T, true>;
-    kernel<<<grid, 256, 0, stream>>>(static_cast<uint32_t>(rows), static_cast<int32_t>(K), static_cast<const uint8_t*>(q.codes), q.ld,
+    return launch_behind(kernel, grid, stream, static_cast<uint32_t>(rows), static_cast<int32_t>(K), static_cast<const uint8_t*>(q.codes), q.ld,
                                      static_cast<const uint8_t*>(q.scales), mx_tiles_k(kFormat, K), q.factor, static_cast<T*>(Y),
                                      ldy, log_x);
-    return cudaGetLastError();
 }
 
 }  // namespace
