@@ -63,6 +63,9 @@ SIGNATURES = {
     "dga_mx_linear": (_CI, [_CI, _CI, _CI, _I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _VP,
                             _VP, _VP, _I64, _VP, _SZ, _VP]),
     "dga_mx_linear_workspace_size": (_SZ, [_CI, _I64, _I64]),
+    "dga_mx_linear_backward": (_CI, [_CI, _CI, _CI, _CI, _I64, _I64, _I64, _VP, _I64, _VP, _VP, _I64, _VP,
+                                     _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP, _VP, _SZ, _VP]),
+    "dga_mx_linear_backward_workspace_size": (_SZ, [_CI, _I64, _I64, _I64]),
     "dga_orthogonalize": (_CI, [_CI, _CI, _I64, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _CI, _VP,
                                 ctypes.c_float, _VP, _SZ, _VP]),
     "dga_orthogonalize_workspace_size": (_SZ, [_CI, _I64, _I64, _I64]),
@@ -231,6 +234,18 @@ def dga_mx_linear(format, x_dtype, out_dtype, M, N, K, X, ldx, x_tensor_scale, W
 
 def dga_mx_linear_workspace_size(format, M, K):
     return lib().dga_mx_linear_workspace_size(format, M, K)
+
+
+def dga_mx_linear_backward(format, x_dtype, w_dtype, g_dtype, M, N, K, X, ldx, x_tensor_scale, W, ldw,
+                           w_tensor_scale, G, ldg, g_tensor_scale, dX, lddx, dW, lddw, db,
+                           workspace=None, workspace_bytes=0, stream=0):
+    return lib().dga_mx_linear_backward(format, x_dtype, w_dtype, g_dtype, M, N, K, X, ldx, x_tensor_scale,
+                                        W, ldw, w_tensor_scale, G, ldg, g_tensor_scale, dX, lddx, dW,
+                                        lddw, db, workspace, workspace_bytes, stream)
+
+
+def dga_mx_linear_backward_workspace_size(format, M, N, K):
+    return lib().dga_mx_linear_backward_workspace_size(format, M, N, K)
 
 
 def dga_orthogonalize(in_dtype, out_dtype, batch, rows, cols, G, ldg, stride_g, O, ldo, stride_o, steps,

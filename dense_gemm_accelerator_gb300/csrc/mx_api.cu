@@ -48,6 +48,14 @@ int device(DeviceInfo* dev) {
     return dev->major == 10 && dev->minor == 3 ? DGA_OK : DGA_ERR_DEVICE;
 }
 
+// rows x K in 4 bits inside a workspace: codes, then scales.
+int64_t held_bytes(int format, int64_t rows, int64_t K) {
+    return round_up(rows * mx_row_bytes(K), 256) + scales_bytes(format, rows, K);
+}
+MxMatrix held_at(uint8_t* ws, int64_t rows, int64_t K, const float* factor) {
+    return {ws, mx_row_bytes(K), ws + round_up(rows * mx_row_bytes(K), 256), factor};
+}
+
 }  // namespace
 
 extern "C" {
@@ -217,6 +225,97 @@ int dga_mx_linear(dga_mx_format format, dga_dtype x_dtype, dga_dtype out_dtype, 
         a.X = nullptr;
     }
     e = mx_gemm_launch(a, dev, &launches);
+    if (e != cudaSuccess) return note_cuda_error(e);
+    set_last_launches(launches);
+    return DGA_OK;
+}
+
+size_t dga_mx_linear_backward_workspace_size(dga_mx_format format, int64_t M, int64_t N, int64_t K) {
+    if (!format_ok(format) || M <= 0 || N <= 0 || K <= 0) return 0;
+    return static_cast<size_t>(held_bytes(format, M, N) + held_bytes(format, K, N) + held_bytes(format, N, M) +
+                               held_bytes(format, K, M));
+}
+
+int dga_mx_linear_backward(dga_mx_format format, dga_dtype x_dtype, dga_dtype w_dtype, dga_dtype g_dtype, int64_t M,
+                           int64_t N, int64_t K, const void* X, int64_t ldx, const float* x_tensor_scale, const void* W,
+                           int64_t ldw, const float* w_tensor_scale, const void* G, int64_t ldg,
+                           const float* g_tensor_scale, void* dX, int64_t lddx, void* dW, int64_t lddw, float* db,
+                           void* workspace, size_t workspace_bytes, dga_stream_t stream) {
+    if (!format_ok(format) || !float_type(x_dtype) || !float_type(w_dtype) || !float_type(g_dtype)) return DGA_ERR_UNSUPPORTED;
+    if (M < 0 || M >= kMaxDim) return -5;
+    if (N < 0 || N >= kMaxDim) return -6;
+    if (K < 0 || K >= kMaxDim) return -7;
+    if (x_tensor_scale && format == DGA_MXFP4) return -10;
+    if (w_tensor_scale && format == DGA_MXFP4) return -13;
+    if (g_tensor_scale && format == DGA_MXFP4) return -16;
+    set_last_launches(0);
+    const bool has_x = M > 0 && K > 0, has_w = N > 0 && K > 0, has_g = M > 0 && N > 0;
+    if (has_x && (!X || ldx < K)) return !X ? -8 : -9;
+    if (has_w && (!W || ldw < K)) return !W ? -11 : -12;
+    if (has_g && (!G || ldg < N)) return !G ? -14 : -15;
+    if (has_x && (!dX || lddx < K)) return !dX ? -17 : -18;
+    if (has_w && (!dW || lddw < K)) return !dW ? -19 : -20;
+    const size_t need = dga_mx_linear_backward_workspace_size(format, M, N, K);
+    if (workspace && !aligned(workspace, 256)) return -22;
+    if (workspace_bytes > 0 && !workspace) return -22;
+    if (workspace_bytes < need) return DGA_ERR_WORKSPACE;
+    const int64_t gs = type_size(g_dtype);
+    // what is read, then what is written
+    Span spans[7];
+    int n = 0;
+    auto matrix = [&](bool there, const void* p, int64_t rows, int64_t ld, int64_t cols, int64_t es) {
+        if (there) spans[n++] = span(p, rows, ld * es, cols * es);
+    };
+    matrix(has_x, X, M, ldx, K, type_size(x_dtype));
+    matrix(has_w, W, N, ldw, K, type_size(w_dtype));
+    matrix(has_g, G, M, ldg, N, gs);
+    const int inputs = n;
+    matrix(has_x, dX, M, lddx, K, gs);
+    matrix(has_w, dW, N, lddw, K, gs);
+    matrix(db != nullptr && N > 0, db, 1, N, N, 4);
+    matrix(need > 0, workspace, 1, static_cast<int64_t>(need), static_cast<int64_t>(need), 1);
+    for (int i = inputs; i < n; ++i)
+        for (int j = 0; j < i; ++j)
+            if (meet(spans[i], spans[j])) return DGA_ERR_OVERLAP;
+    DeviceInfo dev;
+    const int st = device(&dev);
+    if (st != DGA_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int launches = 0;
+    cudaError_t e = cudaSuccess;
+    // rows x K in 4 bits, of T's rows or (transposed) its columns
+    auto quantise = [&](int dtype, bool transpose, const void* T, int64_t ld, int64_t rows, int64_t k, const float* factor) {
+        const MxMatrix q = held_at(ws, rows, k, factor);
+        ws += held_bytes(format, rows, k);
+        if (e != cudaSuccess) return q;
+        MxQuantArgs a{format, dtype, transpose, transpose ? k : rows, transpose ? rows : k, T, ld, factor,
+                      static_cast<uint8_t*>(const_cast<void*>(q.codes)), q.ld, static_cast<uint8_t*>(const_cast<void*>(q.scales)), s};
+        e = mx_quantize_launch(a, dev);
+        if (e == cudaSuccess) ++launches;
+        return q;
+    };
+    // C (rows x cols) <- P Q^T, zero for k == 0
+    auto product = [&](const MxMatrix& P, const MxMatrix& Q, int64_t rows, int64_t cols, int64_t k, void* C, int64_t ldc) {
+        if (e != cudaSuccess || rows == 0 || cols == 0) return;
+        MxGemmArgs a{format, g_dtype, rows, cols, k, 1.0f, 0.0f, P, Q, C, ldc, nullptr, false, s, nullptr, 0, 0};
+        int l = 0;
+        e = mx_gemm_launch(a, dev, &l);
+        launches += l;
+    };
+    MxMatrix g{}, w{}, gt{}, xt{};
+    if (need > 0) {
+        g = quantise(g_dtype, false, G, ldg, M, N, g_tensor_scale);
+        w = quantise(w_dtype, true, W, ldw, K, N, w_tensor_scale);
+        gt = quantise(g_dtype, true, G, ldg, N, M, g_tensor_scale);
+        xt = quantise(x_dtype, true, X, ldx, K, M, x_tensor_scale);
+    }
+    product(g, w, M, K, N, dX, lddx);
+    product(gt, xt, N, K, M, dW, lddw);
+    if (e == cudaSuccess && db && N > 0) {
+        e = sum_rows_launch(g_dtype, M, N, G, ldg, db, s);
+        if (e == cudaSuccess) ++launches;
+    }
     if (e != cudaSuccess) return note_cuda_error(e);
     set_last_launches(launches);
     return DGA_OK;

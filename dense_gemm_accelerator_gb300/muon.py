@@ -7,6 +7,7 @@ import ctypes
 import torch
 
 from . import BF16, F16, F32, DgaError, _raw_stream, lib
+from .mx import on_stream
 
 _CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _TORCH = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
@@ -36,6 +37,8 @@ def orthogonalize(G, steps=5, coefficients=QUINTIC, eps=1e-7, out=None, out_dtyp
     the result, of G's shape (it may be G itself), allocated as out_dtype (G's
     own type if None) when None.  The workspace comes from PyTorch's caching
     allocator unless given (dga_orthogonalize_workspace_size bytes)."""
+    if stream is not None:
+        return on_stream(stream, G.device, orthogonalize, G, steps, coefficients, eps, out, out_dtype, workspace)
     if G.dim() not in (2, 3):
         raise ValueError("G must be a matrix or a batch of matrices")
     code = _CODE.get(G.dtype)
@@ -68,7 +71,7 @@ def orthogonalize(G, steps=5, coefficients=QUINTIC, eps=1e-7, out=None, out_dtyp
     st = L.dga_orthogonalize(code, out_code, batch, rows, cols, G.data_ptr(), ldg, stride_g, out.data_ptr(),
                              ldo, stride_o, steps, (ctypes.c_float * len(flat))(*flat), eps,
                              workspace.data_ptr() or None, have,
-                             _raw_stream(dev.index) if stream is None else stream)
+                             _raw_stream(dev.index))
     if st:
         raise DgaError(st, "dga_orthogonalize")
     return out

@@ -1,8 +1,8 @@
 """4-bit microscaled matrices: quantisation, products and the fully-connected
 layer, as PyTorch-tensor forms of the ``dga_mx_*`` entry points (include/dga.h
 has the formats, roundings and errors).  All work runs in the library's CUDA
-kernels on the current stream of the tensors' device; scratch and results
-come from PyTorch's caching allocator.
+kernels on the current stream of the tensors' device, or the one given;
+scratch and results come from PyTorch's caching allocator, on the same stream.
 """
 from __future__ import annotations
 
@@ -42,8 +42,13 @@ class MXTensor:
                 f"{self.rows}x{self.cols}, {self.codes.device})")
 
 
-def _stream(device, stream):
-    return _raw_stream(device.index) if stream is None else stream
+def on_stream(stream, device, f, *args):
+    """f(*args) with `stream` (an integer) as the current one, so that what it
+    allocates belongs to that stream too: memory that the caller's stream still
+    reads is not handed out again, and scratch is not freed under the work."""
+    s = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(s):
+        return f(*args)
 
 
 def _raise(st, what):
@@ -75,6 +80,8 @@ def mx_quantize(X, format=MXFP4, transpose=False, tensor_scale=None, stream=None
     """X (rows x cols, float32, bfloat16 or float16, row- or column-major) to an
     :class:`MXTensor` quantised along its rows, or, with transpose=True, the
     MXTensor of X's transpose (quantised along X's columns)."""
+    if stream is not None:
+        return on_stream(stream, X.device, mx_quantize, X, format, transpose, tensor_scale)
     if X.dim() != 2:
         raise ValueError("X must be 2-D")
     code = _CODE.get(X.dtype)
@@ -92,7 +99,7 @@ def mx_quantize(X, format=MXFP4, transpose=False, tensor_scale=None, stream=None
     scales = torch.empty(L.dga_mx_scales_size(format, R, K), dtype=torch.uint8, device=dev)
     st = L.dga_mx_quantize(format, code, 1 if transpose else 0, rows, cols, X.data_ptr(), ldx,
                            _factor(tensor_scale, format, dev), codes.data_ptr(), row_bytes,
-                           scales.data_ptr(), _stream(dev, stream))
+                           scales.data_ptr(), _raw_stream(dev.index))
     if st:
         _raise(st, "dga_mx_quantize")
     return MXTensor(format, R, K, codes, scales, tensor_scale)
@@ -100,12 +107,14 @@ def mx_quantize(X, format=MXFP4, transpose=False, tensor_scale=None, stream=None
 
 def mx_dequantize(Q, out_dtype=F32, stream=None):
     """The values an MXTensor stands for, rounded once to out_dtype."""
+    if stream is not None:
+        return on_stream(stream, Q.device, mx_dequantize, Q, out_dtype)
     dev = Q.codes.device
     Y = torch.empty((Q.rows, Q.cols), dtype=_TORCH[out_dtype], device=dev)
     st = lib().dga_mx_dequantize(Q.format, out_dtype, Q.rows, Q.cols, Q.codes.data_ptr(),
                                  Q.codes.stride(0), Q.scales.data_ptr(),
                                  _factor(Q.tensor_scale, Q.format, dev), Y.data_ptr(), Q.cols or 1,
-                                 _stream(dev, stream))
+                                 _raw_stream(dev.index))
     if st:
         _raise(st, "dga_mx_dequantize")
     return Y
@@ -134,6 +143,8 @@ def _bias(bias, N, C):
 def mx_gemm(A, B, C=None, alpha=1.0, beta=0.0, out_dtype=BF16, bias=None, stream=None):
     """C <- alpha * A @ B^T + beta * C (+ bias) of MXTensors A (M x K) and B
     (N x K) of one format; returns C, allocated as out_dtype when None."""
+    if stream is not None:
+        return on_stream(stream, A.device, mx_gemm, A, B, C, alpha, beta, out_dtype, bias)
     if A.format != B.format:
         raise TypeError("A and B must have the same format")
     if A.cols != B.cols:
@@ -147,7 +158,7 @@ def mx_gemm(A, B, C=None, alpha=1.0, beta=0.0, out_dtype=BF16, bias=None, stream
                            A.codes.stride(0), A.scales.data_ptr(), _factor(A.tensor_scale, A.format, dev),
                            B.codes.data_ptr(), B.codes.stride(0), B.scales.data_ptr(),
                            _factor(B.tensor_scale, B.format, dev), ctypes.byref(b), C.data_ptr(), ldc,
-                           _bias(bias, B.rows, C), _stream(dev, stream))
+                           _bias(bias, B.rows, C), _raw_stream(dev.index))
     if st:
         _raise(st, "dga_mx_gemm")
     return C
@@ -157,6 +168,8 @@ def mx_linear_forward(X, W, bias=None, Y=None, tensor_scale=None, workspace=None
     """Y = X @ W^T + bias for X [batch, in] (float32, bfloat16 or float16) and a
     4-bit weight W, an MXTensor [out, in]: X is quantised in W's format
     (tensor_scale: its factor) and multiplied.  Y, of X's type unless given."""
+    if stream is not None:
+        return on_stream(stream, X.device, mx_linear_forward, X, W, bias, Y, tensor_scale, workspace)
     code = _CODE.get(X.dtype)
     if code is None:
         raise TypeError("X must be float32, bfloat16 or float16")
@@ -186,7 +199,7 @@ def mx_linear_forward(X, W, bias=None, Y=None, tensor_scale=None, workspace=None
                          codes.data_ptr(), codes.stride(0), W.scales.data_ptr(),
                          None if W.tensor_scale is None else _factor(W.tensor_scale, fmt, dev),
                          None if bias is None else _bias(bias, N, Y), Y.data_ptr(), ldy,
-                         workspace.data_ptr() if have else None, have, _raw_stream(dev.index) if stream is None else stream)
+                         workspace.data_ptr() if have else None, have, _raw_stream(dev.index))
     if st:
         _raise(st, "dga_mx_linear")
     return Y
@@ -198,14 +211,32 @@ def mx_linear_backward(X, W, G, format=MXFP4, tensor_scales=(None, None, None), 
     and W quantised along out, dW = G^T X with G and X quantised along the
     batch, both of G's type; db = the batch sum of G (fp32, unquantised).
     tensor_scales: the factors of X, W and G."""
+    if stream is not None:
+        return on_stream(stream, G.device, mx_linear_backward, X, W, G, format, tensor_scales, need_bias)
     if X.shape[0] != G.shape[0] or X.shape[1] != W.shape[1] or G.shape[1] != W.shape[0]:
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}, G {tuple(G.shape)}")
     if G.dtype not in _CODE:
         raise TypeError("G must be float32, bfloat16 or float16")
     sx, sw, sg = tensor_scales
-    out = _CODE[G.dtype]
-    dX = mx_gemm(mx_quantize(G, format, False, sg, stream), mx_quantize(W, format, True, sw, stream),
-                 out_dtype=out, stream=stream)
-    dW = mx_gemm(mx_quantize(G, format, True, sg, stream), mx_quantize(X, format, True, sx, stream),
-                 out_dtype=out, stream=stream)
-    return dX, dW, (sum_rows(G, stream=stream) if need_bias else None)
+    out, dev = _CODE[G.dtype], G.device
+    if all(T.stride(1) == 1 and T.is_cuda and T.device == dev and T.dtype in _CODE for T in (X, W, G)):
+        (M, N), K = G.shape, X.shape[1]
+        dX = torch.empty((M, K), dtype=G.dtype, device=dev)
+        dW = torch.empty((N, K), dtype=G.dtype, device=dev)
+        db = torch.empty(N, dtype=torch.float32, device=dev) if need_bias else None
+        L = lib()
+        have = L.dga_mx_linear_backward_workspace_size(format, M, N, K)
+        workspace = torch.empty(have, dtype=torch.uint8, device=dev) if have else None
+        st = L.dga_mx_linear_backward(format, _CODE[X.dtype], _CODE[W.dtype], out, M, N, K, X.data_ptr(),
+                                      max(X.stride(0), K, 1), _factor(sx, format, dev), W.data_ptr(),
+                                      max(W.stride(0), K, 1), _factor(sw, format, dev), G.data_ptr(),
+                                      max(G.stride(0), N, 1), _factor(sg, format, dev), dX.data_ptr(), K or 1,
+                                      dW.data_ptr(), K or 1, db.data_ptr() if need_bias else None,
+                                      workspace.data_ptr() if have else None, have, _raw_stream(dev.index))
+        if st:
+            _raise(st, "dga_mx_linear_backward")
+        return dX, dW, db
+    # column-major operands, which are quantised along the other axis
+    dX = mx_gemm(mx_quantize(G, format, False, sg), mx_quantize(W, format, True, sw), out_dtype=out)
+    dW = mx_gemm(mx_quantize(G, format, True, sg), mx_quantize(X, format, True, sx), out_dtype=out)
+    return dX, dW, (sum_rows(G) if need_bias else None)

@@ -482,6 +482,36 @@ int dga_mx_linear(dga_mx_format format, dga_dtype x_dtype, dga_dtype out_dtype, 
 size_t dga_mx_linear_workspace_size(dga_mx_format format, int64_t M, int64_t K);
 
 /*
+ * dga_mx_linear_backward -- gradients of Y = X W^T + bias for the output
+ * gradient G, with 4-bit products (the roundings' own gradient taken as 1):
+ *   dX <- Q(G) Q(W^T)^T     G and W quantised along N
+ *   dW <- Q(G^T) Q(X^T)^T   G and X quantised along M
+ *   db <- the sum of G's rows, fp32, unquantised
+ * The same results as the dga_mx_quantize, dga_mx_gemm and dga_sum_rows calls
+ * that it stands for.  X is M x K, W N x K, G M x N, dX M x K, dW N x K, all
+ * row-major, each input DGA_F32, DGA_BF16 or DGA_F16; dX and dW have G's type.
+ *   *_tensor_scale  device pointers to the factors of X, W and G (DGA_NVFP4)
+ *   db              N floats, or NULL where it is not wanted
+ *   workspace       device, 256-byte aligned, of
+ *                   dga_mx_linear_backward_workspace_size bytes
+ * Errors: DGA_ERR_UNSUPPORTED; -5 M, -6 N, -7 K, -8 X, -9 ldx,
+ * -10 x_tensor_scale, -11..-13 W, ldw, W_tensor_scale, -14..-16 G's, -17 dX,
+ * -18 lddx, -19 dW, -20 lddw, -22 workspace; DGA_ERR_WORKSPACE;
+ * DGA_ERR_OVERLAP when an output or the workspace meets an input or another
+ * output.
+ */
+int dga_mx_linear_backward(dga_mx_format format, dga_dtype x_dtype, dga_dtype w_dtype,
+                           dga_dtype g_dtype, int64_t M, int64_t N, int64_t K, const void* X,
+                           int64_t ldx, const float* x_tensor_scale, const void* W, int64_t ldw,
+                           const float* w_tensor_scale, const void* G, int64_t ldg,
+                           const float* g_tensor_scale, void* dX, int64_t lddx, void* dW,
+                           int64_t lddw, float* db, void* workspace, size_t workspace_bytes,
+                           dga_stream_t stream);
+
+size_t dga_mx_linear_backward_workspace_size(dga_mx_format format, int64_t M, int64_t N,
+                                             int64_t K);
+
+/*
  * dga_orthogonalize -- orthogonalises an update (the Muon optimiser's step):
  * for each of `batch` row-major matrices G (rows x cols, leading dimension
  * ldg, stride_g elements apart),

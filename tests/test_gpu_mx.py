@@ -302,6 +302,55 @@ def test_on_another_stream_and_in_a_graph():
     assert torch.equal(out, dga.mx_linear_forward(x * 2, W))
 
 
+def test_a_given_stream_owns_what_is_allocated():
+    """Memory freed while the current stream has yet to read it is not handed
+    out to a call on another stream."""
+    x = _values(256, 1024, 3).cuda()
+    q = dga.mx_quantize(x)
+    want = dga.mx_dequantize(q)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda: dga.mx_dequantize(q, stream=s.cuda_stream), lambda: dga.orthogonalize(x, stream=s.cuda_stream),
+                 lambda: dga.mx_gemm(q, q, out_dtype=dga.F32, stream=s.cuda_stream)):
+        old = torch.full_like(want, 7.0)
+        torch.cuda.synchronize()
+        torch.cuda._sleep(100_000_000)
+        copy = old.clone()
+        del old
+        call()
+        torch.cuda.synchronize()
+        assert bool((copy == 7.0).all())
+    assert torch.equal(dga.mx_dequantize(q, stream=torch.cuda.default_stream().cuda_stream), want)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtypes", [(torch.bfloat16,) * 3, (torch.float32, torch.bfloat16, torch.float16)])
+@pytest.mark.parametrize("T,N,K", [(1, 1, 1), (5, 130, 67), (33, 40, 50), (300, 257, 129), (64, 520, 300)])
+def test_linear_backward_is_its_parts(fmt, dtypes, T, N, K):
+    """One call equals quantisations, products and sum called apart, bit for bit,
+    for row-major operands, views and column-major ones."""
+    base = [_values(T, K + 3, 5, dtypes[0]).cuda(), _values(N, K + 3, 6, dtypes[1]).cuda(), _values(T, N + 3, 7, dtypes[2]).cuda()]
+    x, w, g = (t[:, 1:-2] for t in base)
+    f = [_factor(t.cpu(), fmt)[0] for t in (x, w, g)]
+    want_dX = dga.mx_gemm(dga.mx_quantize(g, fmt, tensor_scale=f[2]), dga.mx_quantize(w, fmt, True, f[1]), out_dtype=OUT[dtypes[2]])
+    want_dW = dga.mx_gemm(dga.mx_quantize(g, fmt, True, f[2]), dga.mx_quantize(x, fmt, True, f[0]), out_dtype=OUT[dtypes[2]])
+    for a, b, c in ((x, w, g), (x.contiguous(), w.contiguous(), g.contiguous()), (x.t().contiguous().t(), w, g)):
+        dX, dW, db = dga.mx_linear_backward(a, b, c, fmt, tensor_scales=tuple(f))
+        _sync_ok()
+        assert torch.equal(dX, want_dX) and torch.equal(dW, want_dW) and torch.equal(db, dga.sum_rows(g))
+    assert dga.mx_linear_backward(x, w, g, fmt, need_bias=False)[2] is None
+
+
+def test_linear_backward_of_nothing():
+    for T, N, K in ((0, 5, 7), (4, 0, 7), (4, 5, 0)):
+        x, w, g = torch.ones(T, K, device="cuda"), torch.ones(N, K, device="cuda"), torch.ones(T, N, device="cuda")
+        dX, dW, db = dga.mx_linear_backward(x, w, g)
+        _sync_ok()
+        assert dX.shape == (T, K) and not dX.any()
+        assert dW.shape == (N, K) and not dW.any()
+        assert torch.equal(db, torch.full((N,), float(T), device="cuda"))
+
+
 @pytest.mark.parametrize("fmt", FMT)
 def test_offsets_past_32_bits(fmt):
     """Sources, values and products of more than 2^31 elements: their last rows

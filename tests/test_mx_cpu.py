@@ -146,6 +146,35 @@ def test_linear_arguments(over, code):
     assert _linear(**over) == code
 
 
+def _backward(**over):
+    a = dict(format=dga.NVFP4, x_dtype=gen.BF16, w_dtype=gen.F32, g_dtype=gen.F16, M=20, N=5, K=64, X=A, ldx=64, xt=None,
+             W=B, ldw=64, wt=None, G=C, ldg=5, gt=None, dX=D, lddx=64, dW=E, lddw=64, db=E + (1 << 20), ws=E + (1 << 24),
+             ws_bytes=1 << 20, stream=None)
+    a.update(over)
+    return dga.dga_mx_linear_backward(*a.values())
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(format=7), dga.ERR_UNSUPPORTED), (dict(w_dtype=gen.I8), dga.ERR_UNSUPPORTED), (dict(M=-1), -5), (dict(N=-1), -6),
+    (dict(K=1 << 30), -7), (dict(X=None), -8), (dict(ldx=63), -9), (dict(format=dga.MXFP4, xt=A), -10), (dict(W=None), -11),
+    (dict(ldw=63), -12), (dict(format=dga.MXFP4, wt=A), -13), (dict(G=None), -14), (dict(ldg=4), -15),
+    (dict(format=dga.MXFP4, gt=A), -16), (dict(dX=None), -17), (dict(lddx=63), -18), (dict(dW=None), -19), (dict(lddw=63), -20),
+    (dict(ws=None), -22), (dict(ws=E + (1 << 24) + 16), -22), (dict(ws_bytes=1000), dga.ERR_WORKSPACE),
+    (dict(ws=None, ws_bytes=0), dga.ERR_WORKSPACE), (dict(dX=A), dga.ERR_OVERLAP), (dict(dX=C), dga.ERR_OVERLAP),
+    (dict(dW=B + 256), dga.ERR_OVERLAP), (dict(dW=D), dga.ERR_OVERLAP), (dict(db=C), dga.ERR_OVERLAP), (dict(db=D), dga.ERR_OVERLAP),
+    (dict(ws=A), dga.ERR_OVERLAP), (dict(ws=D), dga.ERR_OVERLAP),
+])
+def test_linear_backward_arguments(over, code):
+    assert _backward(**over) == code
+
+
+def test_linear_backward_workspace():
+    size = dga.dga_mx_linear_backward_workspace_size
+    assert size(dga.MXFP4, 0, 5, 7) == size(dga.NVFP4, 5, 0, 7) == size(dga.MXFP4, 5, 7, -1) == size(9, 1, 1, 1) == 0
+    # G and W^T along 64, G^T and X^T along 32: codes in multiples of 256 bytes, scale tiles of 512
+    assert size(dga.MXFP4, 32, 64, 48) == (32 * 32 + 512) + (48 * 32 + 512) + (64 * 16 + 512) + (48 * 16 + 512)
+
+
 def _ortho(**over):
     a = dict(in_dtype=gen.F32, out_dtype=gen.F32, batch=2, rows=4, cols=8, G=A, ldg=8, stride_g=32, O=B, ldo=8, stride_o=32,
              steps=5, co=(ctypes.c_float * 15)(), eps=1e-7, ws=D, ws_bytes=1 << 24, stream=None)
