@@ -89,6 +89,17 @@ def test_batches_on_cta_pairs_with_thin_last_tiles(dtype, shape):
     assert (frame == 7.0).all(), "written outside the result"
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shape", [(14, 515, 700), (26, 300, 310), (3, 1025, 2050)])
+def test_a_last_round_of_few_tiles(dtype, shape):
+    """Tile counts just past a whole number of rounds, symmetric products among them."""
+    G = _momentum(shape, 13).to(dtype).cuda()
+    got = dga.orthogonalize(G)
+    _ok()
+    assert _rel(got, _formula(G).cpu()) <= TOL[dtype]
+    assert torch.equal(got, dga.orthogonalize(G))
+
+
 def test_offsets_past_32_bits():
     """A 140 x 16,000,000 update (2.24e9 values): the columns at both ends, from
     fp64 products."""
