@@ -7,6 +7,7 @@ scratch and results come from PyTorch's caching allocator, on the same stream.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -16,6 +17,22 @@ MXFP4, NVFP4 = 0, 1
 
 _CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 _TORCH = {F32: torch.float32, BF16: torch.bfloat16, F16: torch.float16}
+
+
+# sizes of scratch and scales, by shape (a library call for one costs 0.7 us)
+@functools.lru_cache(maxsize=4096)
+def _scales_size(format, rows, K):
+    return lib().dga_mx_scales_size(format, rows, K)
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_workspace(format, M, K):
+    return lib().dga_mx_linear_workspace_size(format, M, K)
+
+
+@functools.lru_cache(maxsize=4096)
+def _backward_workspace(format, M, N, K):
+    return lib().dga_mx_linear_backward_workspace_size(format, M, N, K)
 
 
 class MXTensor:
@@ -96,7 +113,7 @@ def mx_quantize(X, format=MXFP4, transpose=False, tensor_scale=None, stream=None
     dev, L = X.device, lib()
     row_bytes = (K + 31) // 32 * 16  # dga_mx_row_bytes
     codes = torch.empty((R, row_bytes), dtype=torch.uint8, device=dev)
-    scales = torch.empty(L.dga_mx_scales_size(format, R, K), dtype=torch.uint8, device=dev)
+    scales = torch.empty(_scales_size(format, R, K), dtype=torch.uint8, device=dev)
     st = L.dga_mx_quantize(format, code, 1 if transpose else 0, rows, cols, X.data_ptr(), ldx,
                            _factor(tensor_scale, format, dev), codes.data_ptr(), row_bytes,
                            scales.data_ptr(), _raw_stream(dev.index))
@@ -189,7 +206,7 @@ def mx_linear_forward(X, W, bias=None, Y=None, tensor_scale=None, workspace=None
         Y, out, ldy = _output(Y, M, N, 0, code, dev)
     L = lib()
     if workspace is None:
-        have = L.dga_mx_linear_workspace_size(fmt, M, K)  # 0 for a few rows
+        have = _linear_workspace(fmt, M, K)  # 0 for a few rows
         if have:
             workspace = torch.empty(have, dtype=torch.uint8, device=dev)
     else:
@@ -225,7 +242,7 @@ def mx_linear_backward(X, W, G, format=MXFP4, tensor_scales=(None, None, None), 
         dW = torch.empty((N, K), dtype=G.dtype, device=dev)
         db = torch.empty(N, dtype=torch.float32, device=dev) if need_bias else None
         L = lib()
-        have = L.dga_mx_linear_backward_workspace_size(format, M, N, K)
+        have = _backward_workspace(format, M, N, K)
         workspace = torch.empty(have, dtype=torch.uint8, device=dev) if have else None
         st = L.dga_mx_linear_backward(format, _CODE[X.dtype], _CODE[W.dtype], out, M, N, K, X.data_ptr(),
                                       max(X.stride(0), K, 1), _factor(sx, format, dev), W.data_ptr(),
