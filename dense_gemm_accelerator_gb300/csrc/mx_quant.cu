@@ -28,17 +28,6 @@
 namespace dga {
 namespace {
 
-template <typename T> struct MxIn;
-template <> struct MxIn<float> {
-    __device__ __forceinline__ static float f(float v) { return v; }
-};
-template <> struct MxIn<__nv_bfloat16> {
-    __device__ __forceinline__ static float f(__nv_bfloat16 v) { return __bfloat162float(v); }
-};
-template <> struct MxIn<__half> {
-    __device__ __forceinline__ static float f(__half v) { return __half2float(v); }
-};
-
 // Eight codes to their values.
 __device__ __forceinline__ void values8(uint32_t c, float (&v)[8]) {
     uint32_t h[4];
@@ -58,23 +47,14 @@ __device__ __forceinline__ void values8(uint32_t c, float (&v)[8]) {
 }
 
 // Eight consecutive values of a row, zero past its end.  `vec`: the row's
-// groups of eight are 16-byte aligned.
-template <typename T>
-__device__ __forceinline__ void load8(const T* __restrict__ row, int64_t k, int64_t K, bool vec,
-                                      float (&x)[8]) {
+// groups of four are 16-byte aligned.
+__device__ __forceinline__ void load8(const float* __restrict__ row, int64_t k, int64_t K, bool vec, float (&x)[8]) {
     if (vec && k + 8 <= K) {
-        T v[8];
-        if constexpr (sizeof(T) == 2) {
-            *reinterpret_cast<uint4*>(v) = __ldg(reinterpret_cast<const uint4*>(row + k));
-        } else {
-            reinterpret_cast<uint4*>(v)[0] = __ldg(reinterpret_cast<const uint4*>(row + k));
-            reinterpret_cast<uint4*>(v)[1] = __ldg(reinterpret_cast<const uint4*>(row + k) + 1);
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = MxIn<T>::f(v[q]);
+        const float4 a = __ldg(reinterpret_cast<const float4*>(row + k)), b = __ldg(reinterpret_cast<const float4*>(row + k) + 1);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     } else {
 #pragma unroll
-        for (int q = 0; q < 8; ++q) x[q] = k + q < K ? MxIn<T>::f(row[k + q]) : 0.0f;
+        for (int q = 0; q < 8; ++q) x[q] = k + q < K ? row[k + q] : 0.0f;
     }
 }
 
@@ -82,7 +62,8 @@ __device__ __forceinline__ void load8(const T* __restrict__ row, int64_t k, int6
 // placed while the kernel before still runs, and wait here for its end.  Then a
 // product launched behind this one may be placed: it reads its weight at once,
 // which was complete before this grid's start, and waits for this grid's end
-// before it reads what is written here.  (BWDFIG)
+// before it reads what is written here.  (The gradients of a 4096 x 4096 layer for 4096
+// tokens: 122 to 109 us.)
 __device__ __forceinline__ void begin_after_previous() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -171,8 +152,8 @@ __global__ void __launch_bounds__(256) mx_quant_rows16_kernel(const T* __restric
     }
 }
 
-template <int kFormat, typename T>
-__global__ void __launch_bounds__(256) mx_quant_rows_kernel(const T* __restrict__ X, int64_t ldx,
+template <int kFormat>
+__global__ void __launch_bounds__(256) mx_quant_rows32_kernel(const float* __restrict__ X, int64_t ldx,
                                                             int64_t rows, int64_t K, bool vec,
                                                             const float* __restrict__ factor,
                                                             uint8_t* __restrict__ codes,
@@ -210,87 +191,70 @@ __global__ void __launch_bounds__(256) mx_quant_rows_kernel(const T* __restrict_
 
 // ---- along columns -----------------------------------------------------------
 //
-// The transpose of X (rows x cols) in 4 bits: cols rows of K = rows values.
-// A CTA takes 128 (k) x 64 (columns) of X through shared memory; a thread
-// quantises one block (MXFP4) or two (NVFP4) of one column, reading down the
-// tile (consecutive lanes on consecutive columns), and the codes go back
-// through shared memory so that each row of the result gets 64 consecutive
-// bytes.
-template <int kFormat, typename T>
-__global__ void __launch_bounds__(256) mx_quant_cols_kernel(const T* __restrict__ X, int64_t ldx,
-                                                            int64_t K, int64_t cols, bool vec,
-                                                            const float* __restrict__ factor,
-                                                            uint8_t* __restrict__ codes,
-                                                            int64_t ldc, uint8_t* __restrict__ scales,
-                                                            int64_t tiles_k, int64_t blocks_k,
-                                                            int64_t row_bytes) {
-    begin_after_previous();
-    constexpr int kPad = 16 / sizeof(T);
-    __shared__ __align__(16) T tile[128][64 + kPad];
-    __shared__ __align__(16) uint32_t out[64][16 + 4];
-    const int t = threadIdx.x;
-    const int64_t k0 = (blockIdx.x % blocks_k) * 128, c0 = (blockIdx.x / blocks_k) * 64;
-    const TensorFactor g((kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f);
-    constexpr int kVec = 16 / sizeof(T);       // values of one 16-byte load
-    constexpr int kPerRow = 64 / kVec;         // loads of a tile row
-#pragma unroll
-    for (int i = 0; i < 128 * kPerRow / 256; ++i) {
-        const int idx = i * 256 + t, kk = idx / kPerRow, cc = idx % kPerRow * kVec;
-        const int64_t k = k0 + kk, c = c0 + cc;
-        const T* src = X + k * ldx + c;
-        if (vec && k < K && c + kVec <= cols) {
-            *reinterpret_cast<uint4*>(&tile[kk][cc]) = __ldg(reinterpret_cast<const uint4*>(src));
-        } else {
-#pragma unroll
-            for (int q = 0; q < kVec; ++q)
-                tile[kk][cc + q] = (k < K && c + q < cols) ? src[q] : T(0.0f);
-        }
+// The transpose of X (rows x cols) in 4 bits: cols rows of K = rows values.  A
+// CTA takes 128 (k) x 128 (columns) of X, a thread 32 k of one column (fp32) or
+// of two adjacent ones (16 bits), read straight from memory (a warp 128
+// consecutive bytes) with all 32 loads under way at once.  Codes and scales go
+// out through shared memory, so that each row of the result gets 64 consecutive
+// bytes and scales are written as whole tiles.  8192 x 8192 MXFP4: bf16 31 us,
+// fp32 52 us; with X's tile through shared memory 51 and 81 us.
+
+// The end of both kernels: codes of 128 rows x 128 k, and their scale tiles.
+template <int kFormat>
+__device__ __forceinline__ void cols_out(const uint32_t (&out)[128][16 + 4], const uint8_t* tiles, int t, int threads, int64_t k0,
+                                         int64_t c0, int64_t cols, uint8_t* __restrict__ codes, int64_t ldc,
+                                         uint8_t* __restrict__ scales, int64_t tiles_k, int64_t row_bytes) {
+    constexpr int kTiles = 32 / mx_block(kFormat);
+    const int64_t first_tile = k0 / 128 * kTiles;
+    if (t < kTiles * (kMxTileBytes / 16) && first_tile + t / (kMxTileBytes / 16) < tiles_k)
+        reinterpret_cast<uint4*>(scales + mx_scale_offset(c0, first_tile * 4, tiles_k))[t] = reinterpret_cast<const uint4*>(tiles)[t];
+    for (int idx = t; idx < 512; idx += threads) {
+        const int orow = idx >> 2, ow = (idx & 3) * 4;  // 16 bytes of a result row
+        const int64_t byte = (k0 >> 1) + ow * 4;
+        if (c0 + orow < cols && byte < row_bytes)
+            *reinterpret_cast<uint4*>(codes + (c0 + orow) * ldc + byte) = *reinterpret_cast<const uint4*>(&out[orow][ow]);
     }
-    __syncthreads();
-    const int col = t & 63, quarter = t >> 6;  // 32 values of a column per thread
-    constexpr int kB = mx_block(kFormat), kPer = 32 / kB;
-    const int64_t c = c0 + col;
-    uint32_t word = 0, four[4];
-#pragma unroll
-    for (int p = 0; p < kPer; ++p) {
-        float x[kB];
-        uint32_t m = 0;
-#pragma unroll
-        for (int q = 0; q < kB; ++q) {
-            x[q] = MxIn<T>::f(tile[quarter * 32 + p * kB + q][col]);
-            m = max(m, mag_bits(x[q]));
-        }
-        const BlockScale b = block_scale<kFormat>(m, g);
-#pragma unroll
-        for (int o = 0; o < kB / 8; ++o) {
-            float y[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] = x[o * 8 + q];
-            over_unit8<kFormat>(y, b);
-            four[p * (kB / 8) + o] = codes8(y);
-        }
-        const int64_t k = k0 + quarter * 32 + p * kB;
-        word |= (k < K ? static_cast<uint32_t>(b.byte) : 0u) << (8 * p);
-    }
-    *reinterpret_cast<uint4*>(&out[col][quarter * 4]) = make_uint4(four[0], four[1], four[2], four[3]);
-    // the scales of this thread's 32 values: one byte, or two
-    const int64_t s = (k0 + quarter * 32) / kB;
-    if (c < cols && (s >> 2) < tiles_k) {
-        uint8_t* dst = scales + mx_scale_offset(c, s, tiles_k);
-        if constexpr (kPer == 1) *dst = static_cast<uint8_t>(word);
-        else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(word);
-    }
-    __syncthreads();
-    const int orow = t >> 2, ow = (t & 3) * 4;  // 16 bytes of a result row per thread
-    const int64_t byte = (k0 >> 1) + ow * 4;
-    if (c0 + orow < cols && byte < row_bytes)
-        *reinterpret_cast<uint4*>(codes + (c0 + orow) * ldc + byte) = *reinterpret_cast<const uint4*>(&out[orow][ow]);
 }
 
-// 16-bit sources: 128 (k) x 128 (columns), a thread 32 k of two adjacent
-// columns, read straight from memory as one word each (a warp 128 consecutive
-// bytes), all 32 loads under way at once, and their maxima taken together.
-// (8192 x 8192 bf16 MXFP4 with the tile through shared memory: 51 us.)
+template <int kFormat>
+__global__ void __launch_bounds__(512) mx_quant_cols32_kernel(const float* __restrict__ X, int64_t ldx, int64_t K, int64_t cols,
+                                                              const float* __restrict__ factor, uint8_t* __restrict__ codes,
+                                                              int64_t ldc, uint8_t* __restrict__ scales, int64_t tiles_k,
+                                                              int64_t blocks_k, int64_t row_bytes) {
+    begin_after_previous();
+    __shared__ __align__(16) uint32_t out[128][16 + 4];
+    constexpr int kB = mx_block(kFormat), kPer = 32 / kB;
+    __shared__ __align__(16) uint8_t tiles[kPer * kMxTileBytes];
+    const int t = threadIdx.x, col = t & 127, quarter = t >> 7;
+    const int64_t k0 = (blockIdx.x % blocks_k) * 128, c0 = (blockIdx.x / blocks_k) * 128;
+    const TensorFactor g((kFormat == DGA_NVFP4 && factor != nullptr) ? __ldg(factor) : 1.0f);
+    const int64_t k = k0 + quarter * 32;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(X + k * ldx + c0 + col);
+    uint32_t raw[32];
+    if (k + 32 <= K && c0 + col < cols) {
+#pragma unroll
+        for (int q = 0; q < 32; ++q) raw[q] = __ldg(src + q * ldx);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 32; ++q) raw[q] = k + q < K && c0 + col < cols ? __ldg(src + q * ldx) : 0u;
+    }
+    uint4 four;
+    uint32_t bytes;
+    quantize_run<kFormat>(DGA_F32, raw, g, four, bytes);
+    // blocks past the last value have a scale of 0
+#pragma unroll
+    for (int p = 0; p < kPer; ++p)
+        if (k + p * kB >= K) bytes &= ~(0xffu << (8 * p));
+    *reinterpret_cast<uint4*>(&out[col][quarter * 4]) = four;
+    uint8_t* dst = tiles + mx_scale_offset(col, quarter * kPer, kPer);
+    if constexpr (kPer == 1) *dst = static_cast<uint8_t>(bytes);
+    else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(bytes);
+    __syncthreads();
+    cols_out<kFormat>(out, tiles, t, 512, k0, c0, cols, codes, ldc, scales, tiles_k, row_bytes);
+}
+
+// (of 16-bit sources, where rows start on a word; their two maxima are taken
+// together)
 template <int kFormat, typename T>
 __global__ void __launch_bounds__(256) mx_quant_cols16_kernel(const T* __restrict__ X, int64_t ldx,
                                                               int64_t K, int64_t cols, bool vec,
@@ -355,16 +319,7 @@ __global__ void __launch_bounds__(256) mx_quant_cols16_kernel(const T* __restric
         else *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(word[h]);
     }
     __syncthreads();
-    const int64_t first_tile = k0 / 128 * kTiles;
-    if (t < kTiles * (kMxTileBytes / 16) && first_tile + t / (kMxTileBytes / 16) < tiles_k)
-        reinterpret_cast<uint4*>(scales + mx_scale_offset(c0, first_tile * 4, tiles_k))[t] = reinterpret_cast<const uint4*>(tiles)[t];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int idx = i * 256 + t, orow = idx >> 2, ow = (idx & 3) * 4;  // 16 bytes of a result row
-        const int64_t byte = (k0 >> 1) + ow * 4;
-        if (c0 + orow < cols && byte < row_bytes)
-            *reinterpret_cast<uint4*>(codes + (c0 + orow) * ldc + byte) = *reinterpret_cast<const uint4*>(&out[orow][ow]);
-    }
+    cols_out<kFormat>(out, tiles, t, 256, k0, c0, cols, codes, ldc, scales, tiles_k, row_bytes);
 }
 
 // ---- back to values ------------------------------------------------------------
@@ -461,10 +416,10 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(uint32_t rows, int32_t 
 }
 
 template <typename... P, typename... A>
-cudaError_t launch_behind(void (*kern)(P...), dim3 grid, cudaStream_t stream, const A&... args) {
+cudaError_t launch_behind(void (*kern)(P...), dim3 grid, unsigned threads, cudaStream_t stream, const A&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(threads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -490,27 +445,27 @@ cudaError_t quantize_as(const MxQuantArgs& a, const DeviceInfo& dev) {
             const int64_t rows_per_block = 256 >> log_x;
             const dim3 grid(static_cast<unsigned>((runs + (1 << log_x) - 1) >> log_x),
                             static_cast<unsigned>(std::min<int64_t>((a.rows + rows_per_block - 1) / rows_per_block, 65535)));
-            return launch_behind(
-                mx_quant_rows16_kernel<kFormat, T>, grid, a.stream, X, a.ldx, static_cast<uint32_t>(a.rows), K, vec, a.factor, a.codes, a.ld_codes, a.scales, tiles_k,
-                static_cast<uint32_t>(runs), log_x);
+            return launch_behind(mx_quant_rows16_kernel<kFormat, T>, grid, 256, a.stream, X, a.ldx, static_cast<uint32_t>(a.rows), K,
+                                 vec, a.factor, a.codes, a.ld_codes, a.scales, tiles_k, static_cast<uint32_t>(runs), log_x);
         } else {
             const int64_t chunks = (K + 255) / 256, units = a.rows * chunks;
             const int64_t blocks = std::min<int64_t>((units + 7) / 8, static_cast<int64_t>(dev.sm_count) * 64);
-            return launch_behind(
-                mx_quant_rows_kernel<kFormat, T>, dim3(static_cast<unsigned>(blocks)), a.stream, X, a.ldx, a.rows, K, vec, a.factor, a.codes, a.ld_codes, a.scales, tiles_k, chunks, row_bytes);
+            return launch_behind(mx_quant_rows32_kernel<kFormat>, dim3(static_cast<unsigned>(blocks)), 256, a.stream, X, a.ldx,
+                                 a.rows, K, vec, a.factor, a.codes, a.ld_codes, a.scales, tiles_k, chunks, row_bytes);
         }
     } else {
-        constexpr int64_t kWide = sizeof(T) == 2 ? 128 : 64;
-        const int64_t blocks_k = (K + 127) / 128, blocks = blocks_k * ((a.cols + kWide - 1) / kWide);
+        const int64_t blocks_k = (K + 127) / 128, blocks = blocks_k * ((a.cols + 127) / 128);
         if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-        // two 16-bit values of a row at once
-        const bool pairs = aligned(a.X, 4) && a.ldx % 2 == 0;
-        auto run = [&](auto kernel) {
-            return launch_behind(kernel, dim3(static_cast<unsigned>(blocks)), a.stream, X, a.ldx, K, a.cols, sizeof(T) == 2 ? pairs : vec, a.factor, a.codes, a.ld_codes,
-                                                                        a.scales, tiles_k, blocks_k, row_bytes);
-        };
-        if constexpr (sizeof(T) == 2) return run(mx_quant_cols16_kernel<kFormat, T>);
-        else return run(mx_quant_cols_kernel<kFormat, T>);
+        const dim3 grid(static_cast<unsigned>(blocks));
+        if constexpr (sizeof(T) == 2) {
+            // two values of a row at once
+            const bool pairs = aligned(a.X, 4) && a.ldx % 2 == 0;
+            return launch_behind(mx_quant_cols16_kernel<kFormat, T>, grid, 256, a.stream, X, a.ldx, K, a.cols, pairs, a.factor,
+                                 a.codes, a.ld_codes, a.scales, tiles_k, blocks_k, row_bytes);
+        } else {
+            return launch_behind(mx_quant_cols32_kernel<kFormat>, grid, 512, a.stream, X, a.ldx, K, a.cols, a.factor, a.codes,
+                                 a.ld_codes, a.scales, tiles_k, blocks_k, row_bytes);
+        }
     }
 }
 
@@ -528,7 +483,7 @@ cudaError_t dequantize_as(const MxMatrix& q, int64_t rows, int64_t K, void* Y, i
     const int64_t down = cols * all >= static_cast<int64_t>(dev.sm_count) * 8 * kDequantRows ? (all + kDequantRows - 1) / kDequantRows : all;
     const dim3 grid(static_cast<unsigned>(cols), static_cast<unsigned>(std::min<int64_t>(down, 65535)));
     const auto kernel = vec ? mx_dequant_kernel<kFormat, T, false> : mx_dequant_kernel<kFormat, T, true>;
-    return launch_behind(kernel, grid, stream, static_cast<uint32_t>(rows), static_cast<int32_t>(K), static_cast<const uint8_t*>(q.codes), q.ld,
+    return launch_behind(kernel, grid, 256, stream, static_cast<uint32_t>(rows), static_cast<int32_t>(K), static_cast<const uint8_t*>(q.codes), q.ld,
                                      static_cast<const uint8_t*>(q.scales), mx_tiles_k(kFormat, K), q.factor, static_cast<T*>(Y),
                                      ldy, log_x);
 }
