@@ -26,15 +26,17 @@
 //     goes to latency and not to products: hi lo + lo hi + hi hi, 22 bits.
 //     The tensor cores' fp32 accumulation cuts off instead of rounding, half a
 //     unit of the sum lost per MMA on average (2.2e-5 off the result at K =
-//     4099 x 3), so the hi hi products are accumulated in chunks of 128 values
-//     of K, added up in registers with rounding: as exact as fp32 products of
-//     the same formula.  The cross products, 2^-11 of the sum, have an
+//     4099 x 3), so the hi hi products are accumulated in chunks of 64 values
+//     of K or fewer, added up in registers with rounding: as exact as fp32
+//     products of the same formula (0.4 to 1.2 times their error; with chunks
+//     of 128 up to 2.4 times it for n >> m, where A's large diagonal makes the
+//     losses of A^2 agree, at the same time but for 4096^2 fp32, 3.1 to 3.2 ms).  The cross products, 2^-11 of the sum, have an
 //     accumulator of their own.
 //
 // Measured (five steps; the floor is 5 (4 m^2 n) operations at the bf16 rate of
 // 1900 TFLOP/s with the triangles, three times that for split products):
-// 4096^2 bf16 1.10 to 1.13 ms (0.72), 4096^2 fp32 3.0 ms (2.2), 2048^2 bf16
-// 250 us (90), 1000 x 4099 fp32 307 us (105), 12 x 1030 x 515 bf16 241 us (30),
+// 4096^2 bf16 1.10 to 1.13 ms (0.72), 4096^2 fp32 3.2 ms (2.2), 2048^2 bf16
+// 250 us (90), 1000 x 4099 fp32 311 us (105), 12 x 1030 x 515 bf16 241 us (30),
 // 256^2 106 us: rounds of tiles that are not full at the large ends, and at the
 // small ones 15 products in a row, of which each has 1.1 us of first loads, 0.5
 // to 2.8 us of joining and 1.1 to 1.8 us from one launch's end to the next.
@@ -68,7 +70,7 @@ namespace {
 constexpr uint64_t kWaitLimitNs = 4000000000ull;  // 4 s
 constexpr float kScale = 4096.0f;                 // stored = kScale * value
 constexpr int kSmallRows = 256;
-constexpr uint32_t kChunk = 2;  // K blocks of one chunk of the hi hi product where operands are split
+constexpr uint32_t kChunk = 1;  // K blocks of one chunk of the hi hi product where operands are split
 constexpr uint32_t kBoxBytes = 64 * 64 * 2;  // an MN-major box: 64 columns x 64 k
 enum : int { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3 };
 
@@ -1033,10 +1035,10 @@ __global__ void __launch_bounds__(256) ns_first_kernel(const T* __restrict__ G, 
 //      of the boxes lie together, so that bulk copies hand them to the others;
 //   3. A^2, B = b A + c A^2 and X <- a X + B X of the slab, in each CTA.
 // Only step 2 crosses CTAs, with one full cluster barrier.  With C = 1 nothing
-// does.  Accumulators: the cross products in one, each 128 values of K of the
-// hi hi product in one of its own.
+// does.  Accumulators: the cross products in one, the hi hi product
+// in up to three, of 32 to 64 values of K each (B X: of 128).
 // For m, n this small the time is latency: 15 products of 1 to 2 us and, with
-// C > 1, an exchange of about 5 us a step.  29 us at 64 x 64, 57 us at 128 x
+// C > 1, an exchange of about 5 us a step.  29 us at 64 x 64, 59 us at 128 x
 // 512; as separate launches (2 + 3 a step) 85 and 134 us.
 
 constexpr int kMaxBoxes = 3;                      // 64-column boxes of a slab
@@ -1176,6 +1178,13 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]) + __uint_as_float(t[j]);
     };
+    auto more16 = [&](uint32_t a, float (&v)[16]) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(tmem + lane_base + a, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
+    };
     // D[128 x 128] (+)= P P'^T over `n` boxes of 64, both K-major
     auto mma_kk = [&](uint32_t acc, uint32_t pa, uint32_t qa, int n, bool fresh) {
         for (int b = 0; b < n; ++b) {
@@ -1185,15 +1194,37 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
                 tc_mma<kFmtF16>(tmem + acc, pd + 2 * k, qd + 2 * k, kIdesc, (fresh && b == 0 && k == 0) ? 0u : 1u);
         }
     };
+    // The same for a symmetric hi hi product of n MMAs (16 of K each), in chunks
+    // of `each` with an accumulator each: columns 128, 256 and 384 on.
+    auto mma_chunks = [&](uint32_t pa, int n, int each) {
+        uint32_t acc = tmem + 128;
+        int left = each;
+        for (int b = 0; b < n; b += 4) {
+            const uint64_t d = smem_desc_kmajor_sw128(pa + (b >> 2) * kXBox);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (left == 0) {
+                    acc += 128;
+                    left = each;
+                }
+                tc_mma<kFmtF16>(acc, d + 2 * k, d + 2 * k, kIdesc, left == each ? 0u : 1u);
+                --left;
+            }
+        }
+    };
+    // up to three chunks: of 64 of K, 48, 48 and 32, or 32
+    const int x_each = boxes == 3 ? 4 : boxes == 2 ? 3 : 2, x_chunks = boxes > 1 ? 3 : 2;
+    const int a_mmas = c.m <= 64 ? 4 : 8;  // of A^2: K to A's last box in use
+    const int a_each = c.m <= 64 ? 2 : 3, a_chunks = c.m <= 64 ? 2 : 3;
     const int per = 128 / c.cluster, shift = 31 - __clz(per);  // columns of the shares, rows of A, that a CTA joins
 
     for (int step = 0; step < c.steps; ++step) {
         const float ca = c.coefficients[3 * step], cb = c.coefficients[3 * step + 1], cc = c.coefficients[3 * step + 2];
-        // ---- 1. this CTA's share of X X^T: columns 0-127 the cross products, then 128 per two boxes
+        // ---- 1. this CTA's share of X X^T: columns 0-127 the cross products, then 128 a chunk
         if (tid == 0 && boxes > 0) {
             mma_kk(0, xh_s, xl_s, boxes, true);
             mma_kk(0, xl_s, xh_s, boxes, false);
-            for (int b = 0; b < boxes; b += 2) mma_kk(128 + 64 * b, xh_s + b * kXBox, xh_s + b * kXBox, min(2, boxes - b), true);
+            mma_chunks(xh_s, 4 * boxes, x_each);
             tc_commit(&done);
         }
         __syncwarp();
@@ -1206,13 +1237,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
             float v[16];
             if (boxes > 0) {
                 add16(b16 * 16, 128 + b16 * 16, v);
-                if (boxes > 2) {
-                    uint32_t r[16];
-                    tmem_ld_32x32b_x16(tmem + lane_base + 256 + b16 * 16, r);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
-                }
+                for (int i = 1; i < x_chunks; ++i) more16(128 + 128 * i + b16 * 16, v);
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j) v[j] = 0.0f;
@@ -1286,7 +1311,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
         if (tid == 0) {
             mma_kk(0, ah_s, al_s, 2, true);
             mma_kk(0, al_s, ah_s, 2, false);
-            mma_kk(128, ah_s, ah_s, 2, true);
+            mma_chunks(ah_s, a_mmas, a_each);
             tc_commit(&done);
         }
         __syncwarp();
@@ -1295,6 +1320,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
         for (int b16 = group * 2; b16 < group * 2 + 2; ++b16) {
             float v[16];
             add16(b16 * 16, 128 + b16 * 16, v);
+            for (int i = 1; i < a_chunks; ++i) more16(128 + 128 * i + b16 * 16, v);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const uint32_t at = (b16 >> 2) * kXBox + box_at(row, (b16 & 3) * 2 + q);
