@@ -288,6 +288,15 @@ def scalar(value, in_dtype):
     return ctypes.c_int32(int(value)) if in_dtype == I8 else ctypes.c_float(float(value))
 
 
+def _check_lines(name, count, length, stride):
+    """Refuses lines (rows, or columns of a column-major tensor) that start less
+    than their length apart, as those of broadcast views do: the ABI's leading
+    dimension cannot say that, and a larger one would reach past the memory."""
+    if stride < length and count > 1:
+        raise ValueError(f"{name} holds {count} lines of {length} values, {stride} apart: they overlap; "
+                         f"a .contiguous() copy does not")
+
+
 def _layout_of(T, name):
     """(layout, ld) of a 2-D tensor viewed as rows x cols: row-major when its
     columns are contiguous, column-major when its rows are; else an error."""

@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from . import BF16, F16, F32, DgaError, _raw_stream, lib
+from . import BF16, F16, F32, DgaError, _check_lines, _raw_stream, lib
 from .mx import on_stream
 
 _CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
@@ -24,7 +24,8 @@ def _layout(T, name):
     rows, cols = shape[-2], shape[-1]
     if stride[-1] != 1 and cols > 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    ld = max(stride[-2], cols) if rows > 1 else cols
+    _check_lines(name, rows, cols, stride[-2])
+    ld = stride[-2] if rows > 1 else cols
     return (1, rows, cols, ld, 0) if len(shape) == 2 else (shape[0], rows, cols, ld, stride[0])
 
 

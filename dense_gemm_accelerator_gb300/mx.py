@@ -11,7 +11,7 @@ import functools
 
 import torch
 
-from . import BF16, F16, F32, DgaError, _raw_stream, lib, sum_rows
+from . import BF16, F16, F32, DgaError, _check_lines, _raw_stream, lib, sum_rows
 
 MXFP4, NVFP4 = 0, 1
 
@@ -90,6 +90,8 @@ def _rows_of(T, name):
     (rows, cols), (ld, step) = T.shape, T.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must be row-major")
+    if ld < cols:
+        _check_lines(name, rows, cols, ld)
     return rows, cols, ld if ld > cols else (cols or 1)
 
 
@@ -197,6 +199,8 @@ def mx_linear_forward(X, W, bias=None, Y=None, tensor_scale=None, workspace=None
     ldx, step = X.stride()
     if step != 1 and K > 1:
         raise ValueError("X must be row-major")
+    if ldx < K:
+        _check_lines("X", M, K, ldx)
     dev, fmt, N, codes = X.device, W.format, W.rows, W.codes
     if codes.device != dev:
         raise ValueError("X and W must be on the same device")
@@ -237,7 +241,7 @@ def mx_linear_backward(X, W, G, format=MXFP4, tensor_scales=(None, None, None), 
     sx, sw, sg = tensor_scales
     out, dev = _CODE[G.dtype], G.device
     if all(T.stride(1) == 1 and T.is_cuda and T.device == dev and T.dtype in _CODE for T in (X, W, G)):
-        (M, N), K = G.shape, X.shape[1]
+        (M, N, ldg), (_, K, ldx), (_, _, ldw) = _rows_of(G, "G"), _rows_of(X, "X"), _rows_of(W, "W")
         dX = torch.empty((M, K), dtype=G.dtype, device=dev)
         dW = torch.empty((N, K), dtype=G.dtype, device=dev)
         db = torch.empty(N, dtype=torch.float32, device=dev) if need_bias else None
@@ -245,9 +249,9 @@ def mx_linear_backward(X, W, G, format=MXFP4, tensor_scales=(None, None, None), 
         have = _backward_workspace(format, M, N, K)
         workspace = torch.empty(have, dtype=torch.uint8, device=dev) if have else None
         st = L.dga_mx_linear_backward(format, _CODE[X.dtype], _CODE[W.dtype], out, M, N, K, X.data_ptr(),
-                                      max(X.stride(0), K, 1), _factor(sx, format, dev), W.data_ptr(),
-                                      max(W.stride(0), K, 1), _factor(sw, format, dev), G.data_ptr(),
-                                      max(G.stride(0), N, 1), _factor(sg, format, dev), dX.data_ptr(), K or 1,
+                                      ldx, _factor(sx, format, dev), W.data_ptr(),
+                                      ldw, _factor(sw, format, dev), G.data_ptr(),
+                                      ldg, _factor(sg, format, dev), dX.data_ptr(), K or 1,
                                       dW.data_ptr(), K or 1, db.data_ptr() if need_bias else None,
                                       workspace.data_ptr() if have else None, have, _raw_stream(dev.index))
         if st:
