@@ -300,10 +300,13 @@ def _check_lines(name, count, length, stride):
 def _layout_of(T, name):
     """(layout, ld) of a 2-D tensor viewed as rows x cols: row-major when its
     columns are contiguous, column-major when its rows are; else an error."""
-    if T.stride(1) == 1 or T.size(1) <= 1:
-        return ROW_MAJOR, max(T.stride(0), max(T.size(1), 1))
+    rows, cols = T.size(0), T.size(1)
+    if T.stride(1) == 1 or cols <= 1:
+        _check_lines(name, rows, cols, T.stride(0))
+        return ROW_MAJOR, max(T.stride(0), max(cols, 1))
     if T.stride(0) == 1:
-        return COL_MAJOR, max(T.stride(1), max(T.size(0), 1))
+        _check_lines(name, cols, rows, T.stride(1))
+        return COL_MAJOR, max(T.stride(1), max(rows, 1))
     raise ValueError(f"{name} must be row-major or column-major")
 
 
@@ -316,12 +319,9 @@ def operand_layout(A, B, C):
         raise ValueError("A must be row-major (unit stride along K)")
     if C.stride(1) != 1 and C.size(1) > 1:
         raise ValueError("C must be row-major (unit stride along N)")
-    if B.stride(1) == 1 or B.size(1) <= 1:
-        layout_b, ldb = ROW_MAJOR, max(B.stride(0), max(B.size(1), 1))
-    elif B.stride(0) == 1:
-        layout_b, ldb = COL_MAJOR, max(B.stride(1), max(B.size(0), 1))
-    else:
-        raise ValueError("B must be row-major or column-major")
+    layout_b, ldb = _layout_of(B, "B")
+    _check_lines("A", A.size(0), A.size(1), A.stride(0))
+    _check_lines("C", C.size(0), C.size(1), C.stride(0))
     lda = max(A.stride(0), max(A.size(1), 1))
     ldc = max(C.stride(0), max(C.size(1), 1))
     return lda, layout_b, ldb, ldc
@@ -366,6 +366,7 @@ def gemm(A, B, C=None, alpha=1.0, beta=0.0, out_dtype=None, path=PATH_AUTO, work
         raise ValueError(f"C must be a row-major ({M}, {N}) tensor")
     layout_a, lda = _layout_of(A, "A")
     layout_b, ldb = _layout_of(B, "B")
+    _check_lines("C", M, N, C.stride(0))
     ldc = max(C.stride(0), max(N, 1))
     if bias is not None:
         if bias.dim() != 1 or bias.numel() != N or bias.stride(0) != 1 or _dtype_code(bias) != out_dtype:
@@ -396,6 +397,7 @@ def sum_rows(G, out=None, stream=None):
     rows, cols = G.shape
     if G.stride(1) != 1 and cols > 1:
         raise ValueError("G must be row-major")
+    _check_lines("G", rows, cols, G.stride(0))
     if out is None:
         out = torch.empty(cols, dtype=torch.float32, device=G.device)
     if stream is None:

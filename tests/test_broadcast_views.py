@@ -48,6 +48,24 @@ def test_layout_of_updates():
             muon._layout(v.expand(3, *v.shape), "G")
 
 
+def test_layout_of_gemm_operands():
+    x = torch.empty(4, 5)
+    for v in _views(4, 5) + [torch.ones(1).expand(4, 1)]:
+        with pytest.raises(ValueError):
+            dga._layout_of(v, "A")
+        with pytest.raises(ValueError):
+            dga._layout_of(v.t(), "A")
+    for v in _views(4, 5):
+        with pytest.raises(ValueError):
+            dga.operand_layout(v, torch.empty(5, 5), x)
+        with pytest.raises(ValueError):
+            dga.operand_layout(x, v.t(), torch.empty(4, 4))
+        with pytest.raises(ValueError):
+            dga.operand_layout(x, torch.empty(5, 5), v)
+        with pytest.raises(ValueError):
+            dga.sum_rows(v)
+
+
 def test_lines_apart_are_taken_as_before():
     x = torch.empty(6, 8)
     assert mx._rows_of(x, "X") == (6, 8, 8)
@@ -59,6 +77,9 @@ def test_lines_apart_are_taken_as_before():
     assert mx._rows_of(torch.empty(5, 0), "X") == (5, 0, 1)
     assert muon._layout(x, "G") == (1, 6, 8, 8, 0)
     assert muon._layout(torch.empty(8).as_strided((1, 8), (0, 1)), "G") == (1, 1, 8, 8, 0)
+    assert dga._layout_of(torch.empty(8).as_strided((1, 8), (0, 1)), "A") == (dga.ROW_MAJOR, 8)
+    assert dga._layout_of(torch.empty(8).as_strided((8, 1), (1, 0)), "A") == (dga.ROW_MAJOR, 1)
+    assert dga._layout_of(torch.empty(5, 0), "A") == (dga.ROW_MAJOR, 1)
     # matrices of a batch may be the same one
     assert muon._layout(x.expand(3, 6, 8), "G") == (3, 6, 8, 8, 0)
 
@@ -99,3 +120,17 @@ def test_refused_by_the_orthogonalisation():
     same = torch.randn(30, 50, generator=torch.Generator().manual_seed(1)).cuda()
     got = dga.orthogonalize(same.expand(3, 30, 50))
     assert all(torch.equal(got[i], dga.orthogonalize(same)) for i in range(3))
+
+
+@pytest.mark.gpu
+def test_refused_by_the_products():
+    rows, cols = 20, 64
+    x, w = torch.ones(rows, cols, device="cuda"), torch.ones(cols, cols, device="cuda")
+    for v in _views(rows, cols, "cuda") + [_gradient_of_a_batch_sum(rows, cols, "cuda")]:
+        for call in (lambda: dga.gemm(v, w), lambda: dga.gemm(v.t(), x), lambda: dga.gemm(w, v.t()), lambda: dga.gemm(x, w, v),
+                     lambda: dga.sum_rows(v), lambda: dga.linear_forward(v, w), lambda: dga.linear_forward(x, w, Y=v),
+                     lambda: dga.linear_backward(x, w, v), lambda: dga.linear_backward(v, w, x)):
+            with pytest.raises(ValueError):
+                call()
+    dX, dW, db = dga.linear_backward(x, w, _gradient_of_a_batch_sum(rows, cols, "cuda").contiguous())
+    assert torch.equal(db, rows * torch.arange(1.0, cols + 1, device="cuda"))
