@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int s = 0; s < kPairStages; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&scales_full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 5);  // the MMAs' commit, one lane of each of this CTA's scale warps
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&scales_ready[b], 8);  // one lane of each scale warp of both CTAs
@@ -395,7 +395,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&scales_ready[fill & 1]), 0));
+                if (lane == 0) {
+                    mbar_signal_cluster(map_to_cta(smem_u32(&scales_ready[fill & 1]), 0));
+                    // that signal orders tensor memory alone; before TMA writes
+                    // the stage's scales anew this warp's reads of them are released
+                    mbar_arrive(&empty[stage]);
+                }
                 if (++stage == kPairStages) { stage = 0; phase ^= 1; }
             }
         }
@@ -685,7 +690,7 @@ __global__ void __launch_bounds__(kFused ? 320 : 192, (SkinnyPlan<kFormat, kN>::
         if (splits > 1) {
             fence_async_shared();
             asm volatile("bar.sync 1, 128;" ::: "memory");  // the four epilogue warps
-            cluster_arrive_relaxed();
+            cluster_arrive();
             cluster_wait();  // every ring is done with
             const int first = static_cast<int>(part) * per, mine = max(0, min(per, rows - first));
             const float* received = sums + kN * 128;  // part q's slot: q, or q - 1 past this CTA's own
@@ -723,7 +728,7 @@ __global__ void __launch_bounds__(kFused ? 320 : 192, (SkinnyPlan<kFormat, kN>::
             cluster_wait();  // and what this CTA sent, at the others
         }
     } else if (splits > 1) {
-        cluster_arrive_relaxed();
+        cluster_arrive();
         cluster_wait();
         cluster_arrive_relaxed();
         cluster_wait();

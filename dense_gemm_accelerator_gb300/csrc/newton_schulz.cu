@@ -557,8 +557,8 @@ __global__ void __launch_bounds__(TileShape<kN>::kThreads, 1)
                 fence_async_shared();
             }
             __syncwarp();
-            cluster_arrive_relaxed();
-            cluster_wait();
+            cluster_arrive();
+            cluster_wait();  // every ring is done with
             if (!joins && lane == 0) {
                 const uint32_t to = block % splits, at = smem_u32(smem + (kTileUnits + part * units + slot) * kUnitSums);
                 bulk_copy_to_cta(map_to_cta(at, to), smem_u32(sent), kUnitSums, map_to_cta(smem_u32(joined), to));
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(TileShape<kN>::kThreads, 1)
         __syncwarp();
         if (splits > 1) cluster_wait();  // and what this CTA sent, at the others
     } else if (splits > 1) {
-        cluster_arrive_relaxed();
+        cluster_arrive();
         cluster_wait();
         cluster_arrive_relaxed();
         cluster_wait();
@@ -1358,7 +1358,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
         }
         const bool last = step + 1 == c.steps;
         __syncwarp();
-        if (c.cluster > 1 && !last) cluster_arrive_relaxed();  // this CTA is done with B
+        if (c.cluster > 1 && !last) cluster_arrive();  // this CTA is done with B
         if (boxes > 0) {
 #pragma unroll 1
             for (int b16 = group * boxes; b16 < (group + 1) * boxes; ++b16) {

@@ -285,9 +285,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
                  : "memory");
 }
 
-// The same for a signal that orders no memory of this thread, such as "this
-// warp's tensor-memory reads (writes) are complete" after tcgen05.wait: the
-// release at cluster scope above costs some 1200 clocks, this arrival none.
+// The same for tensor memory alone: "this warp's tcgen05.ld (st) are complete",
+// to the thread that issues MMAs.  The PTX ISA's tcgen05 memory model orders
+// them by tcgen05.wait, then tcgen05.fence::before_thread_sync, then an arrival
+// that may be relaxed, on one side, and by the wait for it, then
+// tcgen05.fence::after_thread_sync, on the other (its synchronisation pattern
+// for different threads).  It orders no other memory: what else the thread read or
+// wrote needs a release, which at cluster scope costs some 1200 clocks.
 __device__ __forceinline__ void mbar_signal_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                  : "memory");
@@ -404,8 +408,10 @@ __device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst_cluster, uint32_t 
                  "r"(src), "r"(bytes), "r"(bar_cluster)
                  : "memory");
 }
-// The two halves of cluster_sync().  The first without a release: for "this
-// CTA has finished reading", where nothing it wrote is handed over.
+// The two halves of cluster_sync(), and the first without a release: for "the
+// copies sent here have arrived", so that their senders may leave, where no
+// access of this thread has to come before one of another CTA's.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
