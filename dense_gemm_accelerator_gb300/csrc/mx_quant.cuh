@@ -61,7 +61,8 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, const Tens
         b.plain = false;
     } else {
         const float m = __uint_as_float(amax_bits);
-        const float r = f.plain || (m != 0.0f && !mid_range(m)) ? plain_quotient(m, f.six) : quotient(m, f.six, f.inv_six);
+        // (a zero block's scale is 0 whatever the factor, which of a zero tensor is 0 too)
+        const float r = m == 0.0f ? 0.0f : f.plain || !mid_range(m) ? plain_quotient(m, f.six) : quotient(m, f.six, f.inv_six);
         uint16_t two;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(r));
         b.byte = finite ? static_cast<uint8_t>(two & 0xff) : uint8_t(0x7f);

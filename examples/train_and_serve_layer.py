@@ -27,11 +27,11 @@ def relative(a, b):
 
 
 def factor(x, fmt):
-    """An NVFP4 tensor scale (a power of two, so that it rounds nothing), or None."""
+    """An NVFP4 tensor scale (a power of two, so that it rounds nothing; 1 for a zero tensor), or None."""
     if fmt == dga.MXFP4:
         return None
     r = (x.abs().amax().float() / 2688.0).reshape(1)
-    return r / torch.frexp(r).mantissa
+    return torch.ldexp(torch.ones_like(r), torch.frexp(r).exponent)
 
 
 def train(steps, batch, n_in, n_out, fmt, four_bit, seed=0):
@@ -47,7 +47,7 @@ def train(steps, batch, n_in, n_out, fmt, four_bit, seed=0):
         Y = dga.linear_forward(X, W.bfloat16(), b.bfloat16())
         G = ((Y.float() - T.float()) * (2.0 / batch)).bfloat16()
         if four_bit:
-            _, dW, db = dga.mx_linear_backward(X, W.bfloat16(), G, fmt, tensor_scales=(factor(X, fmt), factor(W + 1e-6, fmt), factor(G, fmt)))
+            _, dW, db = dga.mx_linear_backward(X, W.bfloat16(), G, fmt, tensor_scales=(factor(X, fmt), factor(W, fmt), factor(G, fmt)))
         else:
             _, dW, db = dga.linear_backward(X, W.bfloat16(), G)
         momentum.mul_(0.9).add_(dW.float())

@@ -404,9 +404,10 @@ typedef enum { DGA_MXFP4 = 0, DGA_NVFP4 = 1 } dga_mx_format;
  * with an infinity or a NaN gets a NaN scale (every value of it reads back as
  * NaN); a zero unit gives zero codes.
  *
- *   tensor_scale  device pointer to one positive float, or NULL for 1;
- *                 DGA_NVFP4 only.  max|X| / 2688 uses E4M3's whole range;
- *                 rounded up to a power of two it keeps the scaling exact.
+ *   tensor_scale  device pointer to one positive float (0 will do for a zero
+ *                 tensor), or NULL for 1; DGA_NVFP4 only.  max|X| / 2688 uses
+ *                 E4M3's whole range; rounded up to a power of two it keeps
+ *                 the scaling exact.
  *   codes         device, R rows of dga_mx_row_bytes(K) bytes, ld_codes bytes
  *                 apart (a multiple of 16): value k in byte k/2, the even one
  *                 in the low half; a row's unused codes are written as 0
