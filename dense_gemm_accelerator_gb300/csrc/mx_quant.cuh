@@ -42,7 +42,7 @@ struct TensorFactor {
 // multiplies by `inv`, the exact 2^-e; NVFP4 divides by `unit`.
 struct BlockScale {
     uint8_t byte;
-    bool plain;  // a unit where quotient() does not hold
+    bool plain;  // quotient() does not hold for the unit, or the largest value over it
     float unit, inv;
 };
 
@@ -61,8 +61,13 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, const Tens
         b.plain = false;
     } else {
         const float m = __uint_as_float(amax_bits);
+        // Values that may pass fp32's range over the unit, of which quotient()
+        // would make NaN: m / unit is above 12 only where the scale is held to
+        // 448, and 6 / 448 of m / (6 g) there.
+        const bool far = !(m * f.inv_six <= 0x1p90f);
         // (a zero block's scale is 0 whatever the factor, which of a zero tensor is 0 too)
-        const float r = m == 0.0f ? 0.0f : f.plain || !mid_range(m) ? plain_quotient(m, f.six) : quotient(m, f.six, f.inv_six);
+        float r = m == 0.0f ? 0.0f : quotient(m, f.six, f.inv_six);
+        if (m != 0.0f && (f.plain | far | (m < 0x1p-90f))) r = plain_quotient(m, f.six);
         uint16_t two;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.0f), "f"(r));
         b.byte = finite ? static_cast<uint8_t>(two & 0xff) : uint8_t(0x7f);
@@ -71,7 +76,7 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, const Tens
         const float s = __half2float(__ushort_as_half(static_cast<uint16_t>(h2 & 0xffff)));
         b.unit = finite ? __fmul_rn(s, f.g) : 0.0f;
         b.inv = b.unit > 0.0f ? __frcp_rn(b.unit) : 0.0f;
-        b.plain = b.unit != 0.0f && !mid_range(b.unit);  // 0: inv is 0 too, and so is the quotient
+        b.plain = (b.unit != 0.0f) & (far | !mid_range(b.unit));  // 0: inv is 0 too, and so is the quotient
     }
     return b;
 }

@@ -58,3 +58,44 @@ def test_zero_blocks_beside_others_keep_a_zero_scale():
         want = np.zeros((4, 4), np.uint8)
         want[1, 1] = ref.quantize(X.cpu().double().numpy(), dga.NVFP4, 1.0 if f is None else float(f))[1][1, 1]
         assert np.array_equal(scales, want)
+
+
+@pytest.mark.parametrize("rows", [9, 40])
+@pytest.mark.parametrize("log2f", [-14, -40, -80, -88, -120, 30, 80, 100])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_values_far_past_a_tensors_factor(dtype, log2f, rows):
+    """Quotients over fp32's range are the largest codes, of the values' signs,
+    and the largest scales; as far below it they are zeros."""
+    K = 16 * 24
+    g = torch.Generator().manual_seed(rows)
+    x = torch.randn(rows, K, generator=g)
+    exponents = torch.randint(-120, 124, (rows, K // 16), generator=g).float()
+    exponents[:, ::3] = torch.randint(90, 124, (rows, K // 48), generator=g).float()
+    x = (x.reshape(rows, -1, 16) * torch.exp2(exponents)[..., None]).reshape(rows, K).clamp(-3.3e38, 3.3e38)
+    x[0, 0], x[0, 1], x[0, 2] = -2e37, 2e37, -1e3
+    x = x.to(dtype)
+    factor = torch.tensor([2.0 ** log2f], device="cuda")
+    want_c, want_s = ref.quantize(x.double().numpy(), dga.NVFP4, 2.0 ** log2f)
+    for q in (dga.mx_quantize(x.cuda(), dga.NVFP4, tensor_scale=factor),
+              dga.mx_quantize(x.t().contiguous().cuda(), dga.NVFP4, transpose=True, tensor_scale=factor)):
+        codes, scales = _parts(q)
+        assert np.array_equal(scales, want_s)
+        # a zero unit gives zeros, whatever their sign
+        live = np.repeat(want_s != 0, 16, axis=1) | ((codes & 7) != 0)
+        assert np.array_equal(codes[live], want_c[live])
+
+
+@pytest.mark.parametrize("rows", [3, 20])
+def test_the_layer_on_values_far_past_the_factor(rows):
+    """The same codes where the product quantises (up to 16 rows) and where it does not."""
+    x = torch.zeros(rows, 64, device="cuda")
+    x[:, 5], x[:, 20] = -2e37, 3e38
+    f = torch.tensor([1e-4], device="cuda")
+    w = torch.zeros(8, 64, device="cuda")
+    w[0, 5] = w[1, 20] = 6.0
+    y = dga.mx_linear_forward(x, dga.mx_quantize(w, dga.NVFP4), tensor_scale=f)
+    _sync_ok()
+    unit = float(np.float32(448) * np.float32(1e-4))
+    want = torch.zeros(rows, 8)
+    want[:, 0], want[:, 1] = -36.0 * unit, 36.0 * unit
+    assert torch.allclose(y.cpu(), want, rtol=1e-6, atol=0)
