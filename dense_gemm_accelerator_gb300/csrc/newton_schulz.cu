@@ -1464,11 +1464,13 @@ NsPlan plan_of(int out_dtype, int64_t batch, int64_t rows, int64_t cols) {
     return pl;
 }
 
+// most_smem: the most that any launch of this kernel takes.  The limit is set to
+// that, not to this launch's share: another host thread's launch may come between.
 template <typename... P, typename... A>
-cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, unsigned cluster, int smem, bool pdl, cudaStream_t s,
+cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, unsigned cluster, int smem, int most_smem, bool pdl, cudaStream_t s,
                    const A&... args) {
     if (smem > 0) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -1516,8 +1518,8 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
     const int64_t big = tiles(256);
     if (big >= pairs * 3 / 4) {
         return launch(p.split ? ns_pair_kernel<true> : ns_pair_kernel<false>,
-                      dim3(static_cast<unsigned>(2 * std::min(big, pairs))), p.split ? kPairThreads<true> : kPairThreads<false>, 2, static_cast<int>(kPairLaunch), true,
-                      s, maps, p);
+                      dim3(static_cast<unsigned>(2 * std::min(big, pairs))), p.split ? kPairThreads<true> : kPairThreads<false>, 2, static_cast<int>(kPairLaunch),
+                      static_cast<int>(kPairLaunch), true, s, maps, p);
     }
     // Tiles of 64 columns where K is short and even they leave half of the SMs
     // idle (700^2 bf16 115 -> 101 us, 400 x 1000 bf16 109 -> 96 us, 150^2 fp32
@@ -1528,7 +1530,8 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
         const int64_t narrow = tiles(64);
         if (narrow * 2 <= dev.sm_count)
             return launch(p.split ? ns_tile_kernel<true, 64> : ns_tile_kernel<false, 64>, dim3(static_cast<unsigned>(narrow)),
-                          TileShape<64>::kThreads, 1, static_cast<int>(TileShape<64>::kLaunch), true, s, maps, p, 1u);
+                          TileShape<64>::kThreads, 1, static_cast<int>(TileShape<64>::kLaunch), static_cast<int>(TileShape<64>::kLaunch),
+                          true, s, maps, p, 1u);
     }
     // Parts of K while there are idle SMs: joining them takes 2 to 3 us, a slot
     // 0.3 us.  Split operands with 8 slots or more gain from 4 parts (256^2 fp32
@@ -1538,7 +1541,8 @@ cudaError_t launch_product(NsParams p, const NsMaps& maps, int64_t batch, int64_
     uint32_t splits = 1;
     while (splits < 4 && small * splits * 2 <= dev.sm_count && slots >= (p.split ? 8u : splits * 16)) splits *= 2;
     return launch(p.split ? ns_tile_kernel<true, 128> : ns_tile_kernel<false, 128>, dim3(static_cast<unsigned>(small * splits)),
-                  TileShape<128>::kThreads, splits, static_cast<int>(TileShape<128>::kLaunch), true, s, maps, p, splits);
+                  TileShape<128>::kThreads, splits, static_cast<int>(TileShape<128>::kLaunch), static_cast<int>(TileShape<128>::kLaunch),
+                  true, s, maps, p, splits);
 }
 
 // The cluster kernel's shape, or cluster = 0 where it does not apply: up to 128
@@ -1615,7 +1619,7 @@ cudaError_t launch_cluster(const OrthoArgs& a, const NsPlan& pl, const NsParams&
     c.steps = a.steps;
     for (int i = 0; i < 3 * a.steps; ++i) c.coefficients[i] = a.coefficients[i];
     return launch(ns_cluster_kernel<T>, dim3(static_cast<unsigned>(a.batch * shape.cluster)), kClusterThreads, shape.cluster,
-                  shape.smem, false, a.stream, c, p);
+                  shape.smem, cluster_smem(kMaxBoxes), false, a.stream, c, p);
 }
 
 template <typename T>
@@ -1628,11 +1632,11 @@ cudaError_t launch_first(const OrthoArgs& a, const NsPlan& pl, float* partial, _
     const int64_t units = a.rows * ((a.cols + kSegment - 1) / kSegment);
     const int64_t most = std::max<int64_t>(1, std::min<int64_t>(kMaxParts, 4 * dev.sm_count / a.batch));
     const int parts = static_cast<int>(std::min<int64_t>((units + 7) / 8, most));
-    cudaError_t e = launch(ns_squares_kernel<T>, dim3(parts, static_cast<unsigned>(a.batch)), 256, 1, 0, false, s, G, a.rows,
+    cudaError_t e = launch(ns_squares_kernel<T>, dim3(parts, static_cast<unsigned>(a.batch)), 256, 1, 0, 0, false, s, G, a.rows,
                            a.cols, a.ldg, a.stride_g, vec, partial);
     if (e != cudaSuccess) return e;
     const uint32_t tiles_c = static_cast<uint32_t>(pl.np / 64);
-    return launch(ns_first_kernel<T>, dim3(static_cast<unsigned>(pl.mp / 64 * tiles_c), static_cast<unsigned>(a.batch)), 256, 1, 0,
+    return launch(ns_first_kernel<T>, dim3(static_cast<unsigned>(pl.mp / 64 * tiles_c), static_cast<unsigned>(a.batch)), 256, 1, 0, 0,
                   true, s, G, a.rows, a.cols, a.ldg, a.stride_g, vec, pl.transposed, static_cast<const float*>(partial), parts, a.eps,
                   xh, xl, pl.np, pl.mp * pl.np, tiles_c);
 }

@@ -1,5 +1,7 @@
 """Edges of the 4-bit and orthogonalisation calls on the GPU: zero tensors,
 values far past a tensor's factor, host threads, devices and eps = 0."""
+import ctypes
+import threading
 
 import numpy as np
 import pytest
@@ -99,3 +101,39 @@ def test_the_layer_on_values_far_past_the_factor(rows):
     want = torch.zeros(rows, 8)
     want[:, 0], want[:, 1] = -36.0 * unit, 36.0 * unit
     assert torch.allclose(y.cpu(), want, rtol=1e-6, atol=0)
+
+
+def test_host_threads_with_updates_of_other_sizes():
+    """Sizes that take different amounts of shared memory of one kernel, called
+    at the same time by several threads."""
+    g = torch.Generator().manual_seed(4)
+    inputs = [torch.randn(64, 64, generator=g).cuda(), torch.randn(100, 30, 190, generator=g).cuda()]
+    torch.cuda.synchronize()
+    codes, start = [], threading.Barrier(4)
+    coefficients = (ctypes.c_float * 3)(*dga.QUINTIC)
+    call = dga.lib().dga_orthogonalize
+
+    def work(G, out, workspace, stream):
+        *batch, rows, cols = G.shape
+        args = (dga.F32, dga.F32, batch[0] if batch else 1, rows, cols, G.data_ptr(), cols, rows * cols, out.data_ptr(), cols, rows * cols,
+                1, coefficients, 1e-7, workspace.data_ptr(), workspace.numel(), stream.cuda_stream)
+        torch.cuda.set_device(G.device)
+        start.wait()
+        seen = {call(*args) for _ in range(4000)}
+        codes.append((seen, dga.dga_last_cuda_error()))
+
+    threads, kept = [], []
+    for i in (0, 1, 0, 1):
+        G, out = inputs[i], torch.empty_like(inputs[i])
+        size = dga.dga_orthogonalize_workspace_size(dga.F32, G.numel() // (G.shape[-1] * G.shape[-2]), *G.shape[-2:])
+        kept.append((G, out, torch.empty(size, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()))
+        threads.append(threading.Thread(target=work, args=kept[-1]))
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert [seen for seen, _ in codes] == [{dga.OK}] * 4, codes
+    for (G, out, _, _), w in zip(kept, [dga.orthogonalize(inputs[i], steps=1) for i in (0, 1, 0, 1)]):
+        assert torch.equal(out, w)
