@@ -346,7 +346,10 @@ template <bool kBf16, int MT, typename TOut>
 cudaError_t launch_mt(const CUtensorMap& lo, const CUtensorMap& hi, const CUtensorMap& x,
                       const Params& p, int smem, cudaStream_t s) {
     auto kern = skinny_kernel<kBf16, MT, TOut>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the most that any launch takes, not this one's share: another host
+    // thread's launch may come between the two calls
+    constexpr int kMostSmem = static_cast<int>(kRingBudget + kBarrierBytes + kRedBytes + 1024);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));

@@ -137,3 +137,33 @@ def test_host_threads_with_updates_of_other_sizes():
     assert [seen for seen, _ in codes] == [{dga.OK}] * 4, codes
     for (G, out, _, _), w in zip(kept, [dga.orthogonalize(inputs[i], steps=1) for i in (0, 1, 0, 1)]):
         assert torch.equal(out, w)
+
+
+def test_host_threads_with_few_row_products_of_other_widths():
+    """The same of the few-row products, whose shared memory goes by the width."""
+    widths, K = (2432, 4864, 304, 9000), 256
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(4, K, generator=g).bfloat16().cuda()
+    weights = [torch.randn(n, K, generator=g).bfloat16().cuda() for n in widths]
+    want = [dga.gemm(x, w.t(), path=dga.PATH_SKINNY) for w in weights]
+    codes, start = [], threading.Barrier(len(widths))
+    one, zero = ctypes.c_float(1.0), ctypes.c_float(0.0)
+    call = dga.lib().dga_gemm_general
+
+    def work(w, out, stream):
+        args = (dga.BF16, dga.BF16, dga.ROW_MAJOR, dga.COL_MAJOR, 4, w.shape[0], K, ctypes.byref(one), x.data_ptr(), K, w.data_ptr(), K,
+                ctypes.byref(zero), out.data_ptr(), w.shape[0], None, None, 0, dga.PATH_SKINNY, stream.cuda_stream)
+        torch.cuda.set_device(w.device)
+        start.wait()
+        codes.append({call(*args) for _ in range(6000)})
+
+    kept = [(w, torch.empty_like(y), torch.cuda.Stream()) for w, y in zip(weights, want)]
+    threads = [threading.Thread(target=work, args=k) for k in kept]
+    torch.cuda.synchronize()
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{dga.OK}] * len(widths)
+    assert all(torch.equal(out, w) for (_, out, _), w in zip(kept, want))
