@@ -114,6 +114,25 @@ def _raw_stream(device_index):
     return torch.cuda.current_stream(device_index).cuda_stream
 
 
+def _current_device():
+    """The current CUDA device's number."""
+    import torch
+    return torch.cuda.current_device()
+
+
+def _elsewhere(device):
+    """Whether `device` is a CUDA device other than the current one, on which
+    the library launches; the call is then made again by _on_device."""
+    return device.index is not None and device.index != _current_device()
+
+
+def _on_device(device, f, *args):
+    """f(*args) with `device` current."""
+    import torch
+    with torch.cuda.device(device):
+        return f(*args)
+
+
 # ---- the C entry points, same names and arguments ---------------------------
 
 def dga_gemm(in_dtype, out_dtype, layout_b, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc,
@@ -340,6 +359,8 @@ def gemm(A, B, C=None, alpha=1.0, beta=0.0, out_dtype=None, path=PATH_AUTO, work
     (DGA_TF32); fp32 inputs are otherwise multiplied exactly in fp32.
     """
     import torch
+    if _elsewhere(A.device):
+        return _on_device(A.device, gemm, A, B, C, alpha, beta, out_dtype, path, workspace, stream, bias, tf32)
     in_dtype = _dtype_code(A)
     if _dtype_code(B) != in_dtype:
         raise TypeError("A and B must have the same dtype")
@@ -394,6 +415,8 @@ def sum_rows(G, out=None, stream=None):
     """fp32 column sums of a row-major 2-D tensor G (the batch sum of an output
     gradient); returns out."""
     import torch
+    if _elsewhere(G.device):
+        return _on_device(G.device, sum_rows, G, out, stream)
     rows, cols = G.shape
     if G.stride(1) != 1 and cols > 1:
         raise ValueError("G must be row-major")
@@ -418,6 +441,8 @@ def spmv_csr(row_offsets, column_indices, values, x, y=None, alpha=1.0, beta=0.0
     import ctypes as ct
 
     import torch
+    if _elsewhere(values.device):
+        return _on_device(values.device, spmv_csr, row_offsets, column_indices, values, x, y, alpha, beta, cols, workspace, stream)
     rows = row_offsets.numel() - 1
     nnz = values.numel()
     cols = x.numel() if cols is None else cols
@@ -467,6 +492,7 @@ def linear_backward(X, W, G, need_bias=True):
 
 try:  # the same without building a Stream object (2 us less)
     from torch._C import _cuda_getCurrentRawStream as _raw_stream  # noqa: E402,F811
+    from torch._C import _cuda_getDevice as _current_device  # noqa: E402,F811
 except ImportError:  # a CPU build of PyTorch
     pass
 from .mx import (MXFP4, NVFP4, MXTensor, mx_dequantize, mx_gemm, mx_linear_backward,  # noqa: E402,F401

@@ -6,7 +6,7 @@ import ctypes
 
 import torch
 
-from . import BF16, F16, F32, DgaError, _check_lines, _raw_stream, lib
+from . import BF16, F16, F32, DgaError, _check_lines, _elsewhere, _on_device, _raw_stream, lib
 from .mx import on_stream
 
 _CODE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
@@ -48,6 +48,8 @@ def orthogonalize(G, steps=5, coefficients=QUINTIC, eps=1e-7, out=None, out_dtyp
     if not G.is_cuda:
         raise ValueError("G must be a CUDA tensor")
     dev = G.device
+    if _elsewhere(dev):
+        return _on_device(dev, orthogonalize, G, steps, coefficients, eps, out, out_dtype, workspace)
     if out is None:
         out_code = code if out_dtype is None else out_dtype
         out = torch.empty(G.shape, dtype=_TORCH[out_code], device=dev)

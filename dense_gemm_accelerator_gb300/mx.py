@@ -11,7 +11,7 @@ import functools
 
 import torch
 
-from . import BF16, F16, F32, DgaError, _check_lines, _raw_stream, lib, sum_rows
+from . import BF16, F16, F32, DgaError, _check_lines, _elsewhere, _on_device, _raw_stream, lib, sum_rows
 
 MXFP4, NVFP4 = 0, 1
 
@@ -101,6 +101,8 @@ def mx_quantize(X, format=MXFP4, transpose=False, tensor_scale=None, stream=None
     MXTensor of X's transpose (quantised along X's columns)."""
     if stream is not None:
         return on_stream(stream, X.device, mx_quantize, X, format, transpose, tensor_scale)
+    if _elsewhere(X.device):
+        return _on_device(X.device, mx_quantize, X, format, transpose, tensor_scale)
     if X.dim() != 2:
         raise ValueError("X must be 2-D")
     code = _CODE.get(X.dtype)
@@ -129,6 +131,8 @@ def mx_dequantize(Q, out_dtype=F32, stream=None):
     if stream is not None:
         return on_stream(stream, Q.device, mx_dequantize, Q, out_dtype)
     dev = Q.codes.device
+    if _elsewhere(dev):
+        return _on_device(dev, mx_dequantize, Q, out_dtype)
     Y = torch.empty((Q.rows, Q.cols), dtype=_TORCH[out_dtype], device=dev)
     st = lib().dga_mx_dequantize(Q.format, out_dtype, Q.rows, Q.cols, Q.codes.data_ptr(),
                                  Q.codes.stride(0), Q.scales.data_ptr(),
@@ -171,6 +175,8 @@ def mx_gemm(A, B, C=None, alpha=1.0, beta=0.0, out_dtype=BF16, bias=None, stream
     if A.device != B.device:
         raise ValueError("A and B must be on the same device")
     dev = A.codes.device
+    if _elsewhere(dev):
+        return _on_device(dev, mx_gemm, A, B, C, alpha, beta, out_dtype, bias)
     C, code, ldc = _output(C, A.rows, B.rows, beta, out_dtype, dev)
     a, b = ctypes.c_float(alpha), ctypes.c_float(beta)
     st = lib().dga_mx_gemm(A.format, code, A.rows, B.rows, A.cols, ctypes.byref(a), A.codes.data_ptr(),
@@ -204,6 +210,8 @@ def mx_linear_forward(X, W, bias=None, Y=None, tensor_scale=None, workspace=None
     dev, fmt, N, codes = X.device, W.format, W.rows, W.codes
     if codes.device != dev:
         raise ValueError("X and W must be on the same device")
+    if _elsewhere(dev):
+        return _on_device(dev, mx_linear_forward, X, W, bias, Y, tensor_scale, workspace)
     if Y is None:
         Y, out, ldy = torch.empty((M, N), dtype=X.dtype, device=dev), code, N or 1
     else:
@@ -240,6 +248,8 @@ def mx_linear_backward(X, W, G, format=MXFP4, tensor_scales=(None, None, None), 
         raise TypeError("G must be float32, bfloat16 or float16")
     sx, sw, sg = tensor_scales
     out, dev = _CODE[G.dtype], G.device
+    if _elsewhere(dev):
+        return _on_device(dev, mx_linear_backward, X, W, G, format, tensor_scales, need_bias)
     if all(T.stride(1) == 1 and T.is_cuda and T.device == dev and T.dtype in _CODE for T in (X, W, G)):
         (M, N, ldg), (_, K, ldx), (_, _, ldw) = _rows_of(G, "G"), _rows_of(X, "X"), _rows_of(W, "W")
         dX = torch.empty((M, K), dtype=G.dtype, device=dev)

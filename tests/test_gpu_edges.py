@@ -167,3 +167,43 @@ def test_host_threads_with_few_row_products_of_other_widths():
     torch.cuda.synchronize()
     assert codes == [{dga.OK}] * len(widths)
     assert all(torch.equal(out, w) for (_, out, _), w in zip(kept, want))
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """With another device current, a call switches to its tensors' for its own
+    duration (the other device is made up: its number is what the library's
+    callers see as the current one)."""
+    x = torch.randn(20, 64, generator=torch.Generator().manual_seed(3)).cuda()
+    W = dga.mx_quantize(x)
+    rows = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    cols, vals, v = torch.tensor([1, 0], dtype=torch.int32, device="cuda"), torch.ones(2, device="cuda"), torch.ones(2, device="cuda")
+    calls = [lambda: dga.mx_quantize(x).codes, lambda: dga.mx_dequantize(W), lambda: dga.mx_gemm(W, W), lambda: dga.mx_linear_forward(x, W),
+             lambda: dga.mx_linear_backward(x, x, x @ x.t())[0], lambda: dga.orthogonalize(x), lambda: dga.gemm(x, x.t()),
+             lambda: dga.sum_rows(x), lambda: dga.spmv_csr(rows, cols, vals, v)]
+    want = [call() for call in calls]
+    here, entered = x.device.index, []
+    state = {"device": here + 1}
+
+    class Device:
+        def __init__(self, device):
+            self.index = torch.device(device).index
+
+        def __enter__(self):
+            self.before, state["device"] = state["device"], self.index
+            entered.append(self.index)
+
+        def __exit__(self, *_):
+            state["device"] = self.before
+
+    monkeypatch.setattr(dga, "_current_device", lambda: state["device"], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for call, w in zip(calls, want):
+        del entered[:]
+        got = call()
+        assert entered and set(entered) == {here}
+        assert torch.equal(got, w)
+    state["device"] = here
+    for call in calls:
+        del entered[:]
+        call()
+        assert not entered
