@@ -930,6 +930,13 @@ __device__ __forceinline__ float block_sum(float s) {
     return s;
 }
 
+// What G's values are multiplied by, from the sum of their squares: 0 where that
+// passes fp32's range, which takes a norm of 0 and an eps next to it.
+__device__ __forceinline__ float first_unit(float squares, float eps) {
+    const float u = kScale / (sqrtf(squares) + eps);
+    return u <= 3.4028235e38f || u != u ? u : 0.0f;
+}
+
 constexpr int64_t kSegment = 2048;  // columns of a row that a warp takes at once
 
 // Eight consecutive values of a row from column c, zero from `cols` on.
@@ -998,7 +1005,7 @@ __global__ void __launch_bounds__(256) ns_first_kernel(const T* __restrict__ G, 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     float s = 0.0f;
     for (int i = threadIdx.x; i < parts; i += 256) s += partial[blockIdx.y * parts + i];
-    const float u = kScale / (sqrtf(block_sum<8>(s)) + eps);
+    const float u = first_unit(block_sum<8>(s), eps);
     if (transposed) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) tile[tc + j][tr] = x[j / 8][j % 8];
@@ -1128,7 +1135,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) ns_cluster_kernel(NsCluste
         s = 0.0f;
         for (int q = 0; q < c.cluster; ++q) s += norms[q];
     }
-    const float unit = kScale / (sqrtf(s) + c.eps);
+    const float unit = first_unit(s, c.eps);
 #pragma unroll
     for (int b = 0; b < kMaxBoxes; ++b) {
         if (b < boxes) {

@@ -207,3 +207,16 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
         del entered[:]
         call()
         assert not entered
+
+
+@pytest.mark.parametrize("shape", [(3, 60, 70), (3, 100, 500), (3, 70, 2000), (3, 300, 140), (40, 300, 300)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("eps", [0.0, 1e-40])
+def test_a_zero_update_gives_zero_whatever_eps(dtype, shape, eps):
+    G = torch.randn(*shape, generator=torch.Generator().manual_seed(5)).to(dtype)
+    G[1] = 0.0
+    got = dga.orthogonalize(G.cuda(), eps=eps)
+    _sync_ok()
+    assert not got[1].any()
+    assert torch.equal(got[0], dga.orthogonalize(G[:1].expand(shape[0], *shape[1:]).contiguous().cuda(), eps=eps)[0])
+    assert bool(torch.isfinite(got).all())
