@@ -270,4 +270,6 @@ def mx_linear_backward(X, W, G, format=MXFP4, tensor_scales=(None, None, None), 
     # column-major operands, which are quantised along the other axis
     dX = mx_gemm(mx_quantize(G, format, False, sg), mx_quantize(W, format, True, sw), out_dtype=out)
     dW = mx_gemm(mx_quantize(G, format, True, sg), mx_quantize(X, format, True, sx), out_dtype=out)
-    return dX, dW, (sum_rows(G) if need_bias else None)
+    if not need_bias:
+        return dX, dW, None
+    return dX, dW, sum_rows(G if G.stride(1) == 1 or G.shape[1] <= 1 else G.contiguous())  # along its rows

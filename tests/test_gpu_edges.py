@@ -220,3 +220,13 @@ def test_a_zero_update_gives_zero_whatever_eps(dtype, shape, eps):
     assert not got[1].any()
     assert torch.equal(got[0], dga.orthogonalize(G[:1].expand(shape[0], *shape[1:]).contiguous().cuda(), eps=eps)[0])
     assert bool(torch.isfinite(got).all())
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_gradients_of_a_column_major_output_gradient(fmt):
+    x, w = (torch.randn(r, 70, generator=torch.Generator().manual_seed(r)).cuda() for r in (50, 90))
+    g = torch.randn(50, 90, generator=torch.Generator().manual_seed(7)).cuda()
+    want = dga.mx_linear_backward(x, w, g, fmt)
+    got = dga.mx_linear_backward(x, w, g.t().contiguous().t(), fmt)
+    _sync_ok()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
