@@ -230,3 +230,52 @@ def test_gradients_of_a_column_major_output_gradient(fmt):
     got = dga.mx_linear_backward(x, w, g.t().contiguous().t(), fmt)
     _sync_ok()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("T", [7, 40, 300])
+def test_chains_in_a_graph(fmt, T):
+    """Quantisation and back, the layer and both its gradients, captured and
+    replayed on new inputs."""
+    def values(seed, rows, cols):
+        return torch.randn(rows, cols, generator=torch.Generator().manual_seed(seed)).cuda()
+    x, w, g = values(1, T, 200), values(2, 150, 200), values(3, T, 150)
+
+    def chain():
+        W = dga.mx_quantize(w, fmt)
+        back = dga.mx_dequantize(dga.mx_quantize(x, fmt, transpose=True))
+        return (back, dga.mx_linear_forward(x, W), *dga.mx_linear_backward(x, w, g, fmt))
+
+    chain()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = chain()
+    for t, seed in ((x, 11), (w, 12), (g, 13)):
+        t.copy_(values(seed, *t.shape))
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    _sync_ok()
+    for got, want in zip(out, chain()):
+        assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T,N,K", [(5, 130, 300), (16, 300, 1000), (17, 300, 257), (200, 140, 520), (300, 260, 800)])
+def test_products_with_factors_that_are_no_powers_of_two(T, N, K):
+    """The product and the layer against fp64 products of the values their codes
+    stand for.  Beside the sums' bound: alpha times both factors, and each
+    operand's scale times factor and that times code, are rounded to fp32: six
+    roundings of 2^-24, doubled."""
+    g = torch.Generator().manual_seed(T)
+    x, w = torch.randn(T, K, generator=g), torch.randn(N, K, generator=g) / K ** 0.5
+    fx, fw = (torch.tensor([float(t.abs().max()) / 2688.0], device="cuda") for t in (x, w))
+    X, W = dga.mx_quantize(x.cuda(), dga.NVFP4, tensor_scale=fx), dga.mx_quantize(w.cuda(), dga.NVFP4, tensor_scale=fw)
+    A, B = dga.mx_dequantize(X).cpu().double().numpy(), dga.mx_dequantize(W).cpu().double().numpy()
+    want = A @ B.T
+    tol = ref.product_bound(A, B, K) + 12 * 2.0 ** -24 * (np.abs(A) @ np.abs(B).T) + np.abs(want) * 2.0 ** -23
+    y = dga.mx_linear_forward(x.cuda(), W, tensor_scale=fx)
+    p = dga.mx_gemm(X, W, out_dtype=dga.F32)
+    _sync_ok()
+    assert torch.equal(y, p)
+    assert (np.abs(p.cpu().double().numpy() - want) <= tol).all()
