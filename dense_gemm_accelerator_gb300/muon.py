@@ -34,6 +34,10 @@ def orthogonalize(G, steps=5, coefficients=QUINTIC, eps=1e-7, out=None, out_dtyp
     """G (rows x cols, or a batch of such matrices) orthogonalised by `steps`
     Newton-Schulz steps: every singular value towards 1.
 
+    bfloat16 results of more than 256 rows and columns come from products of
+    11-bit operands (up to 1.7e-3 off, as much as their own rounding); float32
+    ones, with out_dtype=F32, from 22-bit operands.
+
     coefficients: (a, b, c) for all steps, or one such triple per step.  out:
     the result, of G's shape (it may be G itself), allocated as out_dtype (G's
     own type if None) when None.  The workspace comes from PyTorch's caching

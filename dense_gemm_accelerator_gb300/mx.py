@@ -3,6 +3,14 @@ layer, as PyTorch-tensor forms of the ``dga_mx_*`` entry points (include/dga.h
 has the formats, roundings and errors).  All work runs in the library's CUDA
 kernels on the current stream of the tensors' device, or the one given;
 scratch and results come from PyTorch's caching allocator, on the same stream.
+
+NVFP4 needs a factor per tensor (``tensor_scale``, one float32 value on the
+device; None is 1): under a factor f, blocks of magnitudes up to f / 170 become
+zeros and magnitudes over 2688 f are held to 2688 f.  max|X| / 2688 takes the
+whole range, and a power of two above it rounds nothing besides:
+
+    r = (X.abs().amax().float() / 2688).reshape(1)
+    f = torch.ldexp(torch.ones_like(r), torch.frexp(r).exponent)
 """
 from __future__ import annotations
 
@@ -98,7 +106,8 @@ def _rows_of(T, name):
 def mx_quantize(X, format=MXFP4, transpose=False, tensor_scale=None, stream=None):
     """X (rows x cols, float32, bfloat16 or float16, row- or column-major) to an
     :class:`MXTensor` quantised along its rows, or, with transpose=True, the
-    MXTensor of X's transpose (quantised along X's columns)."""
+    MXTensor of X's transpose (quantised along X's columns).  tensor_scale: X's
+    factor (NVFP4)."""
     if stream is not None:
         return on_stream(stream, X.device, mx_quantize, X, format, transpose, tensor_scale)
     if _elsewhere(X.device):
@@ -127,7 +136,8 @@ def mx_quantize(X, format=MXFP4, transpose=False, tensor_scale=None, stream=None
 
 
 def mx_dequantize(Q, out_dtype=F32, stream=None):
-    """The values an MXTensor stands for, rounded once to out_dtype."""
+    """The values an MXTensor stands for, code * (scale * factor) in fp32, rounded
+    to out_dtype."""
     if stream is not None:
         return on_stream(stream, Q.device, mx_dequantize, Q, out_dtype)
     dev = Q.codes.device
@@ -239,7 +249,8 @@ def mx_linear_backward(X, W, G, format=MXFP4, tensor_scales=(None, None, None), 
     4-bit products (the roundings' own gradient taken as 1): dX = G W with G
     and W quantised along out, dW = G^T X with G and X quantised along the
     batch, both of G's type; db = the batch sum of G (fp32, unquantised).
-    tensor_scales: the factors of X, W and G."""
+    tensor_scales: the factors of X, W and G (NVFP4: without them gradients
+    near 1e-3 and below are quantised to zeros)."""
     if stream is not None:
         return on_stream(stream, G.device, mx_linear_backward, X, W, G, format, tensor_scales, need_bias)
     if X.shape[0] != G.shape[0] or X.shape[1] != W.shape[1] or G.shape[1] != W.shape[0]:

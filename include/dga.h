@@ -407,7 +407,10 @@ typedef enum { DGA_MXFP4 = 0, DGA_NVFP4 = 1 } dga_mx_format;
  *   tensor_scale  device pointer to one positive float (0 will do for a zero
  *                 tensor), or NULL for 1; DGA_NVFP4 only.  max|X| / 2688 uses
  *                 E4M3's whole range; rounded up to a power of two it keeps
- *                 the scaling exact.
+ *                 the scaling exact.  Under a factor f a block of magnitudes
+ *                 up to 6 f / 1024 becomes zeros and one over 2688 f is held
+ *                 to 2688 f, so that with NULL values near 1e-3 are lost:
+ *                 weights, activations and gradients each need their factor.
  *   codes         device, R rows of dga_mx_row_bytes(K) bytes, ld_codes bytes
  *                 apart (a multiple of 16): value k in byte k/2, the even one
  *                 in the low half; a row's unused codes are written as 0
@@ -433,7 +436,8 @@ size_t dga_mx_scales_size(dga_mx_format format, int64_t rows, int64_t K);
 /*
  * dga_mx_dequantize -- Y (rows x cols, row-major, ldy; DGA_F32, DGA_BF16 or
  * DGA_F16) <- what a 4-bit matrix stands for: code * (scale * tensor_scale),
- * rounded once to the output type.  Errors: DGA_ERR_UNSUPPORTED, -3 rows,
+ * both products in fp32 (exact, but for their own roundings where the factor is
+ * no power of two), then rounded to the output type.  Errors: DGA_ERR_UNSUPPORTED, -3 rows,
  * -4 cols, -5 codes, -6 ld_codes, -7 scales, -8 tensor_scale, -9 Y, -10 ldy,
  * DGA_ERR_OVERLAP.  One launch.
  */
@@ -528,9 +532,14 @@ size_t dga_mx_linear_backward_workspace_size(dga_mx_format format, int64_t M, in
  * the tensor cores with fp32 accumulation from operands of 22 bits (as exact
  * as fp32 products), or, for DGA_BF16 output of matrices with more than 256
  * rows and columns, of 11 bits, X itself being kept to 22 (1e-4 to 1.7e-3 off
- * in all, bf16's own rounding being 1.7e-3).  Intermediates of magnitude 16 or
- * more overflow (the quintic above stays below 4), as do squares of G past
- * fp32's range in the norm.  Results repeat bit for bit.
+ * in all, bf16's own rounding being 1.7e-3; DGA_F32 output of the same matrices
+ * has 22 bits).  Intermediates of magnitude 16 or more overflow (the quintic
+ * above stays below 4), as do squares of G past fp32's range in the norm.  At
+ * the other end X is held to 2^-37: with s = |G|_F / (|G|_F + eps) the result is
+ * off by some 2^-37 sqrt(rows cols) / s, 5e-4 for values near 1e-15 under an eps
+ * of 1e-7; and squares below fp32's normal range lose digits of the norm (1e-6
+ * at values near 1e-21, 1e-3 near 1e-22), which counts where eps is as small.
+ * Results repeat bit for bit.
  *   coefficients  HOST, 3 * steps floats: a, b, c of each step
  *   O             may be G itself (the same pointer, type and strides); must
  *                 not overlap it otherwise
