@@ -170,7 +170,7 @@ __device__ __forceinline__ void store_unit(const MxParams& p, const CUtensorMap*
     }
 }
 
-// The same where TMA cannot store (C's rows not 16-byte aligned) or C is read
+// The same where TMA cannot store (C's rows start or end off 16 bytes) or C is read
 // (beta): the unit, transposed through the boxes, row by row with a lane on
 // columns l and 32 + l.  Element (row, c) lies at word row * 64 + (c + row) % 64,
 // so that neither direction meets in a bank.  (8192 x 8192 x 2048 to bf16 with
@@ -849,9 +849,10 @@ cudaError_t launch_pair(const MxGemmArgs& a, MxParams p, const DeviceInfo& dev) 
     const double panel = 256.0 * static_cast<double>(a.K) / 2;
     p.group_m = std::min(p.tiles_m, std::max(8u, std::min(64u, static_cast<uint32_t>(32.0 * 1024 * 1024 / panel))));
     const unsigned clusters = std::min<unsigned>(p.num_tiles, dev.sm_count / 2);
-    // C by TMA stores where its rows allow them and it is only written
+    // C by TMA stores where it is only written and its rows start and end on 16
+    // bytes: TMA writes the whole 16 bytes that a row's end lies in
     constexpr int64_t kEs = sizeof(TOut);
-    p.tma_store = a.beta == 0.0f && aligned(a.C, 16) && a.ldc * kEs % 16 == 0;
+    p.tma_store = a.beta == 0.0f && aligned(a.C, 16) && a.ldc * kEs % 16 == 0 && a.N * kEs % 16 == 0;
     if (p.tma_store)
         e = make_map(&m[4], kEs == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16,
                      CU_TENSOR_MAP_SWIZZLE_128B, a.C, a.N, a.M, a.ldc * kEs, 128 / kEs, 32);

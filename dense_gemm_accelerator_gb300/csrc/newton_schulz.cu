@@ -1690,7 +1690,8 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
     base.transposed = pl.transposed;
     const int64_t per16 = a.out_dtype == DGA_F32 ? 4 : 8;
     base.result_vec = aligned(a.O, 16) && a.ldo % per16 == 0 && (a.batch == 1 || a.stride_o % per16 == 0);
-    base.result_tma = base.result_vec;
+    // TMA writes the whole 16 bytes that a row's end lies in
+    base.result_tma = base.result_vec && a.cols % per16 == 0;
     base.ldo = a.ldo;
     base.stride_o = a.stride_o;
     bool done = false;

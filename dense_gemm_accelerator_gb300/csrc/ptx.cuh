@@ -369,8 +369,10 @@ __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// 2-D tiled store of a box from shared memory (what lies outside the tensor is
-// left out), in this thread's current bulk group.
+// 2-D tiled store of a box from shared memory, in this thread's current bulk
+// group.  What lies outside the tensor is left out, but by 16 bytes at a time:
+// where the innermost extent is no multiple of them, a row's last piece is
+// written whole, past the extent.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src, int32_t x, int32_t y) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                      reinterpret_cast<uint64_t>(map)),

@@ -279,3 +279,67 @@ def test_products_with_factors_that_are_no_powers_of_two(T, N, K):
     _sync_ok()
     assert torch.equal(y, p)
     assert (np.abs(p.cpu().double().numpy() - want) <= tol).all()
+
+
+def _inside(rows, cols, dtype, left):
+    """(memory, its part rows x cols) with 24 columns or more on the right, rows
+    above and below, and rows that start on 16 bytes (for left = 0 or 8)."""
+    memory = torch.full((rows + 8, cols + -cols % 8 + 32), 7.0, dtype=dtype, device="cuda")
+    return memory, memory[4:4 + rows, left:left + cols]
+
+
+@pytest.mark.parametrize("left", [0, 3, 8])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N", [(3, 77), (100, 505), (300, 505), (700, 131), (600, 1021), (600, 1028)])
+def test_products_leave_what_is_beside_c(M, N, dtype, left):
+    """Results whose rows start on 16 bytes and end anywhere."""
+    g = torch.Generator().manual_seed(N)
+    a, b = torch.randn(M, 200, generator=g).cuda(), torch.randn(N, 200, generator=g).cuda()
+    A, B = dga.mx_quantize(a), dga.mx_quantize(b)
+    memory, C = _inside(M, N, dtype, left)
+    dga.mx_gemm(A, B, C)
+    _sync_ok()
+    assert torch.equal(C, dga.mx_gemm(A, B, out_dtype=OUT[dtype]))
+    C.fill_(7.0)
+    assert bool((memory == 7.0).all())
+    memory, Y = _inside(M, N, dtype, left)
+    dga.mx_linear_forward(a, B, Y=Y)
+    _sync_ok()
+    Y.fill_(7.0)
+    assert bool((memory == 7.0).all())
+
+
+@pytest.mark.parametrize("left", [0, 3, 8])
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("batch,m,n", [(2, 60, 77), (1, 140, 333), (1, 333, 140), (1, 200, 1003), (3, 300, 333), (3, 333, 301), (10, 630, 1482),
+                                       (10, 1482, 630), (2, 1100, 1100)])
+def test_updates_leave_what_is_beside_the_result(batch, m, n, dtype, left):
+    G = torch.randn(batch, m, n, generator=torch.Generator().manual_seed(m)).to(dtype).cuda()
+    memory, O = _inside(batch * m, n, dtype, left)
+    O = O.unflatten(0, (batch, m))
+    dga.orthogonalize(G, out=O)
+    _sync_ok()
+    assert torch.equal(O, dga.orthogonalize(G))
+    O.fill_(7.0)
+    assert bool((memory == 7.0).all())
+
+
+def test_gradients_leave_what_is_beside_them():
+    """The C call's own leading dimensions of both gradients."""
+    T, N, K = 520, 300, 397
+    g = torch.Generator().manual_seed(9)
+    x, w, d = (torch.randn(*s, generator=g).bfloat16().cuda() for s in ((T, K), (N, K), (T, N)))
+    want = dga.mx_linear_backward(x, w, d, dga.MXFP4)
+    memory_x, dX = _inside(T, K, torch.bfloat16, 8)
+    memory_w, dW = _inside(N, K, torch.bfloat16, 0)
+    size = dga.dga_mx_linear_backward_workspace_size(dga.MXFP4, T, N, K)
+    workspace = torch.empty(size, dtype=torch.uint8, device="cuda")
+    st = dga.dga_mx_linear_backward(dga.MXFP4, dga.BF16, dga.BF16, dga.BF16, T, N, K, x.data_ptr(), K, None, w.data_ptr(), K, None,
+                                    d.data_ptr(), N, None, dX.data_ptr(), dX.stride(0), dW.data_ptr(), dW.stride(0), None,
+                                    workspace.data_ptr(), size, torch.cuda.current_stream().cuda_stream)
+    assert st == dga.OK
+    _sync_ok()
+    assert torch.equal(dX, want[0]) and torch.equal(dW, want[1])
+    for memory, part in ((memory_x, dX), (memory_w, dW)):
+        part.fill_(7.0)
+        assert bool((memory == 7.0).all())
