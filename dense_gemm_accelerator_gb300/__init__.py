@@ -394,8 +394,11 @@ def gemm(A, B, C=None, alpha=1.0, beta=0.0, out_dtype=None, path=PATH_AUTO, work
             raise ValueError("bias must be a contiguous (N,) tensor of C's dtype")
     if stream is None:
         stream = torch.cuda.current_stream(A.device).cuda_stream
+    # operands that do not start on 16 bytes are repacked, as those are whose
+    # leading dimension is odd: the size is asked for as if it were
+    odd_a, odd_b = (in_dtype != F32 and T.data_ptr() % 16 != 0 for T in (A, B))
     ws_bytes = dga_gemm_general_workspace_size(in_dtype, out_dtype, layout_a, layout_b, M, N, K,
-                                               lda, ldb, ldc, path)
+                                               lda | odd_a, ldb | odd_b, ldc, path)
     if ws_bytes and workspace is None:
         workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=A.device)
     ws_ptr = workspace.data_ptr() if workspace is not None else None

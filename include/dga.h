@@ -193,7 +193,8 @@ int dga_gemm_ex(dga_dtype in_dtype, dga_dtype out_dtype, dga_layout layout_b,
  * tensor-core path, optional bytes for the SIMT path (see dga_gemm).
  * Pointers are not needed: the answer depends on dtypes, layout, sizes,
  * leading dimensions and the current device's SM count (152 is assumed when
- * no device can be queried). */
+ * no device can be queried), and is for A and B that start on 16 bytes; for one
+ * that does not, give its leading dimension as an odd number no smaller. */
 size_t dga_gemm_workspace_size(dga_dtype in_dtype, dga_dtype out_dtype, dga_layout layout_b,
                                int64_t M, int64_t N, int64_t K,
                                int64_t lda, int64_t ldb, int64_t ldc, dga_path path);
