@@ -69,6 +69,21 @@ SIGNATURES = {
     "dga_orthogonalize": (_CI, [_CI, _CI, _I64, _I64, _I64, _VP, _I64, _I64, _VP, _I64, _I64, _CI, _VP,
                                 ctypes.c_float, _VP, _SZ, _VP]),
     "dga_orthogonalize_workspace_size": (_SZ, [_CI, _I64, _I64, _I64]),
+    "dga_gated": (_CI, [_CI, _CI, _I64, _I64, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP,
+                        _SZ, _VP]),
+    "dga_gated_workspace_size": (_SZ, [_CI, _I64, _I64, _I64, _I64, _I64, _CI]),
+    "dga_gated_backward": (_CI, [_CI, _CI, _I64, _I64, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64,
+                                 _VP, _I64, _VP, _I64, _VP, _VP, _SZ, _VP]),
+    "dga_gated_backward_workspace_size": (_SZ, [_CI, _I64, _I64, _I64, _I64, _I64]),
+    "dga_q4_quantize": (_CI, [_CI, _CI, _I64, _I64, _CI, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP]),
+    "dga_q4_dequantize": (_CI, [_CI, _CI, _I64, _I64, _CI, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64,
+                                _VP]),
+    "dga_q4_linear": (_CI, [_CI, _I64, _I64, _I64, _CI, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP,
+                            _VP, _I64, _VP, _SZ, _VP]),
+    "dga_q4_linear_workspace_size": (_SZ, [_CI, _I64, _I64, _I64, _I64]),
+    "dga_q4_gated": (_CI, [_CI, _CI, _I64, _I64, _I64, _CI, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64,
+                           _VP, _VP, _I64, _VP, _SZ, _VP]),
+    "dga_q4_gated_workspace_size": (_SZ, [_CI, _I64, _I64, _I64, _I64]),
     "dga_probe_fp32_fma": (_CI, [_CI, _I64, _VP, _I64, _VP, _VP]),
     "dga_probe_fp32_fma_out_floats": (_I64, []),
     "dga_probe_int8_mma": (_CI, [_I64, _VP, _I64, _VP, _VP]),
@@ -276,6 +291,57 @@ def dga_orthogonalize(in_dtype, out_dtype, batch, rows, cols, G, ldg, stride_g, 
 
 def dga_orthogonalize_workspace_size(out_dtype, batch, rows, cols):
     return lib().dga_orthogonalize_workspace_size(out_dtype, batch, rows, cols)
+
+
+def dga_gated(dtype, act, M, F, K, X, ldx, W, ldw, bias, H, ldh, P, ldp, workspace, workspace_bytes, stream):
+    return lib().dga_gated(dtype, act, M, F, K, X, ldx, W, ldw, bias, H, ldh, P, ldp, workspace,
+                           workspace_bytes, stream)
+
+
+def dga_gated_workspace_size(dtype, M, F, K, ldx, ldw, save):
+    return lib().dga_gated_workspace_size(dtype, M, F, K, ldx, ldw, save)
+
+
+def dga_gated_backward(dtype, act, M, F, K, X, ldx, W, ldw, P, ldp, G, ldg, dX, lddx, dW, lddw, db,
+                       workspace, workspace_bytes, stream):
+    return lib().dga_gated_backward(dtype, act, M, F, K, X, ldx, W, ldw, P, ldp, G, ldg, dX, lddx, dW,
+                                    lddw, db, workspace, workspace_bytes, stream)
+
+
+def dga_gated_backward_workspace_size(dtype, M, F, K, ldx, ldw):
+    return lib().dga_gated_backward_workspace_size(dtype, M, F, K, ldx, ldw)
+
+
+def dga_q4_quantize(in_dtype, scale_dtype, rows, cols, group, W, ldw, codes, ld_codes, scales, ld_scales,
+                    zeros, ld_zeros, stream):
+    return lib().dga_q4_quantize(in_dtype, scale_dtype, rows, cols, group, W, ldw, codes, ld_codes, scales,
+                                 ld_scales, zeros, ld_zeros, stream)
+
+
+def dga_q4_dequantize(scale_dtype, out_dtype, rows, cols, group, codes, ld_codes, scales, ld_scales, zeros,
+                      ld_zeros, Y, ldy, stream):
+    return lib().dga_q4_dequantize(scale_dtype, out_dtype, rows, cols, group, codes, ld_codes, scales,
+                                   ld_scales, zeros, ld_zeros, Y, ldy, stream)
+
+
+def dga_q4_linear(dtype, M, N, K, group, X, ldx, codes, ld_codes, scales, ld_scales, zeros, ld_zeros, bias,
+                  Y, ldy, workspace, workspace_bytes, stream):
+    return lib().dga_q4_linear(dtype, M, N, K, group, X, ldx, codes, ld_codes, scales, ld_scales, zeros,
+                               ld_zeros, bias, Y, ldy, workspace, workspace_bytes, stream)
+
+
+def dga_q4_linear_workspace_size(dtype, M, N, K, ldx):
+    return lib().dga_q4_linear_workspace_size(dtype, M, N, K, ldx)
+
+
+def dga_q4_gated(dtype, act, M, F, K, group, X, ldx, codes, ld_codes, scales, ld_scales, zeros, ld_zeros,
+                 bias, H, ldh, workspace, workspace_bytes, stream):
+    return lib().dga_q4_gated(dtype, act, M, F, K, group, X, ldx, codes, ld_codes, scales, ld_scales, zeros,
+                              ld_zeros, bias, H, ldh, workspace, workspace_bytes, stream)
+
+
+def dga_q4_gated_workspace_size(dtype, M, F, K, ldx):
+    return lib().dga_q4_gated_workspace_size(dtype, M, F, K, ldx)
 
 
 def dga_probe_fp32_fma(packed, iters, out, out_floats, flops, stream):
@@ -501,3 +567,5 @@ except ImportError:  # a CPU build of PyTorch
 from .mx import (MXFP4, NVFP4, MXTensor, mx_dequantize, mx_gemm, mx_linear_backward,  # noqa: E402,F401
                  mx_linear_forward, mx_quantize)
 from .muon import QUINTIC, orthogonalize  # noqa: E402,F401
+from .gated import ACTIVATIONS, gated_backward, gated_forward  # noqa: E402,F401
+from .q4 import Q4Tensor, q4_dequantize, q4_gated_forward, q4_linear_forward, q4_quantize  # noqa: E402,F401

@@ -182,12 +182,34 @@ size_t workspace_wanted(int path, const GemmArgs& g) {
     return workspace_required(path, g);
 }
 
+cudaError_t launch_path(int path, const GemmArgs& g, const DeviceInfo& dev, int* launches) {
+    switch (path) {
+    case DGA_PATH_GENERIC: return generic_launch(g, launches);
+    case DGA_PATH_SIMT: return simt_launch(g, dev, launches);
+    case DGA_PATH_SKINNY: return skinny_launch(g, dev, launches);
+    case DGA_PATH_TCGEN05: return tc_launch(g, dev, launches);
+    default: return cudaErrorInvalidValue;
+    }
+}
+
 int fail_cuda(cudaError_t e) {
     t_last_cuda_error = static_cast<int>(e);
     return DGA_ERR_CUDA;
 }
 
 }  // namespace
+
+cudaError_t gemm_run(const GemmArgs& g, const DeviceInfo& dev, int* launches) {
+    if (g.M == 0 || g.N == 0) return cudaSuccess;
+    const int path = choose_path(g);
+    if (g.ws_bytes < workspace_required(path, g)) return cudaErrorInvalidValue;
+    return launch_path(path, g, dev, launches);
+}
+
+size_t gemm_wanted(const GemmArgs& g) {
+    if (g.M == 0 || g.N == 0 || g.K == 0) return 0;
+    return workspace_wanted(choose_path(g), g);
+}
 
 int note_cuda_error(cudaError_t e) { return fail_cuda(e); }
 
@@ -243,13 +265,7 @@ int gemm_impl(const ArgPos& pos, dga_dtype in_dtype, dga_dtype out_dtype, dga_la
     if (workspace_bytes < workspace_required(chosen, g)) return DGA_ERR_WORKSPACE;
 
     int launches = 0;
-    switch (chosen) {
-    case DGA_PATH_GENERIC: e = generic_launch(g, &launches); break;
-    case DGA_PATH_SIMT: e = simt_launch(g, dev, &launches); break;
-    case DGA_PATH_SKINNY: e = skinny_launch(g, dev, &launches); break;
-    case DGA_PATH_TCGEN05: e = tc_launch(g, dev, &launches); break;
-    default: return DGA_ERR_PATH;
-    }
+    e = launch_path(chosen, g, dev, &launches);
     if (e != cudaSuccess) return fail_cuda(e);
     t_last_path = chosen;
     t_last_launches = launches;
@@ -560,7 +576,7 @@ const char* dga_status_string(int status) {
     }
 }
 
-int dga_version(void) { return 400; }  // 0.4.0: 4-bit microscaled matrices, Newton-Schulz orthogonalisation
+int dga_version(void) { return 500; }  // 0.5.0: the gated layer, 4-bit weights with group scales
 
 }  // extern "C"
 

@@ -169,6 +169,49 @@ cudaError_t ortho_launch(const OrthoArgs& a, const DeviceInfo& dev, int* launche
 // Reads and clears this device's status word of the orthogonalisation.
 cudaError_t ns_status_take(int* status);
 
+// ---- the gated feed-forward layer (validated arguments; P = [g | u], M x 2F)
+
+// H, and P in its type (Pout) where not null, from fp32 pre-activations, to
+// which a bias (2F values, or null) is still to be added.
+cudaError_t gated_act_launch(int dtype, int act, int64_t M, int64_t F, const float* P, int64_t ldp, const void* bias, void* H,
+                             int64_t ldh, void* Pout, int64_t ld_out, cudaStream_t stream);
+
+// dP (M x 2F of dtype, leading dimension ldd) and, where db is not null, the
+// column sums of its unrounded values; `partials` holds
+// gated_grad_partials(M, F) floats for them.
+size_t gated_grad_partials(int64_t M, int64_t F);
+cudaError_t gated_grad_launch(int dtype, int act, int64_t M, int64_t F, const void* P, int64_t ldp, const void* G,
+                              int64_t ldg, void* dP, int64_t ldd, float* db, float* partials, cudaStream_t stream,
+                              int* launches);
+
+// ---- 4-bit weights with group scales
+
+struct Q4Matrix {
+    const uint8_t* codes;
+    int64_t ld;  // bytes
+    const void* scales;
+    int64_t ld_scales;
+    const uint8_t* zeros;  // or null: 8
+    int64_t ld_zeros;
+    int group;
+};
+
+cudaError_t q4_quantize_launch(int in_dtype, int scale_dtype, int64_t rows, int64_t cols, const void* W, int64_t ldw,
+                               const Q4Matrix& q, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t q4_dequantize_launch(int scale_dtype, int out_dtype, int64_t rows, int64_t cols, const Q4Matrix& q, void* Y,
+                                 int64_t ldy, const DeviceInfo& dev, cudaStream_t stream);
+
+// Y (M x N) = X W^T + bias for up to kQ4Rows rows and K >= 1, or (gated) the gated
+// layer's M x N result on a weight of 2N rows.
+constexpr int64_t kQ4Rows = 64;
+cudaError_t q4_rows_launch(int dtype, int act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const Q4Matrix& q,
+                           const void* bias, void* Y, int64_t ldy, bool gated, cudaStream_t stream);
+
+// The GEMM as dga_gemm_general runs it, for validated arguments: the chosen
+// family's launch, and the workspace it would use.
+cudaError_t gemm_run(const GemmArgs& g, const DeviceInfo& dev, int* launches);
+size_t gemm_wanted(const GemmArgs& g);
+
 // Sets what dga_last_launch_count() returns on this host thread.
 void set_last_launches(int n);
 

@@ -1,0 +1,113 @@
+// gated_act.cuh -- the gated layer's activations and their slopes, and the
+// 16-bit vectors that its kernels load and store.
+//
+//   silu       g s(g)          s(g) = 1 / (1 + e^-g)
+//   gelu       g Phi(g)        Phi(g) = (1 + erf(g / sqrt 2)) / 2
+//   gelu_tanh  g s(v)          v = 2 sqrt(2/pi) (g + 0.044715 g^3), since
+//                              (1 + tanh(v / 2)) / 2 = s(v)
+//   relu       max(g, 0)
+//   sigmoid    s(g)
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+
+#include "dga.h"
+
+namespace dga {
+
+// s(x).  kFast: the hardware's exponential and division, 2^-21 off, for results
+// that are rounded to 16 bits (2^-9, 2^-12) next.
+template <bool kFast>
+__device__ __forceinline__ float logistic(float x) {
+    if constexpr (kFast) return __fdividef(1.0f, 1.0f + __expf(-x));
+    else return 1.0f / (1.0f + expf(-x));
+}
+
+constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2/pi)
+constexpr float kGeluB = 0.071354816272600f;    // 0.044715 * kGeluA
+constexpr float kGeluC = 0.21406444881780f;     // 3 * kGeluB
+constexpr float kInvSqrt2Pi = 0.3989422804014327f;
+
+template <int kAct, bool kFast>
+__device__ __forceinline__ float act_value(float g) {
+    if constexpr (kAct == DGA_SILU) return g * logistic<kFast>(g);
+    else if constexpr (kAct == DGA_GELU) return g * normcdff(g);
+    else if constexpr (kAct == DGA_GELU_TANH) return g * logistic<kFast>(g * fmaf(kGeluB * g, g, kGeluA));
+    else if constexpr (kAct == DGA_RELU) return g < 0.0f ? 0.0f : g;  // a NaN stays one
+    else return logistic<kFast>(g);
+}
+
+// The value and the slope.
+template <int kAct, bool kFast>
+__device__ __forceinline__ void act_both(float g, float& value, float& slope) {
+    if constexpr (kAct == DGA_SILU) {
+        const float s = logistic<kFast>(g);
+        value = g * s;
+        slope = fmaf(value, 1.0f - s, s);
+    } else if constexpr (kAct == DGA_GELU) {
+        const float c = normcdff(g);
+        const float e = kInvSqrt2Pi * (kFast ? __expf(-0.5f * g * g) : expf(-0.5f * g * g));
+        value = g * c;
+        slope = fmaf(g, e, c);
+    } else if constexpr (kAct == DGA_GELU_TANH) {
+        const float s = logistic<kFast>(g * fmaf(kGeluB * g, g, kGeluA));
+        const float t = s * (1.0f - s);
+        value = g * s;
+        // far out t is 0 and v' past fp32's range
+        slope = t > 0.0f ? fmaf(g * t, fmaf(kGeluC * g, g, kGeluA), s) : s;
+    } else if constexpr (kAct == DGA_RELU) {
+        value = g < 0.0f ? 0.0f : g;
+        slope = g > 0.0f ? 1.0f : (g == g ? 0.0f : g);
+    } else {
+        value = logistic<kFast>(g);
+        slope = value * (1.0f - value);
+    }
+}
+
+// kVec values of T, loaded and stored as one access.
+template <typename T, int kVec>
+struct Pack {
+    static constexpr int kBytes = kVec * static_cast<int>(sizeof(T));
+    __device__ __forceinline__ static void load(const T* p, float (&v)[kVec]) {
+        T t[kVec];
+        if constexpr (kBytes == 16) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p);
+            memcpy(t, &w, 16);
+        } else if constexpr (kBytes == 8) {
+            const uint2 w = *reinterpret_cast<const uint2*>(p);
+            memcpy(t, &w, 8);
+        } else {
+            static_assert(kVec == 1, "16 or 8 bytes, or one value");
+            t[0] = *p;
+        }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] = static_cast<float>(t[i]);
+    }
+    __device__ __forceinline__ static void store(T* p, const float (&v)[kVec]) {
+        T t[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            if constexpr (sizeof(T) == 4) t[i] = v[i];
+            else if constexpr (std::is_same<T, __half>::value) t[i] = __float2half_rn(v[i]);
+            else t[i] = __float2bfloat16_rn(v[i]);
+        }
+        if constexpr (kBytes == 16) {
+            uint4 w;
+            memcpy(&w, t, 16);
+            *reinterpret_cast<uint4*>(p) = w;
+        } else if constexpr (kBytes == 8) {
+            uint2 w;
+            memcpy(&w, t, 8);
+            *reinterpret_cast<uint2*>(p) = w;
+        } else {
+            *p = t[0];
+        }
+    }
+};
+
+}  // namespace dga

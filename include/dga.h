@@ -563,6 +563,151 @@ int dga_orthogonalize(dga_dtype in_dtype, dga_dtype out_dtype, int64_t batch, in
 size_t dga_orthogonalize_workspace_size(dga_dtype out_dtype, int64_t batch, int64_t rows,
                                         int64_t cols);
 
+/* ---- the gated feed-forward layer ------------------------------------------
+ *
+ *     P = X W^T + bias,  P = [g | u],  H = act(g) * u
+ *
+ * X is M x K, W 2F x K (the gate's F rows, then the up projection's), the bias
+ * 2F values or NULL, P M x 2F, H M x F; all row-major and of one type, DGA_F32,
+ * DGA_BF16 or DGA_F16.  Products are summed in fp32 (DGA_F32 by exact FP32
+ * arithmetic, never TF32); the activation and the product are computed from
+ * the fp32 sums, and H and P are each rounded once.
+ *   DGA_SILU       g / (1 + e^-g)
+ *   DGA_GELU       g Phi(g), Phi the normal distribution's integral
+ *   DGA_GELU_TANH  g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2
+ *   DGA_RELU       g where g > 0, else 0 (a NaN stays one)
+ *   DGA_SIGMOID    1 / (1 + e^-g)                                            */
+typedef enum {
+    DGA_SILU = 0,
+    DGA_GELU = 1,
+    DGA_GELU_TANH = 2,
+    DGA_RELU = 3,
+    DGA_SIGMOID = 4
+} dga_activation;
+
+/*
+ * dga_gated -- H, and, where P is not NULL, the pre-activations P that
+ * dga_gated_backward reads.  K == 0: P is the bias (or 0).
+ *   workspace   device, 16-byte aligned, of dga_gated_workspace_size(...) bytes
+ * Errors: DGA_ERR_UNSUPPORTED (type, activation); -3 M, -4 F, -5 K (outside
+ * [0, 2^30), as every size of the calls below), -6 X, -7 ldx, -8 W, -9 ldw,
+ * -10 bias, -11 H, -12 ldh, -13 P, -14 ldp, -15 workspace (each array's own
+ * alignment, its type's size, included); DGA_ERR_WORKSPACE; DGA_ERR_OVERLAP when H, P or the workspace
+ * meets another array.  M == 0 or F == 0 is a no-op.
+ */
+int dga_gated(dga_dtype dtype, dga_activation act, int64_t M, int64_t F, int64_t K, const void* X,
+              int64_t ldx, const void* W, int64_t ldw, const void* bias, void* H, int64_t ldh,
+              void* P, int64_t ldp, void* workspace, size_t workspace_bytes, dga_stream_t stream);
+
+/* For X and W that start on 16 bytes; for one that does not, give its leading
+ * dimension as an odd number no smaller.  save: whether P is given. */
+size_t dga_gated_workspace_size(dga_dtype dtype, int64_t M, int64_t F, int64_t K, int64_t ldx,
+                                int64_t ldw, int save);
+
+/*
+ * dga_gated_backward -- the gradients for H's gradient G (M x F):
+ *     dP = [G u act'(g) | G act(g)];  dX = dP W,  dW = dP^T X,  db = the sum of
+ *     dP's rows
+ * with P as dga_gated wrote it.  dX (M x K) and dW (2F x K) have the type of
+ * the inputs; each may be NULL where it is not wanted.  dP is computed in fp32
+ * and rounded to the type for the two products (16-bit types: half a step of
+ * each value, as the tensor cores take them); db (2F floats, or NULL) is summed
+ * in fp32 from the unrounded values.  relu's slope at 0 is 0.  M == 0 gives
+ * zero dW and db.  Results repeat bit for bit.
+ *   workspace   device, 256-byte aligned, of dga_gated_backward_workspace_size bytes
+ * Errors: as dga_gated; -6 X, -7 ldx, -8 W, -9 ldw, -10 P, -11 ldp, -12 G,
+ * -13 ldg, -14 dX, -15 lddx, -16 dW, -17 lddw, -18 db, -19 workspace.
+ */
+int dga_gated_backward(dga_dtype dtype, dga_activation act, int64_t M, int64_t F, int64_t K,
+                       const void* X, int64_t ldx, const void* W, int64_t ldw, const void* P,
+                       int64_t ldp, const void* G, int64_t ldg, void* dX, int64_t lddx, void* dW,
+                       int64_t lddw, float* db, void* workspace, size_t workspace_bytes,
+                       dga_stream_t stream);
+
+/* As for dga_gated_workspace_size. */
+size_t dga_gated_backward_workspace_size(dga_dtype dtype, int64_t M, int64_t F, int64_t K,
+                                         int64_t ldx, int64_t ldw);
+
+/* ---- 4-bit weights with group scales ------------------------------------------
+ *
+ * A weight of N rows and K columns as codes q in 0..15 with a scale s and a
+ * zero point z per row and group of 32, 64 or 128 consecutive columns:
+ *     w = (q - z) * s
+ *   codes   device, 16-byte aligned, rows ld_codes bytes apart (a multiple of
+ *           16, at least dga_mx_row_bytes(K)): column k in byte k/2, the even
+ *           one in the low half.  What a row holds past K is never used.
+ *   scales  device, N x ceil(K / group) values of DGA_BF16 or DGA_F16, rows
+ *           ld_scales values apart
+ *   zeros   device, one byte per scale, of which the low four bits count, rows
+ *           ld_zeros bytes apart; NULL for z = 8 throughout                   */
+
+/*
+ * dga_q4_quantize -- W (rows x cols; DGA_F32, DGA_BF16 or DGA_F16) to that form,
+ * scales of scale_dtype.  For a group with least value lo and greatest hi, in
+ * correctly rounded fp32 arithmetic:
+ *   zeros given  s = (max(hi, 0) - min(lo, 0)) / 15 rounded to scale_dtype,
+ *                z = round(-min(lo, 0) / s), q = round(w / s + z), both held
+ *                to [0, 15]
+ *   zeros NULL   s = max |w| / 7 rounded to scale_dtype, q = round(w / s + 8)
+ *                held to [0, 15]
+ * rounding ties to even.  A group whose scale is 0 gets codes equal to its
+ * zero point (0 or 8); one with an infinity or a NaN, or a scale past
+ * scale_dtype's range, a NaN scale.  Codes past cols, to the row's last 16
+ * bytes, are written as 0.
+ * Errors: DGA_ERR_UNSUPPORTED (types, group); -3 rows, -4 cols, -6 W, -7 ldw,
+ * -8 codes, -9 ld_codes, -10 scales, -11 ld_scales, -13 ld_zeros;
+ * DGA_ERR_OVERLAP.
+ */
+int dga_q4_quantize(dga_dtype in_dtype, dga_dtype scale_dtype, int64_t rows, int64_t cols,
+                    int group, const void* W, int64_t ldw, void* codes, int64_t ld_codes,
+                    void* scales, int64_t ld_scales, void* zeros, int64_t ld_zeros,
+                    dga_stream_t stream);
+
+/*
+ * dga_q4_dequantize -- Y (rows x cols; DGA_F32, DGA_BF16 or DGA_F16) <- (q - z)
+ * * s, exact in fp32, rounded once.  Errors: DGA_ERR_UNSUPPORTED; -3 rows,
+ * -4 cols, -6 codes, -7 ld_codes, -8 scales, -9 ld_scales, -11 ld_zeros, -12 Y,
+ * -13 ldy; DGA_ERR_OVERLAP.
+ */
+int dga_q4_dequantize(dga_dtype scale_dtype, dga_dtype out_dtype, int64_t rows, int64_t cols,
+                      int group, const void* codes, int64_t ld_codes, const void* scales,
+                      int64_t ld_scales, const void* zeros, int64_t ld_zeros, void* Y,
+                      int64_t ldy, dga_stream_t stream);
+
+/*
+ * dga_q4_linear -- Y <- X W^T + bias on such a weight (N x K): X (M x K,
+ * row-major), the scales, the bias (N values or NULL) and Y (M x N, row-major)
+ * of one type, DGA_BF16 or DGA_F16; sums in fp32.
+ *   workspace   device, 256-byte aligned, of dga_q4_linear_workspace_size bytes
+ * Errors: DGA_ERR_UNSUPPORTED (type, group); -2 M, -3 N, -4 K, -6 X, -7 ldx,
+ * -8 codes, -9 ld_codes, -10 scales, -11 ld_scales, -13 ld_zeros, -14 bias,
+ * -15 Y, -16 ldy, -17 workspace; DGA_ERR_WORKSPACE, DGA_ERR_OVERLAP.
+ */
+int dga_q4_linear(dga_dtype dtype, int64_t M, int64_t N, int64_t K, int group, const void* X,
+                  int64_t ldx, const void* codes, int64_t ld_codes, const void* scales,
+                  int64_t ld_scales, const void* zeros, int64_t ld_zeros, const void* bias,
+                  void* Y, int64_t ldy, void* workspace, size_t workspace_bytes,
+                  dga_stream_t stream);
+
+/* For an X that starts on 16 bytes; else give ldx as an odd number no smaller. */
+size_t dga_q4_linear_workspace_size(dga_dtype dtype, int64_t M, int64_t N, int64_t K, int64_t ldx);
+
+/*
+ * dga_q4_gated -- the gated layer H = act(g) * u, [g | u] = X W^T + bias, on
+ * such a weight of 2F rows (the gate's, then the up projection's); types and
+ * roundings as above, the activation and the product in fp32.
+ * Errors: DGA_ERR_UNSUPPORTED; -3 M, -4 F, -5 K, -7 X, -8 ldx, -9 codes,
+ * -10 ld_codes, -11 scales, -12 ld_scales, -14 ld_zeros, -15 bias, -16 H,
+ * -17 ldh, -18 workspace; DGA_ERR_WORKSPACE, DGA_ERR_OVERLAP.
+ */
+int dga_q4_gated(dga_dtype dtype, dga_activation act, int64_t M, int64_t F, int64_t K, int group,
+                 const void* X, int64_t ldx, const void* codes, int64_t ld_codes,
+                 const void* scales, int64_t ld_scales, const void* zeros, int64_t ld_zeros,
+                 const void* bias, void* H, int64_t ldh, void* workspace, size_t workspace_bytes,
+                 dga_stream_t stream);
+
+size_t dga_q4_gated_workspace_size(dga_dtype dtype, int64_t M, int64_t F, int64_t K, int64_t ldx);
+
 /* Library version: major*10000 + minor*100 + patch. */
 int dga_version(void);
 
