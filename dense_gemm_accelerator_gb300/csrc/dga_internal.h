@@ -201,11 +201,17 @@ cudaError_t q4_quantize_launch(int in_dtype, int scale_dtype, int64_t rows, int6
 cudaError_t q4_dequantize_launch(int scale_dtype, int out_dtype, int64_t rows, int64_t cols, const Q4Matrix& q, void* Y,
                                  int64_t ldy, const DeviceInfo& dev, cudaStream_t stream);
 
-// Y (M x N) = X W^T + bias for up to kQ4Rows rows and K >= 1, or (gated) the gated
+// Rows of 16-bit values copied to rows that start on 16 bytes (ldy a multiple of 8).
+cudaError_t copy_rows_launch(int64_t rows, int64_t cols, const void* X, int64_t ldx, void* Y, int64_t ldy, const DeviceInfo& dev,
+                             cudaStream_t stream);
+
+// Y (M x N) = X W^T + bias for up to kQ4Rows rows (that start on 16 bytes) and K >= 1, or (gated) the gated
 // layer's M x N result on a weight of 2N rows.
 constexpr int64_t kQ4Rows = 64;
 cudaError_t q4_rows_launch(int dtype, int act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const Q4Matrix& q,
-                           const void* bias, void* Y, int64_t ldy, bool gated, cudaStream_t stream);
+                           const void* bias, void* Y, int64_t ldy, bool gated, const DeviceInfo& dev, cudaStream_t stream);
+// Reads and clears this device's status word of these products.
+cudaError_t q4_status_take(int* status);
 
 // The GEMM as dga_gemm_general runs it, for validated arguments: the chosen
 // family's launch, and the workspace it would use.

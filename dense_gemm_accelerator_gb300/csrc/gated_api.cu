@@ -136,21 +136,43 @@ void q4_arrays(Arrays& a, const Q4Matrix& q, int64_t N, int64_t K, bool written)
     add(q.zeros, q.ld_zeros, groups);
 }
 
-// Scratch of a product on a 4-bit weight of more than kQ4Rows rows: its values, what a gated one keeps
-// of P, the product's own.
+// Scratch of a product on a 4-bit weight.  Up to kQ4Rows rows: X in rows that
+// start on 16 bytes, where it has none.  More: the weight's values, what a gated
+// one keeps of P, the product's own.
 struct Q4Plan {
+    bool few;
     int64_t ldv, values, held, gemm;
     int64_t total() const { return values + held + gemm; }
 };
 Q4Plan q4_plan(int dtype, int64_t M, int64_t N, int64_t K, int64_t ldx, bool gated, const void* X) {
     Q4Plan pl{};
-    if (M <= kQ4Rows && K > 0) return pl;
     pl.ldv = round_up(K, 8);
+    pl.few = M <= kQ4Rows && K > 0;
+    if (pl.few) {
+        if (ldx % 8 != 0 || (X && !aligned(X, 16))) pl.values = round_up(M * pl.ldv * 2, 256);
+        return pl;
+    }
     pl.values = round_up(N * pl.ldv * 2, 256);
     pl.held = gated ? held_bytes(M, N / 2) : 0;
     pl.gemm = static_cast<int64_t>(gemm_wanted(product(dtype, gated ? DGA_F32 : dtype, DGA_ROW_MAJOR, DGA_COL_MAJOR, M, N, K, X,
                                                        ldx, nullptr, pl.ldv, nullptr, N, nullptr, nullptr)));
     return pl;
+}
+
+// Few rows: Y, or (gated) the gated layer's result.
+cudaError_t q4_by_rows(const Q4Plan& pl, int dtype, int act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                       const Q4Matrix& q, const void* bias, void* Y, int64_t ldy, bool gated, uint8_t* ws, const DeviceInfo& dev,
+                       cudaStream_t s, int* launches) {
+    if (pl.values) {
+        const cudaError_t e = copy_rows_launch(M, K, X, ldx, ws, pl.ldv, dev, s);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+        X = ws;
+        ldx = pl.ldv;
+    }
+    const cudaError_t e = q4_rows_launch(dtype, act, M, N, K, X, ldx, q, bias, Y, ldy, gated, dev, s);
+    if (e == cudaSuccess) ++*launches;
+    return e;
 }
 
 // [X W^T + bias] of a 4-bit W through its values: into Y, or (gated) into P's place in the workspace.
@@ -391,9 +413,8 @@ int dga_q4_linear(dga_dtype dtype, int64_t M, int64_t N, int64_t K, int group, c
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int launches = 0;
     cudaError_t e;
-    if (M <= kQ4Rows && K > 0) {
-        e = q4_rows_launch(dtype, 0, M, N, K, X, ldx, q, bias, Y, ldy, false, s);
-        launches = 1;
+    if (pl.few) {
+        e = q4_by_rows(pl, dtype, 0, M, N, K, X, ldx, q, bias, Y, ldy, false, static_cast<uint8_t*>(workspace), dev, s, &launches);
     } else {
         e = q4_by_values(pl, dtype, dtype, M, N, K, X, ldx, q, bias, Y, ldy, static_cast<uint8_t*>(workspace), dev, s, &launches);
     }
@@ -440,14 +461,11 @@ int dga_q4_gated(dga_dtype dtype, dga_activation act, int64_t M, int64_t F, int6
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     int launches = 0;
     cudaError_t e;
-    if (M <= kQ4Rows && K > 0) {
-        e = q4_rows_launch(dtype, act, M, F, K, X, ldx, q, bias, H, ldh, true, s);
+    if (pl.few) {
+        e = q4_by_rows(pl, dtype, act, M, F, K, X, ldx, q, bias, H, ldh, true, ws, dev, s, &launches);
+    } else {
+        e = q4_by_values(pl, dtype, DGA_F32, M, 2 * F, K, X, ldx, q, nullptr, ws + pl.values, held_ld(F), ws, dev, s, &launches);
         if (e != cudaSuccess) return note_cuda_error(e);
-        set_last_launches(1);
-        return DGA_OK;
-    }
-    e = q4_by_values(pl, dtype, DGA_F32, M, 2 * F, K, X, ldx, q, nullptr, ws + pl.values, held_ld(F), ws, dev, s, &launches);
-    if (e == cudaSuccess) {
         e = gated_act_launch(dtype, act, M, F, reinterpret_cast<const float*>(ws + pl.values), held_ld(F), bias, H, ldh, nullptr, 0, s);
         if (e == cudaSuccess) ++launches;
     }
