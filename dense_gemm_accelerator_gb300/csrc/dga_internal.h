@@ -171,6 +171,30 @@ cudaError_t ns_status_take(int* status);
 
 // ---- the gated feed-forward layer (validated arguments; P = [g | u], M x 2F)
 
+struct GatedArgs {
+    int dtype, act;
+    int64_t M, F, K;
+    const void* X;
+    int64_t ldx;
+    const void* W;  // 2F x K, the gate's rows first
+    int64_t ldw;
+    const void* bias;  // 2F values, or null
+    void* H;
+    int64_t ldh;
+    void* P;  // or null
+    int64_t ldp;
+    cudaStream_t stream;
+};
+
+// The layer in one kernel on the tensor cores (16-bit types, X and W in rows
+// that start on 16 bytes): few rows, bound by W's bytes, and any number.
+bool gated_skinny_supports(const GatedArgs& a);
+cudaError_t gated_skinny_launch(const GatedArgs& a, const DeviceInfo& dev);
+bool gated_tc_supports(const GatedArgs& a);
+cudaError_t gated_tc_launch(const GatedArgs& a, const DeviceInfo& dev);
+// Reads and clears this device's status word of the gated layer's kernels.
+cudaError_t gated_status_take(int* status);
+
 // H, and P in its type (Pout) where not null, from fp32 pre-activations, to
 // which a bias (2F values, or null) is still to be added.
 cudaError_t gated_act_launch(int dtype, int act, int64_t M, int64_t F, const float* P, int64_t ldp, const void* bias, void* H,

@@ -135,6 +135,37 @@ __global__ void __launch_bounds__(256) sum_slices_kernel(int64_t cols, int slice
     out[c] = s;
 }
 
+// ---- rows of 16-bit values to rows that start on 16 bytes -------------------------------
+//
+// Eight values to a thread, zero past the row's end; read by words of two, and
+// shifted where the row starts between two (at the array's ends one by one).
+__global__ void __launch_bounds__(256)
+    copy_rows_kernel(int64_t rows, int64_t cols, const uint16_t* __restrict__ X, int64_t ldx, uint16_t* __restrict__ Y, int64_t ldy) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t pieces = ldy / 8, total = rows * pieces;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t row = i / pieces, k = (i - row * pieces) * 8;
+        const uint16_t* src = X + row * ldx + k;
+        uint32_t w[5] = {0, 0, 0, 0, 0};
+        if (k + 8 < cols && (row > 0 || k > 0)) {
+            const uint32_t odd = (reinterpret_cast<uintptr_t>(src) >> 1) & 1;
+            const uint32_t* words = reinterpret_cast<const uint32_t*>(src - odd);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = __ldg(words + j);
+            if (odd) {
+                w[4] = __ldg(words + 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (k + j < cols) w[j / 2] |= static_cast<uint32_t>(__ldg(src + j)) << (16 * (j & 1));
+        }
+        *reinterpret_cast<uint4*>(Y + row * ldy + k) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 // Row slices of the gradient pass: about 16 blocks to an SM at 256 columns to
 // a block, none under 32 rows.
 int grad_slices(int64_t M, int64_t F) {
@@ -170,6 +201,14 @@ bool vectors(const void* p, int64_t ld, int vec, int64_t size) {
 }
 
 }  // namespace
+
+cudaError_t copy_rows_launch(int64_t rows, int64_t cols, const void* X, int64_t ldx, void* Y, int64_t ldy, const DeviceInfo& dev,
+                             cudaStream_t stream) {
+    const int64_t work = (rows * (ldy / 8) + 255) / 256;
+    copy_rows_kernel<<<static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(work, int64_t{64} * dev.sm_count))), 256, 0, stream>>>(
+        rows, cols, static_cast<const uint16_t*>(X), ldx, static_cast<uint16_t*>(Y), ldy);
+    return cudaGetLastError();
+}
 
 cudaError_t gated_act_launch(int dtype, int act, int64_t M, int64_t F, const float* P, int64_t ldp, const void* bias, void* H,
                              int64_t ldh, void* Pout, int64_t ld_out, cudaStream_t stream) {

@@ -28,6 +28,28 @@ __device__ __forceinline__ float logistic(float x) {
     else return 1.0f / (1.0f + expf(-x));
 }
 
+// Phi(g).  kFast: erfc(x) = t 2^(-x^2 log2 e + p(t)), t = 1 / (1 + x / 2), x = |g| / sqrt 2,
+// p the polynomial of degree 7 that a Chebyshev fit of log2(erfcx(x) / t) over t gives;
+// 7e-7 off relative to the value near 0, 2e-5 at |g| = 13 (fp32's x^2), where the library
+// function (the other case) took three times the tensor cores' time of K = 512.
+template <bool kFast>
+__device__ __forceinline__ float normal_cdf(float g) {
+    if constexpr (!kFast) return normcdff(g);
+    const float x = fabsf(g) * 0.70710678f, t = __fdividef(1.0f, fmaf(0.5f, x, 1.0f));
+    float q = -0.2702641784782f;
+    q = fmaf(q, t, 1.0810290575f);
+    q = fmaf(q, t, -1.4374856949f);
+    q = fmaf(q, t, 0.4973544180f);
+    q = fmaf(q, t, -0.0525670536f);
+    q = fmaf(q, t, 0.5666871667f);
+    q = fmaf(q, t, 1.4409651756f);
+    q = fmaf(q, t, -1.8257199526f);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fmaf(-1.44269504f * x, x, q)));
+    e *= 0.5f * t;
+    return g < 0.0f ? e : 1.0f - e;
+}
+
 constexpr float kGeluA = 1.5957691216057308f;   // 2 sqrt(2/pi)
 constexpr float kGeluB = 0.071354816272600f;    // 0.044715 * kGeluA
 constexpr float kGeluC = 0.21406444881780f;     // 3 * kGeluB
@@ -36,7 +58,7 @@ constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 template <int kAct, bool kFast>
 __device__ __forceinline__ float act_value(float g) {
     if constexpr (kAct == DGA_SILU) return g * logistic<kFast>(g);
-    else if constexpr (kAct == DGA_GELU) return g * normcdff(g);
+    else if constexpr (kAct == DGA_GELU) return g * normal_cdf<kFast>(g);
     else if constexpr (kAct == DGA_GELU_TANH) return g * logistic<kFast>(g * fmaf(kGeluB * g, g, kGeluA));
     else if constexpr (kAct == DGA_RELU) return g < 0.0f ? 0.0f : g;  // a NaN stays one
     else return logistic<kFast>(g);
@@ -50,7 +72,7 @@ __device__ __forceinline__ void act_both(float g, float& value, float& slope) {
         value = g * s;
         slope = fmaf(value, 1.0f - s, s);
     } else if constexpr (kAct == DGA_GELU) {
-        const float c = normcdff(g);
+        const float c = normal_cdf<kFast>(g);
         const float e = kInvSqrt2Pi * (kFast ? __expf(-0.5f * g * g) : expf(-0.5f * g * g));
         value = g * c;
         slope = fmaf(g, e, c);

@@ -87,13 +87,24 @@ GemmArgs product(int in, int out, int layout_a, int layout_b, int64_t M, int64_t
 int64_t held_ld(int64_t F) { return round_up(2 * F, 4); }
 int64_t held_bytes(int64_t M, int64_t F) { return round_up(M * held_ld(F) * 4, 256); }
 
-// Scratch of dga_gated: P where the caller keeps none in fp32, the product's own.
+// Scratch of dga_gated.  16-bit types: X and W in rows that start on 16 bytes,
+// where they have none.  fp32, and K = 0: P where the caller keeps none in fp32,
+// the product's own.
 struct ForwardPlan {
-    int64_t held, gemm;
+    bool fused;
+    int64_t x, w, held, gemm;
+    int64_t total() const { return x + w + held + gemm; }
 };
 ForwardPlan forward_plan(int dtype, int64_t M, int64_t F, int64_t K, int64_t ldx, int64_t ldw, bool save, const void* X,
                          const void* W) {
     ForwardPlan pl{};
+    pl.fused = dtype != DGA_F32 && K > 0;
+    if (pl.fused) {
+        const int64_t row = round_up(K, 8) * 2;
+        if (ldx % 8 != 0 || (X && !aligned(X, 16))) pl.x = round_up(M * row, 256);
+        if (ldw % 8 != 0 || (W && !aligned(W, 16))) pl.w = round_up(2 * F * row, 256);
+        return pl;
+    }
     const bool direct = dtype == DGA_F32 && save;
     pl.held = direct ? 0 : held_bytes(M, F);
     pl.gemm = static_cast<int64_t>(gemm_wanted(product(dtype, DGA_F32, DGA_ROW_MAJOR, DGA_COL_MAJOR, M, 2 * F, K, X, ldx, W,
@@ -198,7 +209,7 @@ extern "C" {
 size_t dga_gated_workspace_size(dga_dtype dtype, int64_t M, int64_t F, int64_t K, int64_t ldx, int64_t ldw, int save) {
     if (!float_type(dtype) || M <= 0 || F <= 0 || K < 0 || !dim_ok(M) || !dim_ok(F) || !dim_ok(K)) return 0;
     const ForwardPlan pl = forward_plan(dtype, M, F, K, ldx, ldw, save != 0, nullptr, nullptr);
-    return static_cast<size_t>(pl.held + pl.gemm);
+    return static_cast<size_t>(pl.total());
 }
 
 int dga_gated(dga_dtype dtype, dga_activation act, int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W,
@@ -222,7 +233,7 @@ int dga_gated(dga_dtype dtype, dga_activation act, int64_t M, int64_t F, int64_t
     if (P && ldp < 2 * F) return -14;
     if ((workspace_bytes > 0 && !workspace) || (workspace && !aligned(workspace, 16))) return -15;
     const ForwardPlan pl = forward_plan(dtype, M, F, K, ldx, ldw, P != nullptr, X, W);
-    const int64_t need = pl.held + pl.gemm;
+    const int64_t need = pl.total();
     if (workspace_bytes < static_cast<size_t>(need)) return DGA_ERR_WORKSPACE;
     Arrays a;
     if (K > 0) a.in(X, M, ldx * es, K * es), a.in(W, 2 * F, ldw * es, K * es);
@@ -237,6 +248,26 @@ int dga_gated(dga_dtype dtype, dga_activation act, int64_t M, int64_t F, int64_t
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     int launches = 0;
+    cudaError_t e = cudaSuccess;
+    if (pl.fused) {
+        GatedArgs g{dtype, act, M, F, K, X, ldx, W, ldw, bias, H, ldh, P, ldp, s};
+        const int64_t ld = round_up(K, 8);
+        if (pl.x) {
+            e = copy_rows_launch(M, K, X, ldx, ws, ld, dev, s);
+            g.X = ws, g.ldx = ld;
+            ++launches;
+        }
+        if (e == cudaSuccess && pl.w) {
+            e = copy_rows_launch(2 * F, K, W, ldw, ws + pl.x, ld, dev, s);
+            g.W = ws + pl.x, g.ldw = ld;
+            ++launches;
+        }
+        if (e == cudaSuccess)
+            e = gated_skinny_supports(g) ? gated_skinny_launch(g, dev) : gated_tc_supports(g) ? gated_tc_launch(g, dev) : cudaErrorNotSupported;
+        if (e != cudaSuccess) return note_cuda_error(e);
+        set_last_launches(launches + 1);
+        return DGA_OK;
+    }
     const bool direct = pl.held == 0;
     void* sums = direct ? P : ws;
     const int64_t lds = direct ? ldp : held_ld(F);
@@ -246,7 +277,7 @@ int dga_gated(dga_dtype dtype, dga_activation act, int64_t M, int64_t F, int64_t
                          dtype == DGA_F32 ? bias : nullptr, s);
     g.ws = ws + pl.held;
     g.ws_bytes = static_cast<size_t>(pl.gemm);
-    cudaError_t e = gemm_run(g, dev, &launches);
+    e = gemm_run(g, dev, &launches);
     if (e == cudaSuccess) {
         e = gated_act_launch(dtype, act, M, F, static_cast<const float*>(sums), lds, dtype == DGA_F32 ? nullptr : bias, H, ldh,
                              direct ? nullptr : P, ldp, s);

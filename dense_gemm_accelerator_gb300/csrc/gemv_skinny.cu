@@ -45,6 +45,10 @@
 //    to become visible before touching global memory, so results and stream
 //    order are exactly those of a plain launch; back-to-back calls only
 //    overlap launch and set-up with the previous call's tail.
+//  * The gated layer, H = act(g) * u with [g | u] = X W^T + b, W of 2N rows: a CTA
+//    takes up to 32 gate rows (tiles 0 and 1) and the up rows that go with them
+//    (tiles 2 and 3), and a gate tile's warp gets its u from the up tile's through
+//    the same 4 KB.
 //  * Every wait is bounded; a wait that expires records a code in this
 //    family's status word (read by dga_sync_status) and the CTA returns after
 //    its copies in flight have landed.
@@ -57,6 +61,7 @@
 
 #include "dga_internal.h"
 #include "epilogue.cuh"
+#include "gated_act.cuh"
 #include "ptx.cuh"
 
 namespace dga {
@@ -91,6 +96,10 @@ struct Params {
     uint32_t w_box_bytes;  // stride of the weight boxes: (rows_lo + 1) * 128 rounded to 1 KB
     uint32_t stages;       // ring stages (<= kMaxStages)
     uint32_t n_kstages;    // ceil(K / 256)
+    // the gated layer (N: its outputs; Y: H)
+    void* P;               // pre-activations, or null
+    int64_t ldp;
+    int act;
 };
 
 __host__ __device__ inline uint32_t stage_bytes(uint32_t w_box_bytes) {
@@ -144,7 +153,7 @@ __device__ __forceinline__ uint32_t sw128(uint32_t box, uint32_t row, uint32_t c
 //   [W box 0][W box 1][W box 2][W box 3][X box 0][X box 1][X box 2][X box 3]
 // then the barriers, then the 4 KB hand-over area of the final reduction.
 // MT = 8-row activation tiles (1 for M <= 8, 2 for M <= 16).
-template <bool kBf16, int MT, typename TOut>
+template <bool kBf16, int MT, typename TOut, bool kGated = false>
 __global__ void __launch_bounds__(kThreads, 1)
     skinny_kernel(const __grid_constant__ CUtensorMap tmW_lo, const __grid_constant__ CUtensorMap tmW_hi,
                   const __grid_constant__ CUtensorMap tmX, Params p) {
@@ -186,12 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[m][i] = 0.0f;
     const int tile = warp & 3, khalf = warp >> 2;  // consumer warps: 16-row tile, k-step half
+    const int row_tile = kGated ? tile & 1 : tile;  // of the CTA's rows (gated: of gate or up ones)
 
     if (warp == kConsumerWarps) {
         // ------------------------------------------------ TMA producer
         if (lane == 0) {
             const CUtensorMap* tmW = rows == p.rows_lo ? &tmW_lo : &tmW_hi;
-            const uint32_t tx_bytes = kBoxesPerStage * (rows * kBoxK * 2 + kXBoxBytes);
+            const uint32_t tx_bytes = kBoxesPerStage * ((kGated ? 2 : 1) * rows * kBoxK * 2 + kXBoxBytes);
             tma_prefetch_desc(tmW);
             tma_prefetch_desc(&tmX);
             uint32_t stage = 0, phase = 0;
@@ -211,6 +221,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int32_t k0 = static_cast<int32_t>((ks * kBoxesPerStage + b) * kBoxK);
                     tma_load_2d(base + b * p.w_box_bytes, tmW, &full[stage], k0,
                                 static_cast<int32_t>(n0));
+                    if constexpr (kGated)
+                        tma_load_2d(base + b * p.w_box_bytes + 2 * 16 * 128, tmW, &full[stage], k0,
+                                    static_cast<int32_t>(n0 + p.N));
                     tma_load_2d(base + kBoxesPerStage * p.w_box_bytes + b * kXBoxBytes, &tmX,
                                 &full[stage], k0, 0);
                 }
@@ -229,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ consumer warps
         // warp w: rows [16 * (w % 4), +16) and k-steps [8 * (w / 4), +8) of
         // every stage (k-step s: box s / 4, 16-byte chunks 2 (s % 4), +1)
-        const bool active = tile < rt_used;
+        const bool active = row_tile < rt_used;
         const uint32_t a_row = lane & 15, a_half = lane >> 4;
         const uint32_t b_row = lane & 7, b_half = (lane >> 3) & 1;
         uint32_t stage = 0, phase = 0;
@@ -261,13 +274,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     if (warp == kConsumerWarps) return;  // the producer has waited for its copies
-    const bool active = tile < rt_used;
+    const bool active = row_tile < rt_used;
     if (active && khalf == 1) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
             red[(tile * MT + m) * 32 + lane] = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
     }
     asm volatile("bar.sync 1, %0;" ::"n"(kConsumerWarps * 32) : "memory");  // consumer warps only
+    if constexpr (kGated) {
+        if (khalf == 1) return;
+        // both halves of K together; an up tile's sums wait in its place for the gate tile's warp
+        if (active) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float4& slot = red[(tile * MT + m) * 32 + lane];
+                const float4 o = slot;
+                acc[m][0] += o.x, acc[m][1] += o.y, acc[m][2] += o.z, acc[m][3] += o.w;
+                if (tile >= 2) slot = make_float4(acc[m][0], acc[m][1], acc[m][2], acc[m][3]);
+            }
+        }
+        asm volatile("bar.sync 2, %0;" ::"n"(kConsumerWarps / 2 * 32) : "memory");
+        if (!active || tile >= 2 || *abort_flag) return;
+        const TOut* bias = static_cast<const TOut*>(p.bias);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const float4 o = red[((tile + 2) * MT + m) * 32 + lane];
+            const float up[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t row = tile * 16 + (lane >> 2) + 8 * (i >> 1);
+                const int token = m * 8 + 2 * (lane & 3) + (i & 1);
+                if (row >= rows || token >= p.M) continue;
+                const int64_t n = n0 + row;
+                float g = acc[m][i], u = up[i];
+                if (bias != nullptr) {
+                    g += OutT<TOut>::load(bias + n);
+                    u += OutT<TOut>::load(bias + p.N + n);
+                }
+                if (p.P != nullptr) {
+                    OutT<TOut>::store(static_cast<TOut*>(p.P) + token * p.ldp + n, g);
+                    OutT<TOut>::store(static_cast<TOut*>(p.P) + token * p.ldp + p.N + n, u);
+                }
+                switch (p.act) {
+                case DGA_SILU: g = act_value<DGA_SILU, true>(g); break;
+                case DGA_GELU: g = act_value<DGA_GELU, true>(g); break;
+                case DGA_GELU_TANH: g = act_value<DGA_GELU_TANH, true>(g); break;
+                case DGA_RELU: g = act_value<DGA_RELU, true>(g); break;
+                default: g = act_value<DGA_SIGMOID, true>(g); break;
+                }
+                OutT<TOut>::store(static_cast<TOut*>(p.Y) + token * p.ldy + n, g * u);
+            }
+        }
+        return;
+    }
     if (!active || khalf == 1 || *abort_flag) return;
 
     // D fragment of n-tile m: acc[m][2h + j] is weight row g + 8h of the
@@ -342,10 +401,10 @@ int64_t skinny_ctas(int64_t N, int sm_count) {
     return std::max<int64_t>(1, std::min(waves * sms, (N + 15) / 16));
 }
 
-template <bool kBf16, int MT, typename TOut>
+template <bool kBf16, int MT, typename TOut, bool kGated = false>
 cudaError_t launch_mt(const CUtensorMap& lo, const CUtensorMap& hi, const CUtensorMap& x,
                       const Params& p, int smem, cudaStream_t s) {
-    auto kern = skinny_kernel<kBf16, MT, TOut>;
+    auto kern = skinny_kernel<kBf16, MT, TOut, kGated>;
     // the most that any launch takes, not this one's share: another host
     // thread's launch may come between the two calls
     constexpr int kMostSmem = static_cast<int>(kRingBudget + kBarrierBytes + kRedBytes + 1024);
@@ -419,6 +478,43 @@ cudaError_t skinny_launch(const GemmArgs& a, const DeviceInfo& dev, int* launche
     else e = cudaErrorInvalidValue;
     if (e == cudaSuccess) ++*launches;
     return e;
+}
+
+bool gated_skinny_supports(const GatedArgs& a) {
+    return a.dtype != DGA_F32 && a.M >= 1 && a.M <= kXRows && a.K >= 1 && a.ldx % 8 == 0 && a.ldw % 8 == 0 && aligned(a.X, 16) &&
+           aligned(a.W, 16) && encode_fn() != nullptr;
+}
+
+cudaError_t gated_skinny_launch(const GatedArgs& a, const DeviceInfo& dev) {
+    constexpr int kMostGate = kMaxRows / 2;
+    Params p{};
+    p.M = a.M, p.N = a.F, p.K = a.K;
+    p.Y = a.H, p.ldy = a.ldh;
+    p.P = a.P, p.ldp = a.ldp;
+    p.act = a.act;
+    p.bias = a.bias;
+    // whole waves, as skinny_ctas
+    const int64_t least = (a.F + kMostGate - 1) / kMostGate, waves = (least + dev.sm_count - 1) / dev.sm_count;
+    p.ctas = std::min(waves * dev.sm_count, (a.F + 15) / 16);
+    if (p.ctas > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    p.rows_lo = static_cast<uint32_t>(a.F / p.ctas);
+    const uint32_t rows_hi = std::min<uint32_t>(p.rows_lo + 1, kMostGate);
+    p.w_box_bytes = kMaxRows * kBoxK * 2;
+    p.stages = std::min<uint32_t>(kMaxStages, kRingBudget / stage_bytes(p.w_box_bytes));
+    p.n_kstages = static_cast<uint32_t>((a.K + kBoxK * kBoxesPerStage - 1) / (kBoxK * kBoxesPerStage));
+    const int smem = static_cast<int>(p.stages * stage_bytes(p.w_box_bytes) + kBarrierBytes + kRedBytes + 1024);
+    if (smem > dev.max_smem_optin) return cudaErrorInvalidConfiguration;
+    const bool bf = a.dtype == DGA_BF16;
+    CUtensorMap lo, hi, x;
+    cudaError_t e = make_map(&lo, a.W, 2 * a.F, a.K, a.ldw, p.rows_lo, bf);
+    if (e == cudaSuccess) e = make_map(&hi, a.W, 2 * a.F, a.K, a.ldw, rows_hi, bf);
+    if (e == cudaSuccess) e = make_map(&x, a.X, a.M, a.K, a.ldx, kXRows, bf);
+    if (e != cudaSuccess) return e;
+    if (bf)
+        return a.M <= 8 ? launch_mt<true, 1, __nv_bfloat16, true>(lo, hi, x, p, smem, a.stream)
+                        : launch_mt<true, 2, __nv_bfloat16, true>(lo, hi, x, p, smem, a.stream);
+    return a.M <= 8 ? launch_mt<false, 1, __half, true>(lo, hi, x, p, smem, a.stream)
+                    : launch_mt<false, 2, __half, true>(lo, hi, x, p, smem, a.stream);
 }
 
 cudaError_t skinny_status_take(int* status) {

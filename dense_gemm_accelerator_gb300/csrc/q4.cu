@@ -100,22 +100,6 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// Rows of 16-bit values to rows of whole 16 bytes, eight values to a thread, zero
-// past the row's end.
-__global__ void __launch_bounds__(256)
-    copy_rows_kernel(int64_t rows, int64_t cols, const uint16_t* __restrict__ X, int64_t ldx, uint16_t* __restrict__ Y, int64_t ldy) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t pieces = ldy / 8, total = rows * pieces;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t row = i / pieces, k = (i - row * pieces) * 8;
-        uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (k + j < cols) w[j / 2] |= static_cast<uint32_t>(__ldg(X + row * ldx + k + j)) << (16 * (j & 1));
-        *reinterpret_cast<uint4*>(Y + row * ldy + k) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-}
-
 int group_shift(int group) { return group == 32 ? 5 : group == 64 ? 6 : 7; }
 
 template <typename Fn>
@@ -153,13 +137,6 @@ cudaError_t q4_quantize_launch(int in_dtype, int scale_dtype, int64_t rows, int6
             return cudaGetLastError();
         });
     });
-}
-
-cudaError_t copy_rows_launch(int64_t rows, int64_t cols, const void* X, int64_t ldx, void* Y, int64_t ldy, const DeviceInfo& dev,
-                             cudaStream_t stream) {
-    copy_rows_kernel<<<blocks_for(rows * (ldy / 8), 256, dev), 256, 0, stream>>>(rows, cols, static_cast<const uint16_t*>(X), ldx,
-                                                                                static_cast<uint16_t*>(Y), ldy);
-    return cudaGetLastError();
 }
 
 cudaError_t q4_dequantize_launch(int scale_dtype, int out_dtype, int64_t rows, int64_t cols, const Q4Matrix& q, void* Y,

@@ -34,7 +34,7 @@ def _gated(**over):
     (dict(X=None), -6), (dict(X=P[0] + 1), -6), (dict(ldx=15), -7), (dict(W=None), -8), (dict(ldw=15), -9), (dict(bias=P[4] + 1), -10),
     (dict(H=None), -11), (dict(H=P[2] + 1), -11), (dict(ldh=7), -12), (dict(P=P[5] + 1, ldp=16), -13), (dict(P=P[5], ldp=15), -14),
     (dict(workspace=None), -15), (dict(workspace=P[3] + 8), -15),
-    (dict(H=P[0]), 6), (dict(H=P[1] + 32), 6), (dict(P=P[2] + 2, ldp=16), 6), (dict(bias=P[2]), 6), (dict(workspace=P[1]), 6),
+    (dict(H=P[0]), 6), (dict(H=P[1] + 32), 6), (dict(P=P[2] + 2, ldp=16), 6), (dict(bias=P[2]), 6), (dict(workspace=P[1], dtype=gen.F32), 6),
     (dict(M=0, X=None, W=None, H=None), 0), (dict(F=0, W=None, H=None), 0)])
 def test_gated_arguments(over, code):
     assert _gated(M=over.get("M", 40), **{k: v for k, v in over.items() if k != "M"}) == code
