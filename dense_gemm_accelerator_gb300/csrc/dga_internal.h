@@ -223,7 +223,7 @@ struct Q4Matrix {
 cudaError_t q4_quantize_launch(int in_dtype, int scale_dtype, int64_t rows, int64_t cols, const void* W, int64_t ldw,
                                const Q4Matrix& q, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t q4_dequantize_launch(int scale_dtype, int out_dtype, int64_t rows, int64_t cols, const Q4Matrix& q, void* Y,
-                                 int64_t ldy, const DeviceInfo& dev, cudaStream_t stream);
+                                 int64_t ldy, cudaStream_t stream);
 
 // Rows of 16-bit values copied to rows that start on 16 bytes (ldy a multiple of 8).
 cudaError_t copy_rows_launch(int64_t rows, int64_t cols, const void* X, int64_t ldx, void* Y, int64_t ldy, const DeviceInfo& dev,

@@ -192,7 +192,7 @@ cudaError_t q4_by_values(const Q4Plan& pl, int dtype, int out, int64_t M, int64_
                          cudaStream_t s, int* launches) {
     cudaError_t e = cudaSuccess;
     if (K > 0) {
-        e = q4_dequantize_launch(dtype, dtype, N, K, q, ws, pl.ldv, dev, s);
+        e = q4_dequantize_launch(dtype, dtype, N, K, q, ws, pl.ldv, s);
         if (e != cudaSuccess) return e;
         ++*launches;
     }
@@ -401,7 +401,7 @@ int dga_q4_dequantize(dga_dtype scale_dtype, dga_dtype out_dtype, int64_t rows, 
     DeviceInfo dev;
     const int st = device(&dev);
     if (st != DGA_OK) return st;
-    const cudaError_t e = q4_dequantize_launch(scale_dtype, out_dtype, rows, cols, q, Y, ldy, dev, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = q4_dequantize_launch(scale_dtype, out_dtype, rows, cols, q, Y, ldy, reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return note_cuda_error(e);
     set_last_launches(1);
     return DGA_OK;

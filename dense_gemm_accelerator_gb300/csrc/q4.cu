@@ -69,33 +69,48 @@ __global__ void __launch_bounds__(256)
     }
 }
 
-// A thread 8 values: one word of codes.
+// A thread a word of codes, eight values; the grid's y walks the rows, four at a
+// time with their loads together (a row's division out of one index took longer
+// than the copy).
 template <typename TS, typename T, bool kVec>
 __global__ void __launch_bounds__(256)
     q4_dequantize_kernel(int64_t rows, int64_t cols, Q4Matrix q, int shift, T* __restrict__ Y, int64_t ldy) {
-    const int64_t words = (cols + 7) / 8, total = rows * words;
-    const TS* scales = static_cast<const TS*>(q.scales);
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total; i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t row = i / words, k = (i - row * words) * 8, group = k >> shift;
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(q.codes + row * q.ld + k / 2);
-        const float s = OutT<TS>::load(scales + row * q.ld_scales + group);
-        const float z = q.zeros ? static_cast<float>(q.zeros[row * q.ld_zeros + group] & 15) : 8.0f;
-        float v[8];
+    constexpr int kRows = 4;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t k = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+    if (k >= cols) return;
+    const int64_t group = k >> shift;
+    const TS* scales = static_cast<const TS*>(q.scales) + group;
+    for (int64_t row0 = static_cast<int64_t>(blockIdx.y) * kRows; row0 < rows; row0 += static_cast<int64_t>(gridDim.y) * kRows) {
+        uint32_t c[kRows];
+        float s[kRows], z[kRows];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (static_cast<float>((c >> (4 * j)) & 15u) - z) * s;
-        T* out = Y + row * ldy + k;
-        if (kVec && k + 8 <= cols) {
-            if constexpr (sizeof(T) == 2) {
-                Pack<T, 8>::store(out, v);
+        for (int r = 0; r < kRows; ++r) {
+            const int64_t row = min(row0 + r, rows - 1);
+            c[r] = __ldg(reinterpret_cast<const uint32_t*>(q.codes + row * q.ld + k / 2));
+            s[r] = OutT<TS>::load(scales + row * q.ld_scales);
+            z[r] = q.zeros ? static_cast<float>(__ldg(q.zeros + row * q.ld_zeros + group) & 15) : 8.0f;
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+            if (row0 + r >= rows) break;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = (static_cast<float>((c[r] >> (4 * j)) & 15u) - z[r]) * s[r];
+            T* out = Y + (row0 + r) * ldy + k;
+            if (kVec && k + 8 <= cols) {
+                if constexpr (sizeof(T) == 2) {
+                    Pack<T, 8>::store(out, v);
+                } else {
+                    const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
+                    Pack<T, 4>::store(out, a);
+                    Pack<T, 4>::store(out + 4, b);
+                }
             } else {
-                const float a[4] = {v[0], v[1], v[2], v[3]}, b[4] = {v[4], v[5], v[6], v[7]};
-                Pack<T, 4>::store(out, a);
-                Pack<T, 4>::store(out + 4, b);
-            }
-        } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (k + j < cols) OutT<T>::store(out + j, v[j]);
+                for (int j = 0; j < 8; ++j)
+                    if (k + j < cols) OutT<T>::store(out + j, v[j]);
+            }
         }
     }
 }
@@ -140,8 +155,8 @@ cudaError_t q4_quantize_launch(int in_dtype, int scale_dtype, int64_t rows, int6
 }
 
 cudaError_t q4_dequantize_launch(int scale_dtype, int out_dtype, int64_t rows, int64_t cols, const Q4Matrix& q, void* Y,
-                                 int64_t ldy, const DeviceInfo& dev, cudaStream_t stream) {
-    const unsigned grid = blocks_for(rows * ((cols + 7) / 8), 256, dev);
+                                 int64_t ldy, cudaStream_t stream) {
+    const dim3 grid(static_cast<unsigned>((cols + 2047) / 2048), static_cast<unsigned>(std::min<int64_t>((rows + 3) / 4, 65535)));
     const bool vec = aligned(Y, 16) && ldy % 8 == 0;
     return for_half(scale_dtype, [&](auto ts) {
         return for_float(out_dtype, [&](auto t) {

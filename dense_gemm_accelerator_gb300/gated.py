@@ -12,7 +12,7 @@ import functools
 
 import torch
 
-from . import DgaError, _elsewhere, _on_device, _raw_stream, lib
+from . import F32, DgaError, _current_device, _elsewhere, _on_device, _raw_stream, lib
 from .mx import _CODE, _rows_of, on_stream
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
@@ -73,36 +73,41 @@ def gated_forward(X, W, bias=None, activation="silu", save=False, H=None, P=None
     H, P and the workspace are allocated unless given; a P that is given is written."""
     if stream is not None:
         return on_stream(stream, X.device, gated_forward, X, W, bias, activation, save, H, P, workspace)
-    dtype, dev = X.dtype, X.device
-    code, act = _CODE.get(dtype), activation_code(activation)
+    dtype, act, d = X.dtype, activation_code(activation), X.get_device()
+    code = _CODE.get(dtype)
     if code is None:
         raise TypeError("X must be float32, bfloat16 or float16")
-    if not X.is_cuda:
+    if d < 0:
         raise ValueError("X must be a CUDA tensor")
-    if W.dtype is not dtype or W.device != dev:
-        _check(W, "W", dtype, dev)
-    if _elsewhere(dev):
-        return _on_device(dev, gated_forward, X, W, bias, activation, save, H, P, workspace)
+    if W.dtype is not dtype or W.get_device() != d:
+        _check(W, "W", dtype, X.device)
+    if d != _current_device():
+        return _on_device(X.device, gated_forward, X, W, bias, activation, save, H, P, workspace)
     M, K, ldx = _rows_of(X, "X")
     N, k, ldw = _rows_of(W, "W")
     if k != K or N % 2:
         raise ValueError(f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)} (an even number of rows of X's length)")
     F = N // 2
-    H, ldh = result(H, M, F, dtype, dev, "H")
+    if H is None:
+        H, ldh = torch.empty((M, F), dtype=dtype, device=d), F or 1
+    else:
+        H, ldh = result(H, M, F, dtype, X.device, "H")
     save = save or P is not None
     p, ldp = None, 0
     if save:
-        P, ldp = result(P, M, N, dtype, dev, "P")
+        P, ldp = result(P, M, N, dtype, X.device, "P")
         p = P.data_ptr()
     x, w = X.data_ptr(), W.data_ptr()
     if workspace is None:
-        have = _forward_workspace(code, M, F, K, odd_where_off(ldx, x), odd_where_off(ldw, w), 1 if save else 0)
+        have = 0
+        if ldx % 8 or ldw % 8 or (x | w) % 16 or code == F32 or not K:  # else none is needed
+            have = _forward_workspace(code, M, F, K, odd_where_off(ldx, x), odd_where_off(ldw, w), 1 if save else 0)
         if have:
-            workspace = torch.empty(have, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(have, dtype=torch.uint8, device=d)
     else:
         have = workspace.numel() * workspace.element_size()
-    st = lib().dga_gated(code, act, M, F, K, x, ldx, w, ldw, vector(bias, N, dtype, dev), H.data_ptr(), ldh, p, ldp,
-                         workspace.data_ptr() if have else None, have, _raw_stream(dev.index))
+    st = lib().dga_gated(code, act, M, F, K, x, ldx, w, ldw, None if bias is None else vector(bias, N, dtype, X.device), H.data_ptr(),
+                         ldh, p, ldp, workspace.data_ptr() if have else None, have, _raw_stream(d))
     if st:
         raise DgaError(st, "dga_gated")
     return (H, P) if save else H

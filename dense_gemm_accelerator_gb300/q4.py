@@ -12,10 +12,11 @@ import functools
 
 import torch
 
-from . import F32, DgaError, _check_lines, _elsewhere, _on_device, _raw_stream, lib
-from .gated import activation_code, odd_where_off, result, vector
+from . import F32, DgaError, _check_lines, _current_device, _elsewhere, _on_device, _raw_stream, lib
+from .gated import activation_code, result, vector
 from .mx import _CODE, _TORCH, _rows_of, on_stream
 
+_U8 = torch.uint8
 _HALF = {torch.bfloat16: _CODE[torch.bfloat16], torch.float16: _CODE[torch.float16]}
 
 
@@ -56,24 +57,24 @@ class Q4Tensor:
         return f"Q4Tensor({self.rows}x{self.cols}, groups of {self.group}, {self.codes.device})"
 
 
-def _arguments(Q, dev):
-    """(rows, code of the scales' type, the weight's arguments of the C calls)."""
-    codes, scales, zeros = Q.codes, Q.scales, Q.zeros
-    rows, width = codes.shape
-    (n, groups), (ls, step) = scales.shape, scales.stride()
-    lc, one = codes.stride()
+def _arguments(Q, d):
+    """(rows, code of the scales' type, the weight's arguments of the C calls); d: the
+    number of the device that it must be on.  (The checks cost a call 2 us.)"""
+    codes, scales, zeros, cols, group = Q.codes, Q.scales, Q.zeros, Q.cols, Q.group
     code = _HALF.get(scales.dtype)
     if code is None:
         raise TypeError("scales must be bfloat16 or float16")
-    if codes.dtype is not torch.uint8 or (zeros is not None and zeros.dtype is not torch.uint8):
-        raise TypeError("codes and zeros must be uint8")
-    cols, group = Q.cols, Q.group
-    if group not in (32, 64, 128):
+    if codes.dtype is not _U8:
+        raise TypeError("codes must be uint8")
+    if group != 128 and group != 64 and group != 32:
         raise ValueError("groups have 32, 64 or 128 columns")
-    if n != rows or groups != -(-cols // group) or width < (cols + 31) // 32 * 16:
+    (rows, width), (lc, one) = codes.shape, codes.stride()
+    shape, (ls, step) = scales.shape, scales.stride()
+    groups = (cols + group - 1) // group
+    if shape[0] != rows or shape[1] != groups or width < (cols + 31) // 32 * 16:
         raise ValueError(f"a {rows} x {cols} weight in groups of {group} has codes ({rows}, {(cols + 31) // 32 * 16}) and "
-                         f"scales ({rows}, {-(-cols // group)}), not {tuple(codes.shape)} and {tuple(scales.shape)}")
-    if codes.device != dev or scales.device != dev:
+                         f"scales ({rows}, {groups}), not {tuple(codes.shape)} and {tuple(shape)}")
+    if codes.get_device() != d or scales.get_device() != d:
         raise ValueError("the weight's tensors must be on the device of X")
     if (one != 1 and width > 1) or (step != 1 and groups > 1):
         raise ValueError("codes and scales must be row-major")
@@ -83,18 +84,19 @@ def _arguments(Q, dev):
     if ls < groups:
         _check_lines("scales", rows, groups, ls)
         ls = groups
-    z, lz = None, 0
-    if zeros is not None:
-        if zeros.shape != scales.shape or zeros.device != dev:
-            raise ValueError("zeros must have the shape and device of the scales")
-        lz, step = zeros.stride()
-        if step != 1 and groups > 1:
-            raise ValueError("zeros must be row-major")
-        if lz < groups:
-            _check_lines("zeros", rows, groups, lz)
-            lz = groups
-        z = zeros.data_ptr()
-    return rows, code, codes.data_ptr(), lc, scales.data_ptr(), ls, z, lz
+    if zeros is None:
+        return rows, code, codes.data_ptr(), lc, scales.data_ptr(), ls, None, 0
+    if zeros.dtype is not _U8:
+        raise TypeError("zeros must be uint8")
+    if zeros.shape != shape or zeros.get_device() != d:
+        raise ValueError("zeros must have the shape and device of the scales")
+    lz, step = zeros.stride()
+    if step != 1 and groups > 1:
+        raise ValueError("zeros must be row-major")
+    if lz < groups:
+        _check_lines("zeros", rows, groups, lz)
+        lz = groups
+    return rows, code, codes.data_ptr(), lc, scales.data_ptr(), ls, zeros.data_ptr(), lz
 
 
 def q4_quantize(W, group=128, zeros=True, scale_dtype=None, stream=None):
@@ -135,9 +137,11 @@ def q4_dequantize(Q, out_dtype=F32, stream=None):
     if stream is not None:
         return on_stream(stream, Q.device, q4_dequantize, Q, out_dtype)
     dev = Q.codes.device
+    if dev.type != "cuda":
+        raise ValueError("Q must be on a CUDA device")
     if _elsewhere(dev):
         return _on_device(dev, q4_dequantize, Q, out_dtype)
-    rows, code, c, lc, s, ls, z, lz = _arguments(Q, dev)
+    rows, code, c, lc, s, ls, z, lz = _arguments(Q, dev.index)
     Y = torch.empty((rows, Q.cols), dtype=_TORCH[out_dtype], device=dev)
     st = lib().dga_q4_dequantize(code, out_dtype, rows, Q.cols, Q.group, c, lc, s, ls, z, lz, Y.data_ptr(), Q.cols or 1,
                                  _raw_stream(dev.index))
@@ -148,36 +152,47 @@ def q4_dequantize(Q, out_dtype=F32, stream=None):
 
 def _rows_for(X, Q):
     """(M, K, ldx) of activations for a weight."""
-    if not X.is_cuda:
-        raise ValueError("X must be a CUDA tensor")
     if X.dtype is not Q.scales.dtype:
         raise TypeError("X must have the type of the weight's scales (bfloat16 or float16)")
-    M, K, ldx = _rows_of(X, "X")
-    if K != Q.cols:
-        raise ValueError(f"shape mismatch: X {tuple(X.shape)}, the weight {Q.shape}")
-    return M, K, ldx
+    shape = X.shape
+    if len(shape) != 2 or shape[1] != Q.cols:
+        raise ValueError(f"shape mismatch: X {tuple(shape)}, the weight {Q.shape}")
+    M, K = shape
+    ldx, step = X.stride()
+    if step != 1 and K > 1:
+        raise ValueError("X must be row-major")
+    if ldx < K:
+        _check_lines("X", M, K, ldx)
+    return M, K, ldx if ldx > K else K or 1
 
 
 def q4_linear_forward(X, W, bias=None, Y=None, workspace=None, stream=None):
     """Y = X @ W^T + bias for X [batch, in] and a 4-bit weight W, a Q4Tensor [out, in];
-    X, the scales, the bias and Y of one type, bfloat16 or float16."""
+    X, the scales, the bias and Y of one type, bfloat16 or float16.  Up to 64 rows
+    multiply the codes as they are; more go through W's values rounded to X's type."""
     if stream is not None:
         return on_stream(stream, X.device, q4_linear_forward, X, W, bias, Y, workspace)
-    dev, dtype = X.device, X.dtype
+    d = X.get_device()
+    if d < 0:
+        raise ValueError("X must be a CUDA tensor")
+    if d != _current_device():
+        return _on_device(X.device, q4_linear_forward, X, W, bias, Y, workspace)
     M, K, ldx = _rows_for(X, W)
-    if _elsewhere(dev):
-        return _on_device(dev, q4_linear_forward, X, W, bias, Y, workspace)
-    N, code, c, lc, s, ls, z, lz = _arguments(W, dev)
-    Y, ldy = result(Y, M, N, dtype, dev, "Y")
+    N, code, c, lc, s, ls, z, lz = _arguments(W, d)
+    if Y is None:
+        Y, ldy = torch.empty((M, N), dtype=X.dtype, device=d), N or 1
+    else:
+        Y, ldy = result(Y, M, N, X.dtype, X.device, "Y")
     x = X.data_ptr()
     if workspace is None:
-        have = _linear_workspace(code, M, N, K, odd_where_off(ldx, x))
+        have = _linear_workspace(code, M, N, K, ldx if x % 16 == 0 else ldx | 1) if M > 64 or ldx % 8 or x % 16 or not K else 0
         if have:
-            workspace = torch.empty(have, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(have, dtype=_U8, device=d)
     else:
         have = workspace.numel() * workspace.element_size()
-    st = lib().dga_q4_linear(code, M, N, K, W.group, x, ldx, c, lc, s, ls, z, lz, vector(bias, N, dtype, dev), Y.data_ptr(),
-                             ldy, workspace.data_ptr() if have else None, have, _raw_stream(dev.index))
+    st = lib().dga_q4_linear(code, M, N, K, W.group, x, ldx, c, lc, s, ls, z, lz,
+                             None if bias is None else vector(bias, N, X.dtype, X.device), Y.data_ptr(), ldy,
+                             workspace.data_ptr() if have else None, have, _raw_stream(d))
     if st:
         raise DgaError(st, "dga_q4_linear")
     return Y
@@ -189,24 +204,30 @@ def q4_gated_forward(X, W, bias=None, activation="silu", H=None, workspace=None,
     activations as for gated_forward."""
     if stream is not None:
         return on_stream(stream, X.device, q4_gated_forward, X, W, bias, activation, H, workspace)
-    dev, dtype, act = X.device, X.dtype, activation_code(activation)
+    d, act = X.get_device(), activation_code(activation)
+    if d < 0:
+        raise ValueError("X must be a CUDA tensor")
+    if d != _current_device():
+        return _on_device(X.device, q4_gated_forward, X, W, bias, activation, H, workspace)
     M, K, ldx = _rows_for(X, W)
-    if _elsewhere(dev):
-        return _on_device(dev, q4_gated_forward, X, W, bias, activation, H, workspace)
-    N, code, c, lc, s, ls, z, lz = _arguments(W, dev)
+    N, code, c, lc, s, ls, z, lz = _arguments(W, d)
     if N % 2:
         raise ValueError("the weight must have an even number of rows")
     F = N // 2
-    H, ldh = result(H, M, F, dtype, dev, "H")
+    if H is None:
+        H, ldh = torch.empty((M, F), dtype=X.dtype, device=d), F or 1
+    else:
+        H, ldh = result(H, M, F, X.dtype, X.device, "H")
     x = X.data_ptr()
     if workspace is None:
-        have = _gated_workspace(code, M, F, K, odd_where_off(ldx, x))
+        have = _gated_workspace(code, M, F, K, ldx if x % 16 == 0 else ldx | 1) if M > 64 or ldx % 8 or x % 16 or not K else 0
         if have:
-            workspace = torch.empty(have, dtype=torch.uint8, device=dev)
+            workspace = torch.empty(have, dtype=_U8, device=d)
     else:
         have = workspace.numel() * workspace.element_size()
-    st = lib().dga_q4_gated(code, act, M, F, K, W.group, x, ldx, c, lc, s, ls, z, lz, vector(bias, N, dtype, dev),
-                            H.data_ptr(), ldh, workspace.data_ptr() if have else None, have, _raw_stream(dev.index))
+    st = lib().dga_q4_gated(code, act, M, F, K, W.group, x, ldx, c, lc, s, ls, z, lz,
+                            None if bias is None else vector(bias, N, X.dtype, X.device), H.data_ptr(), ldh,
+                            workspace.data_ptr() if have else None, have, _raw_stream(d))
     if st:
         raise DgaError(st, "dga_q4_gated")
     return H

@@ -159,7 +159,7 @@ def test_python_refusals():
                        (dga.Q4Tensor(20, 32, codes, scales.expand(3, 1).t().expand(3, 3)[:, :1].t(), None), ValueError),
                        (dga.Q4Tensor(20, 32, codes[:1].expand(3, 16), scales), ValueError)):
         with pytest.raises(error):
-            _arguments(bad, codes.device)
+            _arguments(bad, codes.get_device())
 
 
 # ---- the reference ------------------------------------------------------------------
