@@ -484,16 +484,17 @@ int dga_last_launch_count(void) { return t_last_launches; }
 int dga_sync_status(dga_stream_t stream) {
     cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return fail_cuda(e);
-    int st = 0, st_skinny = 0, st_spmv = 0, st_mx = 0, st_ns = 0, st_q4 = 0, st_gated = 0;
+    int st = 0, st_skinny = 0, st_spmv = 0, st_mx = 0, st_ns = 0, st_q4 = 0, st_q4_tc = 0, st_gated = 0;
     e = tc_status_take(&st);
     if (e == cudaSuccess) e = skinny_status_take(&st_skinny);
     if (e == cudaSuccess) e = spmv_status_take(&st_spmv);
     if (e == cudaSuccess) e = mx_status_take(&st_mx);
     if (e == cudaSuccess) e = ns_status_take(&st_ns);
     if (e == cudaSuccess) e = q4_status_take(&st_q4);
+    if (e == cudaSuccess) e = q4_tc_status_take(&st_q4_tc);
     if (e == cudaSuccess) e = gated_status_take(&st_gated);
     if (e != cudaSuccess) return fail_cuda(e);
-    if (st != 0 || st_skinny != 0 || st_mx != 0 || st_ns != 0 || st_q4 != 0 || st_gated != 0) return DGA_ERR_DEVICE_TIMEOUT;
+    if (st != 0 || st_skinny != 0 || st_mx != 0 || st_ns != 0 || st_q4 != 0 || st_q4_tc != 0 || st_gated != 0) return DGA_ERR_DEVICE_TIMEOUT;
     return st_spmv != 0 ? DGA_ERR_BAD_INDEX : DGA_OK;
 }
 

@@ -28,6 +28,10 @@ struct GemmArgs {
     void* ws;
     size_t ws_bytes;
     cudaStream_t stream;
+    // cut the tiles along K further than the GEMM entry points do, which keep the
+    // order of their sums: also on the tensor cores where the tiles are fewer than
+    // the clusters
+    int deep;
 };
 
 struct DeviceInfo {
@@ -229,13 +233,17 @@ cudaError_t q4_dequantize_launch(int scale_dtype, int out_dtype, int64_t rows, i
 cudaError_t copy_rows_launch(int64_t rows, int64_t cols, const void* X, int64_t ldx, void* Y, int64_t ldy, const DeviceInfo& dev,
                              cudaStream_t stream);
 
-// Y (M x N) = X W^T + bias for up to kQ4Rows rows (that start on 16 bytes) and K >= 1, or (gated) the gated
+// Y (M x N) = X W^T + bias for up to 64 rows (that start on 16 bytes) and K >= 1, or (gated) the gated
 // layer's M x N result on a weight of 2N rows.
-constexpr int64_t kQ4Rows = 64;
 cudaError_t q4_rows_launch(int dtype, int act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const Q4Matrix& q,
                            const void* bias, void* Y, int64_t ldy, bool gated, const DeviceInfo& dev, cudaStream_t stream);
 // Reads and clears this device's status word of these products.
 cudaError_t q4_status_take(int* status);
+// The same for any number of rows, on the weight's values rounded to X's type; the most it is given.
+constexpr int64_t kQ4TensorRows = 1024, kQ4GatedTensorRows = 512;
+cudaError_t q4_tc_launch(int dtype, int act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const Q4Matrix& q,
+                         const void* bias, void* Y, int64_t ldy, bool gated, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t q4_tc_status_take(int* status);
 
 // The GEMM as dga_gemm_general runs it, for validated arguments: the chosen
 // family's launch, and the workspace it would use.

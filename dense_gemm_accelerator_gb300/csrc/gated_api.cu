@@ -80,6 +80,7 @@ GemmArgs product(int in, int out, int layout_a, int layout_b, int64_t M, int64_t
     g.ldc = ldc;
     g.bias = bias;
     g.stream = s;
+    g.deep = 1;
     return g;
 }
 
@@ -147,20 +148,32 @@ void q4_arrays(Arrays& a, const Q4Matrix& q, int64_t N, int64_t K, bool written)
     add(q.zeros, q.ld_zeros, groups);
 }
 
-// Scratch of a product on a 4-bit weight.  Up to kQ4Rows rows: X in rows that
-// start on 16 bytes, where it has none.  More: the weight's values, what a gated
-// one keeps of P, the product's own.
+// How a product on a 4-bit weight goes, and its scratch: X in rows that start on 16
+// bytes, where a kernel needs them and it has none; the weight's values; a gated
+// one's P (K = 0); the library's product's own.
+//
+//   rows    q4_rows, on the codes as they are: few rows.  8192 x 8192 in groups of 128,
+//           32 rows: 24.5 us, q4_tc 22.4; 4096 x 4096: 8.7 and 10.0.  48 rows, 8192 x
+//           8192: 45 and 23; 4096 x 4096: 12.7 and 10.4; 2048 x 2048: 5.4 and 7.2.
+//   tensor  q4_tc, which makes the values as it goes, once for each 256 (gated: 128)
+//           rows of X.  1024 rows of 8192 x 8192: 112 us, through the values 137;
+//           2048: 223 and 201.  A gated one's values go to the fused layer:
+//           8192 gate and up rows, K = 4096, 512 rows: 46 us on the codes, 63 through
+//           the values; 1024: 90 and 65.
+//   else the values are written out first.
 struct Q4Plan {
-    bool few;
-    int64_t ldv, values, held, gemm;
-    int64_t total() const { return values + held + gemm; }
+    bool rows, tensor;
+    int64_t ldv, x, values, held, gemm;
+    int64_t total() const { return x + values + held + gemm; }
 };
 Q4Plan q4_plan(int dtype, int64_t M, int64_t N, int64_t K, int64_t ldx, bool gated, const void* X) {
     Q4Plan pl{};
     pl.ldv = round_up(K, 8);
-    pl.few = M <= kQ4Rows && K > 0;
-    if (pl.few) {
-        if (ldx % 8 != 0 || (X && !aligned(X, 16))) pl.values = round_up(M * pl.ldv * 2, 256);
+    pl.rows = K > 0 && (M <= 32 || (M <= 64 && N * K <= (int64_t{1} << 22)));
+    pl.tensor = K > 0 && !pl.rows && M <= (gated ? kQ4GatedTensorRows : kQ4TensorRows);
+    if (pl.rows || pl.tensor || (gated && K > 0)) {
+        if (ldx % 8 != 0 || (X && !aligned(X, 16))) pl.x = round_up(M * pl.ldv * 2, 256);
+        if (!pl.rows && !pl.tensor) pl.values = round_up(N * pl.ldv * 2, 256);
         return pl;
     }
     pl.values = round_up(N * pl.ldv * 2, 256);
@@ -170,18 +183,30 @@ Q4Plan q4_plan(int dtype, int64_t M, int64_t N, int64_t K, int64_t ldx, bool gat
     return pl;
 }
 
-// Few rows: Y, or (gated) the gated layer's result.
-cudaError_t q4_by_rows(const Q4Plan& pl, int dtype, int act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
-                       const Q4Matrix& q, const void* bias, void* Y, int64_t ldy, bool gated, uint8_t* ws, const DeviceInfo& dev,
-                       cudaStream_t s, int* launches) {
-    if (pl.values) {
-        const cudaError_t e = copy_rows_launch(M, K, X, ldx, ws, pl.ldv, dev, s);
+// Y, or (gated, N its outputs) the gated layer's result, by q4_rows, q4_tc or the gated
+// layer's kernel on the values.
+cudaError_t q4_by_kernel(const Q4Plan& pl, int dtype, int act, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                         const Q4Matrix& q, const void* bias, void* Y, int64_t ldy, bool gated, uint8_t* ws, const DeviceInfo& dev,
+                         cudaStream_t s, int* launches) {
+    cudaError_t e = cudaSuccess;
+    if (pl.x) {
+        e = copy_rows_launch(M, K, X, ldx, ws, pl.ldv, dev, s);
         if (e != cudaSuccess) return e;
         ++*launches;
         X = ws;
         ldx = pl.ldv;
     }
-    const cudaError_t e = q4_rows_launch(dtype, act, M, N, K, X, ldx, q, bias, Y, ldy, gated, dev, s);
+    if (pl.rows) {
+        e = q4_rows_launch(dtype, act, M, N, K, X, ldx, q, bias, Y, ldy, gated, dev, s);
+    } else if (pl.tensor) {
+        e = q4_tc_launch(dtype, act, M, N, K, X, ldx, q, bias, Y, ldy, gated, dev, s);
+    } else {
+        e = q4_dequantize_launch(dtype, dtype, 2 * N, K, q, ws + pl.x, pl.ldv, s);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+        const GatedArgs g{dtype, act, M, N, K, X, ldx, ws + pl.x, pl.ldv, bias, Y, ldy, nullptr, 0, s};
+        e = gated_tc_supports(g) ? gated_tc_launch(g, dev) : cudaErrorNotSupported;
+    }
     if (e == cudaSuccess) ++*launches;
     return e;
 }
@@ -444,8 +469,8 @@ int dga_q4_linear(dga_dtype dtype, int64_t M, int64_t N, int64_t K, int group, c
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int launches = 0;
     cudaError_t e;
-    if (pl.few) {
-        e = q4_by_rows(pl, dtype, 0, M, N, K, X, ldx, q, bias, Y, ldy, false, static_cast<uint8_t*>(workspace), dev, s, &launches);
+    if (pl.rows || pl.tensor) {
+        e = q4_by_kernel(pl, dtype, 0, M, N, K, X, ldx, q, bias, Y, ldy, false, static_cast<uint8_t*>(workspace), dev, s, &launches);
     } else {
         e = q4_by_values(pl, dtype, dtype, M, N, K, X, ldx, q, bias, Y, ldy, static_cast<uint8_t*>(workspace), dev, s, &launches);
     }
@@ -492,8 +517,8 @@ int dga_q4_gated(dga_dtype dtype, dga_activation act, int64_t M, int64_t F, int6
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     int launches = 0;
     cudaError_t e;
-    if (pl.few) {
-        e = q4_by_rows(pl, dtype, act, M, F, K, X, ldx, q, bias, H, ldh, true, ws, dev, s, &launches);
+    if (K > 0) {
+        e = q4_by_kernel(pl, dtype, act, M, F, K, X, ldx, q, bias, H, ldh, true, ws, dev, s, &launches);
     } else {
         e = q4_by_values(pl, dtype, DGA_F32, M, 2 * F, K, X, ldx, q, nullptr, ws + pl.values, held_ld(F), ws, dev, s, &launches);
         if (e != cudaSuccess) return note_cuda_error(e);

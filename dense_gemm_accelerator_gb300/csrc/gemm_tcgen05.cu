@@ -1444,6 +1444,15 @@ uint32_t split_parts(uint32_t rem, uint32_t nc, uint32_t num_kb) {
     return best;
 }
 
+// Parts per tile where the tiles are fewer than the clusters (GemmArgs::deep):
+// as many as give each cluster one part, none shallower than kMinDeepKb.
+// A gated layer's gradient of X at 256 x 4096, K = 16384 has 16 tiles for 76
+// clusters: the layer's backward pass took 280 us with whole tiles, 234 with four parts each.
+constexpr uint32_t kMaxDeepSplits = 16, kMinDeepKb = 4;
+uint32_t deep_parts(uint32_t tiles, uint32_t nc, uint32_t num_kb) {
+    return std::max(1u, std::min({kMaxDeepSplits, nc / std::max(tiles, 1u), num_kb / kMinDeepKb}));
+}
+
 // The CTA-pair GEMM, and for floating point, when split_ws holds enough and a
 // split shortens the last, part-filled wave (split_parts), the split of that
 // wave's tiles along K into work units of their own and the reduce that adds
@@ -1451,15 +1460,15 @@ uint32_t split_parts(uint32_t rem, uint32_t nc, uint32_t num_kb) {
 template <uint32_t kFmt, bool kI8, typename TOut>
 cudaError_t launch_pair_kernel(const CUtensorMap& ma, const CUtensorMap& mb, const TcParams& p0,
                                const DeviceInfo& dev, cudaStream_t s, bool pdl, uint32_t* split_ws,
-                               size_t split_bytes, int* extra_launches) {
+                               size_t split_bytes, bool deep, int* extra_launches) {
     auto kern = tc_gemm_pair_kernel<kFmt, kI8, TOut>;
     const int smem = static_cast<int>(PairSmem<kI8 ? 8 : 4>::kLaunchBytes);
     const int threads = kI8 ? 576 : 192;
     if (smem > dev.max_smem_optin) return cudaErrorInvalidConfiguration;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    const int clusters = std::min<int64_t>(
-        p0.num_tiles, max_pair_clusters<kFmt, kI8, TOut>(kern, smem, threads, dev));
+    const int most = max_pair_clusters<kFmt, kI8, TOut>(kern, smem, threads, dev);
+    int clusters = std::min<int64_t>(p0.num_tiles, most);
     TcParams p = p0;
     p.full_tiles = p.num_tiles;
     p.splits = 1;
@@ -1474,6 +1483,15 @@ cudaError_t launch_pair_kernel(const CUtensorMap& ma, const CUtensorMap& mb, con
             p.splits = sp;
             p.num_units = p.full_tiles + rem * sp;
             p.partials = split_ws;
+        }
+    } else if (!kI8 && deep && split_ws != nullptr) {
+        const uint32_t sp = deep_parts(p.num_tiles, static_cast<uint32_t>(most), p.num_kb);
+        if (sp >= 2 && static_cast<size_t>(p.num_tiles) * sp * kSplitSlotBytes <= split_bytes) {
+            p.full_tiles = 0;
+            p.splits = sp;
+            p.num_units = p.num_tiles * sp;
+            p.partials = split_ws;
+            clusters = static_cast<int>(p.num_units);
         }
     }
     cudaLaunchConfig_t cfg = {};
@@ -1628,6 +1646,10 @@ size_t tc_workspace_wanted(const GemmArgs& a, int sm_count) {
     const int64_t tiles = ((a.M + 255) / 256) * ((a.N + kPairBN - 1) / kPairBN);
     const int64_t kb = (a.K + k_per_stage(a.in_dtype == DGA_TF32 ? kFmtTF32 : kFmtBF16) - 1) /
                        k_per_stage(a.in_dtype == DGA_TF32 ? kFmtTF32 : kFmtBF16);
+    if (a.deep && tiles <= sm_count / 2) {
+        const uint32_t sp = deep_parts(static_cast<uint32_t>(tiles), static_cast<uint32_t>(sm_count / 2), static_cast<uint32_t>(kb));
+        return sp >= 2 ? need + static_cast<size_t>(tiles) * sp * kSplitSlotBytes : need;
+    }
     if (tiles <= sm_count / 2 || kb < 2 * static_cast<int64_t>(kMinSplitKb)) return need;
     return need + static_cast<size_t>(2 * (sm_count / 2)) * kSplitSlotBytes;
 }
@@ -1747,14 +1769,14 @@ cudaError_t tc_launch(const GemmArgs& a, const DeviceInfo& dev, int* launches) {
     }
     int extra = 0;  // the split's reduce
 
-    if (i8 && pair) e = launch_pair_kernel<kFmtBF16, true, int32_t>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, &extra);
+    if (i8 && pair) e = launch_pair_kernel<kFmtBF16, true, int32_t>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, a.deep != 0, &extra);
     else if (i8) e = launch_kernel<kFmtBF16, true, kBnI8, int32_t>(ma, mb, p, dev, a.stream, pdl);
-    else if (tf32 && pair) e = launch_pair_kernel<kFmtTF32, false, float>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, &extra);
+    else if (tf32 && pair) e = launch_pair_kernel<kFmtTF32, false, float>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, a.deep != 0, &extra);
     else if (tf32) e = launch_kernel<kFmtTF32, false, kBnFloat, float>(ma, mb, p, dev, a.stream, pdl);
-    else if (pair && bf16 && a.out_dtype == DGA_F32) e = launch_pair_kernel<kFmtBF16, false, float>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, &extra);
-    else if (pair && bf16) e = launch_pair_kernel<kFmtBF16, false, __nv_bfloat16>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, &extra);
-    else if (pair && a.out_dtype == DGA_F32) e = launch_pair_kernel<kFmtF16, false, float>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, &extra);
-    else if (pair) e = launch_pair_kernel<kFmtF16, false, __half>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, &extra);
+    else if (pair && bf16 && a.out_dtype == DGA_F32) e = launch_pair_kernel<kFmtBF16, false, float>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, a.deep != 0, &extra);
+    else if (pair && bf16) e = launch_pair_kernel<kFmtBF16, false, __nv_bfloat16>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, a.deep != 0, &extra);
+    else if (pair && a.out_dtype == DGA_F32) e = launch_pair_kernel<kFmtF16, false, float>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, a.deep != 0, &extra);
+    else if (pair) e = launch_pair_kernel<kFmtF16, false, __half>(ma, mb, p, dev, a.stream, pdl, split_ws, split_bytes, a.deep != 0, &extra);
     else if (bf16 && a.out_dtype == DGA_F32) e = launch_kernel<kFmtBF16, false, kBnFloat, float>(ma, mb, p, dev, a.stream, pdl);
     else if (bf16) e = launch_kernel<kFmtBF16, false, kBnFloat, __nv_bfloat16>(ma, mb, p, dev, a.stream, pdl);
     else if (a.out_dtype == DGA_F32) e = launch_kernel<kFmtF16, false, kBnFloat, float>(ma, mb, p, dev, a.stream, pdl);

@@ -1,4 +1,4 @@
-// q4_rows.cuh -- products of up to 64 rows with a 4-bit weight with group scales,
+// q4_rows.cuh -- products of a few rows (up to 64) with a 4-bit weight with group scales,
 //     Y[M, N] = X[M, K] ((q - z) s)[N, K]^T + bias,
 // and the gated layer H = act(g) * u on them.
 //

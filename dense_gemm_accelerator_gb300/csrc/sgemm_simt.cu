@@ -459,7 +459,11 @@ struct Schedule {
     size_t partial_bytes;
 };
 
-Schedule plan_schedule(int64_t M, int64_t N, int64_t K, int sm_count) {
+//
+// deep (GemmArgs::deep): up to 16 ranges, each at least 64 deep.  A gated
+// layer's gradients at 256 x 512, K = 1400, and 1400 x 512, K = 256, with the pass before
+// them: 72 us with at most 4 ranges of 256, 36 so.
+Schedule plan_schedule(int64_t M, int64_t N, int64_t K, int sm_count, bool deep) {
     Schedule sc{};
     sc.tiles_n = (N + BN - 1) / BN;
     sc.tiles = ((M + BM - 1) / BM) * sc.tiles_n;
@@ -469,8 +473,8 @@ Schedule plan_schedule(int64_t M, int64_t N, int64_t K, int sm_count) {
     const int64_t slots = static_cast<int64_t>(kSimtBlocksPerSm) * sm_count;
     if (slots <= 0 || sc.tiles >= slots) return sc;
     const int64_t tail = sc.tiles;
-    int64_t parts = std::min<int64_t>(4, slots / tail);
-    parts = std::min<int64_t>(parts, K / 256);  // keep every part at least 256 deep
+    int64_t parts = std::min<int64_t>(deep ? 16 : 4, slots / tail);
+    parts = std::min<int64_t>(parts, K / (deep ? 64 : 256));  // no part too shallow
     if (parts < 2) return sc;
     const int64_t part_k = ((K + parts - 1) / parts + BK - 1) / BK * BK;
     parts = (K + part_k - 1) / part_k;
@@ -979,7 +983,7 @@ int64_t simt_top_band_rows(const GemmArgs& a, int sm_count, bool interior_shape)
     const int64_t rows = (tiles - tail) / tiles_n * BM;
     if (rows <= 0 || rows >= a.M) return 0;
     // the bottom band must itself be split at least 3 ways, else one band is as good
-    if (plan_schedule(a.M - rows, a.N, a.K, sm_count).parts < 3) return 0;
+    if (plan_schedule(a.M - rows, a.N, a.K, sm_count, a.deep != 0).parts < 3) return 0;
     return rows;
 }
 
@@ -996,7 +1000,7 @@ size_t simt_workspace_size(const GemmArgs& a, int sm_count) {
     const WidePlan w = plan_wide(a, sm_count);
     if (w.ok) return w.ws_bytes;
     const int64_t top = simt_top_band_rows(a, sm_count, simt_interior_shape(a));
-    return plan_schedule(a.M - top, a.N, a.K, sm_count).partial_bytes;
+    return plan_schedule(a.M - top, a.N, a.K, sm_count, a.deep != 0).partial_bytes;
 }
 
 namespace {
@@ -1053,7 +1057,7 @@ cudaError_t simt_launch(const GemmArgs& a, const DeviceInfo& dev, int* launches)
     }
     const int64_t top = simt_top_band_rows(a, dev.sm_count, simt_interior_shape(a));
     if (top > 0 && a.ws != nullptr &&
-        a.ws_bytes >= plan_schedule(a.M - top, a.N, a.K, dev.sm_count).partial_bytes) {
+        a.ws_bytes >= plan_schedule(a.M - top, a.N, a.K, dev.sm_count, a.deep != 0).partial_bytes) {
         GemmArgs upper = a, lower = a;
         upper.M = top;
         lower.M = a.M - top;
@@ -1070,7 +1074,7 @@ cudaError_t simt_launch(const GemmArgs& a, const DeviceInfo& dev, int* launches)
 namespace {
 
 cudaError_t simt_run(const GemmArgs& a, const DeviceInfo& dev, int* launches) {
-    Schedule sc = plan_schedule(a.M, a.N, a.K, dev.sm_count);
+    Schedule sc = plan_schedule(a.M, a.N, a.K, dev.sm_count, a.deep != 0);
     if (sc.parts > 1 && (a.ws == nullptr || a.ws_bytes < sc.partial_bytes)) {
         // not enough workspace for the split tail: whole tiles only
         sc.full_tiles = sc.tiles;

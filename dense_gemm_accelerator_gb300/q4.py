@@ -168,8 +168,9 @@ def _rows_for(X, Q):
 
 def q4_linear_forward(X, W, bias=None, Y=None, workspace=None, stream=None):
     """Y = X @ W^T + bias for X [batch, in] and a 4-bit weight W, a Q4Tensor [out, in];
-    X, the scales, the bias and Y of one type, bfloat16 or float16.  Up to 64 rows
-    multiply the codes as they are; more go through W's values rounded to X's type."""
+    X, the scales, the bias and Y of one type, bfloat16 or float16.  Up to 32 rows
+    (64 of smaller weights) multiply the codes as they are; more go through W's values
+    rounded to X's type."""
     if stream is not None:
         return on_stream(stream, X.device, q4_linear_forward, X, W, bias, Y, workspace)
     d = X.get_device()
@@ -185,7 +186,7 @@ def q4_linear_forward(X, W, bias=None, Y=None, workspace=None, stream=None):
         Y, ldy = result(Y, M, N, X.dtype, X.device, "Y")
     x = X.data_ptr()
     if workspace is None:
-        have = _linear_workspace(code, M, N, K, ldx if x % 16 == 0 else ldx | 1) if M > 64 or ldx % 8 or x % 16 or not K else 0
+        have = _linear_workspace(code, M, N, K, ldx if x % 16 == 0 else ldx | 1) if M > 512 or ldx % 8 or x % 16 or not K else 0
         if have:
             workspace = torch.empty(have, dtype=_U8, device=d)
     else:
@@ -220,7 +221,7 @@ def q4_gated_forward(X, W, bias=None, activation="silu", H=None, workspace=None,
         H, ldh = result(H, M, F, X.dtype, X.device, "H")
     x = X.data_ptr()
     if workspace is None:
-        have = _gated_workspace(code, M, F, K, ldx if x % 16 == 0 else ldx | 1) if M > 64 or ldx % 8 or x % 16 or not K else 0
+        have = _gated_workspace(code, M, F, K, ldx if x % 16 == 0 else ldx | 1) if M > 512 or ldx % 8 or x % 16 or not K else 0
         if have:
             workspace = torch.empty(have, dtype=_U8, device=d)
     else:

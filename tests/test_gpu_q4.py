@@ -262,3 +262,70 @@ def test_a_block_quantised_and_served():
         # the same block before it was quantised: its gated layer on the values that the codes stand for
         same = dga.gated_forward(X, dga.q4_dequantize(Q, dga.BF16))
         assert float((same.double() - H).norm() / H.norm()) < 4 * ref.HALF[dtype]
+
+
+# rows of X around the tensor-core kernel's stages (128, 208, 256 to a tile), K cut among the CTAs of a
+# cluster unevenly, a weight small and large enough for either kernel at 33 to 64 rows
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,N,K", [(33, 2050, 2090), (64, 600, 7000), (65, 129, 4100), (130, 257, 1290), (207, 384, 1000), (209, 128, 2049),
+                                   (256, 300, 8200), (257, 120, 770), (600, 260, 2111), (1024, 64, 513), (1025, 130, 260)])
+def test_linear_on_the_tensor_cores(M, N, K, group, dtype):
+    Q = _weight(N, K, group, M % 2 == 0, dtype, N + K)
+    X = _x(M, K, dtype, M)
+    b = torch.randn(N, device="cuda").to(dtype) if M % 2 else None
+    v, off = _product(X, Q, b)
+    got = dga.q4_linear_forward(X, Q, b)
+    ref.within(got, v, off + ref.rounding(v, dtype) * (1 + 2.0 ** -7))
+    for _ in range(3):
+        assert torch.equal(dga.q4_linear_forward(X, Q, b), got)
+    assert dga.dga_sync_status(torch.cuda.current_stream().cuda_stream) == dga.OK
+
+
+@pytest.mark.parametrize("dtype", HALVES)
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("M,F,K", [(33, 1100, 2090), (64, 130, 5000), (65, 70, 2100), (128, 129, 1030), (129, 200, 515), (400, 64, 3000),
+                                   (512, 131, 256), (513, 96, 1000), (700, 130, 515)])
+def test_gated_on_the_tensor_cores(M, F, K, group, dtype):
+    name = ref.ACTS[(M + F) % 5]
+    Q = _weight(2 * F, K, group, M % 2 == 1, dtype, F + K)
+    X = _x(M, K, dtype, M)
+    b = torch.randn(2 * F, device="cuda").to(dtype) if M % 2 else None
+    P, off = _product(X, Q, b)
+    H, eh = ref.gated_of(P, off, name, dtype)
+    got = dga.q4_gated_forward(X, Q, b, activation=name)
+    ref.within(got, H, eh, name)
+    assert torch.equal(dga.q4_gated_forward(X, Q, b, activation=name), got)
+    assert dga.dga_sync_status(torch.cuda.current_stream().cuda_stream) == dga.OK
+
+
+@pytest.mark.parametrize("M", [48, 256, 300])
+@pytest.mark.parametrize("group", [32, 128])
+def test_tensor_core_launches_beside_one_another(M, group):
+    """Long loops of few stages on two streams at once, whose warps run apart from one another."""
+    dtype = torch.float16
+    Q = [_weight(1200, 8192, group, i == 0, dtype, i) for i in range(2)]
+    X = _x(M, 8192, dtype, M)
+    want = [(dga.q4_linear_forward(X, q), dga.q4_gated_forward(X, q)) for q in Q]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in Q]
+    for _ in range(20):
+        got = [(dga.q4_linear_forward(X, q, stream=s.cuda_stream), dga.q4_gated_forward(X, q, stream=s.cuda_stream)) for q, s in zip(Q, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for g, w in zip(got, want) for a, b in zip(g, w))
+    assert dga.dga_sync_status(torch.cuda.current_stream().cuda_stream) == dga.OK
+
+
+def test_infinite_scales_stay_what_they_are():
+    """K that ends inside a block of columns: (q - z) inf times X, and no NaN from what lies past K."""
+    for dtype in HALVES:
+        for M in (4, 70, 300):
+            Q = _weight(130, 100, 64, False, dtype, 1)
+            Q.codes.fill_(0x99)  # q - 8 = 1
+            Q.scales.fill_(1.0)
+            Q.scales[5, 1] = math.inf
+            X = torch.ones(M, 100, device="cuda", dtype=dtype)
+            Y = dga.q4_linear_forward(X, Q)
+            want = torch.full_like(Y, 100.0)
+            want[:, 5] = math.inf
+            assert torch.equal(Y, want)
