@@ -63,6 +63,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cstring>
 #include <mutex>
 
 #include "dga_internal.h"
@@ -188,6 +189,36 @@ __device__ __forceinline__ void store_block_staged(const TcParams& p, uint32_t* 
     const int64_t col = col_base + lane;
     const bool col_ok = col < p.N;
     const float bv = (p.bias != nullptr && col_ok) ? OutT<TOut>::load(static_cast<const TOut*>(p.bias) + col) : 0.0f;
+    // Without C and a bias the rows' loads and stores are in flight together, and 16-bit
+    // results leave eight at a time where they can (the loop below, whose every row
+    // branches on beta, took 1.7 us a block: 186 us for 16384 x 4096 results, K = 256;
+    // 76 so).  The arithmetic is the loop's.
+    if (p.beta == 0.0f && p.bias == nullptr && row_base + 32 <= p.M && col_base + 32 <= p.N) {
+        TOut* base = static_cast<TOut*>(p.C) + row_base * p.ldc + col_base;
+        if constexpr (sizeof(TOut) == 2) {
+            if (((reinterpret_cast<uintptr_t>(p.C) | static_cast<uintptr_t>(p.ldc) * 2) & 15) == 0) {
+                const int r0 = lane >> 2, c0 = (lane & 3) * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    TOut out[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        OutT<TOut>::store(&out[j], axpby(p.alpha, __uint_as_float(stage[(i * 8 + r0) * 33 + c0 + j]), p.beta, 0.0f) + 0.0f);
+                    uint4 w;
+                    memcpy(&w, out, 16);
+                    *reinterpret_cast<uint4*>(base + (i * 8 + r0) * p.ldc + c0) = w;
+                }
+                __syncwarp();
+                return;
+            }
+        }
+        TOut* dst = base + lane;
+#pragma unroll 16
+        for (int i = 0; i < 32; ++i)
+            OutT<TOut>::store(dst + i * p.ldc, axpby(p.alpha, __uint_as_float(stage[i * 33 + lane]), p.beta, 0.0f) + 0.0f);
+        __syncwarp();
+        return;
+    }
 #pragma unroll 4
     for (int i = 0; i < 32; ++i) {
         const int64_t row = row_base + i;
@@ -500,7 +531,7 @@ __device__ __forceinline__ void store_block_partial(uint32_t* slot_base, uint32_
 #pragma unroll
     for (int j = 0; j < 32; ++j) stage[lane * 33 + j] = v[j];
     __syncwarp();
-#pragma unroll 4
+#pragma unroll 16
     for (int i = 0; i < 32; ++i)
         slot_base[(row_base + i) * kPairBN + col_base + lane] = stage[i * 33 + lane];
     __syncwarp();
@@ -713,6 +744,13 @@ __global__ void __launch_bounds__(kI8 ? 576 : 192, 1)
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(tmem_base + lane_base + acc * kPairBN + c * 32, r);
                     tmem_ld_wait();
+                    if (c == kPairBN / 32 - 1) {
+                        // the accumulator has been read: its next MMAs need not wait for the
+                        // stores, nor the signal for them to be seen by the cluster
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_signal_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
+                    }
                     if (slot < 0)
                         store_block_staged<TOut>(p, stage, lane, row_base, col0 + c * 32, r);
                     else
@@ -720,9 +758,6 @@ __global__ void __launch_bounds__(kI8 ? 576 : 192, 1)
                                             stage, lane, static_cast<int>(rank * 128 + quarter * 32),
                                             c * 32, r);  // r: the fp32 sums' bits
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_cta(smem_u32(&acc_empty[acc]), 0));
                 if (++acc == 2) { acc = 0; acc_phase ^= 1; }
             } else {
                 // each chunk's exact fp32 sums become int32 and add up (wrapping)
@@ -1444,10 +1479,15 @@ uint32_t split_parts(uint32_t rem, uint32_t nc, uint32_t num_kb) {
     return best;
 }
 
+// More than one 128-row tile; deep products of fewer rows too, with half of each
+// tile unused, where K is long enough to be cut (100 x 4096, K = 16384: 16 tiles of
+// the other kernel, 103 us; here 64 parts, 32).
+bool pair_kernel(const GemmArgs& a) { return a.M > BM || (a.deep && a.in_dtype != DGA_I8 && a.K >= 1024); }
+
 // Parts per tile where the tiles are fewer than the clusters (GemmArgs::deep):
 // as many as give each cluster one part, none shallower than kMinDeepKb.
 // A gated layer's gradient of X at 256 x 4096, K = 16384 has 16 tiles for 76
-// clusters: the layer's backward pass took 280 us with whole tiles, 234 with four parts each.
+// clusters: that product 77 us whole, 33 in four parts each.
 constexpr uint32_t kMaxDeepSplits = 16, kMinDeepKb = 4;
 uint32_t deep_parts(uint32_t tiles, uint32_t nc, uint32_t num_kb) {
     return std::max(1u, std::min({kMaxDeepSplits, nc / std::max(tiles, 1u), num_kb / kMinDeepKb}));
@@ -1642,7 +1682,7 @@ size_t tc_workspace_wanted(const GemmArgs& a, int sm_count) {
     // the split last wave (CTA-pair kernel, floating point): at most two
     // rounds of parts on sm_count / 2 clusters; only for more tiles than
     // clusters and K deep enough for two parts
-    if (a.in_dtype == DGA_I8 || a.M <= BM || sm_count < 2) return need;
+    if (a.in_dtype == DGA_I8 || !pair_kernel(a) || sm_count < 2) return need;
     const int64_t tiles = ((a.M + 255) / 256) * ((a.N + kPairBN - 1) / kPairBN);
     const int64_t kb = (a.K + k_per_stage(a.in_dtype == DGA_TF32 ? kFmtTF32 : kFmtBF16) - 1) /
                        k_per_stage(a.in_dtype == DGA_TF32 ? kFmtTF32 : kFmtBF16);
@@ -1726,7 +1766,7 @@ cudaError_t tc_launch(const GemmArgs& a, const DeviceInfo& dev, int* launches) {
     // (256 x 256 tiles, each CTA loading half of B).
     // More than one 128-row tile: the CTA-pair kernel (256 x 256 tiles, each
     // CTA loading half of B), INT8 included (its chunked exact accumulation).
-    const bool pair = a.M > BM;
+    const bool pair = pair_kernel(a);
     const int BN = pair ? kPairBN : (i8 ? kBnI8 : kBnFloat);
     CUtensorMap ma, mb;
     e = pl.a_mn ? make_mnmajor_map(&ma, A, a.M, a.K, lda, fmt)
