@@ -255,3 +255,35 @@ def test_a_block_trained_as_it_is_used():
     for got, want in ((dX, x.grad), (dW, w.grad), (dWd, wd.grad)):
         # three fp32 sums of up to 200 values behind one another, of mixed signs
         assert float((got.double() - want).norm() / want.norm()) < 3 * ref.sum_error(200)
+
+
+# products with fewer tiles than the machine has places for, over a K that is cut: up to 128 rows and
+# more, at sizes around the parts, with dX's K = 2F and dW's K = M in turn the long one
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,F,K", [(1, 520, 24), (3, 700, 40), (16, 2048, 130), (100, 2048, 300), (128, 1030, 515), (129, 512, 1000),
+                                   (256, 4100, 260), (2050, 64, 96), (4096, 30, 130)])
+def test_gradients_of_few_tiles(M, F, K, dtype):
+    X, W, _ = _inputs(M, F, K, dtype, M + F)
+    g = torch.Generator(device="cuda").manual_seed(M)
+    P = (2 * torch.randn(M, 2 * F, device="cuda", generator=g)).to(dtype)
+    G = torch.randn(M, F, device="cuda", generator=g).to(dtype)
+    first = dga.gated_backward(X, W, P, G, activation="gelu_tanh", need_bias=True)
+    want = ref.gated_grads(X, W, P, G, "gelu_tanh")
+    for got, key in zip(first, ("dX", "dW", "db")):
+        ref.within(got, *want[key], key)
+    for _ in range(3):
+        again = dga.gated_backward(X, W, P, G, activation="gelu_tanh", need_bias=True)
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+    _status_ok()
+
+
+def test_gradients_with_the_least_workspace_and_one_too_small():
+    M, F, K = 100, 1024, 256
+    X, W, _ = _inputs(M, F, K, torch.bfloat16, 5)
+    P, G = (torch.randn(M, n, device="cuda").bfloat16() for n in (2 * F, F))
+    want = dga.gated_backward(X, W, P, G)
+    need = dga.lib().dga_gated_backward_workspace_size(dga.BF16, M, F, K, K, K)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert all(torch.equal(a, b) for a, b in zip(dga.gated_backward(X, W, P, G, workspace=ws)[:2], want))
+    with pytest.raises(dga.DgaError):
+        dga.gated_backward(X, W, P, G, workspace=ws[:need - 256])
