@@ -229,9 +229,16 @@ cudaError_t q4_quantize_launch(int in_dtype, int scale_dtype, int64_t rows, int6
 cudaError_t q4_dequantize_launch(int scale_dtype, int out_dtype, int64_t rows, int64_t cols, const Q4Matrix& q, void* Y,
                                  int64_t ldy, cudaStream_t stream);
 
-// Rows of 16-bit values copied to rows that start on 16 bytes (ldy a multiple of 8).
-cudaError_t copy_rows_launch(int64_t rows, int64_t cols, const void* X, int64_t ldx, void* Y, int64_t ldy, const DeviceInfo& dev,
-                             cudaStream_t stream);
+// Rows of 16-bit values copied to rows that start on 16 bytes (ldy a multiple of 8),
+// of one array or two, rows and cols at least 1.
+struct CopyRows {
+    int64_t rows, cols;
+    const void* X;
+    int64_t ldx;
+    void* Y;
+    int64_t ldy;
+};
+cudaError_t copy_rows_launch(const CopyRows& a, const CopyRows* b, cudaStream_t stream);
 
 // Y (M x N) = X W^T + bias for up to 64 rows (that start on 16 bytes) and K >= 1, or (gated) the gated
 // layer's M x N result on a weight of 2N rows.

@@ -190,7 +190,7 @@ cudaError_t q4_by_kernel(const Q4Plan& pl, int dtype, int act, int64_t M, int64_
                          cudaStream_t s, int* launches) {
     cudaError_t e = cudaSuccess;
     if (pl.x) {
-        e = copy_rows_launch(M, K, X, ldx, ws, pl.ldv, dev, s);
+        e = copy_rows_launch({M, K, X, ldx, ws, pl.ldv}, nullptr, s);
         if (e != cudaSuccess) return e;
         ++*launches;
         X = ws;
@@ -277,14 +277,11 @@ int dga_gated(dga_dtype dtype, dga_activation act, int64_t M, int64_t F, int64_t
     if (pl.fused) {
         GatedArgs g{dtype, act, M, F, K, X, ldx, W, ldw, bias, H, ldh, P, ldp, s};
         const int64_t ld = round_up(K, 8);
-        if (pl.x) {
-            e = copy_rows_launch(M, K, X, ldx, ws, ld, dev, s);
-            g.X = ws, g.ldx = ld;
-            ++launches;
-        }
-        if (e == cudaSuccess && pl.w) {
-            e = copy_rows_launch(2 * F, K, W, ldw, ws + pl.x, ld, dev, s);
-            g.W = ws + pl.x, g.ldw = ld;
+        if (pl.x || pl.w) {
+            const CopyRows x{M, K, X, ldx, ws, ld}, w{2 * F, K, W, ldw, ws + pl.x, ld};
+            e = pl.x ? copy_rows_launch(x, pl.w ? &w : nullptr, s) : copy_rows_launch(w, nullptr, s);
+            if (pl.x) g.X = x.Y, g.ldx = ld;
+            if (pl.w) g.W = w.Y, g.ldw = ld;
             ++launches;
         }
         if (e == cudaSuccess)
