@@ -20,13 +20,21 @@
 
 namespace dga {
 
-// s(x).  kFast: the hardware's exponential and division, 2^-21 off, for results
-// that are rounded to 16 bits (2^-9, 2^-12) next.
+// s(x) and its complement s(-x) = 1 - s(x).  With e = e^-|x| and r = 1 / (1 + e) the
+// larger of the two is r and the smaller e r, so neither is a difference: 1 - s, which is
+// what sigmoid's slope s (1 - s) would take, has lost 9e-3 of itself in fp32 at x = 12 and
+// is 0 from 17 on.  Nor is there an infinity for large -x.
+// kFast: the hardware's exponential and division, for results that are rounded to 16 bits
+// (2^-9, 2^-12) next.  The larger is 2^-21 off, the smaller 2^-20 + 1.2 |x| 2^-23 (the
+// exponential's error grows with its argument: 2^-16 at |x| = 88).
 template <bool kFast>
-__device__ __forceinline__ float logistic(float x) {
-    if constexpr (kFast) return __fdividef(1.0f, 1.0f + __expf(-x));
-    else return 1.0f / (1.0f + expf(-x));
+__device__ __forceinline__ float2 logistic_pair(float x) {
+    const float e = kFast ? __expf(-fabsf(x)) : expf(-fabsf(x));
+    const float r = kFast ? __fdividef(1.0f, 1.0f + e) : 1.0f / (1.0f + e);
+    return x < 0.0f ? make_float2(e * r, r) : make_float2(r, e * r);
 }
+template <bool kFast>
+__device__ __forceinline__ float logistic(float x) { return logistic_pair<kFast>(x).x; }
 
 // Phi(g).  kFast: erfc(x) = t 2^(-x^2 log2 e + p(t)), t = 1 / (1 + x / 2), x = |g| / sqrt 2,
 // p the polynomial of degree 7 that a Chebyshev fit of log2(erfcx(x) / t) over t gives;
@@ -68,26 +76,27 @@ __device__ __forceinline__ float act_value(float g) {
 template <int kAct, bool kFast>
 __device__ __forceinline__ void act_both(float g, float& value, float& slope) {
     if constexpr (kAct == DGA_SILU) {
-        const float s = logistic<kFast>(g);
-        value = g * s;
-        slope = fmaf(value, 1.0f - s, s);
+        const float2 s = logistic_pair<kFast>(g);
+        value = g * s.x;
+        slope = fmaf(value, s.y, s.x);
     } else if constexpr (kAct == DGA_GELU) {
         const float c = normal_cdf<kFast>(g);
         const float e = kInvSqrt2Pi * (kFast ? __expf(-0.5f * g * g) : expf(-0.5f * g * g));
         value = g * c;
         slope = fmaf(g, e, c);
     } else if constexpr (kAct == DGA_GELU_TANH) {
-        const float s = logistic<kFast>(g * fmaf(kGeluB * g, g, kGeluA));
-        const float t = s * (1.0f - s);
-        value = g * s;
+        const float2 s = logistic_pair<kFast>(g * fmaf(kGeluB * g, g, kGeluA));
+        const float t = s.x * s.y;
+        value = g * s.x;
         // far out t is 0 and v' past fp32's range
-        slope = t > 0.0f ? fmaf(g * t, fmaf(kGeluC * g, g, kGeluA), s) : s;
+        slope = t > 0.0f ? fmaf(g * t, fmaf(kGeluC * g, g, kGeluA), s.x) : s.x;
     } else if constexpr (kAct == DGA_RELU) {
         value = g < 0.0f ? 0.0f : g;
         slope = g > 0.0f ? 1.0f : (g == g ? 0.0f : g);
     } else {
-        value = logistic<kFast>(g);
-        slope = value * (1.0f - value);
+        const float2 s = logistic_pair<kFast>(g);
+        value = s.x;
+        slope = s.x * s.y;
     }
 }
 
