@@ -179,6 +179,26 @@ __device__ __forceinline__ void record_failure(int role, volatile int* abort_fla
 // consecutive elements of one row (whole 32-byte sectors), whatever the
 // alignment of C or ldc.
 
+// The block in `stage` over an old C.
+template <typename TOut>
+__device__ __forceinline__ void add_block_staged(const TcParams& p, const uint32_t* stage, int lane, int64_t row_base,
+                                              int64_t col, float bv) {
+    const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.M - row_base));  // that exist
+    if (col >= p.N) return;
+    TOut* dst = static_cast<TOut*>(p.C) + row_base * p.ldc + col;
+#pragma unroll 1
+    for (int i0 = 0; i0 < rows; i0 += 16) {
+        float old[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) old[i] = i0 + i < rows ? OutT<TOut>::load(dst + (i0 + i) * p.ldc) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float v = axpby(p.alpha, __uint_as_float(stage[(i0 + i) * 33 + lane]), p.beta, old[i]) + bv;
+            if (i0 + i < rows) OutT<TOut>::store(dst + (i0 + i) * p.ldc, v);
+        }
+    }
+}
+
 template <typename TOut>
 __device__ __forceinline__ void store_block_staged(const TcParams& p, uint32_t* stage, int lane,
                                                    int64_t row_base, int64_t col_base,
@@ -189,43 +209,47 @@ __device__ __forceinline__ void store_block_staged(const TcParams& p, uint32_t* 
     const int64_t col = col_base + lane;
     const bool col_ok = col < p.N;
     const float bv = (p.bias != nullptr && col_ok) ? OutT<TOut>::load(static_cast<const TOut*>(p.bias) + col) : 0.0f;
-    // Without C and a bias the rows' loads and stores are in flight together, and 16-bit
-    // results leave eight at a time where they can (the loop below, whose every row
-    // branches on beta, took 1.7 us a block: 186 us for 16384 x 4096 results, K = 256;
-    // 76 so).  The arithmetic is the loop's.
-    if (p.beta == 0.0f && p.bias == nullptr && row_base + 32 <= p.M && col_base + 32 <= p.N) {
+    // A loop to each kind of block, none of which branches from row to row, so that the
+    // rows' loads and stores are in flight together (16384 x 4096 16-bit results, K = 256,
+    // with one loop for all and a branch on beta to each row: 185 us, with a bias 202, over
+    // an old C 1256; so 79, 100 and 313.  4096^3: 89, 91 and 307; 83, 83 and 103).
+    if (p.beta != 0.0f) {
+        add_block_staged<TOut>(p, stage, lane, row_base, col, bv);
+    } else if (row_base + 32 <= p.M && col_base + 32 <= p.N) {
         TOut* base = static_cast<TOut*>(p.C) + row_base * p.ldc + col_base;
-        if constexpr (sizeof(TOut) == 2) {
-            if (((reinterpret_cast<uintptr_t>(p.C) | static_cast<uintptr_t>(p.ldc) * 2) & 15) == 0) {
-                const int r0 = lane >> 2, c0 = (lane & 3) * 8;
+        if (sizeof(TOut) == 2 && ((reinterpret_cast<uintptr_t>(p.C) | static_cast<uintptr_t>(p.ldc) * 2) & 15) == 0) {
+            // 16-bit values, eight to a store
+            const int r0 = lane >> 2, c0 = (lane & 3) * 8;
+            float b[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    TOut out[8];
+            for (int j = 0; j < 8; ++j) b[j] = 0.0f;
+            if (p.bias != nullptr) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        OutT<TOut>::store(&out[j], axpby(p.alpha, __uint_as_float(stage[(i * 8 + r0) * 33 + c0 + j]), p.beta, 0.0f) + 0.0f);
-                    uint4 w;
-                    memcpy(&w, out, 16);
-                    *reinterpret_cast<uint4*>(base + (i * 8 + r0) * p.ldc + c0) = w;
-                }
-                __syncwarp();
-                return;
+                for (int j = 0; j < 8; ++j) b[j] = __shfl_sync(0xffffffffu, bv, c0 + j);
             }
-        }
-        TOut* dst = base + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                TOut out[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    OutT<TOut>::store(&out[j], axpby(p.alpha, __uint_as_float(stage[(i * 8 + r0) * 33 + c0 + j]), p.beta, 0.0f) + b[j]);
+                uint4 w;
+                memcpy(&w, out, 16);
+                *reinterpret_cast<uint4*>(base + (i * 8 + r0) * p.ldc + c0) = w;
+            }
+        } else {
+            TOut* dst = base + lane;
 #pragma unroll 16
-        for (int i = 0; i < 32; ++i)
-            OutT<TOut>::store(dst + i * p.ldc, axpby(p.alpha, __uint_as_float(stage[i * 33 + lane]), p.beta, 0.0f) + 0.0f);
-        __syncwarp();
-        return;
-    }
-#pragma unroll 4
-    for (int i = 0; i < 32; ++i) {
-        const int64_t row = row_base + i;
-        if (col_ok && row < p.M) {
-            TOut* dst = static_cast<TOut*>(p.C) + row * p.ldc + col;
-            const float old = p.beta != 0.0f ? OutT<TOut>::load(dst) : 0.0f;
-            OutT<TOut>::store(dst, axpby(p.alpha, __uint_as_float(stage[i * 33 + lane]), p.beta, old) + bv);
+            for (int i = 0; i < 32; ++i)
+                OutT<TOut>::store(dst + i * p.ldc, axpby(p.alpha, __uint_as_float(stage[i * 33 + lane]), p.beta, 0.0f) + bv);
+        }
+    } else {
+        const int rows = static_cast<int>(min(static_cast<int64_t>(32), p.M - row_base));  // that exist
+        TOut* dst = static_cast<TOut*>(p.C) + row_base * p.ldc + col;
+#pragma unroll 16
+        for (int i = 0; i < 32; ++i) {
+            const float out = axpby(p.alpha, __uint_as_float(stage[i * 33 + lane]), p.beta, 0.0f) + bv;
+            if (col_ok && i < rows) OutT<TOut>::store(dst + i * p.ldc, out);
         }
     }
     __syncwarp();  // the next block reuses the square
