@@ -22,7 +22,9 @@
 //  * A word of 8 codes becomes four registers of two: (w >> 4 i) & 0x000f000f
 //    has codes i and i + 4, and or-ed into the mantissa of 128 (bf16) or 1024
 //    (fp16) they are 128 + q or 1024 + q; subtracting 128 + z or 1024 + z is
-//    exact.  X's eight values are paired alike.
+//    exact.  X's eight values are paired alike.  bf16's range is fp32's, so there the
+//    same fused step takes 2^-10 of the difference, which 64 columns of the largest
+//    values and codes cannot overflow; the sums regain it at the end (both exact).
 //  * The warps' sums meet in shared memory and are added in a fixed order; bias,
 //    activation and product follow from there.
 #pragma once
@@ -93,23 +95,28 @@ inline uint32_t stage_columns(int64_t M) {
 
 template <typename T> struct Codes;
 template <> struct Codes<__nv_bfloat16> {
-    static constexpr uint32_t kBase = 0x4300u, kBoth = 0x43004300u;  // 128
-    __device__ __forceinline__ static uint32_t minus(uint32_t a, uint32_t b) {
-        __nv_bfloat162 x, y;
+    static constexpr uint32_t kBoth = 0x43004300u;  // 128
+    static constexpr uint32_t kBase = 0xbe00u;      // -128 / 1024, its last place 1 / 1024
+    static constexpr float kUnit = 1024.0f;         // what the sums are to be multiplied by
+    // a / 1024 + b
+    __device__ __forceinline__ static uint32_t less(uint32_t a, uint32_t b) {
+        const uint32_t factors = 0x3a803a80u;  // 1 / 1024
+        __nv_bfloat162 x, y, f;
         memcpy(&x, &a, 4);
         memcpy(&y, &b, 4);
-        x = __hsub2(x, y);
+        memcpy(&f, &factors, 4);
+        x = __hfma2(x, f, y);
         uint32_t r;
         memcpy(&r, &x, 4);
         return r;
     }
     __device__ __forceinline__ static float scale(uint32_t entry) { return __uint_as_float(entry & 0xffff0000u); }
-    // q - z of a word's codes 0 and 4, 1 and 5, 2 and 6, 3 and 7; z: the base twice.
+    // (q - z) / kUnit of a word's codes 0 and 4, 1 and 5, 2 and 6, 3 and 7; z: the base twice.
     __device__ __forceinline__ static void unpack(uint32_t (&c)[4], uint32_t w, uint32_t z) {
-        c[0] = minus((w & 0x000f000fu) | kBoth, z);
-        c[1] = minus(((w >> 4) & 0x000f000fu) | kBoth, z);
-        c[2] = minus(((w >> 8) & 0x000f000fu) | kBoth, z);
-        c[3] = minus(((w >> 12) & 0x000f000fu) | kBoth, z);
+        c[0] = less((w & 0x000f000fu) | kBoth, z);
+        c[1] = less(((w >> 4) & 0x000f000fu) | kBoth, z);
+        c[2] = less(((w >> 8) & 0x000f000fu) | kBoth, z);
+        c[3] = less(((w >> 12) & 0x000f000fu) | kBoth, z);
     }
     // d = a b + (first ? 0 : d)
     __device__ __forceinline__ static void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool first) {
@@ -126,6 +133,7 @@ template <> struct Codes<__nv_bfloat16> {
 };
 template <> struct Codes<__half> {
     static constexpr uint32_t kBase = 0x6400u, kBoth = 0x64006400u;  // 1024
+    static constexpr float kUnit = 1.0f;
     __device__ __forceinline__ static uint32_t minus(uint32_t a, uint32_t b) {
         __half2 x, y;
         memcpy(&x, &a, 4);
@@ -173,7 +181,7 @@ __device__ __forceinline__ void record_failure(int role, volatile int* abort_fla
     *abort_flag = 1;
 }
 
-// A group's scale and base (128 or 1024 plus the zero point) as the table holds
+// A group's scale and base (fp16: 1024 plus the zero point, bf16: -1/1024 of 128 plus it) as the table holds
 // them: for groups of 32 one word, the scale's bits above the base's, else two,
 // the scale in fp32 and the base twice.
 template <bool kSmall> struct EntryOf { using type = uint2; };
@@ -470,7 +478,7 @@ __global__ void __launch_bounds__(Plan<kMt>::kThreads, 1) q4_rows_kernel(const _
             float v = 0.0f;
 #pragma unroll
             for (int k = 0; k < kParts; ++k) v += sums[(k * 8 * kMt + token) * kPitch + col];
-            return v;
+            return v * Codes<T>::kUnit;
         };
         float v = total(c);
         if (bias) v += OutT<T>::load(bias + n);

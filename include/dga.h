@@ -679,8 +679,9 @@ int dga_q4_dequantize(dga_dtype scale_dtype, dga_dtype out_dtype, int64_t rows, 
  * row-major), the scales, the bias (N values or NULL) and Y (M x N, row-major)
  * of one type, DGA_BF16 or DGA_F16; sums in fp32.  Up to 32 rows (64 where N K
  * is at most 2^22) the codes are multiplied as they are and a group's sum by its
- * scale in fp32; with more, W's values are first rounded to that type (in
- * DGA_F16 one past 65504 to an infinity).
+ * scale in fp32 (DGA_BF16's under a factor of 2^-10 that the result regains, so
+ * that no value of X takes a group's sum out of range); with more, W's values are
+ * first rounded to that type (in DGA_F16 one past 65504 to an infinity).
  *   workspace   device, 256-byte aligned, of dga_q4_linear_workspace_size bytes
  * Errors: DGA_ERR_UNSUPPORTED (type, group); -2 M, -3 N, -4 K, -6 X, -7 ldx,
  * -8 codes, -9 ld_codes, -10 scales, -11 ld_scales, -13 ld_zeros, -14 bias,
