@@ -18,13 +18,15 @@ from .mx import _CODE, _rows_of, on_stream
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
 
 
+# sizes of scratch, by shape and by the (current) device, whose number of SMs decides
+# how far products are cut
 @functools.lru_cache(maxsize=4096)
-def _forward_workspace(code, M, F, K, ldx, ldw, save):
+def _forward_workspace(device, code, M, F, K, ldx, ldw, save):
     return lib().dga_gated_workspace_size(code, M, F, K, ldx, ldw, save)
 
 
 @functools.lru_cache(maxsize=4096)
-def _backward_workspace(code, M, F, K, ldx, ldw):
+def _backward_workspace(device, code, M, F, K, ldx, ldw):
     return lib().dga_gated_backward_workspace_size(code, M, F, K, ldx, ldw)
 
 
@@ -101,7 +103,7 @@ def gated_forward(X, W, bias=None, activation="silu", save=False, H=None, P=None
     if workspace is None:
         have = 0
         if ldx % 8 or ldw % 8 or (x | w) % 16 or code == F32 or not K:  # else none is needed
-            have = _forward_workspace(code, M, F, K, odd_where_off(ldx, x), odd_where_off(ldw, w), 1 if save else 0)
+            have = _forward_workspace(d, code, M, F, K, odd_where_off(ldx, x), odd_where_off(ldw, w), 1 if save else 0)
         if have:
             workspace = torch.empty(have, dtype=torch.uint8, device=d)
     else:
@@ -148,7 +150,7 @@ def gated_backward(X, W, P, G, activation="silu", need_bias=False, need_x=True, 
         dW, lddw = result(dW, N, K, dtype, dev, "dW")
         dw = dW.data_ptr()
     if workspace is None:
-        have = _backward_workspace(code, M, F, K, odd_where_off(ldx, x), odd_where_off(ldw, w))
+        have = _backward_workspace(dev.index, code, M, F, K, odd_where_off(ldx, x), odd_where_off(ldw, w))
         if have:
             workspace = torch.empty(have, dtype=torch.uint8, device=dev)
     else:

@@ -20,13 +20,14 @@ _U8 = torch.uint8
 _HALF = {torch.bfloat16: _CODE[torch.bfloat16], torch.float16: _CODE[torch.float16]}
 
 
+# sizes of scratch, by shape and by the (current) device
 @functools.lru_cache(maxsize=4096)
-def _linear_workspace(code, M, N, K, ldx):
+def _linear_workspace(device, code, M, N, K, ldx):
     return lib().dga_q4_linear_workspace_size(code, M, N, K, ldx)
 
 
 @functools.lru_cache(maxsize=4096)
-def _gated_workspace(code, M, F, K, ldx):
+def _gated_workspace(device, code, M, F, K, ldx):
     return lib().dga_q4_gated_workspace_size(code, M, F, K, ldx)
 
 
@@ -186,7 +187,7 @@ def q4_linear_forward(X, W, bias=None, Y=None, workspace=None, stream=None):
         Y, ldy = result(Y, M, N, X.dtype, X.device, "Y")
     x = X.data_ptr()
     if workspace is None:
-        have = _linear_workspace(code, M, N, K, ldx if x % 16 == 0 else ldx | 1) if M > 512 or ldx % 8 or x % 16 or not K else 0
+        have = _linear_workspace(d, code, M, N, K, ldx if x % 16 == 0 else ldx | 1) if M > 512 or ldx % 8 or x % 16 or not K else 0
         if have:
             workspace = torch.empty(have, dtype=_U8, device=d)
     else:
@@ -221,7 +222,7 @@ def q4_gated_forward(X, W, bias=None, activation="silu", H=None, workspace=None,
         H, ldh = result(H, M, F, X.dtype, X.device, "H")
     x = X.data_ptr()
     if workspace is None:
-        have = _gated_workspace(code, M, F, K, ldx if x % 16 == 0 else ldx | 1) if M > 512 or ldx % 8 or x % 16 or not K else 0
+        have = _gated_workspace(d, code, M, F, K, ldx if x % 16 == 0 else ldx | 1) if M > 512 or ldx % 8 or x % 16 or not K else 0
         if have:
             workspace = torch.empty(have, dtype=_U8, device=d)
     else:
