@@ -67,6 +67,13 @@ def odd_where_off(ld, pointer):
     return ld if pointer % 16 == 0 else ld | 1
 
 
+def scratch(workspace, d):
+    """The bytes of a workspace that a caller gives (to the kernels, an address and these)."""
+    if workspace.get_device() != d or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of X")
+    return workspace.numel() * workspace.element_size()
+
+
 def gated_forward(X, W, bias=None, activation="silu", save=False, H=None, P=None, workspace=None, stream=None):
     """H = act(g) * u with [g | u] = X @ W^T + bias, for X [batch, in], W [2 * hidden,
     in] and bias [2 * hidden] of one type (float32, bfloat16 or float16), row-major;
@@ -107,7 +114,7 @@ def gated_forward(X, W, bias=None, activation="silu", save=False, H=None, P=None
         if have:
             workspace = torch.empty(have, dtype=torch.uint8, device=d)
     else:
-        have = workspace.numel() * workspace.element_size()
+        have = scratch(workspace, d)
     st = lib().dga_gated(code, act, M, F, K, x, ldx, w, ldw, None if bias is None else vector(bias, N, dtype, X.device), H.data_ptr(),
                          ldh, p, ldp, workspace.data_ptr() if have else None, have, _raw_stream(d))
     if st:
@@ -154,7 +161,7 @@ def gated_backward(X, W, P, G, activation="silu", need_bias=False, need_x=True, 
         if have:
             workspace = torch.empty(have, dtype=torch.uint8, device=dev)
     else:
-        have = workspace.numel() * workspace.element_size()
+        have = scratch(workspace, dev.index)
     st = lib().dga_gated_backward(code, act, M, F, K, x, ldx, w, ldw, P.data_ptr(), ldp, G.data_ptr(), ldg, dx, lddx, dw,
                                   lddw, db.data_ptr() if need_bias else None, workspace.data_ptr() if have else None, have,
                                   _raw_stream(dev.index))

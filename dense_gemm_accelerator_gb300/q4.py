@@ -13,7 +13,7 @@ import functools
 import torch
 
 from . import F32, DgaError, _check_lines, _current_device, _elsewhere, _on_device, _raw_stream, lib
-from .gated import activation_code, result, vector
+from .gated import activation_code, result, scratch, vector
 from .mx import _CODE, _TORCH, _rows_of, on_stream
 
 _U8 = torch.uint8
@@ -191,7 +191,7 @@ def q4_linear_forward(X, W, bias=None, Y=None, workspace=None, stream=None):
         if have:
             workspace = torch.empty(have, dtype=_U8, device=d)
     else:
-        have = workspace.numel() * workspace.element_size()
+        have = scratch(workspace, d)
     st = lib().dga_q4_linear(code, M, N, K, W.group, x, ldx, c, lc, s, ls, z, lz,
                              None if bias is None else vector(bias, N, X.dtype, X.device), Y.data_ptr(), ldy,
                              workspace.data_ptr() if have else None, have, _raw_stream(d))
@@ -226,7 +226,7 @@ def q4_gated_forward(X, W, bias=None, activation="silu", H=None, workspace=None,
         if have:
             workspace = torch.empty(have, dtype=_U8, device=d)
     else:
-        have = workspace.numel() * workspace.element_size()
+        have = scratch(workspace, d)
     st = lib().dga_q4_gated(code, act, M, F, K, W.group, x, ldx, c, lc, s, ls, z, lz,
                             None if bias is None else vector(bias, N, X.dtype, X.device), H.data_ptr(), ldh,
                             workspace.data_ptr() if have else None, have, _raw_stream(d))

@@ -83,3 +83,16 @@ def test_each_device_has_its_own_size(fake):
             call()
         assert fake.given == [size] * 4, d
         fake.given.clear()
+
+
+def test_workspaces_that_are_refused(fake):
+    """One on the host, on another device, or whose values are not all its own."""
+    whole = On.of(0, 4096, dtype=torch.uint8)
+    for bad in (torch.zeros(4096, dtype=torch.uint8), On.of(1, 4096, dtype=torch.uint8), On.of(0, 1, dtype=torch.uint8).expand(4096), whole[::2]):
+        for call in _calls(0, bad):
+            with pytest.raises(ValueError):
+                call()
+    assert not fake.given
+    for call in _calls(0, whole):
+        call()
+    assert fake.given == [4096] * 4
