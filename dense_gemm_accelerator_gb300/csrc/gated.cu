@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(256) sum_slices_kernel(int64_t cols, int slice
 // Eight values of a row to a thread, four rows of them in flight; zero past the
 // row's end; read by words of two, and shifted where the row starts between two (at
 // the array's ends one by one).  The grid's z is the array: a call's two in one
-// launch (a gated layer of 300 x 2051 to 700, whose X and W both need it: 23.5 us a
-// call from the host with two launches, 19.6 with one; 24.0 us in a graph).
+// launch (a gated layer of 300 x 2051 to 700, whose X and W both need it: 27.5 us a
+// call from the host, some 4 more with two launches; 23.4 us in a graph).
 constexpr int kCopyX = 64, kCopyY = 4, kCopyRows = 4;
 
 __global__ void __launch_bounds__(kCopyX * kCopyY) copy_rows_kernel(CopyRows a, CopyRows b) {

@@ -3,7 +3,9 @@
 //   w = (q - z) * s,  q and z in 0..15, a scale s (bf16 or fp16) and a zero
 //   point z (a byte, or 8 throughout) per row and group of 32, 64 or 128 columns
 //
-// Both passes are bound by memory.
+// 8192 x 8192, groups of 128, bf16: back to values in 42.5 us, 4 TB/s.  To codes it takes
+// 149 us (groups of 64: 217, of 32: 363) where the bytes take 25: the instructions of a
+// warp to a group, a lane one to four values, fill 83 % of the issue slots.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -71,7 +73,8 @@ __global__ void __launch_bounds__(256)
 
 // A thread a word of codes, eight values; the grid's y walks the rows, four at a
 // time with their loads together (a row's division out of one index took longer
-// than the copy).
+// than the copy).  The gated layer's kernel behind it is a programmatic dependent;
+// the GEMM is one only where it repacks X first, else an ordinary launch.
 template <typename TS, typename T, bool kVec>
 __global__ void __launch_bounds__(256)
     q4_dequantize_kernel(int64_t rows, int64_t cols, Q4Matrix q, int shift, T* __restrict__ Y, int64_t ldy) {

@@ -2,10 +2,13 @@
 //     Y[M, N] = X[M, K] ((q - z) s)[N, K]^T + bias,
 // and the gated layer H = act(g) * u on them.
 //
-// The bytes of the codes bound it (half a byte to a weight), so each is read
+// The bytes of the codes are its floor (half a byte to a weight), so each is read
 // once and multiplied as what it is: q - z is a small integer, exact in bf16 and
 // fp16, and mma.sync m16n8k16 multiplies it by X exactly and sums in fp32; the
 // sum over (a part of) a group is then scaled by s in fp32.  No weight is rounded.
+// 8192 x 8192 in groups of 128, bf16, one row: 14.4 us where the bytes take 5.2; no pipe is
+// full (ALU 57 %, issue 52 %, DRAM 25 %): eleven steps to eight codes, and the scales' table,
+// which is filled before the first of them.
 //
 //  * The grid is whole waves of a block per SM, and the weight's rows are shared
 //    out evenly, up to 64 to a block (of a gated layer up to 32 gate rows and the

@@ -452,17 +452,16 @@ __global__ void __launch_bounds__(kThreads) sgemm_tail_reduce(Params p) {
 // than paired blocks do, and splitting that wave along K measured slower at
 // 4096^3 on GB300.  With fewer tiles than resident blocks, most SMs would
 // idle, so every tile is cut along K into `parts` ranges (2-4, each at least
-// 256 deep) whose partial sums are added afterwards.  parts == 1: no split.
+// 256 deep; `deep`, GemmArgs::deep: 2-16 of at least 64) whose partial sums are
+// added afterwards.  parts == 1: no split.  A gated layer's gradients at 256 x 512,
+// K = 1400, and 1400 x 512, K = 256, with the pass before them: 72 us with at most 4
+// ranges of 256, 36 with deep ones.
 struct Schedule {
     int64_t tiles, tiles_n, full_tiles, part_k;
     int parts;
     size_t partial_bytes;
 };
 
-//
-// deep (GemmArgs::deep): up to 16 ranges, each at least 64 deep.  A gated
-// layer's gradients at 256 x 512, K = 1400, and 1400 x 512, K = 256, with the pass before
-// them: 72 us with at most 4 ranges of 256, 36 so.
 Schedule plan_schedule(int64_t M, int64_t N, int64_t K, int sm_count, bool deep) {
     Schedule sc{};
     sc.tiles_n = (N + BN - 1) / BN;
